@@ -29,6 +29,8 @@ EXPORTS = (
     "ds4c_indexer_topk_noalloc", "ds4c_checkpoint_scatter", "ds4c_payload_header", "ds4c_fma_probe",
     "ds4c_payload_bytes", "ds4c_payload_write", "ds4c_payload_read", "ds4c_compress_prefill_timed",
     "ds4c_indexer_topk_heads", "ds4c_test_set_wait_limit", "ds4c_test_wait_timeout",
+    "ds4c_quant_row_bytes", "ds4c_quant_scale_bytes", "ds4c_rmsnorm_quant", "ds4c_quant_weight", "ds4c_quant_matmul",
+    "ds4c_compress_prefill_quant", "ds4c_compress_decode_step_quant",
 )
 PAYLOAD_U32_FIELDS = 13
 NOALLOC_SCORE_FLOATS = 2 * 1024 * 1024
@@ -54,6 +56,23 @@ class LayerCfg(C.Structure):
 
 class LaneWeights(C.Structure):
     _fields_ = [("wkv", C.c_void_p), ("wgate", C.c_void_p), ("ape", C.c_void_p), ("norm", C.c_void_p)]
+
+
+class LaneWeightsQuant(C.Structure):
+    _fields_ = [("wkv", C.c_void_p), ("wkv_scale", C.c_void_p), ("wgate", C.c_void_p), ("wgate_scale", C.c_void_p),
+                ("ape", C.c_void_p), ("norm", C.c_void_p)]
+
+
+class RmsnormArgs(C.Structure):
+    _fields_ = [("n", C.c_uint32), ("d", C.c_uint32), ("dtype", C.c_uint32), ("eps", C.c_float), ("x", C.c_void_p),
+                ("residual", C.c_void_p), ("residual_out", C.c_void_p), ("y_out", C.c_void_p), ("x_ld", C.c_size_t),
+                ("residual_ld", C.c_size_t), ("residual_out_ld", C.c_size_t), ("y_ld", C.c_size_t),
+                ("gain", C.c_void_p), ("q", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class QuantMatrix(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("scale", C.c_void_p), ("out", C.c_void_p), ("out_ld", C.c_size_t),
+                ("n", C.c_uint32)]
 
 
 class PayloadInfo(C.Structure):
@@ -84,6 +103,7 @@ def lib() -> C.CDLL:
     L = C.CDLL(LIB_PATH)
     P, U32, U64, SZ = C.c_void_p, C.c_uint32, C.c_uint64, C.c_size_t
     cfgp, lwp, lsp = C.POINTER(LayerCfg), C.POINTER(LaneWeights), C.POINTER(LayerState)
+    lqp = C.POINTER(LaneWeightsQuant)
     st = C.c_int
     sig = {
         "ds4c_workspace_bytes": (SZ, [cfgp, U32, U32]),
@@ -104,6 +124,13 @@ def lib() -> C.CDLL:
         "ds4c_payload_write": (st, [C.POINTER(PayloadInfo), cfgp, lsp, U32, U32, P, P, P, SZ, C.POINTER(SZ), P]),
         "ds4c_payload_read": (st, [C.POINTER(PayloadInfo), cfgp, lsp, U32, U32, P, SZ, P, SZ, P,
                                    C.POINTER(U32), P]),
+        "ds4c_quant_row_bytes": (SZ, [U32]),
+        "ds4c_quant_scale_bytes": (SZ, [U32]),
+        "ds4c_rmsnorm_quant": (st, [C.POINTER(RmsnormArgs), P]),
+        "ds4c_quant_weight": (st, [U32, U32, U32, P, SZ, P, P, P]),
+        "ds4c_quant_matmul": (st, [U32, U32, P, P, C.POINTER(QuantMatrix), U32, U32, P]),
+        "ds4c_compress_prefill_quant": (st, [cfgp, lqp, lqp, lsp, P, P, U32, U64, P, SZ, P]),
+        "ds4c_compress_decode_step_quant": (st, [cfgp, lqp, lqp, lsp, P, P, C.POINTER(U64), U32, P, SZ, P]),
         "ds4c_fma_probe": (st, [U32, U32, P, C.POINTER(C.c_double), P]),
         "ds4c_test_set_wait_limit": (st, [U64]),
         "ds4c_test_wait_timeout": (st, [U64, P]),
@@ -164,6 +191,40 @@ def ds4c_compress_decode_step(cfg, attn_w, idx_w, state, hidden, pos_h, n_seq, w
     return lib().ds4c_compress_decode_step(C.byref(cfg), C.byref(attn_w) if attn_w is not None else None,
                                            C.byref(idx_w) if idx_w is not None else None, C.byref(state),
                                            hidden, pos_h, n_seq, ws, ws_bytes, stream)
+
+
+def ds4c_quant_row_bytes(k):
+    return lib().ds4c_quant_row_bytes(k)
+
+
+def ds4c_quant_scale_bytes(k):
+    return lib().ds4c_quant_scale_bytes(k)
+
+
+def ds4c_rmsnorm_quant(args, stream):
+    return lib().ds4c_rmsnorm_quant(C.byref(args), stream)
+
+
+def ds4c_quant_weight(n, k, dtype, w, w_ld, q, scale, stream):
+    return lib().ds4c_quant_weight(n, k, dtype, w, w_ld, q, scale, stream)
+
+
+def ds4c_quant_matmul(m, k, a, a_scale, matrices, n_w, out_dtype, stream):
+    """matrices: a ctypes array of QuantMatrix, of which the first n_w are used."""
+    return lib().ds4c_quant_matmul(m, k, a, a_scale, matrices, n_w, out_dtype, stream)
+
+
+def ds4c_compress_prefill_quant(cfg, attn_w, idx_w, state, hidden, hidden_scale, n_tok, pos0, ws, ws_bytes, stream):
+    return lib().ds4c_compress_prefill_quant(C.byref(cfg), C.byref(attn_w) if attn_w is not None else None,
+                                             C.byref(idx_w) if idx_w is not None else None, C.byref(state), hidden,
+                                             hidden_scale, n_tok, pos0, ws, ws_bytes, stream)
+
+
+def ds4c_compress_decode_step_quant(cfg, attn_w, idx_w, state, hidden, hidden_scale, pos_h, n_seq, ws, ws_bytes,
+                                    stream):
+    return lib().ds4c_compress_decode_step_quant(C.byref(cfg), C.byref(attn_w) if attn_w is not None else None,
+                                                 C.byref(idx_w) if idx_w is not None else None, C.byref(state),
+                                                 hidden, hidden_scale, pos_h, n_seq, ws, ws_bytes, stream)
 
 
 def ds4c_indexer_topk(cfg, state, q_idx, pos_h, n_seq, n_tok, topk, scores, score_stride, ws, ws_bytes, stream):

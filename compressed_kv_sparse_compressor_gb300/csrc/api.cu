@@ -12,6 +12,7 @@ namespace {
 
 bool pow2_width(uint32_t w) { return w == 64 || w == 128 || w == 256 || w == 512; }
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }
 
 }  // namespace
 
@@ -155,17 +156,33 @@ ds4c_status check_lane_weights(const ds4c_lane_weights *w) {
     return DS4C_OK;
 }
 
-// Shared front half of prefill and decode compression: projections into the
-// workspace, then the fused compressor.
-ds4c_status run_compress(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *aw, const ds4c_lane_weights *iw,
-                         const ds4c_layer_state *st, const void *hidden, uint32_t rows, uint64_t pos0,
-                         const DecodePos *dp, void *ws, cudaStream_t stream, cudaEvent_t after_projection = nullptr) {
-    const ds4c_layer_cfg &c = *cfg;
-    const WsLayout L = (dp == nullptr) ? ws_prefill(c, rows) : ws_decode(c, rows);
+ds4c_status check_lane_weights(const ds4c_lane_weights_quant *w) {
+    if (!w || !w->wkv || !w->wkv_scale || !w->wgate || !w->wgate_scale || !w->ape) return DS4C_ERR_NULL;
+    if (!aligned16(w->wkv) || !aligned16(w->wgate) || !aligned16(w->ape) || !aligned16(w->norm)) return DS4C_ERR_SHAPE;
+    if (!aligned4(w->wkv_scale) || !aligned4(w->wgate_scale)) return DS4C_ERR_SHAPE;
+    return DS4C_OK;
+}
+
+// The hidden rows of a compress call: cfg->dtype values, or E4M3 rows with their scales.
+struct Hidden {
+    const void *rows;
+    const uint8_t *scale;            // quantised calls only
+};
+ds4c_status check_hidden(const ds4c_lane_weights *, const Hidden &h) {
+    return aligned16(h.rows) ? DS4C_OK : DS4C_ERR_SHAPE;
+}
+ds4c_status check_hidden(const ds4c_lane_weights_quant *, const Hidden &h) {
+    if (!h.scale) return DS4C_ERR_NULL;
+    return aligned16(h.rows) && aligned4(h.scale) ? DS4C_OK : DS4C_ERR_SHAPE;
+}
+
+// Projections of `rows` hidden rows into the workspace's [rows][P] block, in the layer's own weights ...
+cudaError_t project(const ds4c_layer_cfg &c, const ds4c_lane_weights *aw, const ds4c_lane_weights *iw, const Hidden &hidden,
+                    uint32_t rows, const WsLayout &L, void *ws, cudaStream_t stream) {
     float *proj = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + L.proj_off);
     const int Wa = proj_width(c, true), Wi = proj_width(c, false);
     GemmArgs g{};
-    g.A = hidden;
+    g.A = hidden.rows;
     g.M = (int)rows;
     g.K = (int)c.d_model;
     g.dtype = (int)c.dtype;
@@ -187,6 +204,42 @@ ds4c_status run_compress(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *aw,
     cudaError_t e = cudaErrorNotSupported;
     if (c.dtype == DS4C_BF16) e = launch_gemm_tc(g, stream);
     if (e == cudaErrorNotSupported) e = launch_gemm_simt(g, stream);
+    return e;
+}
+
+// ... or in quantised ones.
+cudaError_t project(const ds4c_layer_cfg &c, const ds4c_lane_weights_quant *aw, const ds4c_lane_weights_quant *iw,
+                    const Hidden &hidden, uint32_t rows, const WsLayout &L, void *ws, cudaStream_t stream) {
+    float *proj = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + L.proj_off);
+    const int Wa = proj_width(c, true), Wi = proj_width(c, false);
+    QuantMatmulArgs g{};
+    g.a = static_cast<const uint8_t *>(hidden.rows);
+    g.a_scale = hidden.scale;
+    g.m = (int)rows;
+    g.k = (int)c.d_model;
+    g.out_dtype = DS4C_F32;
+    g.n_w = 2;
+    g.w[0] = ds4c_quant_matrix{aw->wkv, aw->wkv_scale, proj, L.proj_ld, (uint32_t)Wa};
+    g.w[1] = ds4c_quant_matrix{aw->wgate, aw->wgate_scale, proj + Wa, L.proj_ld, (uint32_t)Wa};
+    if (c.ratio == 4) {
+        g.n_w = 4;
+        g.w[2] = ds4c_quant_matrix{iw->wkv, iw->wkv_scale, proj + 2 * Wa, L.proj_ld, (uint32_t)Wi};
+        g.w[3] = ds4c_quant_matrix{iw->wgate, iw->wgate_scale, proj + 2 * Wa + Wi, L.proj_ld, (uint32_t)Wi};
+    }
+    return launch_quant_matmul(g, stream);
+}
+
+// Shared front half of prefill and decode compression: projections into the
+// workspace, then the fused compressor.  W: ds4c_lane_weights or its quantised form.
+template <typename W>
+ds4c_status run_compress(const ds4c_layer_cfg *cfg, const W *aw, const W *iw, const ds4c_layer_state *st,
+                         const Hidden &hidden, uint32_t rows, uint64_t pos0, const DecodePos *dp, void *ws,
+                         cudaStream_t stream, cudaEvent_t after_projection = nullptr) {
+    const ds4c_layer_cfg &c = *cfg;
+    const WsLayout L = (dp == nullptr) ? ws_prefill(c, rows) : ws_decode(c, rows);
+    float *proj = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + L.proj_off);
+    const int Wa = proj_width(c, true), Wi = proj_width(c, false);
+    cudaError_t e = project(c, aw, iw, hidden, rows, L, ws, stream);
     if (e != cudaSuccess) return cuda_status(e);
     if (after_projection && (e = cudaEventRecord(after_projection, stream)) != cudaSuccess) return cuda_status(e);
 
@@ -198,14 +251,14 @@ ds4c_status run_compress(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *aw,
     a.rope = rope_table(c);
     for (int l = 0; l < a.n_lanes; l++) {
         const bool attn = l == 0;
-        const ds4c_lane_weights *w = attn ? aw : iw;
+        const W *w = attn ? aw : iw;
         const ds4c_lane_state &s = attn ? st->attn : st->idx;
         LaneArgs &la = a.lane[l];
         const int col0 = attn ? 0 : 2 * Wa;
-        const int W = attn ? Wa : Wi;
+        const int width = attn ? Wa : Wi;
         la.kv = proj + col0;
         la.kv_ld = (int64_t)L.proj_ld;
-        la.sc = proj + col0 + W;
+        la.sc = proj + col0 + width;
         la.sc_ld = (int64_t)L.proj_ld;
         la.ape = w->ape;
         la.gain = w->norm;
@@ -301,15 +354,19 @@ ds4c_status ds4c_state_init(const ds4c_layer_cfg *cfg, const ds4c_layer_state *s
     return cuda_status(e);
 }
 
-static ds4c_status compress_prefill_impl(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
-                                         const ds4c_lane_weights *idx, const ds4c_layer_state *st,
-                                         const void *hidden, uint32_t n_tok, uint64_t pos0, void *ws,
-                                         size_t ws_bytes, cudaStream_t stream, cudaEvent_t after_projection) {
+}  // extern "C"
+
+namespace {
+
+template <typename W>
+ds4c_status compress_prefill_impl(const ds4c_layer_cfg *cfg, const W *attn, const W *idx, const ds4c_layer_state *st,
+                                  const Hidden &hidden, uint32_t n_tok, uint64_t pos0, void *ws, size_t ws_bytes,
+                                  cudaStream_t stream, cudaEvent_t after_projection) {
     ds4c_status s = check_cfg(cfg);
     if (s != DS4C_OK) return s;
     const ds4c_layer_cfg &c = *cfg;
     if (c.ratio == 0 || n_tok == 0) return DS4C_OK;
-    if (!st || !hidden) return DS4C_ERR_NULL;
+    if (!st || !hidden.rows) return DS4C_ERR_NULL;
     if ((s = check_lane_weights(attn)) != DS4C_OK) return s;
     if ((s = check_lane_state(st->attn)) != DS4C_OK) return s;
     if (c.ratio == 4) {
@@ -318,7 +375,7 @@ static ds4c_status compress_prefill_impl(const ds4c_layer_cfg *cfg, const ds4c_l
     } else if (idx != nullptr) {
         return DS4C_ERR_SHAPE;
     }
-    if (!aligned16(hidden)) return DS4C_ERR_SHAPE;
+    if ((s = check_hidden(attn, hidden)) != DS4C_OK) return s;
     const uint64_t end = pos0 + n_tok;
     if (end / c.ratio > c.comp_cap) return DS4C_ERR_CAPACITY;
     if (c.ratio == 4 && end / 4 > c.idx_cap) return DS4C_ERR_CAPACITY;
@@ -328,25 +385,10 @@ static ds4c_status compress_prefill_impl(const ds4c_layer_cfg *cfg, const ds4c_l
     return run_compress(cfg, attn, idx, st, hidden, n_tok, pos0, nullptr, ws, stream, after_projection);
 }
 
-ds4c_status ds4c_compress_prefill(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
-                                  const ds4c_lane_weights *idx, const ds4c_layer_state *st,
-                                  const void *hidden, uint32_t n_tok, uint64_t pos0,
-                                  void *ws, size_t ws_bytes, cudaStream_t stream) {
-    return compress_prefill_impl(cfg, attn, idx, st, hidden, n_tok, pos0, ws, ws_bytes, stream, nullptr);
-}
-
-ds4c_status ds4c_compress_prefill_timed(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
-                                        const ds4c_lane_weights *idx, const ds4c_layer_state *st,
-                                        const void *hidden, uint32_t n_tok, uint64_t pos0, void *ws,
-                                        size_t ws_bytes, cudaEvent_t after_projection, cudaStream_t stream) {
-    if (!after_projection) return DS4C_ERR_NULL;
-    return compress_prefill_impl(cfg, attn, idx, st, hidden, n_tok, pos0, ws, ws_bytes, stream, after_projection);
-}
-
-ds4c_status ds4c_compress_decode_step(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
-                                      const ds4c_lane_weights *idx, const ds4c_layer_state *st,
-                                      const void *hidden, const uint64_t *pos_h, uint32_t n_seq,
-                                      void *ws, size_t ws_bytes, cudaStream_t stream) {
+template <typename W>
+ds4c_status compress_decode_impl(const ds4c_layer_cfg *cfg, const W *attn, const W *idx, const ds4c_layer_state *st,
+                                 const Hidden &hidden, const uint64_t *pos_h, uint32_t n_seq, void *ws, size_t ws_bytes,
+                                 cudaStream_t stream) {
     ds4c_status s = check_cfg(cfg);
     if (s != DS4C_OK) return s;
     const ds4c_layer_cfg &c = *cfg;
@@ -354,7 +396,7 @@ ds4c_status ds4c_compress_decode_step(const ds4c_layer_cfg *cfg, const ds4c_lane
     if (n_seq > (uint32_t)kMaxDecodeSeq) return DS4C_ERR_UNSUPPORTED;
     if (!pos_h) return DS4C_ERR_NULL;
     if (c.ratio == 0) return DS4C_OK;
-    if (!st || !hidden) return DS4C_ERR_NULL;
+    if (!st || !hidden.rows) return DS4C_ERR_NULL;
     if ((s = check_lane_weights(attn)) != DS4C_OK) return s;
     if ((s = check_lane_state(st->attn)) != DS4C_OK) return s;
     if (c.ratio == 4) {
@@ -363,7 +405,7 @@ ds4c_status ds4c_compress_decode_step(const ds4c_layer_cfg *cfg, const ds4c_lane
     } else if (idx != nullptr) {
         return DS4C_ERR_SHAPE;
     }
-    if (!aligned16(hidden)) return DS4C_ERR_SHAPE;
+    if ((s = check_hidden(attn, hidden)) != DS4C_OK) return s;
     DecodePos dp;
     for (uint32_t b = 0; b < n_seq; b++) {
         const uint64_t end = pos_h[b] + 1;
@@ -375,6 +417,48 @@ ds4c_status ds4c_compress_decode_step(const ds4c_layer_cfg *cfg, const ds4c_lane
     if (!ws) return DS4C_ERR_WORKSPACE;
     if (ws_bytes < ws_decode(c, n_seq).total) return DS4C_ERR_WORKSPACE;
     return run_compress(cfg, attn, idx, st, hidden, n_seq, 0, &dp, ws, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+ds4c_status ds4c_compress_prefill(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
+                                  const ds4c_lane_weights *idx, const ds4c_layer_state *st,
+                                  const void *hidden, uint32_t n_tok, uint64_t pos0,
+                                  void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return compress_prefill_impl(cfg, attn, idx, st, Hidden{hidden, nullptr}, n_tok, pos0, ws, ws_bytes, stream, nullptr);
+}
+
+ds4c_status ds4c_compress_prefill_timed(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
+                                        const ds4c_lane_weights *idx, const ds4c_layer_state *st,
+                                        const void *hidden, uint32_t n_tok, uint64_t pos0, void *ws,
+                                        size_t ws_bytes, cudaEvent_t after_projection, cudaStream_t stream) {
+    if (!after_projection) return DS4C_ERR_NULL;
+    return compress_prefill_impl(cfg, attn, idx, st, Hidden{hidden, nullptr}, n_tok, pos0, ws, ws_bytes, stream,
+                                 after_projection);
+}
+
+ds4c_status ds4c_compress_decode_step(const ds4c_layer_cfg *cfg, const ds4c_lane_weights *attn,
+                                      const ds4c_lane_weights *idx, const ds4c_layer_state *st,
+                                      const void *hidden, const uint64_t *pos_h, uint32_t n_seq,
+                                      void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return compress_decode_impl(cfg, attn, idx, st, Hidden{hidden, nullptr}, pos_h, n_seq, ws, ws_bytes, stream);
+}
+
+ds4c_status ds4c_compress_prefill_quant(const ds4c_layer_cfg *cfg, const ds4c_lane_weights_quant *attn,
+                                        const ds4c_lane_weights_quant *idx, const ds4c_layer_state *st,
+                                        const uint8_t *hidden, const uint8_t *hidden_scale, uint32_t n_tok,
+                                        uint64_t pos0, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return compress_prefill_impl(cfg, attn, idx, st, Hidden{hidden, hidden_scale}, n_tok, pos0, ws, ws_bytes, stream,
+                                 nullptr);
+}
+
+ds4c_status ds4c_compress_decode_step_quant(const ds4c_layer_cfg *cfg, const ds4c_lane_weights_quant *attn,
+                                            const ds4c_lane_weights_quant *idx, const ds4c_layer_state *st,
+                                            const uint8_t *hidden, const uint8_t *hidden_scale, const uint64_t *pos_h,
+                                            uint32_t n_seq, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return compress_decode_impl(cfg, attn, idx, st, Hidden{hidden, hidden_scale}, pos_h, n_seq, ws, ws_bytes, stream);
 }
 
 ds4c_status ds4c_indexer_topk(const ds4c_layer_cfg *cfg, const ds4c_layer_state *st, const float *q_idx,

@@ -203,6 +203,25 @@ cudaError_t launch_gemm_tc(const GemmArgs &a, cudaStream_t s);
 unsigned int gemm_tc_read_clear_error();
 
 // ----------------------------------------------------------------------------
+// 8-bit projections: RMSNorm with E4M3 output, weight quantisation, product
+// ----------------------------------------------------------------------------
+constexpr uint32_t kMaxNormDim = 32768;
+inline size_t quant_row_bytes(uint32_t k) { return align_up(k, 16); }
+inline size_t quant_scale_bytes(uint32_t k) { return align_up(((size_t)k + 127) / 128, 4); }
+cudaError_t launch_rmsnorm_quant(const ds4c_rmsnorm_args &a, cudaStream_t s);
+cudaError_t launch_quant_weight(uint32_t n, uint32_t k, uint32_t dtype, const void *w, size_t w_ld, uint8_t *q,
+                                uint8_t *scale, cudaStream_t s);
+
+struct QuantMatmulArgs {
+    const uint8_t *a, *a_scale;
+    int m, k;
+    int out_dtype;
+    int n_w;
+    ds4c_quant_matrix w[4];
+};
+cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s);
+
+// ----------------------------------------------------------------------------
 // Compressor (store + APE, pool, RMSNorm, tail RoPE, FP8, append, frontier).
 // ----------------------------------------------------------------------------
 struct RopeTable { float inv_freq[kMaxRot / 2]; };

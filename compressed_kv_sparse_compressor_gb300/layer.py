@@ -8,7 +8,7 @@ import ctypes as C
 
 import torch
 
-from . import abi
+from . import abi, fp8
 from .configs import LayerShape
 
 
@@ -67,6 +67,7 @@ class DeviceLayer:
             raise abi.Ds4cError(abi.DS4C_ERR_SHAPE, "ds4c_workspace_bytes")
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.attn_w = self.idx_w = None
+        self.attn_wq = self.idx_wq = None
         self._keep = []
 
     # -- weights -------------------------------------------------------------
@@ -80,6 +81,20 @@ class DeviceLayer:
             self.attn_w = lw(attn)
         if self.shape.ratio == 4:
             self.idx_w = lw(idx)
+
+    def set_weights_quant(self, attn, idx=None):
+        """attn / idx = (wkv, wgate, ape, norm): the projections float tensors, quantised here on the
+        device, or fp8.Fp8Weight; ape and norm as set_weights."""
+        def lw(w):
+            kv, gate = (x if isinstance(x, fp8.Fp8Weight) else fp8.quantize_weight(x.to(self.device)) for x in w[:2])
+            ape, norm = (None if x is None else x.to(self.device).contiguous() for x in w[2:])
+            self._keep.append((kv, gate, ape, norm))
+            return abi.LaneWeightsQuant(_ptr(kv.q), _ptr(kv.scale), _ptr(gate.q), _ptr(gate.scale), _ptr(ape),
+                                        _ptr(norm))
+        if self.shape.ratio:
+            self.attn_wq = lw(attn)
+        if self.shape.ratio == 4:
+            self.idx_wq = lw(idx)
 
     # -- calls -----------------------------------------------------------------
     def state_init(self):
@@ -104,6 +119,22 @@ class DeviceLayer:
         abi.check(abi.ds4c_compress_decode_step(self.cfg, self.attn_w, self.idx_w, self.state, _ptr(hidden), pos,
                                                 len(positions), _ptr(self.ws), self.ws_bytes, _stream()),
                   "ds4c_compress_decode_step")
+
+    def compress_prefill_quant(self, hidden, hidden_scale, pos0: int):
+        """hidden, hidden_scale: quantised rows as fp8.rmsnorm returns them."""
+        fp8.check_rows(hidden, hidden_scale, self.shape.d_model)
+        abi.check(abi.ds4c_compress_prefill_quant(self.cfg, self.attn_wq, self.idx_wq, self.state, _ptr(hidden),
+                                                  _ptr(hidden_scale), hidden.shape[0], pos0, _ptr(self.ws),
+                                                  self.ws_bytes, _stream()), "ds4c_compress_prefill_quant")
+
+    def compress_decode_quant(self, hidden, hidden_scale, positions):
+        fp8.check_rows(hidden, hidden_scale, self.shape.d_model)
+        if hidden.shape[0] != len(positions):
+            raise ValueError(f"{hidden.shape[0]} hidden rows for {len(positions)} positions")
+        pos = abi.u64_array(positions)
+        abi.check(abi.ds4c_compress_decode_step_quant(self.cfg, self.attn_wq, self.idx_wq, self.state, _ptr(hidden),
+                                                      _ptr(hidden_scale), pos, len(positions), _ptr(self.ws),
+                                                      self.ws_bytes, _stream()), "ds4c_compress_decode_step_quant")
 
     def indexer_topk(self, q_idx, positions, n_seq, n_tok, topk, scores=None, score_stride=0):
         pos = abi.u64_array(positions)

@@ -236,6 +236,100 @@ DS4C_API ds4c_status ds4c_sparse_swa_attn(const ds4c_layer_cfg *cfg, const ds4c_
                                  float *out, int commit_ring, void *ws, size_t ws_bytes,
                                  cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit projections: the RMSNorm in front of a layer writing E4M3 rows, weights
+ * quantised in blocks, the product of the two, and the compressor fed by it.
+ *
+ * A quantised row of k values is k OCP E4M3FN bytes with one E8M0 scale byte
+ * (value 2^(byte - 127)) per block of 128 values, the last block shorter; a
+ * value is code * scale.  The rule is the cache's own (the E4M3 round trip of
+ * compressed rows, here per 128 values): with amax the largest finite magnitude
+ * of the block, the scale is the smallest 2^e with amax <= 448 * 2^e, at least
+ * 2^-127, and 1 for a block without a finite value other than 0; codes round to
+ * nearest even, and a value that is not finite becomes the NaN code.
+ *   rows:   [n][ds4c_quant_row_bytes(k)] bytes, k rounded up to 16;
+ *   scales: [n][ds4c_quant_scale_bytes(k)] bytes, ceil(k / 128) rounded up to 4;
+ *   a weight matrix [n][k] has one scale per 128 x 128 block, so its scales
+ *   are [ceil(n / 128)][ds4c_quant_scale_bytes(k)].
+ * Padding bytes are neither read as values nor written.  Rows start on 16-byte
+ * boundaries, scales on 4-byte ones (else DS4C_ERR_SHAPE).  The calls take any
+ * stream, keep nothing between calls and use no workspace; inputs and outputs
+ * of one call must not overlap except where a call says so. */
+DS4C_API size_t ds4c_quant_row_bytes(uint32_t k);
+DS4C_API size_t ds4c_quant_scale_bytes(uint32_t k);
+
+/* RMSNorm of n rows of d values with the residual's addition and an 8-bit output:
+ *   h = x + residual, in float, rounded to dtype (h = x without a residual);
+ *   rstd = float((sum of h^2 / d + eps)^-1/2), the sum carried to more than
+ *          float precision so that the codes do not hang on its order;
+ *   y = float(float(h * rstd) * gain) (gain NULL: ones), quantised as above.
+ * x, residual, residual_out: [n] rows of d elements of dtype (DS4C_F32 or
+ * DS4C_BF16) at pitches of *_ld elements (>= d); residual and residual_out (h)
+ * are optional, and residual_out may be x's or residual's own buffer.
+ * q / scale: the quantised rows, both or neither; y_out (optional): y rounded
+ * to dtype, at a pitch of y_ld.  At least one of residual_out, q and y_out.
+ * gain: [d] float.  1 <= d <= 32768, 1e-12 <= eps <= 1.  n == 0 does nothing. */
+typedef struct {
+    uint32_t n, d;
+    uint32_t dtype;
+    float eps;
+    const void *x;
+    const void *residual;
+    void *residual_out;
+    void *y_out;
+    size_t x_ld, residual_ld, residual_out_ld, y_ld;
+    const float *gain;
+    uint8_t *q;
+    uint8_t *scale;
+} ds4c_rmsnorm_args;
+DS4C_API ds4c_status ds4c_rmsnorm_quant(const ds4c_rmsnorm_args *args, cudaStream_t stream);
+
+/* Quantises a weight matrix w [n][k] of dtype (pitch w_ld >= k elements) in
+ * blocks of 128 x 128.  1 <= n <= 2^18, 1 <= k <= 2^18. */
+DS4C_API ds4c_status ds4c_quant_weight(uint32_t n, uint32_t k, uint32_t dtype, const void *w, size_t w_ld, uint8_t *q,
+                                       uint8_t *scale, cudaStream_t stream);
+
+/* out_g[i][j] = sum over k of a[i][k] * w_g[j][k] for 1 to 4 weight matrices over
+ * the same m quantised rows (a layer's wkv and wgate of both lanes are four),
+ * accumulated in float, out of out_dtype (DS4C_F32, or DS4C_BF16 rounded once) at
+ * a pitch of out_ld >= n elements.  A NaN code or a scale byte of 255 makes the
+ * outputs it enters NaN.  The result does not depend on the rows of the same
+ * call or on the SM count: row i's sums are taken in an order that m, n and k fix.
+ * m <= 2^24, n and k as ds4c_quant_weight; m == 0 does nothing. */
+typedef struct {
+    const uint8_t *q;       /* [n][ds4c_quant_row_bytes(k)] */
+    const uint8_t *scale;   /* [ceil(n / 128)][ds4c_quant_scale_bytes(k)] */
+    void *out;              /* [m] rows of n */
+    size_t out_ld;
+    uint32_t n;
+} ds4c_quant_matrix;
+DS4C_API ds4c_status ds4c_quant_matmul(uint32_t m, uint32_t k, const uint8_t *a, const uint8_t *a_scale,
+                                       const ds4c_quant_matrix *w, uint32_t n_w, uint32_t out_dtype,
+                                       cudaStream_t stream);
+
+/* One compressor lane with quantised projections: as ds4c_lane_weights, wkv and
+ * wgate [coff*Dl][d_model] quantised by ds4c_quant_weight. */
+typedef struct {
+    const uint8_t *wkv, *wkv_scale;
+    const uint8_t *wgate, *wgate_scale;
+    const float *ape;
+    const float *norm;
+} ds4c_lane_weights_quant;
+
+/* ds4c_compress_prefill and ds4c_compress_decode_step over quantised rows and
+ * weights: hidden [n][ds4c_quant_row_bytes(d_model)], hidden_scale [n]
+ * [ds4c_quant_scale_bytes(d_model)], as ds4c_rmsnorm_quant writes them.  cfg->dtype
+ * is not used; state, workspace, positions and errors as the calls they follow. */
+DS4C_API ds4c_status ds4c_compress_prefill_quant(const ds4c_layer_cfg *cfg, const ds4c_lane_weights_quant *attn,
+                                                 const ds4c_lane_weights_quant *idx, const ds4c_layer_state *state,
+                                                 const uint8_t *hidden, const uint8_t *hidden_scale, uint32_t n_tok,
+                                                 uint64_t pos0, void *ws, size_t ws_bytes, cudaStream_t stream);
+DS4C_API ds4c_status ds4c_compress_decode_step_quant(const ds4c_layer_cfg *cfg, const ds4c_lane_weights_quant *attn,
+                                                     const ds4c_lane_weights_quant *idx, const ds4c_layer_state *state,
+                                                     const uint8_t *hidden, const uint8_t *hidden_scale,
+                                                     const uint64_t *pos_h, uint32_t n_seq, void *ws, size_t ws_bytes,
+                                                     cudaStream_t stream);
+
 /* Score capacity of ds4c_indexer_topk_noalloc: 2M floats (8 MiB). */
 #define DS4C_NOALLOC_SCORE_FLOATS (2u * 1024u * 1024u)
 

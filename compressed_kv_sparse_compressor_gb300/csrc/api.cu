@@ -786,6 +786,7 @@ ds4c_status ds4c_test_set_wait_limit(uint64_t limit_ns) {
     cudaError_t e = gemm_tc_set_wait_ns(ns);
     if (e == cudaSuccess) e = attn_tc_set_wait_ns(ns);
     if (e == cudaSuccess) e = idx_set_wait_ns(ns);
+    if (e == cudaSuccess) e = qmm_set_wait_ns(ns);
     return cuda_status(e);
 }
 
@@ -796,8 +797,9 @@ ds4c_status ds4c_test_wait_timeout(uint64_t limit_ns, cudaStream_t stream) {
 ds4c_status ds4c_sync_status(cudaStream_t stream) {
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_status(e);
-    const unsigned int e1 = gemm_tc_read_clear_error(), e2 = attn_tc_read_clear_error(), e3 = idx_read_clear_error();
-    if (e1 != 0 || e2 != 0 || e3 != 0) return DS4C_ERR_DEVICE;
+    const unsigned int e1 = gemm_tc_read_clear_error(), e2 = attn_tc_read_clear_error(), e3 = idx_read_clear_error(),
+                       e4 = qmm_read_clear_error();
+    if (e1 != 0 || e2 != 0 || e3 != 0 || e4 != 0) return DS4C_ERR_DEVICE;
     return DS4C_OK;
 }
 

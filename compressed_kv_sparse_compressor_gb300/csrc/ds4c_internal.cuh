@@ -46,6 +46,7 @@ constexpr unsigned long long kDrainNs = 4000000000ull;
 cudaError_t gemm_tc_set_wait_ns(unsigned long long ns);
 cudaError_t attn_tc_set_wait_ns(unsigned long long ns);
 cudaError_t idx_set_wait_ns(unsigned long long ns);
+cudaError_t qmm_set_wait_ns(unsigned long long ns);
 // One CTA waits on an mbarrier that nothing arrives on, bounded by limit_ns, with
 // the indexer kernels' wait routine: it gives up, raises the indexer's error word
 // and returns (the self-test of the error path; no fault, no hang).
@@ -152,21 +153,31 @@ inline PdlPrev &pdl_prev() {
 }
 inline bool pdl_prev_is(cudaStream_t s, int kind) { return pdl_prev().s == s && pdl_prev().kind == kind; }
 
+// The same in clusters of `cluster` CTAs along x (1: none).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                              Args &&...args) {
+inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                      int cluster, Args &&...args) {
     pdl_prev().kind = PDL_ANY;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              Args &&...args) {
+    return launch_pdl_cluster(kernel, grid, block, smem, s, 1, static_cast<Args &&>(args)...);
 }
 
 // ----------------------------------------------------------------------------
@@ -220,6 +231,7 @@ struct QuantMatmulArgs {
     ds4c_quant_matrix w[4];
 };
 cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s);
+unsigned int qmm_read_clear_error();
 
 // ----------------------------------------------------------------------------
 // Compressor (store + APE, pool, RMSNorm, tail RoPE, FP8, append, frontier).

@@ -1,117 +1,464 @@
-// Product of quantised rows with quantised weights:
+// Product of quantised rows with quantised weights on the 5th-generation tensor cores:
 //   out_g[i][j] = sum_b 2^(ea[i][b] + ew_g[j / 128][b]) sum_{k in block b} a[i][k] w_g[j][k]
-// for 1 to 4 weight matrices over the same rows.
+// for 1 to 4 weight matrices over the same rows, E4M3 codes, float accumulation.
 //
-// 64 x 64 output tiles on the CUDA cores, K in slices of 16 (a slice lies in one
-// block of 128): codes are converted and scaled as they enter shared memory, which
-// is exact in float, and accumulated in float.
-#include "ds4c_internal.cuh"
-
+// The scales are powers of two, so the tensor cores' block-scaled form (kind::mxf8f6f4,
+// one E8M0 scale per operand row and 32 values of K) applies them in the product: a block
+// of 128 values is four MMAs that name the same scale byte.  The weights are the MMA's
+// M = 128 side and lie on the TMEM lanes, the rows are its N side: N follows the number
+// of rows (16 for a single token), and a warp's 32 lanes hold 32 neighbouring outputs of
+// one row, so the accumulator goes to global memory in whole lines straight from the
+// registers.
+//
+//   - K in stages of 128 bytes (one scale block): the weights' [128][128] and the rows'
+//     [BT][128] bytes by TMA in the 128-byte swizzle, a ring of mbarriers.  Rows and
+//     columns past the ends, and K past the last value, are filled with zeros.
+//   - Scales: one warp reads the four scale bytes of 4 stages per row as a word and lays
+//     them out in shared memory as TMEM wants them ([32 lanes][4 words], row r in lane
+//     r % 32, word r / 32); the MMA thread copies them to TMEM (tcgen05.cp, replicated to
+//     the four lane quarters) and the instruction descriptor picks the stage's byte.
+//   - A cluster of `split` CTAs shares an output tile, each with a range of K; the
+//     partial tiles meet through distributed shared memory and are added in rank order.
+//   - Every mbarrier wait is bounded; a wait that gives up raises the library's device
+//     error word and the CTA winds down, freeing its tensor memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
+
+#include "ds4c_internal.cuh"
 
 namespace ds4c {
 
+__device__ unsigned int g_qmm_err;
+__device__ unsigned long long g_qmm_wait_ns = kWaitNsDefault;
+
 namespace {
 
-constexpr int TILE = 64, KS = 16;
+constexpr int BW = 128, BK = 128;              // weight rows and K bytes of a stage
+constexpr int THREADS = 256;
+constexpr int SF_SLOTS = 2;                    // scale words of two groups of 4 stages in flight
+constexpr int SF_BYTES = 512;                  // scales of 128 rows, 4 stages
+constexpr int MAX_SPLIT = 8;
 
-struct Group {
-    const uint8_t *q, *scale;
-    void *out;
-    int64_t out_ld;
-    int n;
+template <int BT>
+struct Shape {
+    static constexpr int W_BYTES = BW * BK, T_BYTES = BT * BK, STAGE_BYTES = W_BYTES + T_BYTES;
+    static constexpr int STAGES = 4;
+    static constexpr int SFT = (BT + 127) / 128;               // 128-row units of the rows' scales
+    static constexpr int SF_SLOT_BYTES = SF_BYTES * (1 + SFT);
+    static constexpr int SF_COLS = 4 * (1 + SFT);
+    static constexpr int COLS = BT + SF_SLOTS * SF_COLS;
+    static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static constexpr int N_BARS = 2 * STAGES + 2 * SF_SLOTS + 2;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
+    // instruction descriptor: A = B = E4M3, both K-major, E8M0 scales, M = 128, N = BT; the
+    // scale byte's index goes to bits 4 (B) and 29 (A)
+    static constexpr uint32_t IDESC = ((uint32_t)(BT >> 3) << 17) | (1u << 23) | ((uint32_t)(BW >> 7) << 27);
+    static_assert(BT % 16 == 0 && BT <= 256, "MMA N");
+    static_assert(BT * BW * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the stages");
 };
+
 struct Params {
-    const uint8_t *a, *a_scale;
-    int m, k, bf16_out;
-    int64_t q_ld, scale_ld;
-    int tile_start[5];
-    int n_w;
-    Group g[4];
+    const uint8_t *a_scale;
+    int m, kb;                   // rows, scale blocks of K
+    int k_tail;                  // MMAs (32 values each) of the last block
+    int scale_ld;
+    int m_tiles, n_w, bf16_out;
+    int tile_start[5];           // prefix sums of output tiles per weight matrix
+    int n[4];
+    const uint8_t *w_scale[4];
+    void *out[4];
+    int64_t out_ld[4];
 };
+struct Maps { CUtensorMap a, w[4]; };
 
-__device__ __forceinline__ float e4m3(uint32_t code) {
-    uint32_t h2;
-    const uint16_t c = (uint16_t)code;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
-    return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-    return byte == 255 ? NAN : byte == 0 ? 0x1p-127f : __uint_as_float(byte << 23);
+__device__ __forceinline__ uint64_t globaltimer() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait for the completion of the phase with the given parity.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if ((i & 255u) == 255u) {
+            if (*abort) return false;
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > g_qmm_wait_ns) {
+                *abort = 1;
+                atomicOr(&g_qmm_err, 1u);
+                return false;
+            }
+        }
+    }
+}
+// Bounded wait that ignores the abort flag: drains copies or MMAs still in
+// flight after a give-up, before the CTA frees its TMEM and exits.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try(bar, parity)) return;
+        if ((i & 255u) == 255u) {
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kDrainNs) return;
+        }
+    }
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// Shared-memory matrix descriptors: K-major operand in the 128-byte swizzle TMA writes
+// (8-row atoms of 1024 bytes), and the unswizzled scale words (8-row cores of 128 bytes).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 cluster_ld(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
 }
 
-__global__ void __launch_bounds__(256) quant_matmul_kernel(Params p) {
-    __shared__ float sa[KS][TILE + 1], sw[KS][TILE + 1];
+__device__ __forceinline__ void store_out(void *out, int64_t i, float v, int bf16) {
+    if (bf16) static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+    else static_cast<float *>(out)[i] = v;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_constant__ Maps maps, const Params p, int split) {
+    using S = Shape<BT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sf = smem + S::STAGES * S::STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sf + SF_SLOTS * S::SF_SLOT_BYTES);
+    uint64_t *empty = full + S::STAGES, *sf_full = empty + S::STAGES, *sf_empty = sf_full + SF_SLOTS;
+    uint64_t *acc_full = sf_empty + SF_SLOTS, *drain = acc_full + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    const int rank = (int)blockIdx.x % split, tile = (int)blockIdx.x / split;
+    int g = 0;
+    while (g + 1 < p.n_w && tile >= p.tile_start[g + 1]) g++;
+    const int nt = (tile - p.tile_start[g]) / p.m_tiles, m0 = (tile - p.tile_start[g]) % p.m_tiles * BT;
+    const int n0 = nt * BW;
+    // the K ranges of the ranks differ by at most one block
+    const int kb0 = (int)((int64_t)p.kb * rank / split), kb1 = (int)((int64_t)p.kb * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; s++) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < SF_SLOTS; s++) {
+            mbar_init(smem_u32(&sf_full[s]), 32);
+            mbar_init(smem_u32(&sf_empty[s]), 1);
+        }
+        mbar_init(smem_u32(acc_full), 1);
+        mbar_init(smem_u32(drain), 1);
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(S::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_launch_dependents();
-    int g = 0;
-    while (g + 1 < p.n_w && (int)blockIdx.y >= p.tile_start[g + 1]) g++;
-    const Group G = p.g[g];
-    const int n0 = ((int)blockIdx.y - p.tile_start[g]) * TILE;
-    const int64_t m0 = (int64_t)blockIdx.x * TILE;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const int lr = threadIdx.x / 4, lk = (threadIdx.x % 4) * 4;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < p.k; k0 += KS) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int k = k0 + lk + i;
-            const int64_t m = m0 + lr;
-            const int n = n0 + lr;
-            float va = 0.f, vw = 0.f;
-            if (k < p.k && m < p.m) va = e4m3(p.a[m * p.q_ld + k]) * scale_value(p.a_scale[m * p.scale_ld + k / 128]);
-            if (k < p.k && n < G.n) vw = e4m3(G.q[n * p.q_ld + k]) * scale_value(G.scale[(n / 128) * p.scale_ld + k / 128]);
-            sa[lk + i][lr] = va;
-            sw[lk + i][lr] = vw;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0;
+            for (int kb = kb0; kb < kb1; kb++, it++) {
+                const int s = it % S::STAGES;
+                if (!mbar_wait(smem_u32(&empty[s]), ((it / S::STAGES) & 1) ^ 1, abort)) { ok = false; break; }
+                const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * S::STAGE_BYTES);
+                mbar_expect_tx(bar, S::STAGE_BYTES);
+                tma_load_2d(dst, &maps.w[g], kb * BK, n0, bar);
+                tma_load_2d(dst + S::W_BYTES, &maps.a, kb * BK, m0, bar);
+            }
+            // after a give-up: the loads still in flight (the last STAGES issued) land before the CTA exits
+            if (!ok)
+                for (uint32_t u = it > (uint32_t)S::STAGES ? it - S::STAGES : 0; u < it; u++)
+                    mbar_drain(smem_u32(&full[u % S::STAGES]), (u / S::STAGES) & 1);
         }
-        __syncthreads();
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0, sl = 0;
+            const uint32_t sf_tmem = tmem + BT;
+            for (int kb = kb0; kb < kb1; kb++, it++) {
+                const int slot = sl % SF_SLOTS;
+                const uint32_t sfa = sf_tmem + slot * S::SF_COLS, sfb = sfa + 4;
+                if (kb == kb0 || kb % 4 == 0) {
+                    if (!mbar_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
+                    fence_after();
+                    const uint32_t src = smem_u32(sf + slot * S::SF_SLOT_BYTES);
 #pragma unroll
-        for (int k = 0; k < KS; k++) {
-            float a[4], w[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) a[i] = sa[k][ty + 16 * i], w[i] = sw[k][tx + 16 * i];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) acc[i][j] = fmaf(a[i], w[j], acc[i][j]);
+                    for (int i = 0; i < 1 + S::SFT; i++) copy_scales(sfa + 4 * i, scale_desc(src + i * SF_BYTES));
+                }
+                const int s = it % S::STAGES;
+                if (!mbar_wait(smem_u32(&full[s]), (it / S::STAGES) & 1, abort)) { ok = false; break; }
+                fence_after();
+                const uint32_t sw = smem_u32(smem + s * S::STAGE_BYTES), st = sw + S::W_BYTES;
+                const uint32_t id = (uint32_t)kb % 4, idesc = S::IDESC | id << 4 | id << 29;
+                const int n_mma = kb == p.kb - 1 ? p.k_tail : BK / 32;
+                for (int k = 0; k < n_mma; k++)
+                    mma_scaled(tmem, sw128_desc(sw + k * 32), sw128_desc(st + k * 32), idesc, sfa, sfb,
+                               (kb > kb0 || k > 0) ? 1u : 0u);
+                mma_commit(smem_u32(&empty[s]));
+                if (kb % 4 == 3) {
+                    mma_commit(smem_u32(&sf_empty[slot]));
+                    sl++;
+                }
+            }
+            if (ok) mma_commit(smem_u32(acc_full));
+            // drain: every MMA issued so far completes (bounded wait, given up or not) before the
+            // TMEM is freed
+            mma_commit(smem_u32(drain));
+            mbar_drain(smem_u32(drain), 0);
         }
-        __syncthreads();
+        __syncwarp();
+    } else if (warp == 2) {
+        // scales of groups of 4 stages (absolute positions, so a group is one word per row)
+        const uint8_t *ws = p.w_scale[g] + (size_t)nt * p.scale_ld;
+        uint32_t sl = 0;
+        for (int q = kb0 / 4; q < (kb1 + 3) / 4; q++, sl++) {
+            const int slot = sl % SF_SLOTS;
+            uint32_t t[S::SFT][4];
+#pragma unroll
+            for (int i = 0; i < S::SFT; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int r = i * 128 + j * 32 + lane;
+                    const bool in = r < BT && m0 + r < p.m;
+                    t[i][j] = in ? __ldg(reinterpret_cast<const uint32_t *>(p.a_scale + (size_t)(m0 + r) * p.scale_ld + 4 * q))
+                                 : 0x7F7F7F7Fu;
+                }
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(ws + 4 * q));
+            if (!mbar_wait(smem_u32(&sf_empty[slot]), ((sl / SF_SLOTS) & 1) ^ 1, abort)) break;
+            uint4 *dst = reinterpret_cast<uint4 *>(sf + slot * S::SF_SLOT_BYTES) + lane;
+            dst[0] = make_uint4(w, w, w, w);
+#pragma unroll
+            for (int i = 0; i < S::SFT; i++) dst[32 * (1 + i)] = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(smem_u32(&sf_full[slot]));
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // epilogue: TMEM lane quarter warp % 4, lane = weight row, column = row of the product
+        const int quarter = warp & 3, n = n0 + quarter * 32 + lane;
+        const int rows = min(BT, p.m - m0);
+        const bool ok = mbar_wait(smem_u32(acc_full), 0, abort);
+        __syncwarp();
+        if (ok) {
+            fence_after();
+            float *part = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < BT; c += 16) {
+                if (c >= rows) break;
+                float v[16];
+                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
+                if (split > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++) part[(c + j) * BW] = v[j];
+                } else if (n < p.n[g]) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (c + j < rows) store_out(p.out[g], (int64_t)(m0 + c + j) * p.out_ld[g] + n, v[j], p.bf16_out);
+                }
+            }
+            fence_before();
+        }
     }
+    if (split > 1) {
+        // partial tiles [row][128] in every CTA's stages (no copy or MMA uses them any more):
+        // each CTA adds a share of them in rank order
+        __syncwarp();
+        cluster_sync();
+        const int total = min(BT, p.m - m0) * (BW / 4);
+        const uint32_t base = smem_u32(smem);
+        for (int e = rank * THREADS + threadIdx.x; e < total; e += split * THREADS) {
+            float4 v = cluster_ld(base + e * 16, 0);
+            for (int r = 1; r < split; r++) {
+                const float4 u = cluster_ld(base + e * 16, r);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+            const int n = n0 + e % (BW / 4) * 4;
+            const int64_t o = (int64_t)(m0 + e / (BW / 4)) * p.out_ld[g] + n;
+            const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t m = m0 + ty + 16 * i;
-        if (m >= p.m) continue;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int n = n0 + tx + 16 * j;
-            if (n >= G.n) continue;
-            if (p.bf16_out) static_cast<__nv_bfloat16 *>(G.out)[m * G.out_ld + n] = __float2bfloat16_rn(acc[i][j]);
-            else static_cast<float *>(G.out)[m * G.out_ld + n] = acc[i][j];
+            for (int j = 0; j < 4; j++)
+                if (n + j < p.n[g]) store_out(p.out[g], o + j, f[j], p.bf16_out);
         }
+        cluster_sync();
     }
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TMEM_COLS) : "memory");
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
+    }();
+    return fn;
+}
+
+// Bytes [rows][k] at the quantised pitch, boxes of box_rows x 128 bytes.
+cudaError_t make_map(CUtensorMap *map, const uint8_t *p, int64_t rows, int k, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)quant_row_bytes((uint32_t)k)};
+    cuuint32_t box[2] = {BK, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t fill_params(const QuantMatmulArgs &a, int bt, Params &p, Maps &maps) {
+    cudaError_t e = make_map(&maps.a, a.a, a.m, a.k, bt);
+    p = Params{};
+    p.a_scale = a.a_scale;
+    p.m = a.m;
+    p.kb = (a.k + BK - 1) / BK;
+    p.k_tail = (a.k - (p.kb - 1) * BK + 31) / 32;
+    p.scale_ld = (int)quant_scale_bytes((uint32_t)a.k);
+    p.m_tiles = (a.m + bt - 1) / bt;
+    p.n_w = a.n_w;
+    p.bf16_out = a.out_dtype == DS4C_BF16;
+    int start = 0;
+    for (int g = 0; g < a.n_w && e == cudaSuccess; g++) {
+        e = make_map(&maps.w[g], a.w[g].q, a.w[g].n, a.k, BW);
+        p.tile_start[g] = start;
+        p.n[g] = (int)a.w[g].n;
+        p.w_scale[g] = a.w[g].scale;
+        p.out[g] = a.w[g].out;
+        p.out_ld[g] = (int64_t)a.w[g].out_ld;
+        start += (p.n[g] + BW - 1) / BW * p.m_tiles;
+    }
+    p.tile_start[a.n_w] = start;
+    for (int g = a.n_w; g < 4; g++) maps.w[g] = maps.w[0];
+    return e;
+}
+
+template <int BT>
+cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
+    using S = Shape<BT>;
+    Maps maps;
+    Params p;
+    cudaError_t e = fill_params(a, BT, p, maps);
+    if (e != cudaSuccess) return e;
+    if ((e = ensure_dyn_smem(qmm_split_kernel<BT>, S::SMEM_BYTES)) != cudaSuccess) return e;
+    const int tiles = p.tile_start[a.n_w];
+    int split = 1;
+    while (split < MAX_SPLIT && tiles * split * 2 <= 2 * 152 && p.kb >= split * 4) split *= 2;
+    return launch_pdl_cluster(qmm_split_kernel<BT>, dim3((unsigned)(tiles * split)), dim3(THREADS), S::SMEM_BYTES, s, split,
+                              maps, p, split);
 }
 
 }  // namespace
 
 cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s) {
-    Params p{};
-    p.a = a.a;
-    p.a_scale = a.a_scale;
-    p.m = a.m;
-    p.k = a.k;
-    p.bf16_out = a.out_dtype == DS4C_BF16;
-    p.q_ld = (int64_t)quant_row_bytes((uint32_t)a.k);
-    p.scale_ld = (int64_t)quant_scale_bytes((uint32_t)a.k);
-    p.n_w = a.n_w;
-    int start = 0;
-    for (int g = 0; g < a.n_w; g++) {
-        p.tile_start[g] = start;
-        p.g[g] = Group{a.w[g].q, a.w[g].scale, a.w[g].out, (int64_t)a.w[g].out_ld, (int)a.w[g].n};
-        start += ((int)a.w[g].n + TILE - 1) / TILE;
-    }
-    p.tile_start[a.n_w] = start;
-    return launch_pdl(quant_matmul_kernel, dim3((a.m + TILE - 1) / TILE, start), dim3(256), 0, s, p);
+    if (a.m <= 16) return launch_split<16>(a, s);
+    if (a.m <= 32) return launch_split<32>(a, s);
+    if (a.m <= 64) return launch_split<64>(a, s);
+    return launch_split<128>(a, s);
+}
+
+cudaError_t qmm_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_qmm_wait_ns, &ns, sizeof ns); }
+
+unsigned int qmm_read_clear_error() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_qmm_err, sizeof v) != cudaSuccess) return 0;
+    if (v) cudaMemcpyToSymbol(g_qmm_err, &z, sizeof z);
+    return v;
 }
 
 }  // namespace ds4c

@@ -100,11 +100,14 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Bounded wait for the completion of the phase with the given parity.
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity);
+// Bounded wait for the completion of the phase with the given parity (CLUSTER: of arrivals
+// from both CTAs of a pair, whose writes it acquires).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
-        if (mbar_try(bar, parity)) return true;
+        if (CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
         if ((i & 255u) == 255u) {
             if (*abort) return false;
             const uint64_t now = globaltimer();
@@ -134,6 +137,52 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// Pair forms: an mbarrier of CTA `rank` of the cluster, arrivals and waits that order memory
+// across the pair, loads that complete on the leader's barrier, commits to both CTAs.
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                                uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
         : "memory");
 }
 // Shared-memory matrix descriptors: K-major operand in the 128-byte swizzle TMA writes
@@ -166,11 +215,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        : "r"(taddr)
+        : "memory");
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
@@ -378,6 +428,253 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
     }
 }
 
+// ---------------------------------------------------------------------------------------
+// Large products: a persistent kernel of CTA pairs.  cta_group::2 MMAs of 256 weight rows x
+// bt rows: each CTA holds 128 weight rows and half of the rows in shared memory, so a stage
+// costs (128 + bt / 2) * 128 bytes of loads per SM where one CTA alone would need
+// (128 + bt) * 128.  bt (a multiple of 32, at most 224) is chosen by the host so that the
+// tiles fill whole rounds over the pairs; two accumulators of bt columns and two slots of
+// scales fit the 512 TMEM columns, so a tile's epilogue runs beside the next tile's MMAs.
+// The tensor core's float accumulation cuts low bits off (its error grows with K: 4e-7 of
+// the result's norm at K = 4096), so an accumulator takes at most CHUNK blocks of K; the
+// epilogue adds the chunks of a tile in registers.
+//
+// Warps: 0 loads (in both CTAs, completing on the leader's barriers), 1 MMAs (leader only),
+// 2 scales (both CTAs: the words of all bt rows and of the CTA's own weight rows), 4-11
+// epilogue (TMEM lane quarter w % 4, half of the columns each).
+// ---------------------------------------------------------------------------------------
+constexpr int PAIR_THREADS = 384, PAIR_STAGES = 7, MAX_BT = 224, CHUNK = 32;
+struct Pair {
+    static constexpr int W_BYTES = BW * BK, STAGE_BYTES = W_BYTES + MAX_BT / 2 * BK;
+    static constexpr int SF_SLOT_BYTES = 3 * SF_BYTES, SF_COLS = 12;
+    static constexpr int N_BARS = 2 * PAIR_STAGES + 2 * SF_SLOTS + 5;
+    static constexpr int SMEM_BYTES = PAIR_STAGES * STAGE_BYTES + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
+    static constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(2 * BW >> 7) << 27);       // M = 256, N added
+    static constexpr int HALF_CHUNKS = MAX_BT / 2 / 16;
+    static_assert(2 * MAX_BT + SF_SLOTS * SF_COLS <= 512, "TMEM columns");
+    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms");
+};
+
+// Output tile -> weight matrix, row tile and weight tile: within a matrix, 8 weight tiles go
+// with each row tile before the next row tile, so that the tiles in flight share their operands in L2.
+__device__ __forceinline__ void pair_coords(const Params &p, int tile, int &g, int &mt, int &nt) {
+    g = 0;
+    while (g + 1 < p.n_w && tile >= p.tile_start[g + 1]) g++;
+    const int local = tile - p.tile_start[g], n_tiles = (p.n[g] + 2 * BW - 1) / (2 * BW);
+    const int band = local / (8 * p.m_tiles), wide = min(8, n_tiles - 8 * band);
+    const int in = local - band * 8 * p.m_tiles;
+    mt = in / wide;
+    nt = 8 * band + in % wide;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sf = smem + PAIR_STAGES * Pair::STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sf + SF_SLOTS * Pair::SF_SLOT_BYTES);
+    uint64_t *empty = full + PAIR_STAGES, *sf_full = empty + PAIR_STAGES, *sf_empty = sf_full + SF_SLOTS;
+    uint64_t *acc_full = sf_empty + SF_SLOTS, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+    const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < PAIR_STAGES; s++) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < SF_SLOTS; s++) {
+            mbar_init(smem_u32(&sf_full[s]), 64);
+            mbar_init(smem_u32(&sf_empty[s]), 1);
+        }
+        for (int a = 0; a < 2; a++) {
+            mbar_init(smem_u32(&acc_full[a]), 1);
+            mbar_init(smem_u32(&acc_empty[a]), 16);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    __syncthreads();
+    cluster_sync();                                  // both CTAs' barriers exist before either uses them
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0;
+            for (int tile = pair; tile < total && ok; tile += pairs) {
+                int g, mt, nt;
+                pair_coords(p, tile, g, mt, nt);
+                const int wy = nt * 2 * BW + rank * BW, ty = mt * bt + rank * (bt / 2);
+                for (int kb = 0; kb < p.kb; kb++, it++) {
+                    const int s = it % PAIR_STAGES;
+                    if (!mbar_wait(smem_u32(&empty[s]), ((it / PAIR_STAGES) & 1) ^ 1, abort)) { ok = false; break; }
+                    const uint32_t dst = smem_u32(smem + s * Pair::STAGE_BYTES);
+                    const uint32_t bar = mapa(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * (Pair::W_BYTES + bt / 2 * BK));
+                    tma_load_2d_pair(dst, &maps.w[g], kb * BK, wy, bar);
+                    tma_load_2d_pair(dst + Pair::W_BYTES, &maps.a, kb * BK, ty, bar);
+                }
+            }
+            // after a give-up the pair's loads still in flight land before it exits: the leader sees them
+            // on its barriers, the other CTA has none and waits a time no load takes
+            if (!ok) {
+                if (rank == 0) {
+                    for (uint32_t u = it > (uint32_t)PAIR_STAGES ? it - PAIR_STAGES : 0; u < it; u++)
+                        mbar_drain(smem_u32(&full[u % PAIR_STAGES]), (u / PAIR_STAGES) & 1);
+                } else {
+                    const uint64_t t0 = globaltimer();
+                    while (globaltimer() - t0 < 2000000ull) {}
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            bool ok = true;
+            uint32_t it = 0, sl = 0, local = 0;
+            const uint32_t sf_tmem = tmem + 2 * (uint32_t)bt;
+            const uint32_t idesc0 = Pair::IDESC | (uint32_t)(bt >> 3) << 17;
+            for (int tile = pair; tile < total && ok; tile += pairs) {
+                for (int c = 0; c < chunks && ok; c++, local++) {
+                    const uint32_t acc = local & 1, d = tmem + acc * (uint32_t)bt;
+                    if (!mbar_wait<true>(smem_u32(&acc_empty[acc]), ((local >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+                    fence_after();
+                    const int kb1 = min(p.kb, (c + 1) * CHUNK);
+                    for (int kb = c * CHUNK; kb < kb1; kb++, it++) {
+                        const int slot = sl % SF_SLOTS;
+                        const uint32_t sfa = sf_tmem + slot * Pair::SF_COLS, sfb = sfa + 4;
+                        if (kb % 4 == 0) {
+                            if (!mbar_wait<true>(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
+                            fence_after();
+                            const uint32_t src = smem_u32(sf + slot * Pair::SF_SLOT_BYTES);
+#pragma unroll
+                            for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, scale_desc(src + i * SF_BYTES));
+                        }
+                        const int s = it % PAIR_STAGES;
+                        if (!mbar_wait<true>(smem_u32(&full[s]), (it / PAIR_STAGES) & 1, abort)) { ok = false; break; }
+                        fence_after();
+                        const uint32_t sw = smem_u32(smem + s * Pair::STAGE_BYTES), st = sw + Pair::W_BYTES;
+                        const uint32_t id = (uint32_t)kb % 4, idesc = idesc0 | id << 4 | id << 29;
+                        const int n_mma = kb == p.kb - 1 ? p.k_tail : BK / 32;
+                        for (int k = 0; k < n_mma; k++)
+                            mma_scaled_pair(d, sw128_desc(sw + k * 32), sw128_desc(st + k * 32), idesc, sfa, sfb,
+                                            (kb > c * CHUNK || k > 0) ? 1u : 0u);
+                        mma_commit_pair(smem_u32(&empty[s]));
+                        if (kb % 4 == 3 || kb == p.kb - 1) {
+                            mma_commit_pair(smem_u32(&sf_empty[slot]));
+                            sl++;
+                        }
+                    }
+                    if (ok) mma_commit_pair(smem_u32(&acc_full[acc]));
+                }
+            }
+            // drain: every MMA issued so far completes (bounded wait, given up or not) before the
+            // TMEM is freed
+            mma_commit_pair(smem_u32(drain));
+            mbar_drain(smem_u32(drain), 0);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        uint32_t sl = 0;
+        bool ok = true;
+        for (int tile = pair; tile < total && ok; tile += pairs) {
+            int g, mt, nt;
+            pair_coords(p, tile, g, mt, nt);
+            // a weight tile past the matrix's end (the second CTA's) feeds no output: any scale
+            const int wb = min(2 * nt + rank, (p.n[g] + BW - 1) / BW - 1), m0 = mt * bt;
+            const uint8_t *ws = p.w_scale[g] + (size_t)wb * p.scale_ld;
+            for (int q = 0; q < (p.kb + 3) / 4; q++, sl++) {
+                const int slot = sl % SF_SLOTS;
+                uint32_t t[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int r = i * 128 + j * 32 + lane;
+                        const bool in = r < bt && m0 + r < p.m;
+                        t[i][j] = in ? __ldg(reinterpret_cast<const uint32_t *>(p.a_scale + (size_t)(m0 + r) * p.scale_ld + 4 * q))
+                                     : 0x7F7F7F7Fu;
+                    }
+                const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(ws + 4 * q));
+                if (!mbar_wait(smem_u32(&sf_empty[slot]), ((sl / SF_SLOTS) & 1) ^ 1, abort)) { ok = false; break; }
+                uint4 *dst = reinterpret_cast<uint4 *>(sf + slot * Pair::SF_SLOT_BYTES) + lane;
+                dst[0] = make_uint4(w, w, w, w);
+#pragma unroll
+                for (int i = 0; i < 2; i++) dst[32 * (1 + i)] = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive_cluster(mapa(smem_u32(&sf_full[slot]), 0));
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) / 4, cols = bt / 2;
+        uint32_t local = 0;
+        bool ok = true;
+        for (int tile = pair; tile < total && ok; tile += pairs) {
+            int g, mt, nt;
+            pair_coords(p, tile, g, mt, nt);
+            float v[Pair::HALF_CHUNKS][16];
+            for (int c = 0; c < chunks; c++, local++) {
+                const uint32_t acc = local & 1;
+                ok = mbar_wait(smem_u32(&acc_full[acc]), (local >> 1) & 1, abort);
+                __syncwarp();
+                if (!ok) break;
+                fence_after();
+                const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + acc * (uint32_t)bt + (uint32_t)(half * cols);
+#pragma unroll
+                for (int i = 0; i < Pair::HALF_CHUNKS; i++) {
+                    if (16 * i < cols) {
+                        if (c == 0) {
+                            tmem_ld16(src + 16 * i, v[i]);
+                        } else {
+                            float u[16];
+                            tmem_ld16(src + 16 * i, u);
+#pragma unroll
+                            for (int j = 0; j < 16; j++) v[i][j] += u[j];
+                        }
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&acc_empty[acc]), 0));
+            }
+            if (!ok) break;
+            const int n = nt * 2 * BW + rank * BW + quarter * 32 + lane, m0 = mt * bt + half * cols;
+            if (n < p.n[g]) {
+                const int64_t ld = p.out_ld[g], o = (int64_t)m0 * ld + n;
+#pragma unroll
+                for (int i = 0; i < Pair::HALF_CHUNKS; i++)
+                    if (16 * i < cols) {
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            if (m0 + 16 * i + j < p.m) store_out(p.out[g], o + (16 * i + j) * ld, v[i][j], p.bf16_out);
+                    }
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    cluster_sync();                                  // the partner's arrivals and MMAs have this CTA's memory until here
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *ptr = nullptr;
@@ -402,8 +699,9 @@ cudaError_t make_map(CUtensorMap *map, const uint8_t *p, int64_t rows, int k, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t fill_params(const QuantMatmulArgs &a, int bt, Params &p, Maps &maps) {
-    cudaError_t e = make_map(&maps.a, a.a, a.m, a.k, bt);
+// Tiles of wrows weight rows x bt rows; a CTA loads box_t of the rows at once.
+cudaError_t fill_params(const QuantMatmulArgs &a, int wrows, int bt, int box_t, Params &p, Maps &maps) {
+    cudaError_t e = make_map(&maps.a, a.a, a.m, a.k, box_t);
     p = Params{};
     p.a_scale = a.a_scale;
     p.m = a.m;
@@ -421,7 +719,7 @@ cudaError_t fill_params(const QuantMatmulArgs &a, int bt, Params &p, Maps &maps)
         p.w_scale[g] = a.w[g].scale;
         p.out[g] = a.w[g].out;
         p.out_ld[g] = (int64_t)a.w[g].out_ld;
-        start += (p.n[g] + BW - 1) / BW * p.m_tiles;
+        start += (p.n[g] + wrows - 1) / wrows * p.m_tiles;
     }
     p.tile_start[a.n_w] = start;
     for (int g = a.n_w; g < 4; g++) maps.w[g] = maps.w[0];
@@ -433,7 +731,7 @@ cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
     using S = Shape<BT>;
     Maps maps;
     Params p;
-    cudaError_t e = fill_params(a, BT, p, maps);
+    cudaError_t e = fill_params(a, BW, BT, BT, p, maps);
     if (e != cudaSuccess) return e;
     if ((e = ensure_dyn_smem(qmm_split_kernel<BT>, S::SMEM_BYTES)) != cudaSuccess) return e;
     const int tiles = p.tile_start[a.n_w];
@@ -443,13 +741,40 @@ cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
                               maps, p, split);
 }
 
+constexpr int PAIRS = 76;
+
+// Rows of a pair tile: the width with the fewest rounds over the pairs times its MMA time.
+int pair_bt(const QuantMatmulArgs &a) {
+    int best = 0;
+    int64_t best_cost = 0;
+    for (int bt = MAX_BT; bt >= 128; bt -= 32) {
+        int64_t tiles = 0;
+        for (int g = 0; g < a.n_w; g++) tiles += (int64_t)((a.w[g].n + 2 * BW - 1) / (2 * BW)) * ((a.m + bt - 1) / bt);
+        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * bt;
+        if (best == 0 || cost < best_cost) best = bt, best_cost = cost;
+    }
+    return best;
+}
+
+cudaError_t launch_pair(const QuantMatmulArgs &a, int bt, cudaStream_t s) {
+    Maps maps;
+    Params p;
+    cudaError_t e = fill_params(a, 2 * BW, bt, bt / 2, p, maps);
+    if (e != cudaSuccess) return e;
+    if ((e = ensure_dyn_smem(qmm_pair_kernel, Pair::SMEM_BYTES)) != cudaSuccess) return e;
+    const int tiles = p.tile_start[a.n_w];
+    return launch_pdl(qmm_pair_kernel, dim3((unsigned)(2 * (tiles < PAIRS ? tiles : PAIRS))), dim3(PAIR_THREADS),
+                      Pair::SMEM_BYTES, s, maps, p, bt);
+}
+
 }  // namespace
 
 cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s) {
     if (a.m <= 16) return launch_split<16>(a, s);
     if (a.m <= 32) return launch_split<32>(a, s);
     if (a.m <= 64) return launch_split<64>(a, s);
-    return launch_split<128>(a, s);
+    if (a.m <= 512) return launch_split<128>(a, s);
+    return launch_pair(a, pair_bt(a), s);
 }
 
 cudaError_t qmm_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_qmm_wait_ns, &ns, sizeof ns); }

@@ -6,7 +6,9 @@ with a row pitch of k rounded up to 16 bytes, scale uint8 with one E8M0 byte (2^
 per 128 values at a pitch of ceil(k / 128) rounded up to 4: [n, pitch] for rows, [ceil(n / 128),
 pitch] for weights.  ``empty`` allocates such a pair.
 
-Calls run on the current stream of the tensors' device."""
+Calls run on the current stream of the tensors' device.  A decode step's kernels take a few
+microseconds, so the checks read each tensor's attributes once and go to the stream's and the
+device's raw handles (a call of ``rmsnorm`` took 14.9 us of host time on torch's stream objects)."""
 
 from __future__ import annotations
 
@@ -34,46 +36,53 @@ def empty(n: int, k: int, device="cuda", rows_per_scale: int = 1):
     return q, torch.empty((n + rows_per_scale - 1) // rows_per_scale, scale_bytes(k), dtype=torch.uint8, device=device)
 
 
-def _dtype(t, what):
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"{what}: {t.dtype} (float32 or bfloat16)")
-    return d
+def _matrix(t, what):
+    """(n, k, ABI dtype, device index) of a float matrix on a GPU."""
+    shape = t.shape
+    dt = _DTYPES.get(t.dtype)
+    dev = t.get_device()
+    if len(shape) != 2 or dt is None or dev < 0:
+        raise ValueError(f"{what}: {t.dtype} {tuple(shape)} on {t.device}, expected a float32 or bfloat16 matrix on a "
+                         "CUDA device")
+    return shape[0], shape[1], dt, dev
 
 
-def _pitch(t, n, k, what, device):
-    """Row pitch of a [n, k] tensor with unit column stride."""
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != k:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(n, k)}")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if k > 1 and t.stride(1) != 1:
+def _pitch(t, n, k, dtype, dev, what):
+    """Row pitch of a [n, k] tensor of `dtype` with unit column stride on device `dev`."""
+    if t.shape != (n, k) or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {(n, k)} on cuda:{dev}")
+    row, col = t.stride()
+    if col != 1 and k > 1:
         raise ValueError(f"{what}: the rows' elements must be contiguous")
-    return t.stride(0) if n > 1 else max(k, t.stride(0))
+    return row if n > 1 else max(k, row)
 
 
 def check_rows(q, scale, k: int, rows_per_scale: int = 1):
-    """Raise unless (q, scale) is a quantised matrix of rows of k values on one CUDA device."""
-    n = q.shape[0] if q.dim() == 2 else -1
-    if q.dtype not in _BYTES or scale.dtype != torch.uint8 or q.device.type != "cuda":
-        raise ValueError(f"quantised rows: {q.dtype} on {q.device} with {scale.dtype} scales")
-    if n < 0 or q.shape[1] != k or (k > 1 and q.stride(1) != 1) or (n > 1 and q.stride(0) != row_bytes(k)):
-        raise ValueError(f"quantised rows: shape {tuple(q.shape)} stride {q.stride()}, expected (*, {k}) at a pitch of "
-                         f"{row_bytes(k)}")
-    if scale.device != q.device or tuple(scale.shape) != ((n + rows_per_scale - 1) // rows_per_scale, scale_bytes(k)) \
-            or not scale.is_contiguous():
-        raise ValueError(f"scales: shape {tuple(scale.shape)} on {scale.device}, expected "
-                         f"{((n + rows_per_scale - 1) // rows_per_scale, scale_bytes(k))}, contiguous, on {q.device}")
+    """Number of rows and device index of a quantised matrix (q, scale) of rows of k values on one CUDA
+    device; raises if it is none."""
+    shape, dev = q.shape, q.get_device()
+    if len(shape) != 2 or shape[1] != k or dev < 0 or q.dtype not in _BYTES:
+        raise ValueError(f"quantised rows: {q.dtype} {tuple(shape)} on {q.device}, expected E4M3 (*, {k}) on a CUDA device")
+    n = shape[0]
+    row, col = q.stride()
+    if (row != (k + 15) // 16 * 16 and n > 1) or (col != 1 and k > 1):
+        raise ValueError(f"quantised rows: stride {(row, col)}, expected {(row_bytes(k), 1)}")
+    want = (n if rows_per_scale == 1 else (n + rows_per_scale - 1) // rows_per_scale, ((k + 127) // 128 + 3) // 4 * 4)
+    if scale.shape != want or scale.dtype != torch.uint8 or scale.get_device() != dev or not scale.is_contiguous():
+        raise ValueError(f"scales: {scale.dtype} {tuple(scale.shape)} on {scale.device}, expected contiguous uint8 {want} on "
+                         f"cuda:{dev}")
+    return n, dev
 
 
-def _run(device, call):
-    """call(stream) with `device` current, on its current stream."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors on {device}: a CUDA device is needed")
-    if device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        return call(torch.cuda.current_stream().cuda_stream)
+def _run(dev, fn, *args):
+    """fn(*args, stream) with device `dev` current, on its current stream; raises the ABI's errors."""
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != abi.DS4C_OK:
+        raise abi.Ds4cError(status, fn.__name__)
 
 
 def rmsnorm(x, gain=None, *, residual=None, residual_out=None, eps: float = 1e-6, q=None, scale=None, y=None):
@@ -82,32 +91,30 @@ def rmsnorm(x, gain=None, *, residual=None, residual_out=None, eps: float = 1e-6
     With a residual the norm is of h = x + residual rounded to x's type; h goes to residual_out, which
     may be x or residual itself.  gain: [d] float32 or None (ones).  q, scale: outputs as ``empty``
     gives them, allocated if None.  y: optional output of x's type, the norm before its quantisation."""
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected two dimensions")
-    n, d = x.shape
-    dev = x.device
-    dt = _dtype(x, "x")
-    a = abi.RmsnormArgs(n, d, dt, eps, x.data_ptr())
-    a.x_ld = _pitch(x, n, d, "x", dev)
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        if t is not None:
-            if t.dtype != x.dtype:
-                raise ValueError(f"{name}: {t.dtype}, expected x's {x.dtype}")
-            setattr(a, "y_out" if name == "y" else name, t.data_ptr())
-            setattr(a, name + "_ld", _pitch(t, n, d, name, dev))
-    if gain is not None:
-        if gain.dtype != torch.float32 or tuple(gain.shape) != (d,) or gain.device != dev or not gain.is_contiguous():
-            raise ValueError(f"gain: {gain.dtype} {tuple(gain.shape)} on {gain.device}, expected contiguous float32 {(d,)}")
-        a.gain = gain.data_ptr()
+    n, d, dt, dev = _matrix(x, "x")
     if q is None and scale is None:
-        q, scale = empty(n, d, dev)
+        q, scale = empty(n, d, x.device)
     if q is None or scale is None:
         raise ValueError("q and scale: both or neither")
-    check_rows(q, scale, d)
-    if q.shape[0] != n or q.device != dev:
-        raise ValueError(f"q: {q.shape[0]} rows on {q.device}, expected {n} on {dev}")
-    a.q, a.scale = q.data_ptr(), scale.data_ptr()
-    abi.check(_run(dev, lambda s: abi.ds4c_rmsnorm_quant(a, s)), "ds4c_rmsnorm_quant")
+    if check_rows(q, scale, d) != (n, dev):
+        raise ValueError(f"q: {q.shape[0]} rows on {q.device}, expected {n} on cuda:{dev}")
+    xt = x.dtype
+    r = h = yp = g = None
+    r_ld = h_ld = y_ld = 0
+    if residual is not None:
+        r, r_ld = residual.data_ptr(), _pitch(residual, n, d, xt, dev, "residual")
+    if residual_out is not None:
+        h, h_ld = residual_out.data_ptr(), _pitch(residual_out, n, d, xt, dev, "residual_out")
+    if y is not None:
+        yp, y_ld = y.data_ptr(), _pitch(y, n, d, xt, dev, "y")
+    if gain is not None:
+        if gain.shape != (d,) or gain.dtype != torch.float32 or gain.get_device() != dev or not gain.is_contiguous():
+            raise ValueError(f"gain: {gain.dtype} {tuple(gain.shape)} on {gain.device}, expected contiguous float32 {(d,)} on "
+                             f"cuda:{dev}")
+        g = gain.data_ptr()
+    a = abi.RmsnormArgs(n, d, dt, eps, x.data_ptr(), r, h, yp, _pitch(x, n, d, xt, dev, "x"), r_ld, h_ld, y_ld, g,
+                        q.data_ptr(), scale.data_ptr())
+    _run(dev, abi.ds4c_rmsnorm_quant, a)
     return q, scale
 
 
@@ -115,7 +122,7 @@ class Fp8Weight:
     """A weight matrix [n, k] in E4M3 with one scale per 128 x 128 block."""
 
     def __init__(self, q, scale):
-        check_rows(q, scale, q.shape[1], 128)
+        self.device_index = check_rows(q, scale, q.shape[-1], 128)[1]
         self.q, self.scale = q, scale
 
     @property
@@ -125,52 +132,56 @@ class Fp8Weight:
 
 def quantize_weight(w, q=None, scale=None) -> Fp8Weight:
     """w [n, k] (float32 or bfloat16; rows may be strided) quantised in blocks of 128 x 128."""
-    if w.dim() != 2:
-        raise ValueError(f"w: shape {tuple(w.shape)}, expected two dimensions")
-    n, k = w.shape
-    dt = _dtype(w, "w")
-    ld = _pitch(w, n, k, "w", w.device)
+    n, k, dt, dev = _matrix(w, "w")
     if q is None and scale is None:
         q, scale = empty(n, k, w.device, 128)
     if q is None or scale is None:
         raise ValueError("q and scale: both or neither")
     out = Fp8Weight(q, scale)
-    if tuple(q.shape) != (n, k) or q.device != w.device:
-        raise ValueError(f"q: shape {tuple(q.shape)} on {q.device}, expected {(n, k)} on {w.device}")
-    abi.check(_run(w.device, lambda s: abi.ds4c_quant_weight(n, k, dt, w.data_ptr(), ld, q.data_ptr(), scale.data_ptr(), s)),
-              "ds4c_quant_weight")
+    if q.shape != (n, k) or out.device_index != dev:
+        raise ValueError(f"q: {tuple(q.shape)} on {q.device}, expected {(n, k)} on cuda:{dev}")
+    _run(dev, abi.ds4c_quant_weight, n, k, dt, w.data_ptr(), _pitch(w, n, k, w.dtype, dev, "w"), q.data_ptr(),
+         scale.data_ptr())
     return out
 
 
 class Linear:
-    """1 to 4 weight matrices of one width over the same rows: out_g = rows @ w_g.T in one launch."""
+    """1 to 4 weight matrices of one width over the same rows: out_g = rows @ w_g.T in one launch.
+
+    Holds the weights; their addresses are read once, here."""
 
     def __init__(self, weights):
         self.weights = list(weights)
         if not 1 <= len(self.weights) <= 4:
             raise ValueError(f"{len(self.weights)} weight matrices: 1 to 4")
         self.k = self.weights[0].shape[1]
-        self.device = self.weights[0].q.device
+        self.device_index = self.weights[0].device_index
         for w in self.weights:
-            if w.shape[1] != self.k or w.q.device != self.device:
-                raise ValueError(f"weights of {w.shape[1]} columns on {w.q.device}, expected {self.k} on {self.device}")
+            if w.shape[1] != self.k or w.device_index != self.device_index:
+                raise ValueError(f"weights of {w.shape[1]} columns on {w.q.device}, expected {self.k} on "
+                                 f"cuda:{self.device_index}")
+        self._n = [w.shape[0] for w in self.weights]
+        self._mats_t = abi.QuantMatrix * len(self.weights)
+        self._mats = bytes(self._mats_t(*[abi.QuantMatrix(w.q.data_ptr(), w.scale.data_ptr(), None, 0, w.shape[0])
+                                          for w in self.weights]))
 
     def __call__(self, q, scale, out=None, dtype=torch.float32):
         """q, scale: quantised rows [m, k].  out: list of [m, n_g] tensors of one type (float32 or bfloat16;
         rows may be strided), allocated in `dtype` if None.  Returns them."""
-        check_rows(q, scale, self.k)
-        m = q.shape[0]
-        if q.device != self.device:
-            raise ValueError(f"rows on {q.device}, weights on {self.device}")
+        m, dev = check_rows(q, scale, self.k)
+        if dev != self.device_index:
+            raise ValueError(f"rows on {q.device}, weights on cuda:{self.device_index}")
         if out is None:
-            out = [torch.empty(m, w.shape[0], dtype=dtype, device=self.device) for w in self.weights]
-        if len(out) != len(self.weights) or any(o.dtype != out[0].dtype for o in out):
-            raise ValueError(f"{len(out)} outputs for {len(self.weights)} weight matrices, of one type")
-        dt = _dtype(out[0], "out")
-        mats = (abi.QuantMatrix * len(out))()
-        for g, (w, o) in enumerate(zip(self.weights, out)):
-            n = w.shape[0]
-            mats[g] = abi.QuantMatrix(w.q.data_ptr(), w.scale.data_ptr(), o.data_ptr(), _pitch(o, m, n, "out", self.device), n)
-        abi.check(_run(self.device, lambda s: abi.ds4c_quant_matmul(m, self.k, q.data_ptr(), scale.data_ptr(), mats,
-                                                                    len(out), dt, s)), "ds4c_quant_matmul")
+            out = [torch.empty(m, n, dtype=dtype, device=q.device) for n in self._n]
+        if len(out) != len(self._n):
+            raise ValueError(f"{len(out)} outputs for {len(self._n)} weight matrices")
+        odt = out[0].dtype
+        dt = _DTYPES.get(odt)
+        if dt is None:
+            raise ValueError(f"out: {odt} (float32 or bfloat16)")
+        mats = self._mats_t.from_buffer_copy(self._mats)        # of this call: another thread may be in its own
+        for mat, o, n in zip(mats, out, self._n):
+            mat.out_ld = _pitch(o, m, n, odt, dev, "out")
+            mat.out = o.data_ptr()
+        _run(dev, abi.ds4c_quant_matmul, m, self.k, q.data_ptr(), scale.data_ptr(), mats, len(out), dt)
         return out

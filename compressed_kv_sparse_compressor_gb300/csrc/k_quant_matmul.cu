@@ -80,6 +80,16 @@ __device__ __forceinline__ uint64_t globaltimer() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -477,7 +487,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     uint64_t *acc_full = sf_empty + SF_SLOTS, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
 
@@ -543,48 +553,63 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             bool ok = true;
-            uint32_t it = 0, sl = 0, local = 0;
+            uint32_t s = 0, s_par = 0, sl = 0, local = 0;
             const uint32_t sf_tmem = tmem + 2 * (uint32_t)bt;
             const uint32_t idesc0 = Pair::IDESC | (uint32_t)(bt >> 3) << 17;
+            const uint64_t w_desc = sw128_desc(smem_u32(smem)), t_desc = sw128_desc(smem_u32(smem) + Pair::W_BYTES);
+            const uint64_t sf_desc = scale_desc(smem_u32(sf));
             for (int tile = pair; tile < total && ok; tile += pairs) {
                 for (int c = 0; c < chunks && ok; c++, local++) {
                     const uint32_t acc = local & 1, d = tmem + acc * (uint32_t)bt;
                     if (!mbar_wait<true>(smem_u32(&acc_empty[acc]), ((local >> 1) & 1) ^ 1, abort)) { ok = false; break; }
                     fence_after();
                     const int kb1 = min(p.kb, (c + 1) * CHUNK);
-                    for (int kb = c * CHUNK; kb < kb1; kb++, it++) {
-                        const int slot = sl % SF_SLOTS;
+                    uint32_t accumulate = 0;
+                    for (int kb = c * CHUNK; kb < kb1; kb++) {
+                        const uint32_t slot = sl % SF_SLOTS;
                         const uint32_t sfa = sf_tmem + slot * Pair::SF_COLS, sfb = sfa + 4;
                         if (kb % 4 == 0) {
                             if (!mbar_wait<true>(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
                             fence_after();
-                            const uint32_t src = smem_u32(sf + slot * Pair::SF_SLOT_BYTES);
+                            const uint64_t src = sf_desc + (uint64_t)(slot * (Pair::SF_SLOT_BYTES >> 4));
+                            if (elect()) {
 #pragma unroll
-                            for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, scale_desc(src + i * SF_BYTES));
+                                for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
+                            }
                         }
-                        const int s = it % PAIR_STAGES;
-                        if (!mbar_wait<true>(smem_u32(&full[s]), (it / PAIR_STAGES) & 1, abort)) { ok = false; break; }
+                        if (!mbar_wait<true>(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
                         fence_after();
-                        const uint32_t sw = smem_u32(smem + s * Pair::STAGE_BYTES), st = sw + Pair::W_BYTES;
+                        const uint64_t wd = w_desc + (uint64_t)(s * (Pair::STAGE_BYTES >> 4));
+                        const uint64_t td = t_desc + (uint64_t)(s * (Pair::STAGE_BYTES >> 4));
                         const uint32_t id = (uint32_t)kb % 4, idesc = idesc0 | id << 4 | id << 29;
-                        const int n_mma = kb == p.kb - 1 ? p.k_tail : BK / 32;
-                        for (int k = 0; k < n_mma; k++)
-                            mma_scaled_pair(d, sw128_desc(sw + k * 32), sw128_desc(st + k * 32), idesc, sfa, sfb,
-                                            (kb > c * CHUNK || k > 0) ? 1u : 0u);
-                        mma_commit_pair(smem_u32(&empty[s]));
-                        if (kb % 4 == 3 || kb == p.kb - 1) {
-                            mma_commit_pair(smem_u32(&sf_empty[slot]));
-                            sl++;
+                        const bool group_end = kb % 4 == 3 || kb == p.kb - 1;
+                        if (elect()) {
+                            if (kb < p.kb - 1 || p.k_tail == BK / 32) {
+#pragma unroll
+                                for (int k = 0; k < BK / 32; k++)
+                                    mma_scaled_pair(d, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                            } else {
+                                for (int k = 0; k < p.k_tail; k++)
+                                    mma_scaled_pair(d, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                            }
+                            mma_commit_pair(smem_u32(&empty[s]));
+                            if (group_end) mma_commit_pair(smem_u32(&sf_empty[slot]));
                         }
+                        __syncwarp();
+                        accumulate = 1;
+                        sl += group_end ? 1 : 0;
+                        if (++s == PAIR_STAGES) s = 0, s_par ^= 1;
                     }
-                    if (ok) mma_commit_pair(smem_u32(&acc_full[acc]));
+                    if (ok && elect()) mma_commit_pair(smem_u32(&acc_full[acc]));
+                    __syncwarp();
                 }
             }
             // drain: every MMA issued so far completes (bounded wait, given up or not) before the
             // TMEM is freed
-            mma_commit_pair(smem_u32(drain));
+            if (elect()) mma_commit_pair(smem_u32(drain));
+            __syncwarp();
             mbar_drain(smem_u32(drain), 0);
         }
         __syncwarp();

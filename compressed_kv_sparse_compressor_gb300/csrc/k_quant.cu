@@ -15,6 +15,36 @@ namespace ds4c {
 
 namespace {
 
+// Two floats in a 64-bit register: sm_103a adds, multiplies and fuses both in one issue slot.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// a - b, rounded once (the product with -1 is exact)
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, f2(-1.f, -1.f), a); }
+
 // a + b rounded, and the error of that rounding, itself a float (Knuth, The Art of
 // Computer Programming vol. 2, 4.2.2, theorem B).
 __device__ __forceinline__ float add_error(float a, float b, float &err) {
@@ -29,9 +59,15 @@ __device__ __forceinline__ void add_exact(float &s, float &c, float v) {
     s = add_error(s, v, err);
     c = __fadd_rn(c, err);
 }
+// The same for s >= v >= 0, where the error is v - ((s + v) - s) (Dekker, 1971).
+__device__ __forceinline__ void add_smaller(F2 &s, F2 &c, F2 v) {
+    const F2 t = add2(s, v);
+    c = add2(c, sub2(v, sub2(t, s)));
+    s = t;
+}
 
-// Sum of (s, c) pairs over the block, the same value in every thread.  sm: 2 * 32 floats.
-__device__ __forceinline__ void block_sum(float &s, float &c, float *sm) {
+// Sum of (s, c) pairs over a row's threads (blockDim.x), the same value in each.  sm: 2 * 32 floats.
+__device__ __forceinline__ void row_sum(float &s, float &c, float *sm) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float os = __shfl_xor_sync(0xffffffffu, s, o), oc = __shfl_xor_sync(0xffffffffu, c, o);
@@ -81,6 +117,12 @@ __device__ __forceinline__ float finite_abs(float v) {
     const float a = fabsf(v);
     return a < INFINITY ? a : 0.f;
 }
+// Largest of m, |a| and |b|; NaN if one is NaN.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 
 // Scale byte e + 127 of a block from its largest finite magnitude: 448 is 1.75 * 2^8,
 // so e is the exponent of amax less 8, one more when its significand exceeds 1.75; at
@@ -92,105 +134,210 @@ __device__ __forceinline__ int scale_byte(float amax) {
 // 2^-e, exact: e lies in -127 .. 120.
 __device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
-// Codes of 8 values at the inverse scale; not-finite values become NaN.
-__device__ __forceinline__ uint2 codes(const float (&y)[8], float inv) {
+// Codes of two values (the lower byte a's); NaN gives the NaN code.
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float nan_unless_finite(float v) { return fabsf(v) < INFINITY ? v : NAN; }
+// Codes of 8 values at the inverse scale; FINITE: none is infinite (an infinity would saturate).
+template <bool FINITE>
+__device__ __forceinline__ uint2 codes(const F2 (&y)[4], float inv) {
     uint32_t w[4];
+    const F2 inv2 = f2(inv, inv);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        float a = y[2 * i] * inv, b = y[2 * i + 1] * inv;
-        a = fabsf(a) < INFINITY ? a : NAN;
-        b = fabsf(b) < INFINITY ? b : NAN;
-        uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-        w[i] = r;
+        float2 v = unpack(mul2(y[i], inv2));
+        if (!FINITE) v.x = nan_unless_finite(v.x), v.y = nan_unless_finite(v.y);
+        w[i] = codes2(v.x, v.y);
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// 8 consecutive values of a row: vector accesses when VEC (base + 8 <= d then), single ones
-// bounded by d otherwise.
+// A thread's 8 values of a 128-block group.  VEC: 8 consecutive ones (base is a multiple of 8, d too,
+// everything aligned), 16 lanes to a block of 128.  Otherwise the warp's 256 values lie lane by
+// lane: value j of the thread is at base + 32 j, so that single accesses are coalesced whatever the
+// rows' alignment, and values 0-3 and 4-7 belong to two blocks of 128 over all 32 lanes.
 template <bool VEC>
-__device__ __forceinline__ void load8(const float *p, int base, int d, float (&v)[8]) {
+__device__ __forceinline__ int first_of(int i) {
+    const int t = threadIdx.x;
+    return VEC ? (i * (int)blockDim.x + t) * 8 : i * (int)blockDim.x * 8 + t / 32 * 256 + t % 32;
+}
+// 8 values as they are stored: bf16 pairs in words, floats in pairs.
+struct Bf16x8 { uint32_t w[4]; };
+struct F32x8 { F2 v[4]; };
+template <typename T> struct Held;
+template <> struct Held<float> { using type = F32x8; };
+template <> struct Held<__nv_bfloat16> { using type = Bf16x8; };
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *p, int base, int d, F32x8 &h) {
     if (VEC) {
         const float4 a = __ldcs(reinterpret_cast<const float4 *>(p + base));
         const float4 b = __ldcs(reinterpret_cast<const float4 *>(p + base) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        h.v[0] = f2(a.x, a.y), h.v[1] = f2(a.z, a.w), h.v[2] = f2(b.x, b.y), h.v[3] = f2(b.z, b.w);
     } else {
+        float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = base + i < d ? p[base + i] : 0.f;
+        for (int i = 0; i < 8; i++) f[i] = base + 32 * i < d ? p[base + 32 * i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) h.v[i] = f2(f[2 * i], f[2 * i + 1]);
     }
 }
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int base, int d, float (&v)[8]) {
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int base, int d, Bf16x8 &h) {
     if (VEC) {
         const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p + base));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        h.w[0] = a.x, h.w[1] = a.y, h.w[2] = a.z, h.w[3] = a.w;
     } else {
+        uint32_t f[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = base + i < d ? __bfloat162float(p[base + i]) : 0.f;
+        for (int i = 0; i < 8; i++) f[i] = base + 32 * i < d ? reinterpret_cast<const uint16_t *>(p)[base + 32 * i] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; i++) h.w[i] = f[2 * i] | f[2 * i + 1] << 16;
     }
 }
 template <bool VEC>
-__device__ __forceinline__ void store8(float *p, int base, int d, const float (&v)[8]) {
+__device__ __forceinline__ void store8(float *p, int base, int d, const F32x8 &h) {
     if (VEC) {
-        reinterpret_cast<float4 *>(p + base)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p + base)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        const float2 a = unpack(h.v[0]), b = unpack(h.v[1]), c = unpack(h.v[2]), e = unpack(h.v[3]);
+        reinterpret_cast<float4 *>(p + base)[0] = make_float4(a.x, a.y, b.x, b.y);
+        reinterpret_cast<float4 *>(p + base)[1] = make_float4(c.x, c.y, e.x, e.y);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            if (base + i < d) p[base + i] = v[i];
+            if (base + 32 * i < d) p[base + 32 * i] = i % 2 ? unpack(h.v[i / 2]).y : unpack(h.v[i / 2]).x;
     }
 }
 template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, int base, int d, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, int base, int d, const Bf16x8 &h) {
     if (VEC) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&t);
-        }
-        *reinterpret_cast<uint4 *>(p + base) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(p + base) = make_uint4(h.w[0], h.w[1], h.w[2], h.w[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            if (base + i < d) p[base + i] = __float2bfloat16_rn(v[i]);
+            if (base + 32 * i < d) reinterpret_cast<uint16_t *>(p)[base + 32 * i] = (uint16_t)(h.w[i / 2] >> (16 * (i % 2)));
     }
 }
-__device__ __forceinline__ float round_to(float v, const float *) { return v; }
-__device__ __forceinline__ float round_to(float v, const __nv_bfloat16 *) {
-    return __bfloat162float(__float2bfloat16_rn(v));
+// h + r rounded to the type.  Of two bf16 values the float sum is exact or lies too near the larger
+// one to reach a bf16 midpoint, so rounding it again gives what one rounding to bf16 gives.
+__device__ __forceinline__ void add8(F32x8 &h, const F32x8 &r) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) h.v[i] = add2(h.v[i], r.v[i]);
+}
+__device__ __forceinline__ void add8(Bf16x8 &h, const Bf16x8 &r) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(h.w[i]) : "r"(r.w[i]));
+}
+__device__ __forceinline__ void zero8(F32x8 &h) { h.v[0] = h.v[1] = h.v[2] = h.v[3] = 0; }
+__device__ __forceinline__ void zero8(Bf16x8 &h) { h.w[0] = h.w[1] = h.w[2] = h.w[3] = 0; }
+__device__ __forceinline__ F2 pair_of(const F32x8 &h, int i) { return h.v[i]; }
+__device__ __forceinline__ F2 pair_of(const Bf16x8 &h, int i) {
+    return f2(__uint_as_float(h.w[i] << 16), __uint_as_float(h.w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void round8(const F2 (&y)[4], F32x8 &h) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) h.v[i] = y[i];
+}
+__device__ __forceinline__ void round8(const F2 (&y)[4], Bf16x8 &h) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = unpack(y[i]);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
+        h.w[i] = *reinterpret_cast<const uint32_t *>(&t);
+    }
 }
 
-__device__ __forceinline__ void store_codes(uint8_t *q, int base, int d, uint2 c) {
-    if (base + 8 <= d) {
-        *reinterpret_cast<uint2 *>(q + base) = c;        // rows start on 16 bytes, base is a multiple of 8
+// Scale bytes and codes of a thread's 8 values (every lane of the warp calls this; lanes past d
+// hold zeros): the block's maximum over its lanes, NaN or infinite if the block holds such a value,
+// then once more over the finite ones (the whole warp together).
+template <bool VEC>
+__device__ __forceinline__ void quantise8(const F2 (&y)[4], int base, int d, uint8_t *q, uint8_t *scale) {
+    float m[2] = {0.f, 0.f};                             // VEC: one block; else one for each half
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 v = unpack(y[i]);
+        m[!VEC && i >= 2] = max_abs(m[!VEC && i >= 2], v.x, v.y);
+    }
+    bool finite = m[0] < INFINITY && m[1] < INFINITY;
+    finite = __all_sync(0xffffffffu, finite);
+    if (!finite) {
+        m[0] = m[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 v = unpack(y[i]);
+            m[!VEC && i >= 2] = fmaxf(m[!VEC && i >= 2], fmaxf(finite_abs(v.x), finite_abs(v.y)));
+        }
+    }
+#pragma unroll
+    for (int o = VEC ? 8 : 16; o; o >>= 1) {
+        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+        if (!VEC) m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+    }
+    const int b0 = scale_byte(m[0]);
+    if (VEC) {
+        if (base >= d) return;
+        const float inv = inverse_scale(b0);
+        // rows start on 16 bytes and base is a multiple of 8
+        *reinterpret_cast<uint2 *>(q + base) = finite ? codes<true>(y, inv) : codes<false>(y, inv);
+        if (threadIdx.x % 16 == 0) scale[base / 128] = (uint8_t)b0;
     } else {
-        for (int i = 0; base + i < d; i++) q[base + i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+        const int b1 = scale_byte(m[1]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float2 v = unpack(y[i / 2]);
+            const float f = nan_unless_finite((i % 2 ? v.y : v.x) * inverse_scale(i < 4 ? b0 : b1));
+            if (base + 32 * i < d) q[base + 32 * i] = (uint8_t)codes2(f, 0.f);
+        }
+        if (threadIdx.x % 32 == 0) {
+            if (base < d) scale[base / 128] = (uint8_t)b0;
+            if (base + 128 < d) scale[base / 128 + 1] = (uint8_t)b1;
+        }
     }
 }
 
-// Adds the squares of h * f (f a power of two) to (s, c); T: what the values h * f are exact in.
-template <typename T, int NI>
-__device__ __forceinline__ void sum_squares(const float (&h)[NI][8], float f, float &s, float &c) {
+// (s, c) = sum of the squares of h * f, f a power of two.  Each half of the running pair starts at
+// the thread's largest square, which makes every term the smaller one of its addition.  EXACT: the
+// values are bf16, whose squares float holds; otherwise the squares' own errors are added too.
+template <bool EXACT, int NI, typename H>
+__device__ __forceinline__ void sum_squares(const H (&h)[NI], float f, float &s, float &c) {
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; i++)
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float v = h[i][j] * f;
-            const float sq = __fmul_rn(v, v);
-            add_exact(s, c, sq);
-            if (sizeof(T) == 4) c = __fadd_rn(c, fmaf(v, v, -sq));
+        for (int j = 0; j < 4; j++) {
+            const float2 v = unpack(pair_of(h[i], j));
+            m = max_abs(m, v.x, v.y);
         }
+    m *= f;
+    const float top = __fmul_rn(m, m);
+    if (!(top < INFINITY)) {                             // an infinity, NaN, or a square past float's range
+        s = top;
+        c = 0.f;
+        return;
+    }
+    F2 s2 = f2(top, top), c2 = 0;
+    const F2 ff = f2(f, f);
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const F2 v = f == 1.f ? pair_of(h[i], j) : mul2(pair_of(h[i], j), ff);
+            const F2 sq = mul2(v, v);
+            add_smaller(s2, c2, sq);
+            if (!EXACT) c2 = add2(c2, fma2(v, v, mul2(sq, f2(-1.f, -1.f))));
+        }
+    const float2 sv = unpack(s2), cv = unpack(c2);
+    s = sv.x;
+    c = __fadd_rn(cv.x, cv.y);
+    add_exact(s, c, -top);
+    add_exact(s, c, sv.y);
+    add_exact(s, c, -top);
 }
 
 struct NormParams {
-    int d;
+    int n, d;
     float eps, inv_d, inv_d_lo;      // inv_d + inv_d_lo = 1 / d
     const void *x, *residual;
     void *residual_out, *y_out;
@@ -199,132 +346,157 @@ struct NormParams {
     uint8_t *q, *scale;
 };
 
-// One block per row; thread t holds the groups of 8 values at (i * blockDim + t) * 8, so a
-// block of 128 values is 16 consecutive lanes.
-template <typename T, int NI, bool VEC>
-__global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(NormParams p) {
+// blockDim.x threads per row (up to NI * 8 values each), blockDim.y rows per block (above one only
+// where a row is one warp's).  The row is held as it is stored (a bf16 value in half a register), so
+// that a thread can take many values and the fixed work per thread, the meeting of the sums, is spread
+// over them.  MAXT: the most threads per block.
+template <typename T, int NI, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kernel(NormParams p) {
+    using H = typename Held<T>::type;
     __shared__ float sm[64];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (row >= p.n) return;                              // a whole warp: rows of one block are warps then
     const int d = p.d;
     const T *x = static_cast<const T *>(p.x) + row * p.x_ld;
-    float h[NI][8];
+    H h[NI];
 #pragma unroll
     for (int i = 0; i < NI; i++) {
-        const int base = (i * blockDim.x + threadIdx.x) * 8;
-        if (base < d) {
-            load8<VEC>(x, base, d, h[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++) h[i][j] = 0.f;
-        }
+        const int base = first_of<VEC>(i);
+        zero8(h[i]);
+        if (base < d) load8<VEC>(x, base, d, h[i]);
     }
     if (p.residual) {
-        const T *r = static_cast<const T *>(p.residual) + row * p.residual_ld;
+        const T *rp = static_cast<const T *>(p.residual) + row * p.residual_ld;
+        H r[NI];
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            const int base = (i * blockDim.x + threadIdx.x) * 8;
-            if (base < d) {
-                float v[8];
-                load8<VEC>(r, base, d, v);
-#pragma unroll
-                for (int j = 0; j < 8; j++) h[i][j] = round_to(__fadd_rn(h[i][j], v[j]), static_cast<const T *>(nullptr));
-            }
+            const int base = first_of<VEC>(i);
+            zero8(r[i]);
+            if (base < d) load8<VEC>(rp, base, d, r[i]);
         }
+#pragma unroll
+        for (int i = 0; i < NI; i++) add8(h[i], r[i]);
     }
     if (p.residual_out) {
         T *o = static_cast<T *>(p.residual_out) + row * p.residual_out_ld;
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            const int base = (i * blockDim.x + threadIdx.x) * 8;
+            const int base = first_of<VEC>(i);
             if (base < d) store8<VEC>(o, base, d, h[i]);
         }
     }
     if (!p.q && !p.y_out) return;
 
-    // sum of squares: a bf16 square is exact in float, a float's error is kept too
-    float s = 0.f, c = 0.f;
-    sum_squares<T, NI>(h, 1.f, s, c);
-    block_sum(s, c, sm);
+    float s, c;
+    sum_squares<sizeof(T) == 2, NI>(h, 1.f, s, c);
+    row_sum(s, c, sm);
     float rstd;
     if (s < 0x1p90f) {
         rstd = rstd_of(s, c, p.inv_d, p.inv_d_lo, p.eps);
     } else {
         // squares near the end of float's range or past it (elements above about 1e13, infinities,
         // NaN): the sum of (h * 2^-80)^2, in which eps vanishes, and 2^-80 put back
-        __syncthreads();
-        s = c = 0.f;
-        sum_squares<float, NI>(h, 0x1p-80f, s, c);
-        block_sum(s, c, sm);
-        rstd = s < INFINITY ? rstd_of(s, c, p.inv_d, p.inv_d_lo, 0.f) * 0x1p-80f : rsqrtf(s);
+        if (blockDim.x > 32) __syncthreads();
+        sum_squares<false, NI>(h, 0x1p-80f, s, c);
+        row_sum(s, c, sm);
+        rstd = s < INFINITY ? rstd_of(s, c, p.inv_d, p.inv_d_lo, 0.f) * 0x1p-80f : s > 0.f ? 0.f : s;
     }
 
+    const F2 rstd2 = f2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NI; i++) {
-        const int base = (i * blockDim.x + threadIdx.x) * 8;
-        float y[8];
-        float amax = 0.f;
+        const int base = first_of<VEC>(i);
+        F2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) y[j] = mul2(pair_of(h[i], j), rstd2);
         if (base < d) {
             if (p.gain) {
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float g = VEC || base + j < d ? __ldg(p.gain + base + j) : 0.f;
-                    y[j] = __fmul_rn(__fmul_rn(h[i][j], rstd), g);
+                F32x8 g;
+                if (VEC) {
+                    const float4 a = __ldg(reinterpret_cast<const float4 *>(p.gain + base));
+                    const float4 b = __ldg(reinterpret_cast<const float4 *>(p.gain + base) + 1);
+                    g.v[0] = f2(a.x, a.y), g.v[1] = f2(a.z, a.w), g.v[2] = f2(b.x, b.y), g.v[3] = f2(b.z, b.w);
+                } else {
+                    load8<false>(p.gain, base, d, g);
                 }
-            } else {
 #pragma unroll
-                for (int j = 0; j < 8; j++) y[j] = __fmul_rn(h[i][j], rstd);
+                for (int j = 0; j < 4; j++) y[j] = mul2(y[j], g.v[j]);
             }
-            if (p.y_out) store8<VEC>(static_cast<T *>(p.y_out) + row * p.y_ld, base, d, y);
-            if (!VEC) {
-#pragma unroll
-                for (int j = 0; j < 8; j++) y[j] = base + j < d ? y[j] : 0.f;
+            if (p.y_out) {
+                H t;
+                round8(y, t);
+                store8<VEC>(static_cast<T *>(p.y_out) + row * p.y_ld, base, d, t);
             }
-#pragma unroll
-            for (int j = 0; j < 8; j++) amax = fmaxf(amax, finite_abs(y[j]));
         }
         if (p.q) {
+            // places past d hold 0 * rstd: zeros, but NaN in a row that is NaN throughout
+            if (!(rstd < INFINITY)) {
 #pragma unroll
-            for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int byte = scale_byte(amax);
-            if (base < d) {
-                store_codes(p.q + row * p.q_ld, base, d, codes(y, inverse_scale(byte)));
-                if (threadIdx.x % 16 == 0) p.scale[row * p.scale_ld + base / 128] = (uint8_t)byte;
+                for (int j = 0; j < 4; j++) {
+                    const float2 v = unpack(y[j]);
+                    const int step = VEC ? 1 : 32, b = base + 2 * j * step;
+                    y[j] = f2(b < d ? v.x : 0.f, b + step < d ? v.y : 0.f);
+                }
             }
+            quantise8<VEC>(y, base, d, p.q + row * p.q_ld, p.scale + row * p.scale_ld);
         }
     }
 }
 
-// One block of 256 threads per 128 x 128 block of weights, 64 values in each thread.
+// One block of 256 threads per 128 x 128 block of weights, 64 values in each thread: VEC a row's
+// 128 values in 16 threads, otherwise 4 single ones in each of 32 lanes (two rows per step).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quant_weight_kernel(int n, int k, const T *__restrict__ w, int64_t w_ld,
-                                                           uint8_t *__restrict__ q, int64_t q_ld,
-                                                           uint8_t *__restrict__ scale, int64_t scale_ld) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
+quant_weight_kernel(int n, int k, const T *__restrict__ w, int64_t w_ld, uint8_t *__restrict__ q, int64_t q_ld,
+                    uint8_t *__restrict__ scale, int64_t scale_ld) {
+    using H = typename Held<T>::type;
     __shared__ float sm[8];
     pdl_wait();
     pdl_launch_dependents();
-    const int base = blockIdx.x * 128 + (threadIdx.x % 16) * 8;
-    const int row0 = blockIdx.y * 128 + threadIdx.x / 16;
-    float v[8][8];
-    float amax = 0.f;
+    const int t = threadIdx.x;
+    const int base = blockIdx.x * 128 + (VEC ? t % 16 * 8 : t % 32);
+    const int row0 = blockIdx.y * 128 + (VEC ? t / 16 : t / 32 * 2);
+    // step i, VEC: row row0 + 16 i; else values 0-3 of row row0 + 16 i, 4-7 of the next
+    H h[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = row0 + 16 * i;
-        if (r < n && base < k) {
-            load8<VEC>(w + r * w_ld, base, k, v[i]);
+        zero8(h[i]);
+        if (VEC) {
+            if (r < n && base < k) load8<true>(w + r * w_ld, base, k, h[i]);
         } else {
+            float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[i][j] = 0.f;
+            for (int j = 0; j < 8; j++)
+                f[j] = r + j / 4 < n && base + 32 * (j % 4) < k ? (float)w[(r + j / 4) * w_ld + base + 32 * (j % 4)] : 0.f;
+            const F2 y[4] = {f2(f[0], f[1]), f2(f[2], f[3]), f2(f[4], f[5]), f2(f[6], f[7])};
+            round8(y, h[i]);                             // exact: the values are of the type
         }
     }
+    float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
-        for (int j = 0; j < 8; j++) amax = fmaxf(amax, finite_abs(v[i][j]));
+        for (int j = 0; j < 4; j++) {
+            const float2 a = unpack(pair_of(h[i], j));
+            amax = max_abs(amax, a.x, a.y);
+        }
+    const bool finite = __syncthreads_and(amax < INFINITY);
+    if (!finite) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 a = unpack(pair_of(h[i], j));
+                amax = fmaxf(amax, fmaxf(finite_abs(a.x), finite_abs(a.y)));
+            }
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = amax;
+    if (t % 32 == 0) sm[t / 32] = amax;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; i++) amax = fmaxf(amax, sm[i]);
@@ -333,25 +505,44 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(int n, int k, const T
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const int r = row0 + 16 * i;
-        if (r < n && base < k) store_codes(q + r * q_ld, base, k, codes(v[i], inv));
+        const F2 y[4] = {pair_of(h[i], 0), pair_of(h[i], 1), pair_of(h[i], 2), pair_of(h[i], 3)};
+        const uint2 c = finite ? codes<true>(y, inv) : codes<false>(y, inv);
+        if (VEC) {
+            if (r < n && base < k) *reinterpret_cast<uint2 *>(q + r * q_ld + base) = c;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (r + j / 4 < n && base + 32 * (j % 4) < k)
+                    q[(r + j / 4) * q_ld + base + 32 * (j % 4)] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j % 4)));
+        }
     }
-    if (threadIdx.x == 0) scale[blockIdx.y * scale_ld + blockIdx.x] = (uint8_t)byte;
+    if (t == 0) scale[blockIdx.y * scale_ld + blockIdx.x] = (uint8_t)byte;
 }
 
-template <typename T, int NI>
-cudaError_t launch_norm(const NormParams &p, bool vec, uint32_t n, int threads, cudaStream_t s) {
-    return vec ? launch_pdl(rmsnorm_quant_kernel<T, NI, true>, dim3(n), dim3(threads), 0, s, p)
-               : launch_pdl(rmsnorm_quant_kernel<T, NI, false>, dim3(n), dim3(threads), 0, s, p);
+template <typename T, int NI, int MAXT>
+cudaError_t launch_norm(const NormParams &p, bool vec, int threads, cudaStream_t s) {
+    // rows of one warp: four to a block
+    const int rows = threads == 32 && p.n > 4 ? 4 : 1;
+    const dim3 grid((unsigned)((p.n + rows - 1) / rows)), block(threads, rows);
+    return vec ? launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT>, grid, block, 0, s, p)
+               : launch_pdl(rmsnorm_quant_kernel<T, NI, false, MAXT>, grid, block, 0, s, p);
 }
 
+// Threads per row.  Few rows: one group of 8 values in each thread, the shortest chain (a row of 4096
+// bf16 values in 2.6 us).  Many rows: as few warps as hold the row in 2 groups of each thread, 4 for
+// aligned bf16 rows, which are half as wide (4096 x 4096: 26 us; 28 with 2 groups, 33 with 8; 16384 x
+// 7168: 142, 238, 156; 16384 x 1024 floats: 39 with 2, 42 with 4; 3000 unaligned rows of 1541: 16 with
+// 2, 22 with 4).
 template <typename T>
-cudaError_t launch_norm_t(const NormParams &p, bool vec, uint32_t n, cudaStream_t s) {
-    const int groups = (p.d + 7) / 8;
+cudaError_t launch_norm_t(const NormParams &p, bool vec, cudaStream_t s) {
+    const int most = sizeof(T) == 2 && vec ? 4 : 2, groups = (p.d + 7) / 8;
     int ni = 1;
-    while (groups > 1024 * ni) ni *= 2;
+    while (ni < most && groups > (p.n >= 512 ? 32 : 1024) * ni) ni *= 2;
+    while (groups > 1024 * ni) ni *= 2;                  // d = 32768 is 4 groups in each of 1024 threads
     const int threads = ((groups + ni - 1) / ni + 31) / 32 * 32;
-    return ni == 1 ? launch_norm<T, 1>(p, vec, n, threads, s)
-                   : ni == 2 ? launch_norm<T, 2>(p, vec, n, threads, s) : launch_norm<T, 4>(p, vec, n, threads, s);
+    if (ni == 1) return launch_norm<T, 1, 1024>(p, vec, threads, s);
+    if (ni == 2) return launch_norm<T, 2, 1024>(p, vec, threads, s);
+    return threads <= 256 ? launch_norm<T, 4, 256>(p, vec, threads, s) : launch_norm<T, 4, 1024>(p, vec, threads, s);
 }
 
 template <typename T>
@@ -363,6 +554,7 @@ bool vec_ok(const void *p, size_t ld) {
 
 cudaError_t launch_rmsnorm_quant(const ds4c_rmsnorm_args &a, cudaStream_t s) {
     NormParams p{};
+    p.n = (int)a.n;
     p.d = (int)a.d;
     p.eps = a.eps;
     p.inv_d = (float)(1.0 / a.d);
@@ -380,16 +572,17 @@ cudaError_t launch_rmsnorm_quant(const ds4c_rmsnorm_args &a, cudaStream_t s) {
     p.gain = a.gain;
     p.q = a.q;
     p.scale = a.scale;
+    const bool gain_ok = ((uintptr_t)a.gain & 15) == 0;
     if (a.dtype == DS4C_F32) {
         using T = float;
         const bool vec = a.d % 8 == 0 && vec_ok<T>(a.x, a.x_ld) && vec_ok<T>(a.residual, a.residual_ld) &&
-                         vec_ok<T>(a.residual_out, a.residual_out_ld) && vec_ok<T>(a.y_out, a.y_ld);
-        return launch_norm_t<T>(p, vec, a.n, s);
+                         vec_ok<T>(a.residual_out, a.residual_out_ld) && vec_ok<T>(a.y_out, a.y_ld) && gain_ok;
+        return launch_norm_t<T>(p, vec, s);
     }
     using T = __nv_bfloat16;
     const bool vec = a.d % 8 == 0 && vec_ok<T>(a.x, a.x_ld) && vec_ok<T>(a.residual, a.residual_ld) &&
-                     vec_ok<T>(a.residual_out, a.residual_out_ld) && vec_ok<T>(a.y_out, a.y_ld);
-    return launch_norm_t<T>(p, vec, a.n, s);
+                     vec_ok<T>(a.residual_out, a.residual_out_ld) && vec_ok<T>(a.y_out, a.y_ld) && gain_ok;
+    return launch_norm_t<T>(p, vec, s);
 }
 
 cudaError_t launch_quant_weight(uint32_t n, uint32_t k, uint32_t dtype, const void *w, size_t w_ld, uint8_t *q,

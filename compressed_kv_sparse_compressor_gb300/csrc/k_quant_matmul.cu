@@ -465,16 +465,16 @@ struct Pair {
     static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms");
 };
 
-// Output tile -> weight matrix, row tile and weight tile: within a matrix, 8 weight tiles go
+// Output tile -> weight matrix, row tile and weight tile: within a matrix, 16 weight tiles go
 // with each row tile before the next row tile, so that the tiles in flight share their operands in L2.
 __device__ __forceinline__ void pair_coords(const Params &p, int tile, int &g, int &mt, int &nt) {
     g = 0;
     while (g + 1 < p.n_w && tile >= p.tile_start[g + 1]) g++;
     const int local = tile - p.tile_start[g], n_tiles = (p.n[g] + 2 * BW - 1) / (2 * BW);
-    const int band = local / (8 * p.m_tiles), wide = min(8, n_tiles - 8 * band);
-    const int in = local - band * 8 * p.m_tiles;
+    const int band = local / (16 * p.m_tiles), wide = min(16, n_tiles - 16 * band);
+    const int in = local - band * 16 * p.m_tiles;
     mt = in / wide;
-    nt = 8 * band + in % wide;
+    nt = 16 * band + in % wide;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
@@ -775,7 +775,7 @@ int pair_bt(const QuantMatmulArgs &a) {
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
         int64_t tiles = 0;
         for (int g = 0; g < a.n_w; g++) tiles += (int64_t)((a.w[g].n + 2 * BW - 1) / (2 * BW)) * ((a.m + bt - 1) / bt);
-        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * bt;
+        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * (bt + 64);
         if (best == 0 || cost < best_cost) best = bt, best_cost = cost;
     }
     return best;

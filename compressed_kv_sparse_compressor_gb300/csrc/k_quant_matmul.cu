@@ -13,10 +13,12 @@
 //   - K in stages of 128 bytes (one scale block): the weights' [128][128] and the rows'
 //     [BT][128] bytes by TMA in the 128-byte swizzle, a ring of mbarriers.  Rows and
 //     columns past the ends, and K past the last value, are filled with zeros.
-//   - Scales: one warp reads the four scale bytes of 4 stages per row as a word and lays
-//     them out in shared memory as TMEM wants them ([32 lanes][4 words], row r in lane
-//     r % 32, word r / 32); the MMA thread copies them to TMEM (tcgen05.cp, replicated to
-//     the four lane quarters) and the instruction descriptor picks the stage's byte.
+//   - Scales: one warp copies the four scale bytes of 4 stages per row as a word (cp.async,
+//     up to three groups of 4 stages in flight: read one group at a time, their latency held
+//     an 8192 x 8192 x 8192 product at 372 us where it takes 252) into shared memory as
+//     TMEM wants them ([32 lanes][4 words], row r in lane r % 32, word r / 32); the MMA
+//     thread copies them to TMEM (tcgen05.cp, replicated to the four lane quarters) and
+//     the instruction descriptor picks the stage's byte.
 //   - A cluster of `split` CTAs shares an output tile, each with a range of K; the
 //     partial tiles meet through distributed shared memory and are added in rank order.
 //   - Every mbarrier wait is bounded; a wait that gives up raises the library's device
@@ -36,7 +38,8 @@ namespace {
 
 constexpr int BW = 128, BK = 128;              // weight rows and K bytes of a stage
 constexpr int THREADS = 256;
-constexpr int SF_SLOTS = 2;                    // scale words of two groups of 4 stages in flight
+constexpr int SF_SLOTS = 5;                    // groups of 4 stages whose scales shared memory and TMEM hold
+constexpr int SF_AHEAD = 3;                    // groups whose copies are in flight (below SF_SLOTS)
 constexpr int SF_BYTES = 512;                  // scales of 128 rows, 4 stages
 constexpr int MAX_SPLIT = 8;
 
@@ -156,6 +159,10 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Without memory ordering: for a barrier that guards TMEM only, which tcgen05.fence orders.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -247,6 +254,36 @@ __device__ __forceinline__ float4 cluster_ld(uint32_t addr, uint32_t rank) {
         : "r"(addr), "r"(rank)
         : "memory");
     return v;
+}
+
+// Copies the scale words of group q (4 stages) of 128 rows, row r of them at src + r * ld, into their
+// slot; rows from `rows` on get zero bytes (their codes are zeros too).  One warp.
+__device__ __forceinline__ void copy_words(uint32_t dst, const uint8_t *src, int ld, int rows, int q, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int r = j * 32 + lane;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + lane * 16 + j * 4),
+                     "l"(r < rows ? src + (size_t)r * ld + 4 * q : src), "r"(r < rows ? 4 : 0)
+                     : "memory");
+    }
+}
+// The same with one word for all rows.
+__device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t *src, int q, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + lane * 16 + j * 4), "l"(src + 4 * q) : "memory");
+}
+// Arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `left` groups of this thread's copies are in flight, and shows the others to
+// the asynchronous proxy.
+template <int left>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 __device__ __forceinline__ void store_out(void *out, int64_t i, float v, int bf16) {
@@ -359,29 +396,25 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         __syncwarp();
     } else if (warp == 2) {
         // scales of groups of 4 stages (absolute positions, so a group is one word per row)
-        const uint8_t *ws = p.w_scale[g] + (size_t)nt * p.scale_ld;
-        uint32_t sl = 0;
-        for (int q = kb0 / 4; q < (kb1 + 3) / 4; q++, sl++) {
-            const int slot = sl % SF_SLOTS;
-            uint32_t t[S::SFT][4];
+        const uint8_t *ws = p.w_scale[g] + (size_t)nt * p.scale_ld, *ts = p.a_scale + (size_t)m0 * p.scale_ld;
+        uint32_t issued = 0, done = 0;
+        for (int q = kb0 / 4; q < (kb1 + 3) / 4; q++, issued++) {
+            const int slot = issued % SF_SLOTS;
+            if (!mbar_wait(smem_u32(&sf_empty[slot]), ((issued / SF_SLOTS) & 1) ^ 1, abort)) break;
+            const uint32_t dst = smem_u32(sf + slot * S::SF_SLOT_BYTES);
+            copy_word(dst, ws, q, lane);
 #pragma unroll
             for (int i = 0; i < S::SFT; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int r = i * 128 + j * 32 + lane;
-                    const bool in = r < BT && m0 + r < p.m;
-                    t[i][j] = in ? __ldg(reinterpret_cast<const uint32_t *>(p.a_scale + (size_t)(m0 + r) * p.scale_ld + 4 * q))
-                                 : 0x7F7F7F7Fu;
-                }
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(ws + 4 * q));
-            if (!mbar_wait(smem_u32(&sf_empty[slot]), ((sl / SF_SLOTS) & 1) ^ 1, abort)) break;
-            uint4 *dst = reinterpret_cast<uint4 *>(sf + slot * S::SF_SLOT_BYTES) + lane;
-            dst[0] = make_uint4(w, w, w, w);
-#pragma unroll
-            for (int i = 0; i < S::SFT; i++) dst[32 * (1 + i)] = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(smem_u32(&sf_full[slot]));
+                copy_words(dst + (1 + i) * SF_BYTES, ts + (size_t)i * 128 * p.scale_ld, p.scale_ld, min(BT, p.m - m0) - i * 128, q,
+                           lane);
+            copies_commit();
+            if (issued - done == SF_AHEAD) {
+                copies_wait<SF_AHEAD>();
+                mbar_arrive(smem_u32(&sf_full[done++ % SF_SLOTS]));
+            }
         }
+        copies_wait<0>();
+        for (; done < issued; done++) mbar_arrive(smem_u32(&sf_full[done % SF_SLOTS]));
         __syncwarp();
     } else if (warp >= 4) {
         // epilogue: TMEM lane quarter warp % 4, lane = weight row, column = row of the product
@@ -443,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 // bt rows: each CTA holds 128 weight rows and half of the rows in shared memory, so a stage
 // costs (128 + bt / 2) * 128 bytes of loads per SM where one CTA alone would need
 // (128 + bt) * 128.  bt (a multiple of 32, at most 224) is chosen by the host so that the
-// tiles fill whole rounds over the pairs; two accumulators of bt columns and two slots of
+// tiles fill whole rounds over the pairs; two accumulators of bt columns and five slots of
 // scales fit the 512 TMEM columns, so a tile's epilogue runs beside the next tile's MMAs.
 // The tensor core's float accumulation cuts low bits off (its error grows with K: 4e-7 of
 // the result's norm at K = 4096), so an accumulator takes at most CHUNK blocks of K; the
@@ -457,7 +490,7 @@ constexpr int PAIR_THREADS = 384, PAIR_STAGES = 7, MAX_BT = 224, CHUNK = 32;
 struct Pair {
     static constexpr int W_BYTES = BW * BK, STAGE_BYTES = W_BYTES + MAX_BT / 2 * BK;
     static constexpr int SF_SLOT_BYTES = 3 * SF_BYTES, SF_COLS = 12;
-    static constexpr int N_BARS = 2 * PAIR_STAGES + 2 * SF_SLOTS + 5;
+    static constexpr int N_BARS = 2 * PAIR_STAGES + 3 * SF_SLOTS + 5;
     static constexpr int SMEM_BYTES = PAIR_STAGES * STAGE_BYTES + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
     static constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(2 * BW >> 7) << 27);       // M = 256, N added
     static constexpr int HALF_CHUNKS = MAX_BT / 2 / 16;
@@ -477,6 +510,24 @@ __device__ __forceinline__ void pair_coords(const Params &p, int tile, int &g, i
     nt = 16 * band + in % wide;
 }
 
+// One thread: passes on every STEP-th group of scales from `first`, landed in this CTA, to the MMA
+// thread's barrier.  In the leader's CTA (STEP 1) that is an ordinary arrival.  From the other CTA it
+// is a release at cluster scope, which waits for all that its thread has in flight and takes about a
+// microsecond beside the loads (made by the copying threads themselves it held an 8192 x 8192 x 8192
+// product at 415 us, the whole time of a group of stages): two threads without copies of their own
+// take turns.
+template <int STEP>
+__device__ __forceinline__ void signal_scales(uint64_t *loaded, uint32_t full, uint32_t first, uint32_t groups,
+                                              volatile int *abort) {
+    for (uint32_t n = first; n < groups; n += STEP) {
+        const int slot = n % SF_SLOTS;
+        if (!mbar_wait(smem_u32(&loaded[slot]), (n / SF_SLOTS) & 1, abort)) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (STEP == 1) mbar_arrive(full + 8 * slot);
+        else mbar_arrive_cluster(full + 8 * slot);
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     extern __shared__ uint8_t smem_raw[];
@@ -484,12 +535,15 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     uint8_t *sf = smem + PAIR_STAGES * Pair::STAGE_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(sf + SF_SLOTS * Pair::SF_SLOT_BYTES);
     uint64_t *empty = full + PAIR_STAGES, *sf_full = empty + PAIR_STAGES, *sf_empty = sf_full + SF_SLOTS;
-    uint64_t *acc_full = sf_empty + SF_SLOTS, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
+    uint64_t *sf_loaded = sf_empty + SF_SLOTS, *acc_full = sf_loaded + SF_SLOTS, *acc_empty = acc_full + 2;
+    uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
+    // groups of scales over all of this pair's tiles
+    const uint32_t groups = pair < total ? (uint32_t)((total - pair + pairs - 1) / pairs) * ((p.kb + 3) / 4) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < PAIR_STAGES; s++) {
@@ -497,8 +551,9 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < SF_SLOTS; s++) {
-            mbar_init(smem_u32(&sf_full[s]), 64);
+            mbar_init(smem_u32(&sf_full[s]), 2);
             mbar_init(smem_u32(&sf_empty[s]), 1);
+            mbar_init(smem_u32(&sf_loaded[s]), 32);
         }
         for (int a = 0; a < 2; a++) {
             mbar_init(smem_u32(&acc_full[a]), 1);
@@ -522,38 +577,43 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     pdl_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t it = 0;
-            for (int tile = pair; tile < total && ok; tile += pairs) {
-                int g, mt, nt;
-                pair_coords(p, tile, g, mt, nt);
-                const int wy = nt * 2 * BW + rank * BW, ty = mt * bt + rank * (bt / 2);
-                for (int kb = 0; kb < p.kb; kb++, it++) {
-                    const int s = it % PAIR_STAGES;
-                    if (!mbar_wait(smem_u32(&empty[s]), ((it / PAIR_STAGES) & 1) ^ 1, abort)) { ok = false; break; }
-                    const uint32_t dst = smem_u32(smem + s * Pair::STAGE_BYTES);
-                    const uint32_t bar = mapa(smem_u32(&full[s]), 0);
-                    if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * (Pair::W_BYTES + bt / 2 * BK));
-                    tma_load_2d_pair(dst, &maps.w[g], kb * BK, wy, bar);
+        bool ok = true;
+        uint32_t it = 0, s = 0, par = 1;
+        const uint32_t bytes = 2 * (Pair::W_BYTES + bt / 2 * BK);
+        const uint32_t base = smem_u32(smem), full0 = mapa(smem_u32(full), 0);
+        for (int tile = pair; tile < total && ok; tile += pairs) {
+            int g, mt, nt;
+            pair_coords(p, tile, g, mt, nt);
+            const int wy = nt * 2 * BW + rank * BW, ty = mt * bt + rank * (bt / 2);
+            const CUtensorMap *mw = &maps.w[g];
+            for (int kb = 0; kb < p.kb; kb++, it++) {
+                if (!mbar_wait(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
+                const uint32_t dst = base + s * Pair::STAGE_BYTES, bar = full0 + 8 * s;
+                if (elect()) {
+                    if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), bytes);
+                    tma_load_2d_pair(dst, mw, kb * BK, wy, bar);
                     tma_load_2d_pair(dst + Pair::W_BYTES, &maps.a, kb * BK, ty, bar);
                 }
+                __syncwarp();
+                if (++s == PAIR_STAGES) s = 0, par ^= 1;
             }
-            // after a give-up the pair's loads still in flight land before it exits: the leader sees them
-            // on its barriers, the other CTA has none and waits a time no load takes
-            if (!ok) {
-                if (rank == 0) {
-                    for (uint32_t u = it > (uint32_t)PAIR_STAGES ? it - PAIR_STAGES : 0; u < it; u++)
-                        mbar_drain(smem_u32(&full[u % PAIR_STAGES]), (u / PAIR_STAGES) & 1);
-                } else {
-                    const uint64_t t0 = globaltimer();
-                    while (globaltimer() - t0 < 2000000ull) {}
-                }
+        }
+        // after a give-up the pair's loads still in flight land before it exits: the leader sees them
+        // on its barriers, the other CTA has none and waits a time no load takes
+        if (!ok) {
+            if (rank == 0) {
+                for (uint32_t u = it > (uint32_t)PAIR_STAGES ? it - PAIR_STAGES : 0; u < it; u++)
+                    mbar_drain(smem_u32(&full[u % PAIR_STAGES]), (u / PAIR_STAGES) & 1);
+            } else {
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 2000000ull) {}
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (rank == 0) {
+        if (rank != 0) {
+            if (lane == 0) signal_scales<2>(sf_loaded, mapa(smem_u32(sf_full), 0), 0, groups, abort);
+        } else {
             bool ok = true;
             uint32_t s = 0, s_par = 0, sl = 0, local = 0;
             const uint32_t sf_tmem = tmem + 2 * (uint32_t)bt;
@@ -579,7 +639,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                                 for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
                             }
                         }
-                        if (!mbar_wait<true>(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
+                        if (!mbar_wait(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
                         fence_after();
                         const uint64_t wd = w_desc + (uint64_t)(s * (Pair::STAGE_BYTES >> 4));
                         const uint64_t td = t_desc + (uint64_t)(s * (Pair::STAGE_BYTES >> 4));
@@ -614,38 +674,35 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
         }
         __syncwarp();
     } else if (warp == 2) {
-        uint32_t sl = 0;
+        uint32_t n = 0;
         bool ok = true;
         for (int tile = pair; tile < total && ok; tile += pairs) {
             int g, mt, nt;
             pair_coords(p, tile, g, mt, nt);
             // a weight tile past the matrix's end (the second CTA's) feeds no output: any scale
             const int wb = min(2 * nt + rank, (p.n[g] + BW - 1) / BW - 1), m0 = mt * bt;
+            const int rows = min(bt, p.m - m0);
             const uint8_t *ws = p.w_scale[g] + (size_t)wb * p.scale_ld;
-            for (int q = 0; q < (p.kb + 3) / 4; q++, sl++) {
-                const int slot = sl % SF_SLOTS;
-                uint32_t t[2][4];
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int r = i * 128 + j * 32 + lane;
-                        const bool in = r < bt && m0 + r < p.m;
-                        t[i][j] = in ? __ldg(reinterpret_cast<const uint32_t *>(p.a_scale + (size_t)(m0 + r) * p.scale_ld + 4 * q))
-                                     : 0x7F7F7F7Fu;
-                    }
-                const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(ws + 4 * q));
-                if (!mbar_wait(smem_u32(&sf_empty[slot]), ((sl / SF_SLOTS) & 1) ^ 1, abort)) { ok = false; break; }
-                uint4 *dst = reinterpret_cast<uint4 *>(sf + slot * Pair::SF_SLOT_BYTES) + lane;
-                dst[0] = make_uint4(w, w, w, w);
-#pragma unroll
-                for (int i = 0; i < 2; i++) dst[32 * (1 + i)] = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive_cluster(mapa(smem_u32(&sf_full[slot]), 0));
+            const uint8_t *ts = p.a_scale + (size_t)m0 * p.scale_ld;
+            for (int sq = 0; sq < (p.kb + 3) / 4; sq++, n++) {
+                const int slot = n % SF_SLOTS;
+                if (!mbar_wait(smem_u32(&sf_empty[slot]), ((n / SF_SLOTS) & 1) ^ 1, abort)) { ok = false; break; }
+                const uint32_t dst = smem_u32(sf + slot * Pair::SF_SLOT_BYTES);
+                copy_word(dst, ws, sq, lane);
+                copy_words(dst + SF_BYTES, ts, p.scale_ld, rows, sq, lane);
+                copy_words(dst + 2 * SF_BYTES, rows > 128 ? ts + (size_t)128 * p.scale_ld : ts, p.scale_ld, rows - 128, sq, lane);
+                copies_arrive(smem_u32(&sf_loaded[slot]));
             }
         }
+        copies_wait<0>();
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        if (lane == 0) {
+            if (rank == 0) signal_scales<1>(sf_loaded, smem_u32(sf_full), 0, groups, abort);
+            else signal_scales<2>(sf_loaded, mapa(smem_u32(sf_full), 0), 1, groups, abort);
+        }
+        __syncwarp();
+    } else {
         const int quarter = warp & 3, half = (warp - 4) / 4, cols = bt / 2;
         uint32_t local = 0;
         bool ok = true;
@@ -675,7 +732,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&acc_empty[acc]), 0));
+                if (lane == 0) mbar_arrive_relaxed(mapa(smem_u32(&acc_empty[acc]), 0));
             }
             if (!ok) break;
             const int n = nt * 2 * BW + rank * BW + quarter * 32 + lane, m0 = mt * bt + half * cols;
@@ -775,7 +832,7 @@ int pair_bt(const QuantMatmulArgs &a) {
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
         int64_t tiles = 0;
         for (int g = 0; g < a.n_w; g++) tiles += (int64_t)((a.w[g].n + 2 * BW - 1) / (2 * BW)) * ((a.m + bt - 1) / bt);
-        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * (bt + 64);
+        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * (bt + 256);
         if (best == 0 || cost < best_cost) best = bt, best_cost = cost;
     }
     return best;

@@ -486,16 +486,17 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 // 2 scales (both CTAs: the words of all bt rows and of the CTA's own weight rows), 4-11
 // epilogue (TMEM lane quarter w % 4, half of the columns each).
 // ---------------------------------------------------------------------------------------
-constexpr int PAIR_THREADS = 384, PAIR_STAGES = 7, MAX_BT = 224, CHUNK = 32;
+constexpr int PAIR_THREADS = 384, MAX_BT = 224, CHUNK = 32;
+constexpr int PAIR_STAGES = 4, PAIR_RING = 216 * 1024;       // most stages, bytes of the ring
 struct Pair {
-    static constexpr int W_BYTES = BW * BK, STAGE_BYTES = W_BYTES + MAX_BT / 2 * BK;
+    static constexpr int W_BYTES = BW * BK;
     static constexpr int SF_SLOT_BYTES = 3 * SF_BYTES, SF_COLS = 12;
     static constexpr int N_BARS = 2 * PAIR_STAGES + 3 * SF_SLOTS + 5;
-    static constexpr int SMEM_BYTES = PAIR_STAGES * STAGE_BYTES + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
+    static constexpr int SMEM_BYTES = PAIR_RING + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
     static constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(2 * BW >> 7) << 27);       // M = 256, N added
     static constexpr int HALF_CHUNKS = MAX_BT / 2 / 16;
     static_assert(2 * MAX_BT + SF_SLOTS * SF_COLS <= 512, "TMEM columns");
-    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms");
+    static_assert(3 * 2 * (W_BYTES + MAX_BT / 2 * BK) <= PAIR_RING && SMEM_BYTES <= 232448, "three stages at the widest tile");
 };
 
 // Output tile -> weight matrix, row tile and weight tile: within a matrix, 16 weight tiles go
@@ -532,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sf = smem + PAIR_STAGES * Pair::STAGE_BYTES;
+    uint8_t *sf = smem + PAIR_RING;
     uint64_t *full = reinterpret_cast<uint64_t *>(sf + SF_SLOTS * Pair::SF_SLOT_BYTES);
     uint64_t *empty = full + PAIR_STAGES, *sf_full = empty + PAIR_STAGES, *sf_empty = sf_full + SF_SLOTS;
     uint64_t *sf_loaded = sf_empty + SF_SLOTS, *acc_full = sf_loaded + SF_SLOTS, *acc_empty = acc_full + 2;
@@ -542,6 +543,9 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
+    // a stage is two blocks of K: the handshakes of a stage take some 480 cycles of the MMA warp, the
+    // MMAs of one block 2 bt
+    const uint32_t block = Pair::W_BYTES + (uint32_t)bt / 2 * BK, stages = min((uint32_t)PAIR_STAGES, PAIR_RING / (2 * block));
     // groups of scales over all of this pair's tiles
     const uint32_t groups = pair < total ? (uint32_t)((total - pair + pairs - 1) / pairs) * ((p.kb + 3) / 4) : 0;
 
@@ -579,31 +583,35 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     if (warp == 0) {
         bool ok = true;
         uint32_t it = 0, s = 0, par = 1;
-        const uint32_t bytes = 2 * (Pair::W_BYTES + bt / 2 * BK);
         const uint32_t base = smem_u32(smem), full0 = mapa(smem_u32(full), 0);
         for (int tile = pair; tile < total && ok; tile += pairs) {
             int g, mt, nt;
             pair_coords(p, tile, g, mt, nt);
             const int wy = nt * 2 * BW + rank * BW, ty = mt * bt + rank * (bt / 2);
             const CUtensorMap *mw = &maps.w[g];
-            for (int kb = 0; kb < p.kb; kb++, it++) {
+            for (int kb = 0; kb < p.kb; kb += 2, it++) {
                 if (!mbar_wait(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
-                const uint32_t dst = base + s * Pair::STAGE_BYTES, bar = full0 + 8 * s;
+                const uint32_t dst = base + s * 2 * block, bar = full0 + 8 * s;
+                const bool two = kb + 1 < p.kb;
                 if (elect()) {
-                    if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), bytes);
+                    if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), (two ? 4 : 2) * block);
                     tma_load_2d_pair(dst, mw, kb * BK, wy, bar);
                     tma_load_2d_pair(dst + Pair::W_BYTES, &maps.a, kb * BK, ty, bar);
+                    if (two) {
+                        tma_load_2d_pair(dst + block, mw, kb * BK + BK, wy, bar);
+                        tma_load_2d_pair(dst + block + Pair::W_BYTES, &maps.a, kb * BK + BK, ty, bar);
+                    }
                 }
                 __syncwarp();
-                if (++s == PAIR_STAGES) s = 0, par ^= 1;
+                if (++s == stages) s = 0, par ^= 1;
             }
         }
         // after a give-up the pair's loads still in flight land before it exits: the leader sees them
         // on its barriers, the other CTA has none and waits a time no load takes
         if (!ok) {
             if (rank == 0) {
-                for (uint32_t u = it > (uint32_t)PAIR_STAGES ? it - PAIR_STAGES : 0; u < it; u++)
-                    mbar_drain(smem_u32(&full[u % PAIR_STAGES]), (u / PAIR_STAGES) & 1);
+                for (uint32_t u = it > stages ? it - stages : 0; u < it; u++)
+                    mbar_drain(smem_u32(&full[u % stages]), (u / stages) & 1);
             } else {
                 const uint64_t t0 = globaltimer();
                 while (globaltimer() - t0 < 2000000ull) {}
@@ -618,8 +626,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             uint32_t s = 0, s_par = 0, sl = 0, local = 0;
             const uint32_t sf_tmem = tmem + 2 * (uint32_t)bt;
             const uint32_t idesc0 = Pair::IDESC | (uint32_t)(bt >> 3) << 17;
-            const uint64_t w_desc = sw128_desc(smem_u32(smem)), t_desc = sw128_desc(smem_u32(smem) + Pair::W_BYTES);
-            const uint64_t sf_desc = scale_desc(smem_u32(sf));
+            const uint64_t w_desc = sw128_desc(smem_u32(smem)), sf_desc = scale_desc(smem_u32(sf));
             for (int tile = pair; tile < total && ok; tile += pairs) {
                 for (int c = 0; c < chunks && ok; c++, local++) {
                     const uint32_t acc = local & 1, d = tmem + acc * (uint32_t)bt;
@@ -627,7 +634,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                     fence_after();
                     const int kb1 = min(p.kb, (c + 1) * CHUNK);
                     uint32_t accumulate = 0;
-                    for (int kb = c * CHUNK; kb < kb1; kb++) {
+                    for (int kb = c * CHUNK; kb < kb1; kb += 2) {
                         const uint32_t slot = sl % SF_SLOTS;
                         const uint32_t sfa = sf_tmem + slot * Pair::SF_COLS, sfb = sfa + 4;
                         if (kb % 4 == 0) {
@@ -641,18 +648,24 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                         }
                         if (!mbar_wait(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
                         fence_after();
-                        const uint64_t wd = w_desc + (uint64_t)(s * (Pair::STAGE_BYTES >> 4));
-                        const uint64_t td = t_desc + (uint64_t)(s * (Pair::STAGE_BYTES >> 4));
-                        const uint32_t id = (uint32_t)kb % 4, idesc = idesc0 | id << 4 | id << 29;
-                        const bool group_end = kb % 4 == 3 || kb == p.kb - 1;
+                        const uint64_t wd = w_desc + (uint64_t)(s * (2 * block >> 4)), wd1 = wd + (block >> 4);
+                        constexpr uint64_t T = Pair::W_BYTES >> 4;
+                        const uint32_t id = (uint32_t)kb % 4, idesc = idesc0 | id << 4 | id << 29, idesc1 = idesc + (1u << 4 | 1u << 29);
+                        const bool group_end = kb % 4 == 2 || kb + 2 >= p.kb;
                         if (elect()) {
-                            if (kb < p.kb - 1 || p.k_tail == BK / 32) {
+                            if (kb + 2 < p.kb || (kb + 2 == p.kb && p.k_tail == BK / 32)) {
 #pragma unroll
                                 for (int k = 0; k < BK / 32; k++)
-                                    mma_scaled_pair(d, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
-                            } else {
-                                for (int k = 0; k < p.k_tail; k++)
-                                    mma_scaled_pair(d, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                                    mma_scaled_pair(d, wd + 2 * k, wd + T + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+#pragma unroll
+                                for (int k = 0; k < BK / 32; k++)
+                                    mma_scaled_pair(d, wd1 + 2 * k, wd1 + T + 2 * k, idesc1, sfa, sfb, 1u);
+                            } else {                     // the last one or two blocks, the last one shorter
+                                const int n0 = kb + 1 < p.kb ? BK / 32 : p.k_tail, n1 = kb + 1 < p.kb ? p.k_tail : 0;
+                                for (int k = 0; k < n0; k++)
+                                    mma_scaled_pair(d, wd + 2 * k, wd + T + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                                for (int k = 0; k < n1; k++)
+                                    mma_scaled_pair(d, wd1 + 2 * k, wd1 + T + 2 * k, idesc1, sfa, sfb, 1u);
                             }
                             mma_commit_pair(smem_u32(&empty[s]));
                             if (group_end) mma_commit_pair(smem_u32(&sf_empty[slot]));
@@ -660,7 +673,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                         __syncwarp();
                         accumulate = 1;
                         sl += group_end ? 1 : 0;
-                        if (++s == PAIR_STAGES) s = 0, s_par ^= 1;
+                        if (++s == stages) s = 0, s_par ^= 1;
                     }
                     if (ok && elect()) mma_commit_pair(smem_u32(&acc_full[acc]));
                     __syncwarp();
@@ -832,7 +845,7 @@ int pair_bt(const QuantMatmulArgs &a) {
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
         int64_t tiles = 0;
         for (int g = 0; g < a.n_w; g++) tiles += (int64_t)((a.w[g].n + 2 * BW - 1) / (2 * BW)) * ((a.m + bt - 1) / bt);
-        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * (bt + 256);
+        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * (bt + 96);
         if (best == 0 || cost < best_cost) best = bt, best_cost = cost;
     }
     return best;

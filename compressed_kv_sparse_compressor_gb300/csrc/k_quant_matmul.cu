@@ -46,7 +46,9 @@ constexpr int MAX_SPLIT = 8;
 template <int BT>
 struct Shape {
     static constexpr int W_BYTES = BW * BK, T_BYTES = BT * BK, STAGE_BYTES = W_BYTES + T_BYTES;
-    static constexpr int STAGES = 4;
+    // BT <= 64: two CTAs to an SM, so that one's loads cover the other's start and end
+    static constexpr int PER_SM = BT <= 64 ? 2 : 1;
+    static constexpr int STAGES = BT <= 32 ? 5 : BT <= 64 ? 4 : 6;
     static constexpr int SFT = (BT + 127) / 128;               // 128-row units of the rows' scales
     static constexpr int SF_SLOT_BYTES = SF_BYTES * (1 + SFT);
     static constexpr int SF_COLS = 4 * (1 + SFT);
@@ -59,6 +61,7 @@ struct Shape {
     static constexpr uint32_t IDESC = ((uint32_t)(BT >> 3) << 17) | (1u << 23) | ((uint32_t)(BW >> 7) << 27);
     static_assert(BT % 16 == 0 && BT <= 256, "MMA N");
     static_assert(BT * BW * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the stages");
+    static_assert(PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "CTAs to an SM");
 };
 
 struct Params {
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
     uint64_t *acc_full = sf_empty + SF_SLOTS, *drain = acc_full + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     const int rank = (int)blockIdx.x % split, tile = (int)blockIdx.x / split;
     int g = 0;
@@ -339,60 +342,76 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
     pdl_wait();
     pdl_launch_dependents();
 
+    // warps 0 and 1 run converged and one elected lane issues, so that what the copies and MMAs take lies
+    // in uniform registers
     if (warp == 0) {
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t it = 0;
-            for (int kb = kb0; kb < kb1; kb++, it++) {
-                const int s = it % S::STAGES;
-                if (!mbar_wait(smem_u32(&empty[s]), ((it / S::STAGES) & 1) ^ 1, abort)) { ok = false; break; }
-                const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * S::STAGE_BYTES);
+        bool ok = true;
+        uint32_t it = 0, s = 0, par = 1;
+        const uint32_t base = smem_u32(smem);
+        const CUtensorMap *mw = &maps.w[g];
+        for (int kb = kb0; kb < kb1; kb++, it++) {
+            if (!mbar_wait(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
+            const uint32_t bar = smem_u32(&full[s]), dst = base + s * S::STAGE_BYTES;
+            if (elect()) {
                 mbar_expect_tx(bar, S::STAGE_BYTES);
-                tma_load_2d(dst, &maps.w[g], kb * BK, n0, bar);
+                tma_load_2d(dst, mw, kb * BK, n0, bar);
                 tma_load_2d(dst + S::W_BYTES, &maps.a, kb * BK, m0, bar);
             }
-            // after a give-up: the loads still in flight (the last STAGES issued) land before the CTA exits
-            if (!ok)
-                for (uint32_t u = it > (uint32_t)S::STAGES ? it - S::STAGES : 0; u < it; u++)
-                    mbar_drain(smem_u32(&full[u % S::STAGES]), (u / S::STAGES) & 1);
+            __syncwarp();
+            if (++s == S::STAGES) s = 0, par ^= 1;
         }
+        // after a give-up: the loads still in flight (the last STAGES issued) land before the CTA exits
+        if (!ok)
+            for (uint32_t u = it > (uint32_t)S::STAGES ? it - S::STAGES : 0; u < it; u++)
+                mbar_drain(smem_u32(&full[u % S::STAGES]), (u / S::STAGES) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t it = 0, sl = 0;
-            const uint32_t sf_tmem = tmem + BT;
-            for (int kb = kb0; kb < kb1; kb++, it++) {
-                const int slot = sl % SF_SLOTS;
-                const uint32_t sfa = sf_tmem + slot * S::SF_COLS, sfb = sfa + 4;
-                if (kb == kb0 || kb % 4 == 0) {
-                    if (!mbar_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
-                    fence_after();
-                    const uint32_t src = smem_u32(sf + slot * S::SF_SLOT_BYTES);
-#pragma unroll
-                    for (int i = 0; i < 1 + S::SFT; i++) copy_scales(sfa + 4 * i, scale_desc(src + i * SF_BYTES));
-                }
-                const int s = it % S::STAGES;
-                if (!mbar_wait(smem_u32(&full[s]), (it / S::STAGES) & 1, abort)) { ok = false; break; }
+        bool ok = true;
+        uint32_t s = 0, s_par = 0, sl = 0, accumulate = 0;
+        const uint32_t sf_tmem = tmem + BT;
+        const uint64_t w_desc = sw128_desc(smem_u32(smem)), sf_desc = scale_desc(smem_u32(sf));
+        for (int kb = kb0; kb < kb1; kb++) {
+            const uint32_t slot = sl % SF_SLOTS;
+            const uint32_t sfa = sf_tmem + slot * S::SF_COLS, sfb = sfa + 4;
+            if (kb == kb0 || kb % 4 == 0) {
+                if (!mbar_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
                 fence_after();
-                const uint32_t sw = smem_u32(smem + s * S::STAGE_BYTES), st = sw + S::W_BYTES;
-                const uint32_t id = (uint32_t)kb % 4, idesc = S::IDESC | id << 4 | id << 29;
-                const int n_mma = kb == p.kb - 1 ? p.k_tail : BK / 32;
-                for (int k = 0; k < n_mma; k++)
-                    mma_scaled(tmem, sw128_desc(sw + k * 32), sw128_desc(st + k * 32), idesc, sfa, sfb,
-                               (kb > kb0 || k > 0) ? 1u : 0u);
-                mma_commit(smem_u32(&empty[s]));
-                if (kb % 4 == 3) {
-                    mma_commit(smem_u32(&sf_empty[slot]));
-                    sl++;
+                const uint64_t src = sf_desc + (uint64_t)(slot * (S::SF_SLOT_BYTES >> 4));
+                if (elect()) {
+#pragma unroll
+                    for (int i = 0; i < 1 + S::SFT; i++) copy_scales(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
                 }
             }
-            if (ok) mma_commit(smem_u32(acc_full));
-            // drain: every MMA issued so far completes (bounded wait, given up or not) before the
-            // TMEM is freed
-            mma_commit(smem_u32(drain));
-            mbar_drain(smem_u32(drain), 0);
+            if (!mbar_wait(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
+            fence_after();
+            const uint64_t wd = w_desc + (uint64_t)(s * (S::STAGE_BYTES >> 4)), td = wd + (S::W_BYTES >> 4);
+            const uint32_t id = (uint32_t)kb % 4, idesc = S::IDESC | id << 4 | id << 29;
+            const bool group_end = kb % 4 == 3;
+            if (elect()) {
+                if (kb < p.kb - 1 || p.k_tail == BK / 32) {
+#pragma unroll
+                    for (int k = 0; k < BK / 32; k++)
+                        mma_scaled(tmem, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                } else {
+                    for (int k = 0; k < p.k_tail; k++)
+                        mma_scaled(tmem, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                }
+                mma_commit(smem_u32(&empty[s]));
+                if (group_end) mma_commit(smem_u32(&sf_empty[slot]));
+            }
+            __syncwarp();
+            accumulate = 1;
+            sl += group_end ? 1 : 0;
+            if (++s == S::STAGES) s = 0, s_par ^= 1;
         }
+        // the drain: every MMA issued so far completes (bounded wait, given up or not) before the
+        // TMEM is freed
+        if (elect()) {
+            if (ok) mma_commit(smem_u32(acc_full));
+            mma_commit(smem_u32(drain));
+        }
+        __syncwarp();
+        mbar_drain(smem_u32(drain), 0);
         __syncwarp();
     } else if (warp == 2) {
         // scales of groups of 4 stages (absolute positions, so a group is one word per row)
@@ -821,6 +840,24 @@ cudaError_t fill_params(const QuantMatmulArgs &a, int wrows, int bt, int box_t, 
     return e;
 }
 
+// Output tiles of wrows x rows over all weight matrices.
+int64_t count_tiles(const QuantMatmulArgs &a, int wrows, int rows) {
+    int64_t tiles = 0;
+    for (int g = 0; g < a.n_w; g++) tiles += (int64_t)((a.w[g].n + wrows - 1) / wrows) * ((a.m + rows - 1) / rows);
+    return tiles;
+}
+
+// CTAs that share a tile: as many, up to 8, as leave each two blocks of K and all clusters running at
+// once.  Clusters of 2, 4 and 8 CTAs of one SM each that this GPU's 152 SMs hold: 76, 36 and 15 (a
+// cluster stays within a group of about 19 SMs); 16 x 8 CTAs took 14.3 us where 16 x 4 take 8.6.
+int choose_split(int64_t tiles, int kb, int per_sm) {
+    const int room[4] = {152, 76, 36, 15};
+    int split = 1;
+    for (int i = 1; i < 4; i++)
+        if (tiles <= (int64_t)room[i] * per_sm && kb >= 2 << i) split = 1 << i;
+    return split;
+}
+
 template <int BT>
 cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
     using S = Shape<BT>;
@@ -829,24 +866,28 @@ cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
     cudaError_t e = fill_params(a, BW, BT, BT, p, maps);
     if (e != cudaSuccess) return e;
     if ((e = ensure_dyn_smem(qmm_split_kernel<BT>, S::SMEM_BYTES)) != cudaSuccess) return e;
-    const int tiles = p.tile_start[a.n_w];
-    int split = 1;
-    while (split < MAX_SPLIT && tiles * split * 2 <= 2 * 152 && p.kb >= split * 4) split *= 2;
+    const int tiles = p.tile_start[a.n_w], split = choose_split(tiles, p.kb, S::PER_SM);
     return launch_pdl_cluster(qmm_split_kernel<BT>, dim3((unsigned)(tiles * split)), dim3(THREADS), S::SMEM_BYTES, s, split,
                               maps, p, split);
 }
 
+// Time of the product on split<128>, in 10 ns: 5 us and 0.45 us a block of K.
+int64_t split_cost(const QuantMatmulArgs &a) {
+    const int64_t tiles = count_tiles(a, BW, 128);
+    const int kb = (a.k + BK - 1) / BK, split = choose_split(tiles, kb, 1);
+    return 500 + 45 * ((tiles * split + 151) / 152) * ((kb + split - 1) / split);
+}
+
 constexpr int PAIRS = 76;
 
-// Rows of a pair tile: the width with the fewest rounds over the pairs times its MMA time.
-int pair_bt(const QuantMatmulArgs &a) {
+// Rows of a pair tile: the width with the fewest rounds over the pairs times a block's time; cost: of the
+// product, in 10 ns: 7 us and (8 + 0.085 bt) a block.
+int pair_bt(const QuantMatmulArgs &a, int64_t &cost) {
     int best = 0;
-    int64_t best_cost = 0;
+    const int kb = (a.k + BK - 1) / BK;
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
-        int64_t tiles = 0;
-        for (int g = 0; g < a.n_w; g++) tiles += (int64_t)((a.w[g].n + 2 * BW - 1) / (2 * BW)) * ((a.m + bt - 1) / bt);
-        const int64_t cost = (tiles + PAIRS - 1) / PAIRS * (bt + 96);
-        if (best == 0 || cost < best_cost) best = bt, best_cost = cost;
+        const int64_t c = 700 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (8000 + 85 * bt) / 1000;
+        if (best == 0 || c < cost) best = bt, cost = c;
     }
     return best;
 }
@@ -868,8 +909,12 @@ cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s) {
     if (a.m <= 16) return launch_split<16>(a, s);
     if (a.m <= 32) return launch_split<32>(a, s);
     if (a.m <= 64) return launch_split<64>(a, s);
-    if (a.m <= 512) return launch_split<128>(a, s);
-    return launch_pair(a, pair_bt(a), s);
+    // more rows: one CTA's tiles, K split to fill the GPU, or pairs' tiles, which reuse more; by the two
+    // costs, fitted to 64 products of 65 to 8192 rows with 512 to 8192 columns (256 rows: 4096 x 4096 11.8 us
+    // split and 13.3 in pairs, 8192 x 8192 29 and 23, 1024 x 4096 8.6 and 12.4)
+    int64_t cost;
+    const int bt = pair_bt(a, cost);
+    return a.m <= 128 || split_cost(a) <= cost ? launch_split<128>(a, s) : launch_pair(a, bt, s);
 }
 
 cudaError_t qmm_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_qmm_wait_ns, &ns, sizeof ns); }

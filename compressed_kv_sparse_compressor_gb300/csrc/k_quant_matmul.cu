@@ -21,6 +21,9 @@
 //     the instruction descriptor picks the stage's byte.
 //   - A cluster of `split` CTAs shares an output tile, each with a range of K; the
 //     partial tiles meet through distributed shared memory and are added in rank order.
+//   - The tensor core's float accumulation cuts low bits off (the error grows with K: 4e-7 of
+//     the result's norm at K = 4096), so an accumulator takes at most CHUNK blocks of K; two
+//     take turns, and the epilogue adds the chunks in registers.
 //   - Every mbarrier wait is bounded; a wait that gives up raises the library's device
 //     error word and the CTA winds down, freeing its tensor memory.
 #include <cuda.h>
@@ -41,7 +44,7 @@ constexpr int THREADS = 256;
 constexpr int SF_SLOTS = 5;                    // groups of 4 stages whose scales shared memory and TMEM hold
 constexpr int SF_AHEAD = 3;                    // groups whose copies are in flight (below SF_SLOTS)
 constexpr int SF_BYTES = 512;                  // scales of 128 rows, 4 stages
-constexpr int MAX_SPLIT = 8;
+constexpr int CHUNK = 32;                      // blocks of K that one accumulator takes
 
 template <int BT>
 struct Shape {
@@ -52,15 +55,16 @@ struct Shape {
     static constexpr int SFT = (BT + 127) / 128;               // 128-row units of the rows' scales
     static constexpr int SF_SLOT_BYTES = SF_BYTES * (1 + SFT);
     static constexpr int SF_COLS = 4 * (1 + SFT);
-    static constexpr int COLS = BT + SF_SLOTS * SF_COLS;
+    static constexpr int COLS = 2 * BT + SF_SLOTS * SF_COLS;
     static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static constexpr int N_BARS = 2 * STAGES + 2 * SF_SLOTS + 2;
+    static constexpr int N_BARS = 2 * STAGES + 2 * SF_SLOTS + 5;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
     // instruction descriptor: A = B = E4M3, both K-major, E8M0 scales, M = 128, N = BT; the
     // scale byte's index goes to bits 4 (B) and 29 (A)
     static constexpr uint32_t IDESC = ((uint32_t)(BT >> 3) << 17) | (1u << 23) | ((uint32_t)(BW >> 7) << 27);
     static_assert(BT % 16 == 0 && BT <= 256, "MMA N");
     static_assert(BT * BW * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the stages");
+    static_assert(PER_SM * TMEM_COLS <= 512, "TMEM of the CTAs of an SM");
     static_assert(PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "CTAs to an SM");
 };
 
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
     uint8_t *sf = smem + S::STAGES * S::STAGE_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(sf + SF_SLOTS * S::SF_SLOT_BYTES);
     uint64_t *empty = full + S::STAGES, *sf_full = empty + S::STAGES, *sf_empty = sf_full + SF_SLOTS;
-    uint64_t *acc_full = sf_empty + SF_SLOTS, *drain = acc_full + 1;
+    uint64_t *acc_full = sf_empty + SF_SLOTS, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -324,7 +328,10 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
             mbar_init(smem_u32(&sf_full[s]), 32);
             mbar_init(smem_u32(&sf_empty[s]), 1);
         }
-        mbar_init(smem_u32(acc_full), 1);
+        for (int a = 0; a < 2; a++) {
+            mbar_init(smem_u32(&acc_full[a]), 1);
+            mbar_init(smem_u32(&acc_empty[a]), 4);
+        }
         mbar_init(smem_u32(drain), 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -366,15 +373,19 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
                 mbar_drain(smem_u32(&full[u % S::STAGES]), (u / S::STAGES) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        bool ok = true;
         uint32_t s = 0, s_par = 0, sl = 0, accumulate = 0;
-        const uint32_t sf_tmem = tmem + BT;
+        const uint32_t sf_tmem = tmem + 2 * BT;
         const uint64_t w_desc = sw128_desc(smem_u32(smem)), sf_desc = scale_desc(smem_u32(sf));
         for (int kb = kb0; kb < kb1; kb++) {
-            const uint32_t slot = sl % SF_SLOTS;
+            const uint32_t slot = sl % SF_SLOTS, c = (uint32_t)(kb - kb0) / CHUNK, acc = c & 1, d = tmem + acc * BT;
             const uint32_t sfa = sf_tmem + slot * S::SF_COLS, sfb = sfa + 4;
+            if ((kb - kb0) % CHUNK == 0) {
+                if (!mbar_wait(smem_u32(&acc_empty[acc]), ((c >> 1) & 1) ^ 1, abort)) break;
+                fence_after();
+                accumulate = 0;
+            }
             if (kb == kb0 || kb % 4 == 0) {
-                if (!mbar_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
+                if (!mbar_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) break;
                 fence_after();
                 const uint64_t src = sf_desc + (uint64_t)(slot * (S::SF_SLOT_BYTES >> 4));
                 if (elect()) {
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
                     for (int i = 0; i < 1 + S::SFT; i++) copy_scales(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
                 }
             }
-            if (!mbar_wait(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
+            if (!mbar_wait(smem_u32(&full[s]), s_par, abort)) break;
             fence_after();
             const uint64_t wd = w_desc + (uint64_t)(s * (S::STAGE_BYTES >> 4)), td = wd + (S::W_BYTES >> 4);
             const uint32_t id = (uint32_t)kb % 4, idesc = S::IDESC | id << 4 | id << 29;
@@ -391,13 +402,14 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
                 if (kb < p.kb - 1 || p.k_tail == BK / 32) {
 #pragma unroll
                     for (int k = 0; k < BK / 32; k++)
-                        mma_scaled(tmem, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                        mma_scaled(d, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
                 } else {
                     for (int k = 0; k < p.k_tail; k++)
-                        mma_scaled(tmem, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                        mma_scaled(d, wd + 2 * k, td + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
                 }
                 mma_commit(smem_u32(&empty[s]));
                 if (group_end) mma_commit(smem_u32(&sf_empty[slot]));
+                if ((kb - kb0) % CHUNK == CHUNK - 1 || kb == kb1 - 1) mma_commit(smem_u32(&acc_full[acc]));
             }
             __syncwarp();
             accumulate = 1;
@@ -406,10 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         }
         // the drain: every MMA issued so far completes (bounded wait, given up or not) before the
         // TMEM is freed
-        if (elect()) {
-            if (ok) mma_commit(smem_u32(acc_full));
-            mma_commit(smem_u32(drain));
-        }
+        if (elect()) mma_commit(smem_u32(drain));
         __syncwarp();
         mbar_drain(smem_u32(drain), 0);
         __syncwarp();
@@ -439,26 +448,46 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         // epilogue: TMEM lane quarter warp % 4, lane = weight row, column = row of the product
         const int quarter = warp & 3, n = n0 + quarter * 32 + lane;
         const int rows = min(BT, p.m - m0);
-        const bool ok = mbar_wait(smem_u32(acc_full), 0, abort);
-        __syncwarp();
-        if (ok) {
+        float v[BT / 16][16];
+        bool ok = true;
+        const int chunks = (kb1 - kb0 + CHUNK - 1) / CHUNK;
+        for (int c = 0; c < chunks; c++) {
+            const uint32_t acc = c & 1, src = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BT;
+            ok = mbar_wait(smem_u32(&acc_full[acc]), (c >> 1) & 1, abort);
+            __syncwarp();
+            if (!ok) break;
             fence_after();
-            float *part = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
-#pragma unroll 1
-            for (int c = 0; c < BT; c += 16) {
-                if (c >= rows) break;
-                float v[16];
-                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
-                if (split > 1) {
 #pragma unroll
-                    for (int j = 0; j < 16; j++) part[(c + j) * BW] = v[j];
-                } else if (n < p.n[g]) {
+            for (int i = 0; i < BT / 16; i++)
+                if (16 * i < rows) {
+                    if (c == 0) {
+                        tmem_ld16(src + 16 * i, v[i]);
+                    } else {
+                        float u[16];
+                        tmem_ld16(src + 16 * i, u);
 #pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        if (c + j < rows) store_out(p.out[g], (int64_t)(m0 + c + j) * p.out_ld[g] + n, v[j], p.bf16_out);
+                        for (int j = 0; j < 16; j++) v[i][j] += u[j];
+                    }
                 }
-            }
             fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc]));
+        }
+        if (ok) {
+            float *part = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < BT / 16; i++)
+                if (16 * i < rows) {
+                    if (split > 1) {
+#pragma unroll
+                        for (int j = 0; j < 16; j++) part[(16 * i + j) * BW] = v[i][j];
+                    } else if (n < p.n[g]) {
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            if (16 * i + j < rows)
+                                store_out(p.out[g], (int64_t)(m0 + 16 * i + j) * p.out_ld[g] + n, v[i][j], p.bf16_out);
+                    }
+                }
         }
     }
     if (split > 1) {
@@ -497,15 +526,12 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 // (128 + bt) * 128.  bt (a multiple of 32, at most 224) is chosen by the host so that the
 // tiles fill whole rounds over the pairs; two accumulators of bt columns and five slots of
 // scales fit the 512 TMEM columns, so a tile's epilogue runs beside the next tile's MMAs.
-// The tensor core's float accumulation cuts low bits off (its error grows with K: 4e-7 of
-// the result's norm at K = 4096), so an accumulator takes at most CHUNK blocks of K; the
-// epilogue adds the chunks of a tile in registers.
 //
 // Warps: 0 loads (in both CTAs, completing on the leader's barriers), 1 MMAs (leader only),
 // 2 scales (both CTAs: the words of all bt rows and of the CTA's own weight rows), 4-11
 // epilogue (TMEM lane quarter w % 4, half of the columns each).
 // ---------------------------------------------------------------------------------------
-constexpr int PAIR_THREADS = 384, MAX_BT = 224, CHUNK = 32;
+constexpr int PAIR_THREADS = 384, MAX_BT = 224;
 constexpr int PAIR_STAGES = 4, PAIR_RING = 216 * 1024;       // most stages, bytes of the ring
 struct Pair {
     static constexpr int W_BYTES = BW * BK;

@@ -163,7 +163,8 @@ SHAPES = [
     (17, [127], 1000), (31, [64, 3], 257), (32, [1024, 1024, 256, 256], 4096), (33, [500, 1], 1541), (64, [640], 2048),
     (65, [384, 128, 5], 1153), (127, [129], 520), (128, [256], 1024), (129, [1000], 1541), (200, [1024, 256], 520),
     (255, [300], 4096), (256, [128], 128), (257, [257], 2049), (437, [1000], 1541), (1000, [77, 130, 512, 1], 900),
-    (2048, [1024, 1024, 256, 256], 4096), (5000, [520], 392),
+    (2048, [1024, 1024, 256, 256], 4096), (5000, [520], 392), (5, [300], 20000), (100, [200, 40], 33000), (600, [2600], 9000),
+    (64, [20000], 640), (129, [10000], 300), (3000, [4096], 130),
 ]
 
 
@@ -187,7 +188,8 @@ def test_product_of_whole_numbers_is_exact(m, ns, k, dtype):
 
 
 @pytest.mark.parametrize("m,ns,k", [(1, [1024, 256], 4096), (3, [200], 8192), (33, [1024], 1541), (200, [640], 4096),
-                                    (700, [1000], 8192), (2100, [384], 7168)])
+                                    (700, [1000], 8192), (2100, [384], 7168), (2, [256], 32768),
+                                    (900, [2048], 12000)])
 def test_product_error_is_that_of_float_sums(m, ns, k):
     """K products, each exact, added in float in an unknown order: every addition is off by at most 2^-23
     of a partial sum (2^-24 rounded to nearest), and a partial sum by at most the sum of magnitudes."""

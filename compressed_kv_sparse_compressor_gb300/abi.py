@@ -202,16 +202,16 @@ def ds4c_quant_scale_bytes(k):
 
 
 def ds4c_rmsnorm_quant(args, stream):
-    return lib().ds4c_rmsnorm_quant(C.byref(args), stream)
+    return (_lib or lib()).ds4c_rmsnorm_quant(args, stream)
 
 
 def ds4c_quant_weight(n, k, dtype, w, w_ld, q, scale, stream):
-    return lib().ds4c_quant_weight(n, k, dtype, w, w_ld, q, scale, stream)
+    return (_lib or lib()).ds4c_quant_weight(n, k, dtype, w, w_ld, q, scale, stream)
 
 
 def ds4c_quant_matmul(m, k, a, a_scale, matrices, n_w, out_dtype, stream):
     """matrices: a ctypes array of QuantMatrix, of which the first n_w are used."""
-    return lib().ds4c_quant_matmul(m, k, a, a_scale, matrices, n_w, out_dtype, stream)
+    return (_lib or lib()).ds4c_quant_matmul(m, k, a, a_scale, matrices, n_w, out_dtype, stream)
 
 
 def ds4c_compress_prefill_quant(cfg, attn_w, idx_w, state, hidden, hidden_scale, n_tok, pos0, ws, ws_bytes, stream):

@@ -8,7 +8,7 @@ pitch] for weights.  ``empty`` allocates such a pair.
 
 Calls run on the current stream of the tensors' device.  A decode step's kernels take a few
 microseconds, so the checks read each tensor's attributes once and go to the stream's and the
-device's raw handles (a call of ``rmsnorm`` took 14.9 us of host time on torch's stream objects)."""
+device's raw handles (``rmsnorm`` took 14.9 us of host time on torch's stream objects)."""
 
 from __future__ import annotations
 
@@ -18,6 +18,8 @@ from . import abi
 
 _DTYPES = {torch.float32: abi.DS4C_F32, torch.bfloat16: abi.DS4C_BF16}
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
+_E8M0 = torch.uint8
+_device, _stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def row_bytes(k: int) -> int:
@@ -37,14 +39,18 @@ def empty(n: int, k: int, device="cuda", rows_per_scale: int = 1):
 
 
 def _matrix(t, what):
-    """(n, k, ABI dtype, device index) of a float matrix on a GPU."""
+    """(n, k, ABI dtype, device index, row pitch) of a float matrix with contiguous rows on a GPU."""
     shape = t.shape
     dt = _DTYPES.get(t.dtype)
     dev = t.get_device()
     if len(shape) != 2 or dt is None or dev < 0:
         raise ValueError(f"{what}: {t.dtype} {tuple(shape)} on {t.device}, expected a float32 or bfloat16 matrix on a "
                          "CUDA device")
-    return shape[0], shape[1], dt, dev
+    n, k = shape
+    row, col = t.stride()
+    if col != 1 and k > 1:
+        raise ValueError(f"{what}: the rows' elements must be contiguous")
+    return n, k, dt, dev, row if n > 1 else max(k, row)
 
 
 def _pitch(t, n, k, dtype, dev, what):
@@ -68,7 +74,7 @@ def check_rows(q, scale, k: int, rows_per_scale: int = 1):
     if (row != (k + 15) // 16 * 16 and n > 1) or (col != 1 and k > 1):
         raise ValueError(f"quantised rows: stride {(row, col)}, expected {(row_bytes(k), 1)}")
     want = (n if rows_per_scale == 1 else (n + rows_per_scale - 1) // rows_per_scale, ((k + 127) // 128 + 3) // 4 * 4)
-    if scale.shape != want or scale.dtype != torch.uint8 or scale.get_device() != dev or not scale.is_contiguous():
+    if scale.shape != want or scale.dtype != _E8M0 or scale.get_device() != dev or not scale.is_contiguous():
         raise ValueError(f"scales: {scale.dtype} {tuple(scale.shape)} on {scale.device}, expected contiguous uint8 {want} on "
                          f"cuda:{dev}")
     return n, dev
@@ -76,12 +82,12 @@ def check_rows(q, scale, k: int, rows_per_scale: int = 1):
 
 def _run(dev, fn, *args):
     """fn(*args, stream) with device `dev` current, on its current stream; raises the ABI's errors."""
-    if dev == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _device():
+        status = fn(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if status != abi.DS4C_OK:
+            status = fn(*args, _stream(dev))
+    if status:
         raise abi.Ds4cError(status, fn.__name__)
 
 
@@ -91,11 +97,11 @@ def rmsnorm(x, gain=None, *, residual=None, residual_out=None, eps: float = 1e-6
     With a residual the norm is of h = x + residual rounded to x's type; h goes to residual_out, which
     may be x or residual itself.  gain: [d] float32 or None (ones).  q, scale: outputs as ``empty``
     gives them, allocated if None.  y: optional output of x's type, the norm before its quantisation."""
-    n, d, dt, dev = _matrix(x, "x")
-    if q is None and scale is None:
-        q, scale = empty(n, d, x.device)
+    n, d, dt, dev, x_ld = _matrix(x, "x")
     if q is None or scale is None:
-        raise ValueError("q and scale: both or neither")
+        if q is not scale:
+            raise ValueError("q and scale: both or neither")
+        q, scale = empty(n, d, x.device)
     if check_rows(q, scale, d) != (n, dev):
         raise ValueError(f"q: {q.shape[0]} rows on {q.device}, expected {n} on cuda:{dev}")
     xt = x.dtype
@@ -112,9 +118,8 @@ def rmsnorm(x, gain=None, *, residual=None, residual_out=None, eps: float = 1e-6
             raise ValueError(f"gain: {gain.dtype} {tuple(gain.shape)} on {gain.device}, expected contiguous float32 {(d,)} on "
                              f"cuda:{dev}")
         g = gain.data_ptr()
-    a = abi.RmsnormArgs(n, d, dt, eps, x.data_ptr(), r, h, yp, _pitch(x, n, d, xt, dev, "x"), r_ld, h_ld, y_ld, g,
-                        q.data_ptr(), scale.data_ptr())
-    _run(dev, abi.ds4c_rmsnorm_quant, a)
+    _run(dev, abi.ds4c_rmsnorm_quant, abi.RmsnormArgs(n, d, dt, eps, x.data_ptr(), r, h, yp, x_ld, r_ld, h_ld, y_ld, g,
+                                                      q.data_ptr(), scale.data_ptr()))
     return q, scale
 
 
@@ -132,16 +137,15 @@ class Fp8Weight:
 
 def quantize_weight(w, q=None, scale=None) -> Fp8Weight:
     """w [n, k] (float32 or bfloat16; rows may be strided) quantised in blocks of 128 x 128."""
-    n, k, dt, dev = _matrix(w, "w")
-    if q is None and scale is None:
-        q, scale = empty(n, k, w.device, 128)
+    n, k, dt, dev, ld = _matrix(w, "w")
     if q is None or scale is None:
-        raise ValueError("q and scale: both or neither")
+        if q is not scale:
+            raise ValueError("q and scale: both or neither")
+        q, scale = empty(n, k, w.device, 128)
     out = Fp8Weight(q, scale)
     if q.shape != (n, k) or out.device_index != dev:
         raise ValueError(f"q: {tuple(q.shape)} on {q.device}, expected {(n, k)} on cuda:{dev}")
-    _run(dev, abi.ds4c_quant_weight, n, k, dt, w.data_ptr(), _pitch(w, n, k, w.dtype, dev, "w"), q.data_ptr(),
-         scale.data_ptr())
+    _run(dev, abi.ds4c_quant_weight, n, k, dt, w.data_ptr(), ld, q.data_ptr(), scale.data_ptr())
     return out
 
 
@@ -181,7 +185,12 @@ class Linear:
             raise ValueError(f"out: {odt} (float32 or bfloat16)")
         mats = self._mats_t.from_buffer_copy(self._mats)        # of this call: another thread may be in its own
         for mat, o, n in zip(mats, out, self._n):
-            mat.out_ld = _pitch(o, m, n, odt, dev, "out")
+            if o.shape != (m, n) or o.dtype != odt or o.get_device() != dev:
+                raise ValueError(f"out: {o.dtype} {tuple(o.shape)} on {o.device}, expected {odt} {(m, n)} on cuda:{dev}")
+            row, col = o.stride()
+            if col != 1 and n > 1:
+                raise ValueError("out: the rows' elements must be contiguous")
+            mat.out_ld = row if m > 1 else max(n, row)
             mat.out = o.data_ptr()
         _run(dev, abi.ds4c_quant_matmul, m, self.k, q.data_ptr(), scale.data_ptr(), mats, len(out), dt)
         return out

@@ -515,11 +515,14 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         const int total = min(BT, p.m - m0) * (BW / 4);
         const uint32_t base = smem_u32(smem);
         for (int e = rank * THREADS + threadIdx.x; e < total; e += split * THREADS) {
-            float4 v = cluster_ld(base + e * 16, 0);
-            for (int r = 1; r < split; r++) {
-                const float4 u = cluster_ld(base + e * 16, r);
-                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-            }
+            float4 u[8];                                 // every rank's load in flight before the first addition
+#pragma unroll
+            for (int r = 0; r < 8; r++)
+                if (r < split) u[r] = cluster_ld(base + e * 16, r);
+            float4 v = u[0];
+#pragma unroll
+            for (int r = 1; r < 8; r++)
+                if (r < split) v.x += u[r].x, v.y += u[r].y, v.z += u[r].z, v.w += u[r].w;
             const int n = n0 + e % (BW / 4) * 4;
             const int64_t o = (int64_t)(m0 + e / (BW / 4)) * p.out_ld[g] + n;
             const float f[4] = {v.x, v.y, v.z, v.w};
@@ -910,22 +913,23 @@ cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
                               maps, p, split);
 }
 
-// Time of the product on split<128>, in 10 ns: 5 us and 0.45 us a block of K.
+// Time of the product on split<128>, in 10 ns: 4 us, 1.9 us more for meeting in a cluster, and 0.33 us
+// a block of K.
 int64_t split_cost(const QuantMatmulArgs &a) {
     const int64_t tiles = count_tiles(a, BW, 128);
     const int kb = (a.k + BK - 1) / BK, split = choose_split(tiles, kb, 1);
-    return 500 + 45 * ((tiles * split + 151) / 152) * ((kb + split - 1) / split);
+    return 400 + (split > 1 ? 190 : 0) + 33 * ((tiles * split + 151) / 152) * ((kb + split - 1) / split);
 }
 
 constexpr int PAIRS = 76;
 
 // Rows of a pair tile: the width with the fewest rounds over the pairs times a block's time; cost: of the
-// product, in 10 ns: 7 us and (8 + 0.085 bt) a block.
+// product, in 10 ns: 4.8 us and 0.08 + 0.00085 bt us a block.
 int pair_bt(const QuantMatmulArgs &a, int64_t &cost) {
     int best = 0;
     const int kb = (a.k + BK - 1) / BK;
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
-        const int64_t c = 700 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (8000 + 85 * bt) / 1000;
+        const int64_t c = 480 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (8000 + 85 * bt) / 1000;
         if (best == 0 || c < cost) best = bt, cost = c;
     }
     return best;
@@ -949,11 +953,11 @@ cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s) {
     if (a.m <= 32) return launch_split<32>(a, s);
     if (a.m <= 64) return launch_split<64>(a, s);
     // more rows: one CTA's tiles, K split to fill the GPU, or pairs' tiles, which reuse more; by the two
-    // costs, fitted to 64 products of 65 to 8192 rows with 512 to 8192 columns (256 rows: 4096 x 4096 11.8 us
-    // split and 13.3 in pairs, 8192 x 8192 29 and 23, 1024 x 4096 8.6 and 12.4)
+    // costs, fitted to 64 products of 65 to 1024 rows with 256 to 8192 columns (256 rows: 4096 x 4096 12.4 us
+    // split and 11.5 in pairs, 8192 x 8192 25.8 and 21.5, 1024 x 4096 8.8 and 10.6, 256 x 8192 8.8 and 15.2)
     int64_t cost;
     const int bt = pair_bt(a, cost);
-    return a.m <= 128 || split_cost(a) <= cost ? launch_split<128>(a, s) : launch_pair(a, bt, s);
+    return split_cost(a) <= cost ? launch_split<128>(a, s) : launch_pair(a, bt, s);
 }
 
 cudaError_t qmm_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_qmm_wait_ns, &ns, sizeof ns); }

@@ -171,11 +171,21 @@ template <typename T> struct Held;
 template <> struct Held<float> { using type = F32x8; };
 template <> struct Held<__nv_bfloat16> { using type = Bf16x8; };
 
+// 16 bytes that are read once.  Volatile: the compiler must not move a load of what the previous
+// kernel wrote above the wait for it.
+__device__ __forceinline__ uint4 load16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ F2 f2(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
 template <bool VEC>
 __device__ __forceinline__ void load8(const float *p, int base, int d, F32x8 &h) {
     if (VEC) {
-        const float4 a = __ldcs(reinterpret_cast<const float4 *>(p + base));
-        const float4 b = __ldcs(reinterpret_cast<const float4 *>(p + base) + 1);
+        const uint4 a = load16(p + base), b = load16(p + base + 4);
         h.v[0] = f2(a.x, a.y), h.v[1] = f2(a.z, a.w), h.v[2] = f2(b.x, b.y), h.v[3] = f2(b.z, b.w);
     } else {
         float f[8];
@@ -188,7 +198,7 @@ __device__ __forceinline__ void load8(const float *p, int base, int d, F32x8 &h)
 template <bool VEC>
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, int base, int d, Bf16x8 &h) {
     if (VEC) {
-        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p + base));
+        const uint4 a = load16(p + base);
         h.w[0] = a.x, h.w[1] = a.y, h.w[2] = a.z, h.w[3] = a.w;
     } else {
         uint32_t f[8];
@@ -415,8 +425,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
             if (p.gain) {
                 F32x8 g;
                 if (VEC) {
-                    const float4 a = __ldg(reinterpret_cast<const float4 *>(p.gain + base));
-                    const float4 b = __ldg(reinterpret_cast<const float4 *>(p.gain + base) + 1);
+                    const float4 a = reinterpret_cast<const float4 *>(p.gain + base)[0];
+                    const float4 b = reinterpret_cast<const float4 *>(p.gain + base)[1];
                     g.v[0] = f2(a.x, a.y), g.v[1] = f2(a.z, a.w), g.v[2] = f2(b.x, b.y), g.v[3] = f2(b.z, b.w);
                 } else {
                     load8<false>(p.gain, base, d, g);
@@ -449,8 +459,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
 // 128 values in 16 threads, otherwise 4 single ones in each of 32 lanes (two rows per step).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
-quant_weight_kernel(int n, int k, const T *__restrict__ w, int64_t w_ld, uint8_t *__restrict__ q, int64_t q_ld,
-                    uint8_t *__restrict__ scale, int64_t scale_ld) {
+quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t q_ld, uint8_t *scale, int64_t scale_ld) {
     using H = typename Held<T>::type;
     __shared__ float sm[8];
     pdl_wait();

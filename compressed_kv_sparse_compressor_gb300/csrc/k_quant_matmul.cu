@@ -140,6 +140,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         }
     }
 }
+// The same by a converged warp, with one answer for all of it.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait<CLUSTER>(bar, parity, abort));
+}
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
 // flight after a give-up, before the CTA frees its TMEM and exits.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         const uint32_t base = smem_u32(smem);
         const CUtensorMap *mw = &maps.w[g];
         for (int kb = kb0; kb < kb1; kb++, it++) {
-            if (!mbar_wait(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
+            if (!warp_wait(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
             const uint32_t bar = smem_u32(&full[s]), dst = base + s * S::STAGE_BYTES;
             if (elect()) {
                 mbar_expect_tx(bar, S::STAGE_BYTES);
@@ -400,12 +405,12 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
             const uint32_t slot = sl % SF_SLOTS, c = (uint32_t)(kb - kb0) / CHUNK, acc = c & 1, d = tmem + acc * BT;
             const uint32_t sfa = sf_tmem + slot * S::SF_COLS, sfb = sfa + 4;
             if ((kb - kb0) % CHUNK == 0) {
-                if (!mbar_wait(smem_u32(&acc_empty[acc]), ((c >> 1) & 1) ^ 1, abort)) break;
+                if (!warp_wait(smem_u32(&acc_empty[acc]), ((c >> 1) & 1) ^ 1, abort)) break;
                 fence_after();
                 accumulate = 0;
             }
             if (kb == kb0 || kb % 4 == 0) {
-                if (!mbar_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) break;
+                if (!warp_wait(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) break;
                 fence_after();
                 const uint64_t src = sf_desc + (uint64_t)(slot * (S::SF_SLOT_BYTES >> 4));
                 if (elect()) {
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
                     for (int i = 0; i < 1 + S::SFT; i++) copy_scales(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
                 }
             }
-            if (!mbar_wait(smem_u32(&full[s]), s_par, abort)) break;
+            if (!warp_wait(smem_u32(&full[s]), s_par, abort)) break;
             fence_after();
             const uint64_t wd = w_desc + (uint64_t)(s * (S::STAGE_BYTES >> 4)), td = wd + (S::W_BYTES >> 4);
             const uint32_t id = (uint32_t)kb % 4, idesc = S::IDESC | id << 4 | id << 29;
@@ -448,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         uint32_t issued = 0, done = 0;
         for (int q = kb0 / 4; q < (kb1 + 3) / 4; q++, issued++) {
             const int slot = issued % SF_SLOTS;
-            if (!mbar_wait(smem_u32(&sf_empty[slot]), ((issued / SF_SLOTS) & 1) ^ 1, abort)) break;
+            if (!warp_wait(smem_u32(&sf_empty[slot]), ((issued / SF_SLOTS) & 1) ^ 1, abort)) break;
             const uint32_t dst = smem_u32(sf + slot * S::SF_SLOT_BYTES);
             copy_word(dst, ws, q, lane);
 #pragma unroll
@@ -473,8 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         const int chunks = (kb1 - kb0 + CHUNK - 1) / CHUNK;
         for (int c = 0; c < chunks; c++) {
             const uint32_t acc = c & 1, src = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BT;
-            ok = mbar_wait(smem_u32(&acc_full[acc]), (c >> 1) & 1, abort);
-            __syncwarp();
+            ok = warp_wait(smem_u32(&acc_full[acc]), (c >> 1) & 1, abort);
             if (!ok) break;
             fence_after();
 #pragma unroll
@@ -655,7 +659,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             const int wy = nt * 2 * BW + rank * BW, ty = mt * bt + rank * (bt / 2);
             const CUtensorMap *mw = &maps.w[g];
             for (int kb = 0; kb < p.kb; kb += 2, it++) {
-                if (!mbar_wait<true>(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
+                if (!warp_wait<true>(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
                 const uint32_t dst = base + s * 2 * block, bar = full0 + 8 * s;
                 const bool two = kb + 1 < p.kb;
                 if (elect()) {
@@ -695,7 +699,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             for (int tile = pair; tile < total && ok; tile += pairs) {
                 for (int c = 0; c < chunks && ok; c++, local++) {
                     const uint32_t acc = local & 1, d = tmem + acc * (uint32_t)bt;
-                    if (!mbar_wait<true>(smem_u32(&acc_empty[acc]), ((local >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+                    if (!warp_wait<true>(smem_u32(&acc_empty[acc]), ((local >> 1) & 1) ^ 1, abort)) { ok = false; break; }
                     fence_after();
                     const int kb1 = min(p.kb, (c + 1) * CHUNK);
                     uint32_t accumulate = 0;
@@ -703,7 +707,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                         const uint32_t slot = sl % SF_SLOTS;
                         const uint32_t sfa = sf_tmem + slot * Pair::SF_COLS, sfb = sfa + 4;
                         if (kb % 4 == 0) {
-                            if (!mbar_wait<true>(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
+                            if (!warp_wait<true>(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
                             fence_after();
                             const uint64_t src = sf_desc + (uint64_t)(slot * (Pair::SF_SLOT_BYTES >> 4));
                             if (elect()) {
@@ -711,7 +715,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                                 for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
                             }
                         }
-                        if (!mbar_wait<true>(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
+                        if (!warp_wait<true>(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
                         fence_after();
                         const uint64_t wd = w_desc + (uint64_t)(s * (2 * block >> 4)), wd1 = wd + (block >> 4);
                         constexpr uint64_t T = Pair::W_BYTES >> 4;
@@ -764,7 +768,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             const uint8_t *ts = p.a_scale + (size_t)m0 * p.scale_ld;
             for (int sq = 0; sq < (p.kb + 3) / 4; sq++, n++) {
                 const int slot = n % SF_SLOTS;
-                if (!mbar_wait<true>(smem_u32(&sf_empty[slot]), ((n / SF_SLOTS) & 1) ^ 1, abort)) { ok = false; break; }
+                if (!warp_wait<true>(smem_u32(&sf_empty[slot]), ((n / SF_SLOTS) & 1) ^ 1, abort)) { ok = false; break; }
                 const uint32_t dst = smem_u32(sf + slot * Pair::SF_SLOT_BYTES);
                 copy_word(dst, ws, sq, lane);
                 copy_words(dst + SF_BYTES, ts, p.scale_ld, rows, sq, lane);
@@ -790,8 +794,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             float v[Pair::HALF_CHUNKS][16];
             for (int c = 0; c < chunks; c++, local++) {
                 const uint32_t acc = local & 1;
-                ok = mbar_wait<true>(smem_u32(&acc_full[acc]), (local >> 1) & 1, abort);
-                __syncwarp();
+                ok = warp_wait<true>(smem_u32(&acc_full[acc]), (local >> 1) & 1, abort);
                 if (!ok) break;
                 fence_after();
                 const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + acc * (uint32_t)bt + (uint32_t)(half * cols);

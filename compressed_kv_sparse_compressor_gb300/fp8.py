@@ -80,7 +80,7 @@ def check_rows(q, scale, k: int, rows_per_scale: int = 1):
     return n, dev
 
 
-def _run(dev, fn, *args):
+def run(dev, fn, *args):
     """fn(*args, stream) with device `dev` current, on its current stream; raises the ABI's errors."""
     if dev == _device():
         status = fn(*args, _stream(dev))
@@ -118,7 +118,7 @@ def rmsnorm(x, gain=None, *, residual=None, residual_out=None, eps: float = 1e-6
             raise ValueError(f"gain: {gain.dtype} {tuple(gain.shape)} on {gain.device}, expected contiguous float32 {(d,)} on "
                              f"cuda:{dev}")
         g = gain.data_ptr()
-    _run(dev, abi.ds4c_rmsnorm_quant, abi.RmsnormArgs(n, d, dt, eps, x.data_ptr(), r, h, yp, x_ld, r_ld, h_ld, y_ld, g,
+    run(dev, abi.ds4c_rmsnorm_quant, abi.RmsnormArgs(n, d, dt, eps, x.data_ptr(), r, h, yp, x_ld, r_ld, h_ld, y_ld, g,
                                                       q.data_ptr(), scale.data_ptr()))
     return q, scale
 
@@ -145,7 +145,7 @@ def quantize_weight(w, q=None, scale=None) -> Fp8Weight:
     out = Fp8Weight(q, scale)
     if q.shape != (n, k) or out.device_index != dev:
         raise ValueError(f"q: {tuple(q.shape)} on {q.device}, expected {(n, k)} on cuda:{dev}")
-    _run(dev, abi.ds4c_quant_weight, n, k, dt, w.data_ptr(), ld, q.data_ptr(), scale.data_ptr())
+    run(dev, abi.ds4c_quant_weight, n, k, dt, w.data_ptr(), ld, q.data_ptr(), scale.data_ptr())
     return out
 
 
@@ -192,5 +192,5 @@ class Linear:
                 raise ValueError("out: the rows' elements must be contiguous")
             mat.out_ld = row if m > 1 else max(n, row)
             mat.out = o.data_ptr()
-        _run(dev, abi.ds4c_quant_matmul, m, self.k, q.data_ptr(), scale.data_ptr(), mats, len(out), dt)
+        run(dev, abi.ds4c_quant_matmul, m, self.k, q.data_ptr(), scale.data_ptr(), mats, len(out), dt)
         return out

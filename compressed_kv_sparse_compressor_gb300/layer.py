@@ -85,16 +85,24 @@ class DeviceLayer:
     def set_weights_quant(self, attn, idx=None):
         """attn / idx = (wkv, wgate, ape, norm): the projections float tensors, quantised here on the
         device, or fp8.Fp8Weight; ape and norm as set_weights."""
-        def lw(w):
+        s = self.shape
+
+        def lw(w, dl):
+            width = s.coff * dl
             kv, gate = (x if isinstance(x, fp8.Fp8Weight) else fp8.quantize_weight(x.to(self.device)) for x in w[:2])
             ape, norm = (None if x is None else x.to(self.device).contiguous() for x in w[2:])
+            for x, want in ((kv, (width, s.d_model)), (gate, (width, s.d_model)), (ape, (s.ratio, width)), (norm, (dl,))):
+                if x is not None and tuple(x.shape) != want:
+                    raise ValueError(f"lane weight of shape {tuple(x.shape)}, expected {want}")
+            if kv.device_index != self.raw.get_device() or gate.device_index != self.raw.get_device():
+                raise ValueError(f"weights on cuda:{kv.device_index}, the layer on {self.raw.device}")
             self._keep.append((kv, gate, ape, norm))
             return abi.LaneWeightsQuant(_ptr(kv.q), _ptr(kv.scale), _ptr(gate.q), _ptr(gate.scale), _ptr(ape),
                                         _ptr(norm))
-        if self.shape.ratio:
-            self.attn_wq = lw(attn)
-        if self.shape.ratio == 4:
-            self.idx_wq = lw(idx)
+        if s.ratio:
+            self.attn_wq = lw(attn, s.head_dim)
+        if s.ratio == 4:
+            self.idx_wq = lw(idx, s.idx_head_dim)
 
     # -- calls -----------------------------------------------------------------
     def state_init(self):
@@ -120,21 +128,24 @@ class DeviceLayer:
                                                 len(positions), _ptr(self.ws), self.ws_bytes, _stream()),
                   "ds4c_compress_decode_step")
 
+    def _hidden_quant(self, hidden, hidden_scale):
+        n, dev = fp8.check_rows(hidden, hidden_scale, self.shape.d_model)
+        if dev != self.raw.get_device():
+            raise ValueError(f"hidden rows on cuda:{dev}, the layer on {self.raw.device}")
+        return n, dev
+
     def compress_prefill_quant(self, hidden, hidden_scale, pos0: int):
         """hidden, hidden_scale: quantised rows as fp8.rmsnorm returns them."""
-        fp8.check_rows(hidden, hidden_scale, self.shape.d_model)
-        abi.check(abi.ds4c_compress_prefill_quant(self.cfg, self.attn_wq, self.idx_wq, self.state, _ptr(hidden),
-                                                  _ptr(hidden_scale), hidden.shape[0], pos0, _ptr(self.ws),
-                                                  self.ws_bytes, _stream()), "ds4c_compress_prefill_quant")
+        n, dev = self._hidden_quant(hidden, hidden_scale)
+        fp8.run(dev, abi.ds4c_compress_prefill_quant, self.cfg, self.attn_wq, self.idx_wq, self.state, _ptr(hidden),
+                _ptr(hidden_scale), n, pos0, _ptr(self.ws), self.ws_bytes)
 
     def compress_decode_quant(self, hidden, hidden_scale, positions):
-        fp8.check_rows(hidden, hidden_scale, self.shape.d_model)
-        if hidden.shape[0] != len(positions):
-            raise ValueError(f"{hidden.shape[0]} hidden rows for {len(positions)} positions")
-        pos = abi.u64_array(positions)
-        abi.check(abi.ds4c_compress_decode_step_quant(self.cfg, self.attn_wq, self.idx_wq, self.state, _ptr(hidden),
-                                                      _ptr(hidden_scale), pos, len(positions), _ptr(self.ws),
-                                                      self.ws_bytes, _stream()), "ds4c_compress_decode_step_quant")
+        n, dev = self._hidden_quant(hidden, hidden_scale)
+        if n != len(positions):
+            raise ValueError(f"{n} hidden rows for {len(positions)} positions")
+        fp8.run(dev, abi.ds4c_compress_decode_step_quant, self.cfg, self.attn_wq, self.idx_wq, self.state, _ptr(hidden),
+                _ptr(hidden_scale), abi.u64_array(positions), n, _ptr(self.ws), self.ws_bytes)
 
     def indexer_topk(self, q_idx, positions, n_seq, n_tok, topk, scores=None, score_stride=0):
         pos = abi.u64_array(positions)

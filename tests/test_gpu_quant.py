@@ -293,6 +293,33 @@ def test_same_result_every_time_on_two_streams_and_in_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(o, want))
 
 
+def test_back_to_back_calls_read_what_the_one_before_wrote():
+    """Weights requantised, rows renormalised and multiplied, again and again into the same buffers with nothing
+    in between: each product equals the one of its own inputs with a wait after every call."""
+    g = gen(21)
+    m, n, k = 48, 640, 1032
+    xs, ws = [randn(g, m, k).bfloat16() for _ in range(6)], [0.02 * randn(g, n, k) for _ in range(6)]
+    want = []
+    for x, w in zip(xs, ws):
+        wq = fp8.quantize_weight(w)
+        torch.cuda.synchronize()
+        q, s = fp8.rmsnorm(x)
+        torch.cuda.synchronize()
+        want.append(fp8.Linear([wq])(q, s)[0])
+        torch.cuda.synchronize()
+    q, s = fp8.empty(m, k)
+    wq = fp8.Fp8Weight(*fp8.empty(n, k, "cuda", 128))
+    lin = fp8.Linear([wq])
+    outs = []
+    for _ in range(20):
+        for x, w in zip(xs, ws):
+            fp8.quantize_weight(w, wq.q, wq.scale)
+            fp8.rmsnorm(x, q=q, scale=s)
+            outs.append(lin(q, s)[0])
+    for i, o in enumerate(outs):
+        assert torch.equal(o, want[i % 6]), i
+
+
 # ---- the layer ---------------------------------------------------------------------------------
 
 def _layers(ratio, T, n_seq=1, **kw):
@@ -370,6 +397,21 @@ def test_layer_decode_steps():
     _close(plain, quant)
 
 
+def test_layer_refusals():
+    shape, _, quant = _layers(4, 16)
+    wa, wi = (configs.lane_weights(shape, 5, 0, lane, device="cuda") for lane in ("attn", "idx"))
+    q, scale = fp8.empty(4, shape.d_model)
+    for bad in (lambda: quant.set_weights_quant((wa[0][:-1],) + wa[1:], wi), lambda: quant.set_weights_quant(wi, wi),
+                lambda: quant.set_weights_quant(wa[:2] + (wa[2][:3], wa[3]), wi),
+                lambda: quant.set_weights_quant(wa[:3] + (wa[3][:-4],), wi),
+                lambda: quant.compress_prefill_quant(*fp8.empty(4, shape.d_model + 16), 0),
+                lambda: quant.compress_decode_quant(q, scale, [0, 1])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(abi.Ds4cError):
+        quant.compress_prefill_quant(*fp8.empty(68, shape.d_model), 0)      # past the state's capacity
+
+
 # ---- refusals of the torch calls -----------------------------------------------------------------
 
 def test_refusals_of_the_torch_calls():
@@ -388,6 +430,9 @@ def test_refusals_of_the_torch_calls():
         fp8.rmsnorm(x, eps=0.0)
     with pytest.raises(abi.Ds4cError):
         fp8.rmsnorm(x[:1].expand(4, 256))                   # rows that overlap
+    with pytest.raises(abi.Ds4cError):
+        fp8.rmsnorm(torch.zeros(4, 258, device="cuda"), q=torch.zeros(4, 272, dtype=torch.uint8, device="cuda")[:, 1:259],
+                    scale=torch.zeros(4, 4, dtype=torch.uint8, device="cuda"))   # rows off their 16 bytes
     w = fp8.quantize_weight(x)
     lin = fp8.Linear([w])
     for bad in (lambda: lin(q[:, :128], scale), lambda: lin(q, scale, [torch.zeros(4, 5, device="cuda")]),

@@ -140,9 +140,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         }
     }
 }
-// The same by a converged warp, with one answer for all of it.
+// The same by a converged warp, with one answer for all of it: the first look is one instruction on one
+// address, the same for every lane; the lanes of a wait that goes on vote (a vote on every wait took a
+// sixth of an 8192 x 8192 x 8192 product in tiles of 128 rows).
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
     return __all_sync(0xffffffffu, mbar_wait<CLUSTER>(bar, parity, abort));
 }
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
@@ -213,6 +216,13 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
+}
+// Brings a box to L2.  Made before the wait for the previous kernel: L2 holds one copy of memory, so a
+// box that kernel still writes is read as written later.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
+                 "r"(y)
+                 : "memory");
 }
 // Shared-memory matrix descriptors: K-major operand in the 128-byte swizzle TMA writes
 // (8-row atoms of 1024 bytes), and the unswizzled scale words (8-row cores of 128 bytes).
@@ -367,6 +377,11 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         fence_before();
+    }
+    if (BT <= 32 && warp == 0 && elect()) {
+        // the weights of the first stages, while the previous kernel ends, beside which these small CTAs
+        // can start (2560 x 4096 weights: 1 row 5.6 -> 5.3 us, 32 rows 7.2 -> 6.7; larger tiles lost 1 to 9 %)
+        for (int kb = kb0; kb < min(kb1, kb0 + S::STAGES); kb++) tma_prefetch_2d(&maps.w[g], kb * BK, n0);
     }
     __syncthreads();
     fence_after();
@@ -556,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 // epilogue (TMEM lane quarter w % 4, half of the columns each).
 // ---------------------------------------------------------------------------------------
 constexpr int PAIR_THREADS = 384, MAX_BT = 224;
-constexpr int PAIR_STAGES = 4, PAIR_RING = 216 * 1024;       // most stages, bytes of the ring
+constexpr int PAIR_STAGES = 8, PAIR_RING = 216 * 1024;       // most stages, bytes of the ring
 struct Pair {
     static constexpr int W_BYTES = BW * BK;
     static constexpr int SF_SLOT_BYTES = 3 * SF_BYTES, SF_COLS = 12;
@@ -565,7 +580,7 @@ struct Pair {
     static constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(2 * BW >> 7) << 27);       // M = 256, N added
     static constexpr int HALF_CHUNKS = MAX_BT / 2 / 16;
     static_assert(2 * MAX_BT + SF_SLOTS * SF_COLS <= 512, "TMEM columns");
-    static_assert(3 * 2 * (W_BYTES + MAX_BT / 2 * BK) <= PAIR_RING && SMEM_BYTES <= 232448, "three stages at the widest tile");
+    static_assert(7 * (W_BYTES + MAX_BT / 2 * BK) <= PAIR_RING && SMEM_BYTES <= 232448, "seven stages at the widest tile");
 };
 
 // Output tile -> weight matrix, row tile and weight tile: within a matrix, 16 weight tiles go
@@ -598,6 +613,7 @@ __device__ __forceinline__ void signal_scales(uint64_t *loaded, uint32_t full, u
     }
 }
 
+template <bool joint>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     extern __shared__ uint8_t smem_raw[];
@@ -612,9 +628,12 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
-    // a stage is two blocks of K: the handshakes of a stage take some 480 cycles of the MMA warp, the
-    // MMAs of one block 2 bt
-    const uint32_t block = Pair::W_BYTES + (uint32_t)bt / 2 * BK, stages = min((uint32_t)PAIR_STAGES, PAIR_RING / (2 * block));
+    // The MMA warp takes two blocks of K at a time.  A stage is one block for wide tiles (!joint), whose seven keep
+    // more loads in flight than three stages of two would; two blocks for narrow ones (up to 160 rows), whose MMAs (2 bt
+    // cycles a block) are shorter than the handshakes of a stage (8192 x 8192 x 8192: 224 rows 252 us in
+    // stages of one block and 284 of two, 128 rows 347 and 330)
+    const uint32_t block = Pair::W_BYTES + (uint32_t)bt / 2 * BK, stage = joint ? 2 * block : block;
+    const uint32_t stages = min((uint32_t)PAIR_STAGES, PAIR_RING / stage);
     // groups of scales over all of this pair's tiles
     const uint32_t groups = pair < total ? (uint32_t)((total - pair + pairs - 1) / pairs) * ((p.kb + 3) / 4) : 0;
 
@@ -658,10 +677,10 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             pair_coords(p, tile, g, mt, nt);
             const int wy = nt * 2 * BW + rank * BW, ty = mt * bt + rank * (bt / 2);
             const CUtensorMap *mw = &maps.w[g];
-            for (int kb = 0; kb < p.kb; kb += 2, it++) {
+            for (int kb = 0; kb < p.kb; kb += joint ? 2 : 1, it++) {
                 if (!warp_wait<true>(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
-                const uint32_t dst = base + s * 2 * block, bar = full0 + 8 * s;
-                const bool two = kb + 1 < p.kb;
+                const uint32_t dst = base + s * stage, bar = full0 + 8 * s;
+                const bool two = joint && kb + 1 < p.kb;
                 if (elect()) {
                     if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), (two ? 4 : 2) * block);
                     tma_load_2d_pair(dst, mw, kb * BK, wy, bar);
@@ -715,9 +734,14 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                                 for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
                             }
                         }
+                        const bool two = kb + 1 < p.kb;
+                        // the second block's stage
+                        const uint32_t s1 = joint ? s : s + 1 == stages ? 0 : s + 1, par1 = s + 1 == stages ? s_par ^ 1 : s_par;
                         if (!warp_wait<true>(smem_u32(&full[s]), s_par, abort)) { ok = false; break; }
+                        if (!joint && two && !warp_wait<true>(smem_u32(&full[s1]), par1, abort)) { ok = false; break; }
                         fence_after();
-                        const uint64_t wd = w_desc + (uint64_t)(s * (2 * block >> 4)), wd1 = wd + (block >> 4);
+                        const uint64_t wd = w_desc + (uint64_t)(s * (stage >> 4));
+                        const uint64_t wd1 = joint ? wd + (block >> 4) : w_desc + (uint64_t)(s1 * (stage >> 4));
                         constexpr uint64_t T = Pair::W_BYTES >> 4;
                         const uint32_t id = (uint32_t)kb % 4, idesc = idesc0 | id << 4 | id << 29, idesc1 = idesc + (1u << 4 | 1u << 29);
                         const bool group_end = kb % 4 == 2 || kb + 2 >= p.kb;
@@ -726,23 +750,26 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
 #pragma unroll
                                 for (int k = 0; k < BK / 32; k++)
                                     mma_scaled_pair(d, wd + 2 * k, wd + T + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                                if (!joint) mma_commit_pair(smem_u32(&empty[s]));
 #pragma unroll
                                 for (int k = 0; k < BK / 32; k++)
                                     mma_scaled_pair(d, wd1 + 2 * k, wd1 + T + 2 * k, idesc1, sfa, sfb, 1u);
                             } else {                     // the last one or two blocks, the last one shorter
-                                const int n0 = kb + 1 < p.kb ? BK / 32 : p.k_tail, n1 = kb + 1 < p.kb ? p.k_tail : 0;
+                                const int n0 = two ? BK / 32 : p.k_tail, n1 = two ? p.k_tail : 0;
                                 for (int k = 0; k < n0; k++)
                                     mma_scaled_pair(d, wd + 2 * k, wd + T + 2 * k, idesc, sfa, sfb, k > 0 ? 1u : accumulate);
+                                if (!joint) mma_commit_pair(smem_u32(&empty[s]));
                                 for (int k = 0; k < n1; k++)
                                     mma_scaled_pair(d, wd1 + 2 * k, wd1 + T + 2 * k, idesc1, sfa, sfb, 1u);
                             }
-                            mma_commit_pair(smem_u32(&empty[s]));
+                            if (two || joint) mma_commit_pair(smem_u32(&empty[s1]));
                             if (group_end) mma_commit_pair(smem_u32(&sf_empty[slot]));
                         }
                         __syncwarp();
                         accumulate = 1;
                         sl += group_end ? 1 : 0;
-                        if (++s == stages) s = 0, s_par ^= 1;
+                        s += two && !joint ? 2 : 1;
+                        if (s >= stages) s -= stages, s_par ^= 1;
                     }
                     if (ok && elect()) mma_commit_pair(smem_u32(&acc_full[acc]));
                     __syncwarp();
@@ -927,12 +954,12 @@ int64_t split_cost(const QuantMatmulArgs &a) {
 constexpr int PAIRS = 76;
 
 // Rows of a pair tile: the width with the fewest rounds over the pairs times a block's time; cost: of the
-// product, in 10 ns: 4.8 us and 0.08 + 0.00085 bt us a block.
+// product, in 10 ns: 4.8 us and 0.115 + 0.00058 bt us a block.
 int pair_bt(const QuantMatmulArgs &a, int64_t &cost) {
     int best = 0;
     const int kb = (a.k + BK - 1) / BK;
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
-        const int64_t c = 480 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (8000 + 85 * bt) / 1000;
+        const int64_t c = 480 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (11500 + 58 * bt) / 1000;
         if (best == 0 || c < cost) best = bt, cost = c;
     }
     return best;
@@ -943,10 +970,11 @@ cudaError_t launch_pair(const QuantMatmulArgs &a, int bt, cudaStream_t s) {
     Params p;
     cudaError_t e = fill_params(a, 2 * BW, bt, bt / 2, p, maps);
     if (e != cudaSuccess) return e;
-    if ((e = ensure_dyn_smem(qmm_pair_kernel, Pair::SMEM_BYTES)) != cudaSuccess) return e;
+    auto kernel = bt <= 160 ? qmm_pair_kernel<true> : qmm_pair_kernel<false>;
+    if ((e = ensure_dyn_smem(kernel, Pair::SMEM_BYTES)) != cudaSuccess) return e;
     const int tiles = p.tile_start[a.n_w];
-    return launch_pdl(qmm_pair_kernel, dim3((unsigned)(2 * (tiles < PAIRS ? tiles : PAIRS))), dim3(PAIR_THREADS),
-                      Pair::SMEM_BYTES, s, maps, p, bt);
+    return launch_pdl(kernel, dim3((unsigned)(2 * (tiles < PAIRS ? tiles : PAIRS))), dim3(PAIR_THREADS), Pair::SMEM_BYTES, s,
+                      maps, p, bt);
 }
 
 }  // namespace

@@ -13,12 +13,11 @@
 //   - K in stages of 128 bytes (one scale block): the weights' [128][128] and the rows'
 //     [BT][128] bytes by TMA in the 128-byte swizzle, a ring of mbarriers.  Rows and
 //     columns past the ends, and K past the last value, are filled with zeros.
-//   - Scales: one warp copies the four scale bytes of 4 stages per row as a word (cp.async,
-//     up to three groups of 4 stages in flight: read one group at a time, their latency held
-//     an 8192 x 8192 x 8192 product at 372 us where it takes 252) into shared memory as
-//     TMEM wants them ([32 lanes][4 words], row r in lane r % 32, word r / 32); the MMA
-//     thread copies them to TMEM (tcgen05.cp, replicated to the four lane quarters) and
-//     the instruction descriptor picks the stage's byte.
+//   - Scales: one warp copies the four scale bytes of 4 blocks per row as a word (cp.async,
+//     several groups of 4 blocks in flight) into shared memory as TMEM wants them ([32
+//     lanes][4 words], row r in lane r % 32, word r / 32); the MMA thread copies them to
+//     TMEM (tcgen05.cp, replicated to the four lane quarters) and the instruction
+//     descriptor picks the block's byte.
 //   - A cluster of `split` CTAs shares an output tile, each with a range of K; the
 //     partial tiles meet through distributed shared memory and are added in rank order.
 //   - The tensor core's float accumulation cuts low bits off (the error grows with K: 4e-7 of
@@ -26,6 +25,13 @@
 //     take turns, and the epilogue adds the chunks in registers.
 //   - Every mbarrier wait is bounded; a wait that gives up raises the library's device
 //     error word and the CTA winds down, freeing its tensor memory.
+//
+// What bounds it, on inputs that are not in L2: few rows, the weights' bytes and the chain
+// launch - loads - MMAs - meeting (one row through 2560 x 4096 weights 5.2 us for 1.5 us of
+// bytes, through 8192 x 8192 14.4 us, 4.7 TB/s); many rows, the ring of loads (about 3000
+// cycles from a stage's release to its next data) and then the tensor pipe and the power
+// limit (8192 x 8192 x 8192 304 us, 3.6 PFLOP/s; 352 us, 3.1 PFLOP/s, at 1.35 GHz when run
+// for seconds).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -628,10 +634,10 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
-    // The MMA warp takes two blocks of K at a time.  A stage is one block for wide tiles (!joint), whose seven keep
-    // more loads in flight than three stages of two would; two blocks for narrow ones (up to 160 rows), whose MMAs (2 bt
-    // cycles a block) are shorter than the handshakes of a stage (8192 x 8192 x 8192: 224 rows 252 us in
-    // stages of one block and 284 of two, 128 rows 347 and 330)
+    // The MMA warp takes two blocks of K at a time.  A stage is one block for wide tiles (!joint), whose
+    // seven keep more loads in flight than three stages of two would; two blocks for narrow ones (up to 160
+    // rows), whose MMAs (2 bt cycles a block) are shorter than a stage's handshakes (8192 x 8192 x 8192 on
+    // zeros: 224 rows 251 us in stages of one block and 284 of two, 128 rows 347 and 327)
     const uint32_t block = Pair::W_BYTES + (uint32_t)bt / 2 * BK, stage = joint ? 2 * block : block;
     const uint32_t stages = min((uint32_t)PAIR_STAGES, PAIR_RING / stage);
     // groups of scales over all of this pair's tiles

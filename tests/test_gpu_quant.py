@@ -80,6 +80,13 @@ def test_norm_strided_and_in_place():
     assert torch.equal(r, wh) and torch.equal(q.view(torch.uint8), wq) and torch.equal(scale[:, :5], ws)
     rest[:, 600:600 + d] = wh
     assert torch.equal(big, rest)
+    xx, rr = randn(g, 600, 1032), randn(g, 600, 1032)            # over x itself, and a residual added to itself
+    wh, wy = ref.rmsnorm(xx, rr, None, EPS)
+    q, scale = fp8.rmsnorm(xx, residual=rr, residual_out=xx, eps=EPS)
+    assert torch.equal(xx, wh) and torch.equal(q.view(torch.uint8), ref.quantise(wy, 1)[0])
+    wh, wy = ref.rmsnorm(xx, xx, None, EPS)
+    q, scale = fp8.rmsnorm(xx, residual=xx, residual_out=xx, eps=EPS)
+    assert torch.equal(xx, wh) and torch.equal(q.view(torch.uint8), ref.quantise(wy, 1)[0])
     # without the 8-bit output: the plain fused norm
     x = randn(g, n, d)
     y = torch.empty_like(x)
@@ -241,6 +248,20 @@ def test_product_with_extreme_scales_and_nan(m):
     a = fp8.Linear([fp8.Fp8Weight(wq2, wsc2)])
     wide = a(fullq[:m, :k], fulls[:m])[0]
     assert torch.equal(wide, a(q2, s2)[0]) and not wide.isnan().any()
+
+
+@pytest.mark.parametrize("m", [1, 40, 600])
+@pytest.mark.parametrize("a,w", [(0, 254), (254, 0), (1, 253), (127, 127)])
+def test_product_at_the_ends_of_the_scales(m, a, w):
+    """Scales 2^-127 and 2^127 that cancel: whole numbers again."""
+    g = gen(m + a)
+    n, k = 300, 660
+    q, scale = whole(g, m, k, 1)
+    wq, wsc = whole(g, n, k, 128)
+    scale.fill_(a)
+    wsc.fill_(w)
+    want = q.double() @ wq.double().T
+    assert torch.equal(fp8.Linear([fp8.Fp8Weight(wq, wsc)])(q, scale)[0], want.float())
 
 
 def test_no_rows():

@@ -13,11 +13,11 @@
 //   - K in stages of 128 bytes (one scale block): the weights' [128][128] and the rows'
 //     [BT][128] bytes by TMA in the 128-byte swizzle, a ring of mbarriers.  Rows and
 //     columns past the ends, and K past the last value, are filled with zeros.
-//   - Scales: one warp copies the four scale bytes of 4 blocks per row as a word (cp.async,
-//     several groups of 4 blocks in flight) into shared memory as TMEM wants them ([32
-//     lanes][4 words], row r in lane r % 32, word r / 32); the MMA thread copies them to
-//     TMEM (tcgen05.cp, replicated to the four lane quarters) and the instruction
-//     descriptor picks the block's byte.
+//   - Scales: the four scale bytes of 4 blocks of a row are read as a word, several groups of
+//     4 blocks ahead, and lie in TMEM with row r's in lane r % 32 (of each lane quarter) and
+//     column r / 32; the instruction descriptor picks the block's byte.  The split kernel
+//     copies the words to shared memory (cp.async) and from there to TMEM (tcgen05.cp); the
+//     pair kernel writes TMEM from registers, see there.
 //   - A cluster of `split` CTAs shares an output tile, each with a range of K; the
 //     partial tiles meet through distributed shared memory and are added in rank order.
 //   - The tensor core's float accumulation cuts low bits off (the error grows with K: 4e-7 of
@@ -184,9 +184,6 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -213,9 +210,6 @@ __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t
         "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
-}
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
     asm volatile(
@@ -300,10 +294,6 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const uint8_t *src, int 
 #pragma unroll
     for (int j = 0; j < 4; j++)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + lane * 16 + j * 4), "l"(src + 4 * q) : "memory");
-}
-// Arrival on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most `left` groups of this thread's copies are in flight, and shows the others to
@@ -573,19 +563,22 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 // scales fit the 512 TMEM columns, so a tile's epilogue runs beside the next tile's MMAs.
 //
 // Warps: 0 loads (in both CTAs, completing on the leader's barriers), 1 MMAs (leader only),
-// 2 scales (both CTAs: the words of all bt rows and of the CTA's own weight rows), 4-11
-// epilogue (TMEM lane quarter w % 4, half of the columns each).
+// 4-11 epilogue (TMEM lane quarter w % 4, half of the columns each), 12-15 scales (in both
+// CTAs, the words of all bt rows and of the CTA's own weight rows to lane quarter w % 4).
 // ---------------------------------------------------------------------------------------
-constexpr int PAIR_THREADS = 384, MAX_BT = 224;
+constexpr int PAIR_THREADS = 512, MAX_BT = 224;
+// registers per thread of the epilogue's two warpgroups and of the other two (setmaxnreg), out of 128 at launch
+constexpr int REG_EPILOGUE = 168, REG_OTHER = 80;
 constexpr int PAIR_STAGES = 8, PAIR_RING = 216 * 1024;       // most stages, bytes of the ring
 struct Pair {
     static constexpr int W_BYTES = BW * BK;
-    static constexpr int SF_SLOT_BYTES = 3 * SF_BYTES, SF_COLS = 12;
-    static constexpr int N_BARS = 2 * PAIR_STAGES + 3 * SF_SLOTS + 5;
-    static constexpr int SMEM_BYTES = PAIR_RING + SF_SLOTS * SF_SLOT_BYTES + 8 * N_BARS + 16 + 1024;
+    static constexpr int SF_COLS = 12, WORDS = MAX_BT / 32;      // TMEM columns of a slot, row words of a lane
+    static constexpr int N_BARS = 2 * PAIR_STAGES + 2 * SF_SLOTS + 5;
+    static constexpr int SMEM_BYTES = PAIR_RING + 8 * N_BARS + 16 + 1024;
     static constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(2 * BW >> 7) << 27);       // M = 256, N added
     static constexpr int HALF_CHUNKS = MAX_BT / 2 / 16;
     static_assert(2 * MAX_BT + SF_SLOTS * SF_COLS <= 512, "TMEM columns");
+    static_assert(2 * REG_EPILOGUE + 2 * REG_OTHER <= 4 * 128, "registers of the four warpgroups");
     static_assert(7 * (W_BYTES + MAX_BT / 2 * BK) <= PAIR_RING && SMEM_BYTES <= 232448, "seven stages at the widest tile");
 };
 
@@ -601,33 +594,39 @@ __device__ __forceinline__ void pair_coords(const Params &p, int tile, int &g, i
     nt = 16 * band + in % wide;
 }
 
-// One thread: passes on every STEP-th group of scales from `first`, landed in this CTA, to the MMA
-// thread's barrier.  In the leader's CTA (STEP 1) that is an ordinary arrival.  From the other CTA it
-// is a release at cluster scope, which waits for all that its thread has in flight and takes about a
-// microsecond beside the loads (made by the copying threads themselves it held an 8192 x 8192 x 8192
-// product at 415 us, the whole time of a group of stages): two threads without copies of their own
-// take turns.
-template <int STEP>
-__device__ __forceinline__ void signal_scales(uint64_t *loaded, uint32_t full, uint32_t first, uint32_t groups,
-                                              volatile int *abort) {
-    for (uint32_t n = first; n < groups; n += STEP) {
-        const int slot = n % SF_SLOTS;
-        if (!mbar_wait(smem_u32(&loaded[slot]), (n / SF_SLOTS) & 1, abort)) break;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (STEP == 1) mbar_arrive(full + 8 * slot);
-        else mbar_arrive_cluster(full + 8 * slot);
-    }
+__device__ __forceinline__ uint32_t load_word(const uint8_t *p) {
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
+// A warp's scale words of group q (4 blocks of K): lane l holds row 32 j + l's word in t[j], the weight
+// tile's in w.  Rows from `rows` on get zeros (their codes are zeros too).
+struct ScaleWords { uint32_t w, t[Pair::WORDS]; };
+__device__ __forceinline__ void load_scales(ScaleWords &s, const uint8_t *ws, const uint8_t *ts, int ld, int rows, int q,
+                                            int lane) {
+    s.w = load_word(ws + 4 * q);
+#pragma unroll
+    for (int j = 0; j < Pair::WORDS; j++)
+        s.t[j] = 32 * j + lane < rows ? load_word(ts + (size_t)(32 * j + lane) * ld + 4 * q) : 0u;
+}
+// ... to this warp's lane quarter of a TMEM slot: four columns of the weights' word, eight of the rows'.
+__device__ __forceinline__ void store_scales(uint32_t taddr, const ScaleWords &s) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr), "r"(s.w) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr + 4), "r"(s.t[0]),
+                 "r"(s.t[1]), "r"(s.t[2]), "r"(s.t[3]), "r"(s.t[4]), "r"(s.t[5]), "r"(s.t[6]), "r"(0u)
+                 : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+static_assert(Pair::WORDS == 7, "columns of store_scales");
 
 template <bool joint>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sf = smem + PAIR_RING;
-    uint64_t *full = reinterpret_cast<uint64_t *>(sf + SF_SLOTS * Pair::SF_SLOT_BYTES);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + PAIR_RING);
     uint64_t *empty = full + PAIR_STAGES, *sf_full = empty + PAIR_STAGES, *sf_empty = sf_full + SF_SLOTS;
-    uint64_t *sf_loaded = sf_empty + SF_SLOTS, *acc_full = sf_loaded + SF_SLOTS, *acc_empty = acc_full + 2;
+    uint64_t *acc_full = sf_empty + SF_SLOTS, *acc_empty = acc_full + 2;
     uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -640,8 +639,6 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     // zeros: 224 rows 251 us in stages of one block and 284 of two, 128 rows 347 and 327)
     const uint32_t block = Pair::W_BYTES + (uint32_t)bt / 2 * BK, stage = joint ? 2 * block : block;
     const uint32_t stages = min((uint32_t)PAIR_STAGES, PAIR_RING / stage);
-    // groups of scales over all of this pair's tiles
-    const uint32_t groups = pair < total ? (uint32_t)((total - pair + pairs - 1) / pairs) * ((p.kb + 3) / 4) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < PAIR_STAGES; s++) {
@@ -649,9 +646,8 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < SF_SLOTS; s++) {
-            mbar_init(smem_u32(&sf_full[s]), 2);
+            mbar_init(smem_u32(&sf_full[s]), 8);
             mbar_init(smem_u32(&sf_empty[s]), 1);
-            mbar_init(smem_u32(&sf_loaded[s]), 32);
         }
         for (int a = 0; a < 2; a++) {
             mbar_init(smem_u32(&acc_full[a]), 1);
@@ -674,6 +670,9 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     pdl_wait();
     pdl_launch_dependents();
 
+    // each warpgroup resizes its registers once, its four warps together; the host checked the launch's share
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
     if (warp == 0) {
         bool ok = true;
         uint32_t it = 0, s = 0, par = 1;
@@ -713,14 +712,12 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (rank != 0) {
-            if (lane == 0) signal_scales<2>(sf_loaded, mapa(smem_u32(sf_full), 0), 0, groups, abort);
-        } else {
+        if (rank == 0) {
             bool ok = true;
             uint32_t s = 0, s_par = 0, sl = 0, local = 0;
             const uint32_t sf_tmem = tmem + 2 * (uint32_t)bt;
             const uint32_t idesc0 = Pair::IDESC | (uint32_t)(bt >> 3) << 17;
-            const uint64_t w_desc = sw128_desc(smem_u32(smem)), sf_desc = scale_desc(smem_u32(sf));
+            const uint64_t w_desc = sw128_desc(smem_u32(smem));
             for (int tile = pair; tile < total && ok; tile += pairs) {
                 for (int c = 0; c < chunks && ok; c++, local++) {
                     const uint32_t acc = local & 1, d = tmem + acc * (uint32_t)bt;
@@ -734,11 +731,6 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                         if (kb % 4 == 0) {
                             if (!warp_wait<true>(smem_u32(&sf_full[slot]), (sl / SF_SLOTS) & 1, abort)) { ok = false; break; }
                             fence_after();
-                            const uint64_t src = sf_desc + (uint64_t)(slot * (Pair::SF_SLOT_BYTES >> 4));
-                            if (elect()) {
-#pragma unroll
-                                for (int i = 0; i < 3; i++) copy_scales_pair(sfa + 4 * i, src + (uint64_t)(i * (SF_BYTES >> 4)));
-                            }
                         }
                         const bool two = kb + 1 < p.kb;
                         // the second block's stage
@@ -788,36 +780,9 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             mbar_drain(smem_u32(drain), 0);
         }
         __syncwarp();
-    } else if (warp == 2) {
-        uint32_t n = 0;
-        bool ok = true;
-        for (int tile = pair; tile < total && ok; tile += pairs) {
-            int g, mt, nt;
-            pair_coords(p, tile, g, mt, nt);
-            // a weight tile past the matrix's end (the second CTA's) feeds no output: any scale
-            const int wb = min(2 * nt + rank, (p.n[g] + BW - 1) / BW - 1), m0 = mt * bt;
-            const int rows = min(bt, p.m - m0);
-            const uint8_t *ws = p.w_scale[g] + (size_t)wb * p.scale_ld;
-            const uint8_t *ts = p.a_scale + (size_t)m0 * p.scale_ld;
-            for (int sq = 0; sq < (p.kb + 3) / 4; sq++, n++) {
-                const int slot = n % SF_SLOTS;
-                if (!warp_wait<true>(smem_u32(&sf_empty[slot]), ((n / SF_SLOTS) & 1) ^ 1, abort)) { ok = false; break; }
-                const uint32_t dst = smem_u32(sf + slot * Pair::SF_SLOT_BYTES);
-                copy_word(dst, ws, sq, lane);
-                copy_words(dst + SF_BYTES, ts, p.scale_ld, rows, sq, lane);
-                copy_words(dst + 2 * SF_BYTES, rows > 128 ? ts + (size_t)128 * p.scale_ld : ts, p.scale_ld, rows - 128, sq, lane);
-                copies_arrive(smem_u32(&sf_loaded[slot]));
-            }
-        }
-        copies_wait<0>();
-        __syncwarp();
-    } else if (warp == 3) {
-        if (lane == 0) {
-            if (rank == 0) signal_scales<1>(sf_loaded, smem_u32(sf_full), 0, groups, abort);
-            else signal_scales<2>(sf_loaded, mapa(smem_u32(sf_full), 0), 1, groups, abort);
-        }
-        __syncwarp();
-    } else {
+    }
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_EPILOGUE));
         const int quarter = warp & 3, half = (warp - 4) / 4, cols = bt / 2;
         uint32_t local = 0;
         bool ok = true;
@@ -856,6 +821,57 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                 if (p.bf16_out) store_column(static_cast<__nv_bfloat16 *>(p.out[g]) + o, ld, v, rows);
                 else store_column(static_cast<float *>(p.out[g]) + o, ld, v, rows);
             }
+        }
+        __syncwarp();
+    } else {
+        // Scales: each of four warps writes its lane quarter of TMEM in this CTA, the words of two further
+        // groups already on their way, and tells the leader's MMA warp.  Going through TMEM alone, the signal
+        // is one that tcgen05.fence orders; words in shared memory would need a release at cluster scope,
+        // which beside the loads takes over a microsecond.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
+        const uint32_t sf_tmem = tmem + ((uint32_t)(warp & 3) << 21) + 2 * (uint32_t)bt, sf_full0 = mapa(smem_u32(sf_full), 0);
+        const int groups = (p.kb + 3) / 4;
+        // the group loaded next: tile and its operands, group of K
+        int ltile = pair, lq = 0, rows = 0;
+        const uint8_t *ws = nullptr, *ts = nullptr;
+        auto next = [&](ScaleWords &w) {
+            if (ltile >= total) return;
+            if (lq == 0) {
+                int g, mt, nt;
+                pair_coords(p, ltile, g, mt, nt);
+                // a weight tile past the matrix's end (the second CTA's) feeds no output: any scale
+                const int wb = min(2 * nt + rank, (p.n[g] + BW - 1) / BW - 1), m0 = mt * bt;
+                rows = min(bt, p.m - m0);
+                ws = p.w_scale[g] + (size_t)wb * p.scale_ld;
+                ts = p.a_scale + (size_t)m0 * p.scale_ld;
+            }
+            load_scales(w, ws, ts, p.scale_ld, rows, lq, lane);
+            if (++lq == groups) lq = 0, ltile += pairs;
+        };
+        ScaleWords w0, w1, w2;
+        next(w0);
+        next(w1);
+        next(w2);
+        uint32_t slot = 0, par = 1;
+        bool ok = true;
+        auto put_group = [&](const ScaleWords &w) {
+            ok = ok && warp_wait<true>(smem_u32(&sf_empty[slot]), par, abort);
+            if (!ok) return;
+            fence_after();
+            store_scales(sf_tmem + slot * Pair::SF_COLS, w);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(sf_full0 + 8 * slot);
+            if (++slot == SF_SLOTS) slot = 0, par ^= 1;
+        };
+        const int tiles = pair < total ? (total - pair + pairs - 1) / pairs : 0;
+        for (int64_t left = (int64_t)tiles * groups; left > 0 && ok; left -= 3) {
+            put_group(w0);
+            next(w0);
+            if (left > 1) put_group(w1);
+            next(w1);
+            if (left > 2) put_group(w2);
+            next(w2);
         }
         __syncwarp();
     }
@@ -971,12 +987,21 @@ int pair_bt(const QuantMatmulArgs &a, int64_t &cost) {
     return best;
 }
 
+template <typename F>
+int launch_regs(F *kernel) {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
+}
+
 cudaError_t launch_pair(const QuantMatmulArgs &a, int bt, cudaStream_t s) {
     Maps maps;
     Params p;
     cudaError_t e = fill_params(a, 2 * BW, bt, bt / 2, p, maps);
     if (e != cudaSuccess) return e;
     auto kernel = bt <= 160 ? qmm_pair_kernel<true> : qmm_pair_kernel<false>;
+    // the warpgroups' registers after setmaxnreg have to fit what the launch gives, or their wait for them never ends
+    static const int regs[2] = {launch_regs(qmm_pair_kernel<false>), launch_regs(qmm_pair_kernel<true>)};
+    if (regs[bt <= 160] * 4 < 2 * REG_EPILOGUE + 2 * REG_OTHER) return cudaErrorInvalidConfiguration;
     if ((e = ensure_dyn_smem(kernel, Pair::SMEM_BYTES)) != cudaSuccess) return e;
     const int tiles = p.tile_start[a.n_w];
     return launch_pdl(kernel, dim3((unsigned)(2 * (tiles < PAIRS ? tiles : PAIRS))), dim3(PAIR_THREADS), Pair::SMEM_BYTES, s,

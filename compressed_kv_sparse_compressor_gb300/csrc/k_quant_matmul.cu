@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc]));
+            __syncwarp();
         }
         if (ok && split > 1) {
             float *part = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
@@ -545,6 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
             for (int j = 0; j < 4; j++)
                 if (n + j < p.n[g]) store_out(p.out[g], o + j, f[j], p.bf16_out);
         }
+        __syncwarp();
         cluster_sync();
     }
     __syncthreads();
@@ -812,6 +814,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_relaxed(mapa(smem_u32(&acc_empty[acc]), 0));
+                __syncwarp();
             }
             if (!ok) break;
             const int n = nt * 2 * BW + rank * BW + quarter * 32 + lane, m0 = mt * bt + half * cols;
@@ -821,6 +824,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                 if (p.bf16_out) store_column(static_cast<__nv_bfloat16 *>(p.out[g]) + o, ld, v, rows);
                 else store_column(static_cast<float *>(p.out[g]) + o, ld, v, rows);
             }
+            __syncwarp();                                // the next wait and loads are the whole warp's
         }
         __syncwarp();
     } else {
@@ -862,6 +866,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(sf_full0 + 8 * slot);
+            __syncwarp();
             if (++slot == SF_SLOTS) slot = 0, par ^= 1;
         };
         const int tiles = pair < total ? (total - pair + pairs - 1) / pairs : 0;

@@ -89,11 +89,14 @@ class DeviceLayer:
 
         def lw(w, dl):
             width = s.coff * dl
-            kv, gate = (x if isinstance(x, fp8.Fp8Weight) else fp8.quantize_weight(x.to(self.device)) for x in w[:2])
-            ape, norm = (None if x is None else x.to(self.device).contiguous() for x in w[2:])
+            dev = self.raw.device            # with its index, whatever device is current now
+            kv, gate = (x if isinstance(x, fp8.Fp8Weight) else fp8.quantize_weight(x.to(dev)) for x in w[:2])
+            ape, norm = (None if x is None else x.to(dev).contiguous() for x in w[2:])
             for x, want in ((kv, (width, s.d_model)), (gate, (width, s.d_model)), (ape, (s.ratio, width)), (norm, (dl,))):
                 if x is not None and tuple(x.shape) != want:
                     raise ValueError(f"lane weight of shape {tuple(x.shape)}, expected {want}")
+            if any(x is not None and x.dtype != torch.float32 for x in (ape, norm)):
+                raise ValueError("ape and norm: float32")
             if kv.device_index != self.raw.get_device() or gate.device_index != self.raw.get_device():
                 raise ValueError(f"weights on cuda:{kv.device_index}, the layer on {self.raw.device}")
             self._keep.append((kv, gate, ape, norm))

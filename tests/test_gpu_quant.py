@@ -463,6 +463,16 @@ def test_layer_refusals():
         quant.compress_prefill_quant(*fp8.empty(68, shape.d_model), 0)      # past the state's capacity
 
 
+def test_layer_refuses_a_bias_or_gain_of_another_type():
+    # the library reads both as floats: of a narrower type it would read past their end
+    shape, _, quant = _layers(4, 16)
+    wa, wi = (configs.lane_weights(shape, 5, 0, lane, device="cuda") for lane in ("attn", "idx"))
+    for dt in (torch.bfloat16, torch.float16, torch.float64):
+        for bad in (wa[:2] + (wa[2].to(dt), wa[3]), wa[:3] + (torch.ones(shape.head_dim, dtype=dt, device="cuda"),)):
+            with pytest.raises(ValueError):
+                quant.set_weights_quant(bad, wi)
+
+
 # ---- refusals of the torch calls -----------------------------------------------------------------
 
 def test_refusals_of_the_torch_calls():

@@ -59,10 +59,11 @@ __device__ __forceinline__ void add_exact(float &s, float &c, float v) {
     s = add_error(s, v, err);
     c = __fadd_rn(c, err);
 }
-// The same for s >= v >= 0, where the error is v - ((s + v) - s) (Dekker, 1971).
-__device__ __forceinline__ void add_smaller(F2 &s, F2 &c, F2 v) {
-    const F2 t = add2(s, v);
-    c = add2(c, sub2(v, sub2(t, s)));
+// The same for the pair's squares, 0 <= v^2 <= s: the rounded sum t = s + v^2, whose step t - s is exact
+// (Dekker, 1971), and what the step lacks to v^2 in one fused product.
+__device__ __forceinline__ void add_square(F2 &s, F2 &c, F2 v) {
+    const F2 t = fma2(v, v, s);
+    c = add2(c, fma2(v, v, sub2(s, t)));
     s = t;
 }
 
@@ -280,11 +281,14 @@ __device__ __forceinline__ void quantise8(const F2 (&y)[4], int base, int d, uin
             m[!VEC && i >= 2] = fmaxf(m[!VEC && i >= 2], fmaxf(finite_abs(v.x), finite_abs(v.y)));
         }
     }
-#pragma unroll
-    for (int o = VEC ? 8 : 16; o; o >>= 1) {
-        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-        if (!VEC) m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
-    }
+    // over the block's lanes; magnitudes are ordered as integers.  VEC: each half warp's lanes with zeros
+    // from the other half
+    const uint32_t u0 = __float_as_uint(m[0]), u1 = __float_as_uint(m[1]);
+    const bool upper = threadIdx.x % 32 >= 16;
+    const uint32_t r0 = __reduce_max_sync(0xffffffffu, VEC && upper ? 0u : u0);
+    const uint32_t r1 = __reduce_max_sync(0xffffffffu, VEC ? (upper ? u0 : 0u) : u1);
+    m[0] = __uint_as_float(VEC && upper ? r1 : r0);
+    m[1] = __uint_as_float(r1);
     const int b0 = scale_byte(m[0]);
     if (VEC) {
         if (base >= d) return;
@@ -307,20 +311,35 @@ __device__ __forceinline__ void quantise8(const F2 (&y)[4], int base, int d, uin
     }
 }
 
-// (s, c) = sum of the squares of h * f, f a power of two.  Each half of the running pair starts at
-// the thread's largest square, which makes every term the smaller one of its addition.  EXACT: the
-// values are bf16, whose squares float holds; otherwise the squares' own errors are added too.
-template <bool EXACT, int NI, typename H>
-__device__ __forceinline__ void sum_squares(const H (&h)[NI], float f, float &s, float &c) {
+// Largest magnitude of a thread's values, NaN if one is NaN.  bf16 magnitudes are ordered as 16-bit
+// integers, NaN above infinity: two at a time.
+template <int NI>
+__device__ __forceinline__ float largest(const Bf16x8 (&h)[NI]) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < NI; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) u = __vimax3_u16x2(u, h[i].w[j] & 0x7fff7fffu, h[i].w[j + 1] & 0x7fff7fffu);
+    return __uint_as_float(max(u << 16, u & 0xffff0000u));
+}
+template <int NI>
+__device__ __forceinline__ float largest(const F32x8 (&h)[NI]) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const float2 v = unpack(pair_of(h[i], j));
+            const float2 v = unpack(h[i].v[j]);
             m = max_abs(m, v.x, v.y);
         }
-    m *= f;
+    return m;
+}
+
+// (s, c) = sum of the squares of h * f, f a power of two.  Each half of the running pair starts at
+// the thread's largest square, which makes every term the smaller one of its addition.
+template <int NI, typename H>
+__device__ __forceinline__ void sum_squares(const H (&h)[NI], float f, float &s, float &c) {
+    const float m = largest(h) * f;
     const float top = __fmul_rn(m, m);
     if (!(top < INFINITY)) {                             // an infinity, NaN, or a square past float's range
         s = top;
@@ -332,12 +351,7 @@ __device__ __forceinline__ void sum_squares(const H (&h)[NI], float f, float &s,
 #pragma unroll
     for (int i = 0; i < NI; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const F2 v = f == 1.f ? pair_of(h[i], j) : mul2(pair_of(h[i], j), ff);
-            const F2 sq = mul2(v, v);
-            add_smaller(s2, c2, sq);
-            if (!EXACT) c2 = add2(c2, fma2(v, v, mul2(sq, f2(-1.f, -1.f))));
-        }
+        for (int j = 0; j < 4; j++) add_square(s2, c2, f == 1.f ? pair_of(h[i], j) : mul2(pair_of(h[i], j), ff));
     const float2 sv = unpack(s2), cv = unpack(c2);
     s = sv.x;
     c = __fadd_rn(cv.x, cv.y);
@@ -359,7 +373,9 @@ struct NormParams {
 // blockDim.x threads per row (up to NI * 8 values each), blockDim.y rows per block (above one only
 // where a row is one warp's).  The row is held as it is stored (a bf16 value in half a register), so
 // that a thread can take many values and the fixed work per thread, the meeting of the sums, is spread
-// over them.  MAXT: the most threads per block.
+// over them.  MAXT: the most threads per block.  Many rows are bound by HBM and by how many of them an
+// SM has in flight (56 registers hold 5 blocks of 224 threads: 16384 x 7168 131 us, 92 % of the copy
+// rate; 4 blocks 141; blocks that stay and copy their next row to shared memory beside this one 142 to 163).
 template <typename T, int NI, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kernel(NormParams p) {
     using H = typename Held<T>::type;
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
     if (!p.q && !p.y_out) return;
 
     float s, c;
-    sum_squares<sizeof(T) == 2, NI>(h, 1.f, s, c);
+    sum_squares(h, 1.f, s, c);
     row_sum(s, c, sm);
     float rstd;
     if (s < 0x1p90f) {
@@ -409,7 +425,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
         // squares near the end of float's range or past it (elements above about 1e13, infinities,
         // NaN): the sum of (h * 2^-80)^2, in which eps vanishes, and 2^-80 put back
         if (blockDim.x > 32) __syncthreads();
-        sum_squares<false, NI>(h, 0x1p-80f, s, c);
+        sum_squares(h, 0x1p-80f, s, c);
         row_sum(s, c, sm);
         rstd = s < INFINITY ? rstd_of(s, c, p.inv_d, p.inv_d_lo, 0.f) * 0x1p-80f : s > 0.f ? 0.f : s;
     }
@@ -484,14 +500,7 @@ quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t 
             round8(y, h[i]);                             // exact: the values are of the type
         }
     }
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 a = unpack(pair_of(h[i], j));
-            amax = max_abs(amax, a.x, a.y);
-        }
+    float amax = largest(h);
     const bool finite = __syncthreads_and(amax < INFINITY);
     if (!finite) {
         amax = 0.f;
@@ -503,8 +512,7 @@ quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t 
                 amax = fmaxf(amax, fmaxf(finite_abs(a.x), finite_abs(a.y)));
             }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
     if (t % 32 == 0) sm[t / 32] = amax;
     __syncthreads();
 #pragma unroll
@@ -533,15 +541,16 @@ cudaError_t launch_norm(const NormParams &p, bool vec, int threads, cudaStream_t
     // rows of one warp: four to a block
     const int rows = threads == 32 && p.n > 4 ? 4 : 1;
     const dim3 grid((unsigned)((p.n + rows - 1) / rows)), block(threads, rows);
+    if constexpr (MAXT == 256) return launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT>, grid, block, 0, s, p);
     return vec ? launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT>, grid, block, 0, s, p)
                : launch_pdl(rmsnorm_quant_kernel<T, NI, false, MAXT>, grid, block, 0, s, p);
 }
 
 // Threads per row.  Few rows: one group of 8 values in each thread, the shortest chain (a row of 4096
 // bf16 values in 2.6 us).  Many rows: as few warps as hold the row in 2 groups of each thread, 4 for
-// aligned bf16 rows, which are half as wide (4096 x 4096: 26 us; 28 with 2 groups, 33 with 8; 16384 x
-// 7168: 142, 238, 156; 16384 x 1024 floats: 39 with 2, 42 with 4; 3000 unaligned rows of 1541: 16 with
-// 2, 22 with 4).
+// aligned bf16 rows, which are half as wide (4096 x 4096: 25.5 us; 26.8 with 2 groups, 33.5 with 8; 16384 x
+// 7168: 131, 195, 170; 16384 x 1024 floats: 38 with 2, 42 with 4; 3000 unaligned rows of 1541: 14 with
+// 2, 21 with 4).
 template <typename T>
 cudaError_t launch_norm_t(const NormParams &p, bool vec, cudaStream_t s) {
     const int most = sizeof(T) == 2 && vec ? 4 : 2, groups = (p.d + 7) / 8;
@@ -551,7 +560,9 @@ cudaError_t launch_norm_t(const NormParams &p, bool vec, cudaStream_t s) {
     const int threads = ((groups + ni - 1) / ni + 31) / 32 * 32;
     if (ni == 1) return launch_norm<T, 1, 1024>(p, vec, threads, s);
     if (ni == 2) return launch_norm<T, 2, 1024>(p, vec, threads, s);
-    return threads <= 256 ? launch_norm<T, 4, 256>(p, vec, threads, s) : launch_norm<T, 4, 1024>(p, vec, threads, s);
+    if constexpr (sizeof(T) == 2)                        // aligned rows: others have 4 groups from d = 16385 on
+        if (threads <= 256) return launch_norm<T, 4, 256>(p, vec, threads, s);
+    return launch_norm<T, 4, 1024>(p, vec, threads, s);
 }
 
 template <typename T>

@@ -69,7 +69,10 @@ struct Shape {
     // scale byte's index goes to bits 4 (B) and 29 (A)
     static constexpr uint32_t IDESC = ((uint32_t)(BT >> 3) << 17) | (1u << 23) | ((uint32_t)(BW >> 7) << 27);
     static_assert(BT % 16 == 0 && BT <= 256, "MMA N");
-    static_assert(BT * BW * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the stages");
+    // the last stages hold the partial sums that a CTA receives,
+    // from 8 CTAs, at least 4 rows each
+    static constexpr int PART_STAGES = ((BT < 32 ? 32 : BT) * BW * 4 + STAGE_BYTES - 1) / STAGE_BYTES;
+    static_assert(PART_STAGES < STAGES, "the partial sums reuse stages");
     static_assert(PER_SM * TMEM_COLS <= 512, "TMEM of the CTAs of an SM");
     static_assert(PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "CTAs to an SM");
 };
@@ -263,19 +266,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
-__device__ __forceinline__ float4 cluster_ld(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
+__device__ __forceinline__ void cluster_st4(uint32_t addr, uint32_t rank, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mapa(addr, rank)), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
 }
 
 // Copies the scale words of group q (4 stages) of 128 rows, row r of them at src + r * ld, into their
@@ -349,6 +348,15 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
     const int n0 = nt * BW;
     // the K ranges of the ranks differ by at most one block
     const int kb0 = (int)((int64_t)p.kb * rank / split), kb1 = (int)((int64_t)p.kb * (rank + 1) / split);
+    // Meeting: each CTA adds the groups of 4 rows whose number is its rank modulo split (a power of two), to
+    // which the others write their partial sums, into the last stages: free from the start if no CTA's K
+    // comes that far (`unused`), else once all MMAs of the cluster are done.  The cluster barrier's first
+    // phase says that, the second that the sums have arrived.  (The sums of 32 rows through 2560 x 4096 weights
+    // read from the other CTAs instead, a round trip more: 6.65 us for 5.9; sent value by value, 128 rows:
+    // 11 us for 9.4.)
+    const int log_split = 31 - __clz(split), own = max(1, BT / 4 >> log_split);
+    const bool unused = (p.kb + split - 1) >> log_split <= S::STAGES - S::PART_STAGES;
+    float4 *part = reinterpret_cast<float4 *>(smem + (S::STAGES - S::PART_STAGES) * S::STAGE_BYTES);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::STAGES; s++) {
@@ -382,6 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (split > 1 && unused) cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
 
@@ -509,14 +518,16 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(smem_u32(&acc_empty[acc]));
             __syncwarp();
         }
-        if (ok && split > 1) {
-            float *part = reinterpret_cast<float *>(smem) + quarter * 32 + lane;
+        if (split > 1) {
+            __syncwarp();
+            if (!unused) cluster_arrive();
+            cluster_wait();
+            const uint32_t dst = smem_u32(part + rank * own * BW + quarter * 32 + lane);
 #pragma unroll
-            for (int i = 0; i < BT / 16; i++)
-                if (16 * i < rows) {
-#pragma unroll
-                    for (int j = 0; j < 16; j++) part[(16 * i + j) * BW] = v[i][j];
-                }
+            for (int q = 0; q < BT / 4; q++)
+                if (ok && 4 * q < rows)
+                    cluster_st4(dst + (q >> log_split) * (BW * 16), q & (split - 1), v[q / 4][q % 4 * 4], v[q / 4][q % 4 * 4 + 1],
+                                v[q / 4][q % 4 * 4 + 2], v[q / 4][q % 4 * 4 + 3]);
         } else if (ok && n < p.n[g]) {
             const int64_t ld = p.out_ld[g], o = (int64_t)m0 * ld + n;
             if (p.bf16_out) store_column(static_cast<__nv_bfloat16 *>(p.out[g]) + o, ld, v, rows);
@@ -524,30 +535,31 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         }
     }
     if (split > 1) {
-        // partial tiles [row][128] in every CTA's stages (no copy or MMA uses them any more):
-        // each CTA adds a share of them in rank order
+        // partial sums [source][own group][128 columns][4 rows], added in rank order
         __syncwarp();
+        if (warp < 4) {
+            if (!unused) cluster_arrive();
+            cluster_wait();
+        }
         cluster_sync();
-        const int total = min(BT, p.m - m0) * (BW / 4);
-        const uint32_t base = smem_u32(smem);
-        for (int e = rank * THREADS + threadIdx.x; e < total; e += split * THREADS) {
-            float4 u[8];                                 // every rank's load in flight before the first addition
+        const int rows = min(BT, p.m - m0), total = (((rows + 3) / 4 - rank + split - 1) >> log_split) * BW;
+        for (int e = threadIdx.x; e < total; e += THREADS) {
+            float4 u[8];                                 // every load in flight before the first addition
 #pragma unroll
             for (int r = 0; r < 8; r++)
-                if (r < split) u[r] = cluster_ld(base + e * 16, r);
+                if (r < split) u[r] = part[r * own * BW + e];
             float4 v = u[0];
 #pragma unroll
             for (int r = 1; r < 8; r++)
                 if (r < split) v.x += u[r].x, v.y += u[r].y, v.z += u[r].z, v.w += u[r].w;
-            const int n = n0 + e % (BW / 4) * 4;
-            const int64_t o = (int64_t)(m0 + e / (BW / 4)) * p.out_ld[g] + n;
+            const int n = n0 + e % BW, row = ((e / BW << log_split) + rank) * 4;
+            if (n >= p.n[g]) continue;
+            int64_t o = (int64_t)(m0 + row) * p.out_ld[g] + n;
             const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (n + j < p.n[g]) store_out(p.out[g], o + j, f[j], p.bf16_out);
+            for (int j = 0; j < 4; j++, o += p.out_ld[g])
+                if (row + j < rows) store_out(p.out[g], o, f[j], p.bf16_out);
         }
-        __syncwarp();
-        cluster_sync();
     }
     __syncthreads();
     if (warp == 1) {
@@ -946,14 +958,22 @@ int64_t count_tiles(const QuantMatmulArgs &a, int wrows, int rows) {
     return tiles;
 }
 
-// CTAs that share a tile: as many, up to 8, as leave each two blocks of K and all clusters running at
-// once.  Clusters of 2, 4 and 8 CTAs of one SM each that this GPU's 152 SMs hold: 76, 36 and 15 (a
-// cluster stays within a group of about 19 SMs); 16 x 8 CTAs took 14.3 us where 16 x 4 take 8.6.
-int choose_split(int64_t tiles, int kb, int per_sm) {
+// CTAs that share a tile of bt rows: of 1, 2, 4 and 8 with all clusters running at once, the one with the
+// least time of its own (10 ns): 0.33 us a block of K, half as much again and 0.4 us where clusters share
+// their SMs, 0.6 us and 11 ns a row for the meeting.  Fitted to 216 products of 1 to 128 rows, 256 to 8192
+// columns and K (mean loss to the best choice 0.3 %; as many CTAs as leave each two blocks lost 4.5, 27 at
+// most: 128 x 1024 x 512 4.4 us whole and 5.6 by two, 64 x 256 x 1544 4.0 by eight and 5.0 by four).
+// Clusters of 2, 4 and 8 CTAs of one SM each that this GPU's 152 SMs hold: 76, 36 and 15 (a cluster stays
+// within a group of about 19 SMs); 16 x 8 CTAs took 14.3 us where 16 x 4 take 8.6.
+int choose_split(int64_t tiles, int kb, int bt, int per_sm) {
     const int room[4] = {152, 76, 36, 15};
-    int split = 1;
-    for (int i = 1; i < 4; i++)
-        if (tiles <= (int64_t)room[i] * per_sm && kb >= 2 << i) split = 1 << i;
+    int split = 1, least = 0;
+    for (int i = 0; i < 4; i++) {
+        if (i > 0 && (tiles > (int64_t)room[i] * per_sm || kb < 1 << i)) break;
+        const int blocks = (kb + (1 << i) - 1) >> i;
+        const int cost = (i > 0 ? 60 + 11 * bt / 10 : 0) + (tiles > room[i] ? 40 + 33 * blocks * 3 / 2 : 33 * blocks);
+        if (i == 0 || cost < least) split = 1 << i, least = cost;
+    }
     return split;
 }
 
@@ -965,28 +985,28 @@ cudaError_t launch_split(const QuantMatmulArgs &a, cudaStream_t s) {
     cudaError_t e = fill_params(a, BW, BT, BT, p, maps);
     if (e != cudaSuccess) return e;
     if ((e = ensure_dyn_smem(qmm_split_kernel<BT>, S::SMEM_BYTES)) != cudaSuccess) return e;
-    const int tiles = p.tile_start[a.n_w], split = choose_split(tiles, p.kb, S::PER_SM);
+    const int tiles = p.tile_start[a.n_w], split = choose_split(tiles, p.kb, BT, S::PER_SM);
     return launch_pdl_cluster(qmm_split_kernel<BT>, dim3((unsigned)(tiles * split)), dim3(THREADS), S::SMEM_BYTES, s, split,
                               maps, p, split);
 }
 
-// Time of the product on split<128>, in 10 ns: 4 us, 1.9 us more for meeting in a cluster, and 0.33 us
-// a block of K.
+// Time of the product on split<128>, in 10 ns: 3 us and 0.37 us a block of K for each round of CTAs over the
+// SMs, 1.4 us more for meeting in a cluster.
 int64_t split_cost(const QuantMatmulArgs &a) {
     const int64_t tiles = count_tiles(a, BW, 128);
-    const int kb = (a.k + BK - 1) / BK, split = choose_split(tiles, kb, 1);
-    return 400 + (split > 1 ? 190 : 0) + 33 * ((tiles * split + 151) / 152) * ((kb + split - 1) / split);
+    const int kb = (a.k + BK - 1) / BK, split = choose_split(tiles, kb, 128, 1);
+    return (tiles * split + 151) / 152 * (300 + 37 * ((kb + split - 1) / split)) + (split > 1 ? 140 : 0);
 }
 
 constexpr int PAIRS = 76;
 
 // Rows of a pair tile: the width with the fewest rounds over the pairs times a block's time; cost: of the
-// product, in 10 ns: 4.8 us and 0.115 + 0.00058 bt us a block.
+// product, in 10 ns: 4 us and 0.115 + 0.00058 bt us a block.
 int pair_bt(const QuantMatmulArgs &a, int64_t &cost) {
     int best = 0;
     const int kb = (a.k + BK - 1) / BK;
     for (int bt = MAX_BT; bt >= 128; bt -= 32) {
-        const int64_t c = 480 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (11500 + 58 * bt) / 1000;
+        const int64_t c = 400 + (count_tiles(a, 2 * BW, bt) + PAIRS - 1) / PAIRS * kb * (11500 + 58 * bt) / 1000;
         if (best == 0 || c < cost) best = bt, cost = c;
     }
     return best;
@@ -1020,8 +1040,9 @@ cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s) {
     if (a.m <= 32) return launch_split<32>(a, s);
     if (a.m <= 64) return launch_split<64>(a, s);
     // more rows: one CTA's tiles, K split to fill the GPU, or pairs' tiles, which reuse more; by the two
-    // costs, fitted to 64 products of 65 to 1024 rows with 256 to 8192 columns (256 rows: 4096 x 4096 12.4 us
-    // split and 11.5 in pairs, 8192 x 8192 25.8 and 21.5, 1024 x 4096 8.8 and 10.6, 256 x 8192 8.8 and 15.2)
+    // costs, fitted to 336 products of 96 to 1024 rows with 256 to 8192 columns and K (mean loss to the
+    // better one 0.1 %, most 6.5; 256 rows: 4096 x 4096 11.6 us split and 10.9 in pairs, 8192 x 8192 26.1 and
+    // 20.5, 1024 x 4096 8.3 and 9.8, 256 x 8192 8.1 and 15.4)
     int64_t cost;
     const int bt = pair_bt(a, cost);
     return split_cost(a) <= cost ? launch_split<128>(a, s) : launch_pair(a, bt, s);

@@ -68,6 +68,24 @@ def test_norm_matches_the_definition_bit_for_bit(dtype, n, d, residual, gain):
     check()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,d", [(512, 4096), (600, 4104), (513, 1024), (521, 256), (700, 100), (515, 8192), (512, 7168),
+                                 (530, 1541), (512, 16392)])
+def test_norm_of_many_rows_bit_for_bit(dtype, n, d):
+    # the forms for many rows: rows that fill their threads and rows that do not, several rows to a block
+    g = gen(7 * n + d)
+    x, r, w = randn(g, n, d).to(dtype), (3 * randn(g, n, d)).to(dtype), 1 + 0.1 * randn(g, d)
+    q, scale, check = guarded(n, d)
+    h = torch.empty_like(x)
+    fp8.rmsnorm(x, w, residual=r, residual_out=h, eps=EPS, q=q, scale=scale)
+    wh, wy = ref.rmsnorm(x, r, w, EPS)
+    wq, ws = ref.quantise(wy, 1)
+    assert torch.equal(h, wh)
+    assert torch.equal(scale[:, :-(-d // 128)], ws)
+    assert torch.equal(q.view(torch.uint8), wq)
+    check()
+
+
 def test_norm_strided_and_in_place():
     g = gen(3)
     n, d = 19, 520

@@ -476,13 +476,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
 
 // One block of 256 threads per 128 x 128 block of weights, 64 values in each thread: VEC a row's
 // 128 values in 16 threads, otherwise 4 single ones in each of 32 lanes (two rows per step).
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
-quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t q_ld, uint8_t *scale, int64_t scale_ld) {
+// WHOLE: nothing of the block lies past n or k, so that no load hangs on a comparison (8192 x 8192 floats 52 us,
+// 95 % of the copy rate; 60 with the comparisons).
+template <typename T, bool VEC, bool WHOLE>
+__device__ __forceinline__ void quant_block(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t q_ld, uint8_t *scale,
+                                            int64_t scale_ld, float *sm) {
     using H = typename Held<T>::type;
-    __shared__ float sm[8];
-    pdl_wait();
-    pdl_launch_dependents();
+    if (WHOLE) n = k = INT_MAX;
     const int t = threadIdx.x;
     const int base = blockIdx.x * 128 + (VEC ? t % 16 * 8 : t % 32);
     const int row0 = blockIdx.y * 128 + (VEC ? t / 16 : t / 32 * 2);
@@ -537,6 +537,18 @@ quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t 
         }
     }
     if (t == 0) scale[blockIdx.y * scale_ld + blockIdx.x] = (uint8_t)byte;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
+quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t q_ld, uint8_t *scale, int64_t scale_ld) {
+    __shared__ float sm[8];
+    pdl_wait();
+    pdl_launch_dependents();
+    if ((blockIdx.x + 1) * 128 <= k && (blockIdx.y + 1) * 128 <= n)
+        quant_block<T, VEC, true>(n, k, w, w_ld, q, q_ld, scale, scale_ld, sm);
+    else
+        quant_block<T, VEC, false>(n, k, w, w_ld, q, q_ld, scale, scale_ld, sm);
 }
 
 template <typename T, int NI, int MAXT>

@@ -375,11 +375,11 @@ struct NormParams {
 // blockDim.x threads per row (up to NI * 8 values each), blockDim.y rows per block (above one only
 // where a row is one warp's).  The row is held as it is stored (a bf16 value in half a register), so
 // that a thread can take many values and the fixed work per thread, the meeting of the sums, is spread
-// over them.  MAXT: the most threads per block.  FULL: the rows fill their threads, so that no place has to
-// be compared with d.  Many rows are bound by HBM and by how many of them an SM has in flight (16384 x 7168
-// 127 us, 95 % of the copy rate; 131 with the comparisons; 56 registers hold 5 blocks of 224 threads, 141 us
+// over them.  MAXT: the most threads per block.  INNER: only the last group's places may lie past d (with one group,
+// none), so that the others' loads hang on no comparison.  Many rows are bound by HBM and by how many of
+// them an SM has in flight (16384 x 7168 127 us, 95 % of the copy rate; 131 with every comparison; 56 registers hold 5 blocks of 224 threads, 141 us
 // with 4; blocks that stay and copy their next row to shared memory beside this one 142 to 163).
-template <typename T, int NI, bool VEC, int MAXT, bool FULL>
+template <typename T, int NI, bool VEC, int MAXT, bool INNER>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kernel(NormParams p) {
     using H = typename Held<T>::type;
     __shared__ float sm[64];
@@ -387,12 +387,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
     pdl_launch_dependents();
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= p.n) return;                              // a whole warp: rows of one block are warps then
-    const int d = FULL ? INT_MAX : p.d;                  // what places are compared with
+    // what the places of group i are compared with
+    auto end = [&](int i) { return INNER && (i < NI - 1 || NI == 1) ? INT_MAX : p.d; };
     const T *x = static_cast<const T *>(p.x) + row * p.x_ld;
     H h[NI];
 #pragma unroll
     for (int i = 0; i < NI; i++) {
-        const int base = first_of<VEC>(i);
+        const int base = first_of<VEC>(i), d = end(i);
         zero8(h[i]);
         if (base < d) load8<VEC>(x, base, d, h[i]);
     }
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
         H r[NI];
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            const int base = first_of<VEC>(i);
+            const int base = first_of<VEC>(i), d = end(i);
             zero8(r[i]);
             if (base < d) load8<VEC>(rp, base, d, r[i]);
         }
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
         T *o = static_cast<T *>(p.residual_out) + row * p.residual_out_ld;
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            const int base = first_of<VEC>(i);
+            const int base = first_of<VEC>(i), d = end(i);
             if (base < d) store8<VEC>(o, base, d, h[i]);
         }
     }
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
     const F2 rstd2 = f2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NI; i++) {
-        const int base = first_of<VEC>(i);
+        const int base = first_of<VEC>(i), d = end(i);
         F2 y[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) y[j] = mul2(pair_of(h[i], j), rstd2);
@@ -558,7 +559,7 @@ cudaError_t launch_norm(const NormParams &p, bool vec, int threads, cudaStream_t
     // rows of one warp: four to a block
     const int rows = threads == 32 && p.n > 4 ? 4 : 1;
     const dim3 grid((unsigned)((p.n + rows - 1) / rows)), block(threads, rows);
-    if (vec && p.d == threads * NI * 8)
+    if (vec && p.d >= (NI == 1 ? threads : (NI - 1) * threads) * 8)
         return launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT, true>, grid, block, 0, s, p);
     if constexpr (MAXT > 256)                            // up to 256: aligned rows alone
         if (!vec) return launch_pdl(rmsnorm_quant_kernel<T, NI, false, MAXT, false>, grid, block, 0, s, p);
@@ -568,7 +569,7 @@ cudaError_t launch_norm(const NormParams &p, bool vec, int threads, cudaStream_t
 // Threads per row.  Few rows: one group of 8 values in each thread, the shortest chain (a row of 4096
 // bf16 values in 2.6 us).  Many rows: as few warps as hold the row in 2 groups of each thread, 4 for
 // aligned bf16 rows, which are half as wide (4096 x 4096: 25.5 us; 26.8 with 2 groups, 33.5 with 8; 16384 x
-// 7168: 131, 195, 170, before FULL; 16384 x 1024 floats: 38 with 2, 42 with 4; 3000 unaligned rows of 1541: 14 with
+// 7168: 131, 195, 170, before INNER; 16384 x 1024 floats: 38 with 2, 42 with 4; 3000 unaligned rows of 1541: 14 with
 // 2, 21 with 4).
 template <typename T>
 cudaError_t launch_norm_t(const NormParams &p, bool vec, cudaStream_t s) {

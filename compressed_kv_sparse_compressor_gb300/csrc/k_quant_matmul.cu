@@ -382,9 +382,11 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         fence_before();
     }
-    if (BT <= 32 && warp == 0 && elect()) {
-        // the weights of the first stages, while the previous kernel ends, beside which these small CTAs
-        // can start (2560 x 4096 weights: 1 row 5.6 -> 5.3 us, 32 rows 7.2 -> 6.7; larger tiles lost 1 to 9 %)
+    if (BT <= 32 && warp == 3 && (int)gridDim.x / split * p.kb >= 256 && elect()) {
+        // the weights of the first stages, while the previous kernel ends, beside which these small CTAs can
+        // start.  For weights of 4 MB on (32 rows, K = 1024: 8192 columns 5.4 -> 5.0 us, but 2560 3.65 -> 3.9;
+        // 2560 x 4096 6.1 -> 5.9) and tiles of up to 32 rows (64 rows: 2560 x 4096 8.0 -> 7.4, but 4096 x 4096
+        // 7.9 -> 8.6)
         for (int kb = kb0; kb < min(kb1, kb0 + S::STAGES); kb++) tma_prefetch_2d(&maps.w[g], kb * BK, n0);
     }
     __syncthreads();

@@ -377,7 +377,7 @@ struct NormParams {
 // that a thread can take many values and the fixed work per thread, the meeting of the sums, is spread
 // over them.  MAXT: the most threads per block.  INNER: only the last group's places may lie past d (with one group,
 // none), so that the others' loads hang on no comparison.  Many rows are bound by HBM and by how many of
-// them an SM has in flight (16384 x 7168 127 us, 95 % of the copy rate; 131 with every comparison; 56 registers hold 5 blocks of 224 threads, 141 us
+// them an SM has in flight (16384 x 7168 127 us, 95 % of the copy rate; 131 with every comparison; 54 registers hold 5 blocks of 224 threads, 141 us
 // with 4; blocks that stay and copy their next row to shared memory beside this one 142 to 163).
 template <typename T, int NI, bool VEC, int MAXT, bool INNER>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kernel(NormParams p) {

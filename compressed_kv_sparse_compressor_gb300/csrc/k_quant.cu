@@ -375,10 +375,11 @@ struct NormParams {
 // blockDim.x threads per row (up to NI * 8 values each), blockDim.y rows per block (above one only
 // where a row is one warp's).  The row is held as it is stored (a bf16 value in half a register), so
 // that a thread can take many values and the fixed work per thread, the meeting of the sums, is spread
-// over them.  MAXT: the most threads per block.  INNER: only the last group's places may lie past d (with one group,
-// none), so that the others' loads hang on no comparison.  Many rows are bound by HBM and by how many of
-// them an SM has in flight (16384 x 7168 127 us, 95 % of the copy rate; 131 with every comparison; 54 registers hold 5 blocks of 224 threads, 141 us
-// with 4; blocks that stay and copy their next row to shared memory beside this one 142 to 163).
+// over them.  MAXT: the most threads per block.  INNER: only the last group's places may lie past d (with
+// one group, none), so that the others' loads hang on no comparison (16384 x 7168 131 -> 127 us, 4096
+// unaligned rows of 4101 45 -> 37).  Many rows are bound by HBM and by how many of them an SM has in flight
+// (16384 x 7168 127 us, 95 % of the copy rate: 54 registers hold 5 blocks of 224 threads; 141 us with 4; blocks
+// that stay and copy their next row to shared memory beside this one 142 to 163).
 template <typename T, int NI, bool VEC, int MAXT, bool INNER>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kernel(NormParams p) {
     using H = typename Held<T>::type;
@@ -554,33 +555,38 @@ quant_weight_kernel(int n, int k, const T *w, int64_t w_ld, uint8_t *q, int64_t 
         quant_block<T, VEC, false>(n, k, w, w_ld, q, q_ld, scale, scale_ld, sm);
 }
 
+// Threads that hold a row in ni groups, and the places that its groups but the last cover (one group: all of it).
+int threads_of(int d, int ni) { return (((d + 7) / 8 + ni - 1) / ni + 31) / 32 * 32; }
+int inner_end(int ni, int threads) { return (ni == 1 ? threads : (ni - 1) * threads) * 8; }
+
 template <typename T, int NI, int MAXT>
 cudaError_t launch_norm(const NormParams &p, bool vec, int threads, cudaStream_t s) {
     // rows of one warp: four to a block
     const int rows = threads == 32 && p.n > 4 ? 4 : 1;
     const dim3 grid((unsigned)((p.n + rows - 1) / rows)), block(threads, rows);
-    if (vec && p.d >= (NI == 1 ? threads : (NI - 1) * threads) * 8)
-        return launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT, true>, grid, block, 0, s, p);
-    if constexpr (MAXT > 256)                            // up to 256: aligned rows alone
-        if (!vec) return launch_pdl(rmsnorm_quant_kernel<T, NI, false, MAXT, false>, grid, block, 0, s, p);
-    return launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT, false>, grid, block, 0, s, p);
+    const bool inner = p.d >= inner_end(NI, threads);
+    if (vec && inner) return launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT, true>, grid, block, 0, s, p);
+    if (vec) return launch_pdl(rmsnorm_quant_kernel<T, NI, true, MAXT, false>, grid, block, 0, s, p);
+    if (inner) return launch_pdl(rmsnorm_quant_kernel<T, NI, false, MAXT, true>, grid, block, 0, s, p);
+    return launch_pdl(rmsnorm_quant_kernel<T, NI, false, MAXT, false>, grid, block, 0, s, p);
 }
 
 // Threads per row.  Few rows: one group of 8 values in each thread, the shortest chain (a row of 4096
-// bf16 values in 2.6 us).  Many rows: as few warps as hold the row in 2 groups of each thread, 4 for
-// aligned bf16 rows, which are half as wide (4096 x 4096: 25.5 us; 26.8 with 2 groups, 33.5 with 8; 16384 x
-// 7168: 131, 195, 170, before INNER; 16384 x 1024 floats: 38 with 2, 42 with 4; 3000 unaligned rows of 1541: 14 with
-// 2, 21 with 4).
+// bf16 values in 2.4 us).  Many rows: as few warps as hold the row in 2 groups of each thread, 4 for
+// bf16 rows, which are half as wide (4096 x 4096: 25.5 us; 26.8 with 2 groups, 33.5 with 8; 16384 x
+// 7168: 131, 195, 170, before INNER; 16384 x 1024 floats: 38 with 2, 42 with 4; 4096 unaligned rows of 4101: 32.6
+// with 4, 37 with 2), unaligned ones where that leaves the groups but the last whole (8000 rows of 515: 14.4 with
+// 2, 18.5 with 4).
 template <typename T>
 cudaError_t launch_norm_t(const NormParams &p, bool vec, cudaStream_t s) {
-    const int most = sizeof(T) == 2 && vec ? 4 : 2, groups = (p.d + 7) / 8;
+    const int most = sizeof(T) == 2 ? 4 : 2, groups = (p.d + 7) / 8;
     int ni = 1;
-    while (ni < most && groups > (p.n >= 512 ? 32 : 1024) * ni) ni *= 2;
+    while (ni < most && groups > (p.n >= 512 ? 32 : 1024) * ni && (vec || p.d >= inner_end(2 * ni, threads_of(p.d, 2 * ni)))) ni *= 2;
     while (groups > 1024 * ni) ni *= 2;                  // d = 32768 is 4 groups in each of 1024 threads
-    const int threads = ((groups + ni - 1) / ni + 31) / 32 * 32;
+    const int threads = threads_of(p.d, ni);
     if (ni == 1) return launch_norm<T, 1, 1024>(p, vec, threads, s);
     if (ni == 2) return launch_norm<T, 2, 1024>(p, vec, threads, s);
-    if constexpr (sizeof(T) == 2)                        // aligned rows: others have 4 groups from d = 16385 on
+    if constexpr (sizeof(T) == 2)                        // floats have 4 groups from d = 16385 on
         if (threads <= 256) return launch_norm<T, 4, 256>(p, vec, threads, s);
     return launch_norm<T, 4, 1024>(p, vec, threads, s);
 }

@@ -70,7 +70,7 @@ def test_norm_matches_the_definition_bit_for_bit(dtype, n, d, residual, gain):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("n,d", [(512, 4096), (600, 4104), (513, 1024), (521, 256), (700, 100), (515, 8192), (512, 7168),
-                                 (530, 1541), (512, 16392)])
+                                 (530, 1541), (512, 16392), (512, 5001), (900, 515), (600, 1285), (512, 16391)])
 def test_norm_of_many_rows_bit_for_bit(dtype, n, d):
     # the forms for many rows: rows that fill their threads and rows that do not, several rows to a block
     g = gen(7 * n + d)

@@ -212,6 +212,22 @@ def test_product_of_whole_numbers_is_exact(m, ns, k, dtype):
         assert (f[m] == 7).all() and (f[:, n:] == 7).all()
 
 
+@pytest.mark.parametrize("m,ns,k,pad,off", [(700, [1000, 258], 8192, 6, 0), (701, [1000], 8192, 6, 2), (2050, [384], 640, 0, 0),
+                                            (2050, [386, 385], 640, 4, 2), (999, [514], 512, 5, 1), (3001, [2], 256, 2, 0)])
+def test_bfloat16_outputs_at_even_and_odd_places(m, ns, k, pad, off):
+    """Outputs inside wider matrices at even and odd places and pitches: rounded once, nothing beside them."""
+    g = gen(m + k + pad)
+    q, scale = whole(g, m, k, 1)
+    ws = [whole(g, n, k, 128) for n in ns]
+    full = [torch.full((m + 1, n + pad + off), 7.0, dtype=torch.bfloat16, device="cuda") for n in ns]
+    out = [f[:m, off:off + n] for f, n in zip(full, ns)]
+    fp8.Linear([fp8.Fp8Weight(*w) for w in ws])(q, scale, out)
+    a = ref.values(q.view(torch.uint8), scale, 1)
+    for (wq, wsc), o, f, n in zip(ws, out, full, ns):
+        assert torch.equal(o, (a @ ref.values(wq.view(torch.uint8), wsc, 128).T).float().bfloat16())
+        assert (f[m] == 7).all() and (f[:, :off] == 7).all() and (f[:, off + n:] == 7).all()
+
+
 @pytest.mark.parametrize("m,ns,k", [(1, [1024, 256], 4096), (3, [200], 8192), (33, [1024], 1541), (200, [640], 4096),
                                     (700, [1000], 8192), (2100, [384], 7168), (2, [256], 32768),
                                     (900, [2048], 12000)])

@@ -21,6 +21,7 @@ DS4C_ERR_DEVICE = 6
 DS4C_ERR_WORKSPACE = 7
 DS4C_F32 = 0
 DS4C_BF16 = 1
+DS4C_WAITS_QUANT_MATMUL = 0
 
 EXPORTS = (
     "ds4c_workspace_bytes", "ds4c_state_init", "ds4c_compress_prefill", "ds4c_compress_decode_step",
@@ -28,7 +29,7 @@ EXPORTS = (
     "ds4c_sync_status", "ds4c_status_string", "ds4c_last_cuda_error", "ds4c_attn_uses_tensor_cores",
     "ds4c_indexer_topk_noalloc", "ds4c_checkpoint_scatter", "ds4c_payload_header", "ds4c_fma_probe",
     "ds4c_payload_bytes", "ds4c_payload_write", "ds4c_payload_read", "ds4c_compress_prefill_timed",
-    "ds4c_indexer_topk_heads", "ds4c_test_set_wait_limit", "ds4c_test_wait_timeout",
+    "ds4c_indexer_topk_heads", "ds4c_test_set_wait_limit", "ds4c_test_wait_timeout", "ds4c_test_warp_wait",
     "ds4c_quant_row_bytes", "ds4c_quant_scale_bytes", "ds4c_rmsnorm_quant", "ds4c_quant_weight", "ds4c_quant_matmul",
     "ds4c_compress_prefill_quant", "ds4c_compress_decode_step_quant",
 )
@@ -134,6 +135,7 @@ def lib() -> C.CDLL:
         "ds4c_fma_probe": (st, [U32, U32, P, C.POINTER(C.c_double), P]),
         "ds4c_test_set_wait_limit": (st, [U64]),
         "ds4c_test_wait_timeout": (st, [U64, P]),
+        "ds4c_test_warp_wait": (st, [U32, P, P]),
         "ds4c_sync_status": (st, [P]),
         "ds4c_status_string": (C.c_char_p, [C.c_int]),
         "ds4c_last_cuda_error": (C.c_char_p, []),
@@ -312,6 +314,10 @@ def ds4c_test_set_wait_limit(limit_ns):
 
 def ds4c_test_wait_timeout(limit_ns, stream):
     return lib().ds4c_test_wait_timeout(limit_ns, stream)
+
+
+def ds4c_test_warp_wait(kernels, answers, stream):
+    return lib().ds4c_test_warp_wait(kernels, answers, stream)
 
 
 def ds4c_sync_status(stream):

@@ -794,6 +794,13 @@ ds4c_status ds4c_test_wait_timeout(uint64_t limit_ns, cudaStream_t stream) {
     return cuda_status(launch_wait_selftest(limit_ns, stream));
 }
 
+ds4c_status ds4c_test_warp_wait(uint32_t kernels, int32_t *answers, cudaStream_t stream) {
+    if (!answers) return DS4C_ERR_NULL;
+    if (!aligned4(answers)) return DS4C_ERR_SHAPE;
+    if (kernels == DS4C_WAITS_QUANT_MATMUL) return cuda_status(qmm_wait_selftest(answers, stream));
+    return DS4C_ERR_UNSUPPORTED;
+}
+
 ds4c_status ds4c_sync_status(cudaStream_t stream) {
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_status(e);

@@ -51,6 +51,9 @@ cudaError_t qmm_set_wait_ns(unsigned long long ns);
 // the indexer kernels' wait routine: it gives up, raises the indexer's error word
 // and returns (the self-test of the error path; no fault, no hang).
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
+// One warp whose lanes look at different mbarriers, with the warp-wide wait routine of the named kernels
+// (ds4c_test_warp_wait).
+cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s);
 
 // FP32 FMA-rate probe (the ALU roofline's denominator): flops of one launch
 // of `blocks` 256-thread CTAs running `iters` rounds, and the launch itself.

@@ -105,3 +105,9 @@ def test_compress_refusals():
         for name in ("wkv", "wkv_scale", "wgate", "wgate_scale", "ape"):
             assert call(aw=weights(**{name: None})) == abi.DS4C_ERR_NULL, name
             assert call(iw=weights(**{name: FAKE + 2})) == abi.DS4C_ERR_SHAPE, name
+
+
+def test_warp_wait_refusals():
+    assert abi.ds4c_test_warp_wait(abi.DS4C_WAITS_QUANT_MATMUL, None, None) == abi.DS4C_ERR_NULL
+    assert abi.ds4c_test_warp_wait(abi.DS4C_WAITS_QUANT_MATMUL, FAKE + 2, None) == abi.DS4C_ERR_SHAPE
+    assert abi.ds4c_test_warp_wait(99, FAKE, None) == abi.DS4C_ERR_UNSUPPORTED

@@ -115,6 +115,10 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// Counts `bytes` as if a copy had brought them.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -272,6 +276,9 @@ __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();
 }
+__device__ __forceinline__ void cluster_st(uint32_t addr, uint32_t rank, uint32_t v) {
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(mapa(addr, rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_st4(uint32_t addr, uint32_t rank, float a, float b, float c, float d) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mapa(addr, rank)), "f"(a), "f"(b), "f"(c), "f"(d)
                  : "memory");
@@ -398,13 +405,13 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 
     // warps 0 and 1 run converged and one elected lane issues, so that what the copies and MMAs take lies
     // in uniform registers
+    uint32_t filled = 0;                             // warp 0's: stages it filled
     if (warp == 0) {
-        bool ok = true;
         uint32_t it = 0, s = 0, par = 1;
         const uint32_t base = smem_u32(smem);
         const CUtensorMap *mw = &maps.w[g];
         for (int kb = kb0; kb < kb1; kb++, it++) {
-            if (!warp_wait(smem_u32(&empty[s]), par, abort)) { ok = false; break; }
+            if (!warp_wait(smem_u32(&empty[s]), par, abort)) break;
             const uint32_t bar = smem_u32(&full[s]), dst = base + s * S::STAGE_BYTES;
             if (elect()) {
                 mbar_expect_tx(bar, S::STAGE_BYTES);
@@ -414,10 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
             __syncwarp();
             if (++s == S::STAGES) s = 0, par ^= 1;
         }
-        // after a give-up: the loads still in flight (the last STAGES issued) land before the CTA exits
-        if (!ok)
-            for (uint32_t u = it > (uint32_t)S::STAGES ? it - S::STAGES : 0; u < it; u++)
-                mbar_drain(smem_u32(&full[u % S::STAGES]), (u / S::STAGES) & 1);
+        filled = it;
         __syncwarp();
     } else if (warp == 1) {
         uint32_t s = 0, s_par = 0, sl = 0, accumulate = 0;
@@ -565,6 +569,10 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
         }
     }
     __syncthreads();
+    // after a give-up of any warp the MMAs may not have waited for every load: the last STAGES land before the CTA exits
+    if (warp == 0 && *abort)
+        for (uint32_t u = filled > (uint32_t)S::STAGES ? filled - S::STAGES : 0; u < filled; u++)
+            mbar_drain(smem_u32(&full[u % S::STAGES]), (u / S::STAGES) & 1);
     if (warp == 1) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TMEM_COLS) : "memory");
@@ -586,12 +594,13 @@ __global__ void __launch_bounds__(THREADS, 1) qmm_split_kernel(const __grid_cons
 constexpr int PAIR_THREADS = 512, MAX_BT = 224;
 // registers per thread of the epilogue's two warpgroups and of the other two (setmaxnreg), out of 128 at launch
 constexpr int REG_EPILOGUE = 168, REG_OTHER = 80;
+constexpr uint32_t NOT_ISSUED = ~0u;
 constexpr int PAIR_STAGES = 8, PAIR_RING = 216 * 1024;       // most stages, bytes of the ring
 struct Pair {
     static constexpr int W_BYTES = BW * BK;
     static constexpr int SF_COLS = 12, WORDS = MAX_BT / 32;      // TMEM columns of a slot, row words of a lane
     static constexpr int N_BARS = 2 * PAIR_STAGES + 2 * SF_SLOTS + 5;
-    static constexpr int SMEM_BYTES = PAIR_RING + 8 * N_BARS + 16 + 1024;
+    static constexpr int SMEM_BYTES = PAIR_RING + 8 * N_BARS + 16 + 1024;      // 16: TMEM address, abort, issued[2]
     static constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(2 * BW >> 7) << 27);       // M = 256, N added
     static constexpr int HALF_CHUNKS = MAX_BT / 2 / 16;
     static_assert(2 * MAX_BT + SF_SLOTS * SF_COLS <= 512, "TMEM columns");
@@ -636,6 +645,34 @@ __device__ __forceinline__ void store_scales(uint32_t taddr, const ScaleWords &s
 }
 static_assert(Pair::WORDS == 7, "columns of store_scales");
 
+// The pair's loads land before it exits where the leader's MMAs gave up (else they have waited for every load).  Both
+// CTAs' loads complete on the leader's barriers, so its MMA warp waits for both: issued[r] says how many stages CTA r
+// filled, and a stage that only one filled gets the other's part of its count here.
+__device__ __forceinline__ void pair_drain(uint32_t full, volatile uint32_t *issued, uint32_t stages, uint32_t block, int kb,
+                                           bool joint) {
+    // the loading warps' waits are bounded too, so that the counts come
+    const uint64_t t0 = globaltimer();
+    while ((issued[0] == NOT_ISSUED || issued[1] == NOT_ISSUED) && globaltimer() - t0 <= 2 * kDrainNs) {}
+    __syncwarp();
+    uint32_t n0 = __shfl_sync(0xffffffffu, issued[0], 0), n1 = __shfl_sync(0xffffffffu, issued[1], 0);
+    if (n0 == NOT_ISSUED) n0 = n1;                   // only where the wait limit was set beyond this one's
+    if (n1 == NOT_ISSUED) n1 = n0;
+    if (n0 == NOT_ISSUED) return;
+    const uint32_t n = max(n0, n1), per_tile = joint ? (kb + 1) / 2 : kb;
+    for (uint32_t u = n > stages ? n - stages : 0; u < n; u++) {
+        const uint32_t bar = full + 8 * (u % stages);
+        // what one CTA brings: a stage of two blocks of K but at the end of an odd number of them
+        const uint32_t bytes = joint && !(kb % 2 == 1 && u % per_tile == per_tile - 1) ? 2 * block : block;
+        if (elect()) {
+            if (u >= n0) mbar_expect_tx(bar, bytes);
+            else if (u >= n1) mbar_complete_tx(bar, bytes);
+        }
+        __syncwarp();
+        mbar_drain(bar, (u / stages) & 1);
+        __syncwarp();
+    }
+}
+
 template <bool joint>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
@@ -647,6 +684,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile uint32_t *issued = tmem_slot + 2;       // the leader's: stages that each CTA filled, once that is known
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = (int)blockIdx.x & 1, pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
     const int total = p.tile_start[p.n_w], chunks = (p.kb + CHUNK - 1) / CHUNK;
@@ -672,6 +710,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
         }
         mbar_init(smem_u32(drain), 1);
         *abort = 0;
+        issued[0] = issued[1] = NOT_ISSUED;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -716,17 +755,7 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
                 if (++s == stages) s = 0, par ^= 1;
             }
         }
-        // after a give-up the pair's loads still in flight land before it exits: the leader sees them
-        // on its barriers, the other CTA has none and waits a time no load takes
-        if (!ok) {
-            if (rank == 0) {
-                for (uint32_t u = it > stages ? it - stages : 0; u < it; u++)
-                    mbar_drain(smem_u32(&full[u % stages]), (u / stages) & 1);
-            } else {
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 2000000ull) {}
-            }
-        }
+        if (elect()) cluster_st(smem_u32(tmem_slot + 2 + rank), 0, it);
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -795,6 +824,8 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
             if (elect()) mma_commit_pair(smem_u32(drain));
             __syncwarp();
             mbar_drain(smem_u32(drain), 0);
+            __syncwarp();
+            if (!ok) pair_drain(smem_u32(full), issued, stages, block, p.kb, joint);
         }
         __syncwarp();
     }

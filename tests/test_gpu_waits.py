@@ -4,7 +4,8 @@ warp one answer, raises the device error word and leaves the context usable."""
 import pytest
 import torch
 
-from compressed_kv_sparse_compressor_gb300 import abi
+import quant_ref as ref
+from compressed_kv_sparse_compressor_gb300 import abi, fp8
 from gpu_util import require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,31 @@ def test_lanes_that_see_different_things_get_one_answer(kernels):
         assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
     assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
     assert answers.tolist() == [0] * 64 + [1] * 32
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 2560, 4096), (40, 512, 20000), (200, 1024, 4096), (300, 4096, 4096),
+                                   (1500, 4096, 2176), (4096, 2560, 4096)])
+def test_product_whose_waits_give_up(m, n, k):
+    """The product in each of its forms with a limit of a few nanoseconds: its waits give up or not, as the copies
+    come.  Either way it ends with nothing in flight, and with the default limit the same call is right."""
+    g = torch.Generator(device="cuda").manual_seed(m + k)
+    q, scale = fp8.empty(m, k)
+    w = fp8.Fp8Weight(*fp8.empty(n, k, "cuda", 128))
+    for codes, scales in ((q, scale), (w.q, w.scale)):
+        codes.copy_(torch.randint(-2, 3, codes.shape, generator=g, device="cuda").float().to(torch.float8_e4m3fn))
+        scales.copy_(torch.randint(126, 129, scales.shape, generator=g, device="cuda"))
+    lin = fp8.Linear([w])
+    want = (ref.values(q.view(torch.uint8), scale, 1) @ ref.values(w.q.view(torch.uint8), w.scale, 128).T).float()
+    assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
+    out = [torch.empty(m, n, device="cuda")]
+    assert abi.ds4c_test_set_wait_limit(1) == abi.DS4C_OK
+    try:
+        for _ in range(3):
+            lin(q, scale, out)
+            assert abi.ds4c_sync_status(stream()) in (abi.DS4C_OK, abi.DS4C_ERR_DEVICE)
+    finally:
+        assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
+    out[0].fill_(float("nan"))
+    lin(q, scale, out)
+    assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
+    assert torch.equal(out[0], want)

@@ -930,6 +930,9 @@ qmm_pair_kernel(const __grid_constant__ Maps maps, const Params p, int bt) {
     __syncthreads();
     cluster_sync();                                  // the partner's arrivals and MMAs have this CTA's memory until here
     if (warp == 1) {
+        // the leader has seen its last commit; that arrives in this CTA's memory too, after all others
+        mbar_drain(smem_u32(drain), 0);
+        __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }

@@ -63,3 +63,20 @@ def test_product_whose_waits_give_up(m, n, k):
     lin(q, scale, out)
     assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
     assert torch.equal(out[0], want)
+
+
+def test_products_right_behind_one_another():
+    """Pairs of CTAs and single ones take turns on the same SMs with nothing in between: what one leaves behind in
+    shared memory (an arrival of its last commits) would meet the barriers of the next."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k = 640
+    w = fp8.Linear([fp8.quantize_weight(torch.randint(-2, 3, (1024, k), generator=g, device="cuda").float())])
+    rows = [fp8.rmsnorm(torch.randn(m, k, generator=g, device="cuda")) for m in (2000, 40, 1999, 1)]
+    want = []
+    for q, scale in rows:
+        want.append(w(q, scale)[0])
+        torch.cuda.synchronize()
+    outs = [[w(q, scale)[0] for q, scale in rows] for _ in range(100)]
+    assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
+    for got in outs:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

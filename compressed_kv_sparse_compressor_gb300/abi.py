@@ -22,6 +22,7 @@ DS4C_ERR_WORKSPACE = 7
 DS4C_F32 = 0
 DS4C_BF16 = 1
 DS4C_WAITS_QUANT_MATMUL = 0
+DS4C_WAITS_GEMM = 1
 
 EXPORTS = (
     "ds4c_workspace_bytes", "ds4c_state_init", "ds4c_compress_prefill", "ds4c_compress_decode_step",

@@ -53,6 +53,7 @@ cudaError_t qmm_set_wait_ns(unsigned long long ns);
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
 // One warp whose lanes look at different mbarriers, with the warp-wide wait routine of the named kernels
 // (ds4c_test_warp_wait).
+cudaError_t gemm_tc_wait_selftest(int *answers, cudaStream_t s);
 cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s);
 
 // FP32 FMA-rate probe (the ALU roofline's denominator): flops of one launch

@@ -122,6 +122,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The same by a whole warp, with one answer for all of it: what follows (a TMEM load) is the whole warp's.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
 // flight after a give-up, before the CTA frees its TMEM and exits.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
@@ -338,7 +343,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             tile_coords(p, tile, g, mt, nt, ks, nsplit);
             const int acc = local & 1;
             const uint32_t aph = (local >> 1) & 1;
-            if (!mbar_wait(smem_u32(&acc_full[acc]), aph, abort)) break;
+            if (!warp_wait(smem_u32(&acc_full[acc]), aph, abort)) break;
             fence_after();
             if (p.tail_split > 1 && tile >= p.full_units) {
                 // a tail partial: the whole dense [BM][BN] block, bounds applied by the reduce
@@ -570,6 +575,26 @@ cudaError_t launch_bn(const GemmArgs &a, cudaStream_t s) {
                       (const float *)a.part, n4, p.part_stride, ksplit);
 }
 
+// Self-test of warp_wait: the even lanes at a barrier whose phase is complete, the odd ones at one that nothing arrives
+// on, twice; then all at the complete one.  answers[32 i + lane]: what each lane got.
+__global__ void wait_selftest_kernel(int *answers) {
+    __shared__ uint64_t bars[2];
+    __shared__ int abort;
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        mbar_init(smem_u32(&bars[0]), 1);
+        mbar_init(smem_u32(&bars[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_arrive(smem_u32(&bars[0]));
+    }
+    for (int i = 0; i < 3; i++) {
+        if (lane == 0) abort = 0;
+        __syncthreads();
+        answers[32 * i + lane] = warp_wait(smem_u32(&bars[i < 2 ? lane & 1 : 0]), 0, &abort);
+        __syncthreads();
+    }
+}
+
 }  // namespace
 
 size_t gemm_tail_floats() { return (size_t)sm_count() * BM * 256; }
@@ -583,6 +608,11 @@ cudaError_t launch_gemm_tc(const GemmArgs &a, cudaStream_t s) {
     // byte) over thin stages, split along K to cover the SMs
     if (a.M <= 32) return launch_bn<128, 32>(a, s);
     return a.M <= 256 ? launch_bn<32, BM>(a, s) : launch_bn<256, BM>(a, s);
+}
+
+cudaError_t gemm_tc_wait_selftest(int *answers, cudaStream_t s) {
+    wait_selftest_kernel<<<1, 32, 0, s>>>(answers);
+    return cudaGetLastError();
 }
 
 cudaError_t gemm_tc_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_gemm_wait_ns, &ns, sizeof ns); }

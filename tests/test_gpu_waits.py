@@ -22,7 +22,7 @@ def stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-@pytest.mark.parametrize("kernels", [abi.DS4C_WAITS_QUANT_MATMUL])
+@pytest.mark.parametrize("kernels", [abi.DS4C_WAITS_QUANT_MATMUL, abi.DS4C_WAITS_GEMM])
 def test_lanes_that_see_different_things_get_one_answer(kernels):
     """Half of the lanes find their barrier complete, the others' wait runs out: no lane may go on alone."""
     answers = torch.full((96,), -7, dtype=torch.int32, device="cuda")

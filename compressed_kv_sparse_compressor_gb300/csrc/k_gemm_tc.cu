@@ -294,10 +294,10 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
                     tma_load_2d(smem_u32(sb), mb, kb * BK, nt * BN, bar);
                 }
             }
-            // after a give-up: the loads still in flight (the last STAGES issued) land before the CTA exits
-            if (!ok)
-                for (uint32_t u = it > (uint32_t)STAGES ? it - STAGES : 0; u < it; u++)
-                    mbar_drain(smem_u32(&full[u % STAGES]), (u / STAGES) & 1);
+            // the loads still in flight (the last STAGES issued) land before the CTA exits, whichever role gave
+            // up: the MMAs may not have waited for them
+            for (uint32_t u = it > (uint32_t)STAGES ? it - STAGES : 0; u < it; u++)
+                mbar_drain(smem_u32(&full[u % STAGES]), (u / STAGES) & 1);
         }
     } else if (warp == 1) {
         if (lane == 0) {

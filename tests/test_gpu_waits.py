@@ -5,8 +5,8 @@ import pytest
 import torch
 
 import quant_ref as ref
-from compressed_kv_sparse_compressor_gb300 import abi, fp8
-from gpu_util import require_gpu
+from compressed_kv_sparse_compressor_gb300 import abi, configs, fp8
+from gpu_util import device_layer, require_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,27 @@ def test_products_right_behind_one_another():
     assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
     for got in outs:
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [1, 32, 300, 4096])
+def test_projection_whose_waits_give_up(T):
+    """The bf16 projection under the same limit, prefill chunks and decode-sized ones."""
+    shape = configs.LayerShape(d_model=4096, head_dim=512, n_rot=64, idx_head_dim=128, n_heads=64, ratio=4, top_k=16,
+                               dtype="bf16")
+    dl, _, _ = device_layer(shape, comp_cap=T // 4 + 1, idx_cap=T // 4 + 1, max_rows=T, seed=3)
+    h = configs.hidden(shape, 3, T).cuda()
+    rows = dl.ws[: T * 2560 * 4].view(torch.float32)                    # what the projection wrote
+    dl.compress_prefill(h, 0)
+    dl.sync()
+    want = rows.clone()
+    assert abi.ds4c_test_set_wait_limit(1) == abi.DS4C_OK
+    try:
+        for _ in range(3):
+            dl.compress_prefill(h, 0)
+            assert abi.ds4c_sync_status(stream()) in (abi.DS4C_OK, abi.DS4C_ERR_DEVICE)
+    finally:
+        assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
+    rows.fill_(float("nan"))
+    dl.compress_prefill(h, 0)
+    assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
+    assert torch.equal(rows, want)

@@ -51,10 +51,54 @@ cudaError_t qmm_set_wait_ns(unsigned long long ns);
 // the indexer kernels' wait routine: it gives up, raises the indexer's error word
 // and returns (the self-test of the error path; no fault, no hang).
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
-// One warp whose lanes look at different mbarriers, with the warp-wide wait routine of the named kernels
-// (ds4c_test_warp_wait).
+// One warp that waits with the warp-wide routine of the named kernels (ds4c_test_warp_wait).
 cudaError_t gemm_tc_wait_selftest(int *answers, cudaStream_t s);
 cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s);
+
+// Bounded wait of a whole warp for look() to be true in every lane.  The lanes look together and vote on every look,
+// so that none waits or goes on alone, and all get one answer, whatever each of them saw; what follows a wait (votes,
+// TMEM loads, elections) is the whole warp's.  Every LOOKS looks the time is compared with limit_ns and *abort read;
+// a wait that gives up sets *abort, and the error word if its own limit ran out.
+template <uint32_t LOOKS, typename Look>
+__device__ __forceinline__ bool warp_bounded_wait(Look look, volatile int *abort, const unsigned long long &limit_ns,
+                                                  unsigned int *error) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (__all_sync(0xffffffffu, look())) return true;
+        if (i % LOOKS == LOOKS - 1) {
+            uint64_t now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (t0 == 0) t0 = now;
+            const bool late = now - t0 > limit_ns;
+            if (__any_sync(0xffffffffu, late || *abort)) {
+                *abort = 1;
+                if (late) atomicOr(error, 1u);
+                __syncwarp();
+                return false;
+            }
+        }
+    }
+}
+// Self-test of a unit's waits by one warp (answers of ds4c_test_warp_wait): wait_for(look, abort) with looks that half
+// of the lanes never see true, wait(barrier, phase, abort) at an mbarrier that nothing arrives on and at a complete one.
+template <typename WaitFor, typename Wait>
+__device__ __forceinline__ void warp_wait_selftest(int *answers, WaitFor wait_for, Wait wait) {
+    __shared__ uint64_t bars[2];
+    __shared__ int abort;
+    const uint32_t lane = threadIdx.x % 32, bar = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
+    if (lane == 0) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar + 8) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + 8) : "memory");
+    }
+    for (uint32_t i = 0; i < 3; i++) {
+        if (lane == 0) abort = 0;
+        __syncwarp();
+        answers[32 * i + lane] = i == 0 ? wait_for([lane] { return lane % 2 == 0; }, &abort) : wait(bar + 8 * (i - 1), 0, &abort);
+        __syncwarp();
+    }
+}
 
 // FP32 FMA-rate probe (the ALU roofline's denominator): flops of one launch
 // of `blocks` 256-thread CTAs running `iters` rounds, and the launch itself.

@@ -96,19 +96,23 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait for the completion of the phase with the given parity.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return true;
+        if (mbar_try(bar, parity)) return true;
         if ((i & 255u) == 255u) {
             if (*abort) return false;
             const uint64_t now = globaltimer();
@@ -122,9 +126,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// The same by a whole warp, with one answer for all of it: what follows (a TMEM load) is the whole warp's.
+// The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+    return warp_bounded_wait<256>([=] { return mbar_try(bar, parity); }, abort, g_gemm_wait_ns, &g_gemm_tc_err);
 }
 
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
@@ -132,15 +136,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return;
+        if (mbar_try(bar, parity)) return;
         if ((i & 255u) == 255u) {
             const uint64_t now = globaltimer();
             if (t0 == 0) t0 = now;
@@ -575,24 +571,11 @@ cudaError_t launch_bn(const GemmArgs &a, cudaStream_t s) {
                       (const float *)a.part, n4, p.part_stride, ksplit);
 }
 
-// Self-test of warp_wait: the even lanes at a barrier whose phase is complete, the odd ones at one that nothing arrives
-// on, twice; then all at the complete one.  answers[32 i + lane]: what each lane got.
 __global__ void wait_selftest_kernel(int *answers) {
-    __shared__ uint64_t bars[2];
-    __shared__ int abort;
-    const int lane = threadIdx.x;
-    if (lane == 0) {
-        mbar_init(smem_u32(&bars[0]), 1);
-        mbar_init(smem_u32(&bars[1]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        mbar_arrive(smem_u32(&bars[0]));
-    }
-    for (int i = 0; i < 3; i++) {
-        if (lane == 0) abort = 0;
-        __syncthreads();
-        answers[32 * i + lane] = warp_wait(smem_u32(&bars[i < 2 ? lane & 1 : 0]), 0, &abort);
-        __syncthreads();
-    }
+    warp_wait_selftest(
+        answers,
+        [](auto look, volatile int *abort) { return warp_bounded_wait<256>(look, abort, g_gemm_wait_ns, &g_gemm_tc_err); },
+        [](uint32_t bar, uint32_t parity, volatile int *abort) { return warp_wait(bar, parity, abort); });
 }
 
 }  // namespace

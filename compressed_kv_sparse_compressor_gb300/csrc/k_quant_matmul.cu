@@ -134,32 +134,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity);
-// Bounded wait for the completion of the phase with the given parity (CLUSTER: of arrivals
-// from both CTAs of a pair, whose writes it acquires).
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 0;; ++i) {
-        if (CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
-        if ((i & 255u) == 255u) {
-            if (*abort) return false;
-            const uint64_t now = globaltimer();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > g_qmm_wait_ns) {
-                *abort = 1;
-                atomicOr(&g_qmm_err, 1u);
-                return false;
-            }
-        }
-    }
-}
-// The same by a whole warp, with one answer for all of it: the lanes vote on the first look and again on what each
-// got from its own wait, so that no lane goes on while another still waits, whatever each of them saw (1024 x 4096 x
-// 4096: 17.8 us, 17.6 where a lane left on its own first look).
+// Bounded wait of a whole warp for the completion of the phase with the given parity (CLUSTER: of arrivals
+// from both CTAs of a pair, whose writes it acquires).  (A vote on the first
+// look and then each lane for itself: 1024 x 4096 x 4096 17.8 us for 17.2, 32 rows 5.85 for 5.7.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait<CLUSTER>(bar, parity, abort));
+    return warp_bounded_wait<256>([=] { return CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); }, abort,
+                                  g_qmm_wait_ns, &g_qmm_err);
 }
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
 // flight after a give-up, before the CTA frees its TMEM and exits.
@@ -1050,26 +1031,13 @@ int pair_bt(const QuantMatmulArgs &a, int64_t &cost) {
     return best;
 }
 
-// Self-test of warp_wait in both forms: the even lanes look at a barrier whose phase is complete, the odd ones at one
-// that nothing arrives on; then all at the complete one.  answers[32 i + lane]: what each lane got.
 __global__ void wait_selftest_kernel(int *answers) {
-    __shared__ uint64_t bars[2];
-    __shared__ int abort;
-    const int lane = threadIdx.x;
-    if (lane == 0) {
-        mbar_init(smem_u32(&bars[0]), 1);
-        mbar_init(smem_u32(&bars[1]), 1);
-        abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        mbar_arrive(smem_u32(&bars[0]));
-    }
-    __syncthreads();
-    answers[lane] = warp_wait(smem_u32(&bars[lane & 1]), 0, &abort);
-    __syncthreads();
-    if (lane == 0) abort = 0;
-    __syncthreads();
-    answers[32 + lane] = warp_wait<true>(smem_u32(&bars[lane & 1]), 0, &abort);
-    answers[64 + lane] = warp_wait(smem_u32(&bars[0]), 0, &abort);
+    warp_wait_selftest(
+        answers,
+        [](auto look, volatile int *abort) { return warp_bounded_wait<256>(look, abort, g_qmm_wait_ns, &g_qmm_err); },
+        [](uint32_t bar, uint32_t parity, volatile int *abort) {
+            return warp_wait(bar, parity, abort) && warp_wait<true>(bar, parity, abort);
+        });
 }
 
 template <typename F>

@@ -474,11 +474,10 @@ DS4C_API ds4c_status ds4c_fma_probe(uint32_t blocks, uint32_t iters, float *out,
  * error word (no fault, no hang).
  * ds4c_test_warp_wait launches one warp that waits three times with the warp-wide
  * routine of the named kernels, under the limit that ds4c_test_set_wait_limit set,
- * and writes what each lane got to answers (96 device ints): first and second, in
- * the CTA's and the cluster's form where the kernels have both, with the even lanes
- * at an mbarrier whose phase is complete and the odd ones at one that nothing
- * arrives on (0 for every lane, and the kernels' error word is raised); third with
- * all lanes at the complete one (1 for every lane). */
+ * and writes what each lane got to answers (96 device ints): first for something
+ * that half of the lanes never see, second at an mbarrier that nothing arrives on
+ * (0 for every lane, and the kernels' error word is raised), third at one whose
+ * phase is complete (1 for every lane). */
 enum { DS4C_WAITS_QUANT_MATMUL = 0, DS4C_WAITS_GEMM = 1 };
 DS4C_API ds4c_status ds4c_test_set_wait_limit(uint64_t limit_ns);
 DS4C_API ds4c_status ds4c_test_wait_timeout(uint64_t limit_ns, cudaStream_t stream);

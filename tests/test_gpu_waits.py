@@ -24,7 +24,8 @@ def stream():
 
 @pytest.mark.parametrize("kernels", [abi.DS4C_WAITS_QUANT_MATMUL, abi.DS4C_WAITS_GEMM])
 def test_lanes_that_see_different_things_get_one_answer(kernels):
-    """Half of the lanes find their barrier complete, the others' wait runs out: no lane may go on alone."""
+    """Half of the lanes see what they wait for, the others never do: no lane may go on alone.  Then a barrier that
+    nothing arrives on, and a complete one."""
     answers = torch.full((96,), -7, dtype=torch.int32, device="cuda")
     assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
     assert abi.ds4c_test_set_wait_limit(20000) == abi.DS4C_OK                  # 20 us

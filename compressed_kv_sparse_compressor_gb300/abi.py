@@ -23,6 +23,7 @@ DS4C_F32 = 0
 DS4C_BF16 = 1
 DS4C_WAITS_QUANT_MATMUL = 0
 DS4C_WAITS_GEMM = 1
+DS4C_WAITS_ATTENTION = 2
 
 EXPORTS = (
     "ds4c_workspace_bytes", "ds4c_state_init", "ds4c_compress_prefill", "ds4c_compress_decode_step",

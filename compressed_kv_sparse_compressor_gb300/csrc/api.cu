@@ -799,6 +799,7 @@ ds4c_status ds4c_test_warp_wait(uint32_t kernels, int32_t *answers, cudaStream_t
     if (!aligned4(answers)) return DS4C_ERR_SHAPE;
     if (kernels == DS4C_WAITS_QUANT_MATMUL) return cuda_status(qmm_wait_selftest(answers, stream));
     if (kernels == DS4C_WAITS_GEMM) return cuda_status(gemm_tc_wait_selftest(answers, stream));
+    if (kernels == DS4C_WAITS_ATTENTION) return cuda_status(attn_tc_wait_selftest(answers, stream));
     return DS4C_ERR_UNSUPPORTED;
 }
 

@@ -53,6 +53,7 @@ cudaError_t qmm_set_wait_ns(unsigned long long ns);
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
 // One warp that waits with the warp-wide routine of the named kernels (ds4c_test_warp_wait).
 cudaError_t gemm_tc_wait_selftest(int *answers, cudaStream_t s);
+cudaError_t attn_tc_wait_selftest(int *answers, cudaStream_t s);
 cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s);
 
 // Bounded wait of a whole warp for look() to be true in every lane.  The lanes look together and vote on every look,

@@ -159,31 +159,25 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Each poll may suspend the thread for up to 1 us (woken when the phase completes), so a waiting
-// warp does not keep issuing beside the MMA warp; the time is checked every 16 polls.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 0;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(1000u)
-            : "memory");
-        if (ok) return true;
-        if ((i & 15u) == 15u) {
-            if (*abort) return false;
-            const uint64_t now = globaltimer();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > g_attn_wait_ns) {
-                *abort = 1;
-                atomicOr(&g_attn_tc_err, 1u);
-                return false;
-            }
-        }
-    }
+// One look at a phase.  It may suspend the thread for up to 1 us (woken when the phase completes), so a waiting
+// warp does not keep issuing beside the MMA warp.  All lanes of a warp look together and at one barrier: a lane
+// that looks alone while the others wait for it wakes late (46 ms of attention became 72).
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait of a whole warp for the completion of the phase with the given parity.  (Each lane for itself, one lane
+// for its warp in the producers: attention of a 131072-token prefill 46.2 ms for 42.9.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return warp_bounded_wait<16>([=] { return mbar_try(bar, parity); }, abort, g_attn_wait_ns, &g_attn_tc_err);
 }
 
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
@@ -561,7 +555,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
         bool ok = true;
         auto pair_bar = [&]() -> bool {
             mbar_arrive(bar(B_PBAR));
-            const bool r_ = mbar_wait(bar(B_PBAR), pphase, abort);
+            const bool r_ = warp_wait(bar(B_PBAR), pphase, abort);
             pphase ^= 1;
             return r_;
         };
@@ -576,11 +570,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
             if (itm.tb >= itm.te) continue;
             // this item's split query (buffer tok & 1 of this CTA) has been written
             const int qbuf = tok & 1;
-            if (pw == 0) {
-                int okq = 1;
-                if (lane == 0) okq = mbar_wait(bar(B_QREADY0 + qbuf), (tok >> 1) & 1, abort) ? 1 : 0;
-                if (__shfl_sync(0xffffffffu, okq, 0) == 0) { ok = false; break; }
-            }
+            if (pw == 0 && !warp_wait(bar(B_QREADY0 + qbuf), (tok >> 1) & 1, abort)) { ok = false; break; }
             tok++;
             const int qrow0 = (p.qpre ? it / p.parts : blockIdx.x * 2 + qbuf) * Lay::DC * 2 * H;
             const int dummy = k.seq * p.comp_cap;
@@ -632,9 +622,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
                 const int s_ = unit % RING;
                 const uint32_t ph = (unit / RING) & 1;
                 unit++;
-                int okw = 1;
-                if (lane == 0) okw = mbar_wait(bar(B_EMPTY + s_), ph ^ 1, abort) ? 1 : 0;
-                if (__shfl_sync(0xffffffffu, okw, 0) == 0) {
+                if (!warp_wait(bar(B_EMPTY + s_), ph ^ 1, abort)) {
                     unit--;                                  // nothing was issued for this slot
                     return false;
                 }
@@ -763,9 +751,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
         bool ok = true;
         // The whole warp runs the issue loop (its operands stay warp-uniform); lane 0 issues.
         const uint32_t leader = lane == 0;
-        auto wait_all = [&](uint32_t b, uint32_t parity) -> bool {
-            return __all_sync(0xffffffffu, mbar_wait(b, parity, abort)) != 0;
-        };
+        auto wait_all = [&](uint32_t b, uint32_t parity) -> bool { return warp_wait(b, parity, abort); };
         // slot u of the ring: wait until loaded / hand back once its MMAs finish
         auto wait_slot = [&](uint32_t u, uint32_t &base) -> bool {
             base = smem_u32(sm + Lay::OFF_X + (u % RING) * USLOT);
@@ -909,7 +895,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
         // barrier of the 128 softmax threads on an mbarrier, so that its wait is bounded
         auto soft_bar = [&]() -> bool {
             mbar_arrive(bar(B_SOFT));
-            const bool r_ = mbar_wait(bar(B_SOFT), sphase, abort);
+            const bool r_ = warp_wait(bar(B_SOFT), sphase, abort);
             sphase ^= 1;
             return r_;
         };
@@ -934,7 +920,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
             if (!soft_bar()) { ok = false; break; }
             for (int i = itm.tb; i < itm.te; i++, g++) {
                 const int sb = g & 1;
-                if (!mbar_wait(bar(B_SFULL0 + sb), (g >> 1) & 1, abort)) { ok = false; break; }
+                if (!warp_wait(bar(B_SFULL0 + sb), (g >> 1) & 1, abort)) { ok = false; break; }
                 fence_after();
                 float s[H];
                 tmem_load_s<H>(lane_base + Lay::T_S + sb * 2 * H, s);
@@ -980,7 +966,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
                     lacc0 *= alpha_s[2 * lane];
                     lacc1 *= alpha_s[2 * lane + 1];
                     if (i > itm.tb) {
-                        if (!mbar_wait(bar(B_PVDONE), (g - 1) & 1, abort)) { ok = false; break; }
+                        if (!warp_wait(bar(B_PVDONE), (g - 1) & 1, abort)) { ok = false; break; }
                         waited = true;
                         fence_after();
                         float v[H];
@@ -996,7 +982,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
                 // the P buffers are free once the previous tile's O (of this item or the
                 // previous one) has been computed
                 if (g > 0 && !waited) {
-                    if (!mbar_wait(bar(B_PVDONE), (g - 1) & 1, abort)) { ok = false; break; }
+                    if (!warp_wait(bar(B_PVDONE), (g - 1) & 1, abort)) { ok = false; break; }
                 }
                 // P^T row r (MN-major, 128-byte swizzle), hi and lo
 #pragma unroll
@@ -1026,7 +1012,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
                     // with this tile's rescale factors there).  The denominator words still hold
                     // the previous item's L until its epilogue has read them (which precedes its
                     // first output-free arrival).
-                    if (tok > 0 && !mbar_wait(bar(B_OFREE0), (tok - 1) & 1, abort)) { ok = false; break; }
+                    if (tok > 0 && !warp_wait(bar(B_OFREE0), (tok - 1) & 1, abort)) { ok = false; break; }
                     if (!soft_bar()) { ok = false; break; }
                     float *lb = reinterpret_cast<float *>(tmax);
                     if (q4 == 0) { lfin[2 * lane] = lacc0; lfin[2 * lane + 1] = lacc1; }
@@ -1111,12 +1097,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
             // previous one) has had all its query chunks read
             if (nx < n_items) {
                 const int nb = (tok + 1) & 1;
-                if (tok >= 1 && !mbar_wait(bar(B_QFREE0 + nb), ((tok - 1) >> 1) & 1, abort)) { ok = false; break; }
+                if (tok >= 1 && !warp_wait(bar(B_QFREE0 + nb), ((tok - 1) >> 1) & 1, abort)) { ok = false; break; }
                 prepare(nx, nb);
             }
             // this item's output once its last O and its denominators are complete
-            if (!mbar_wait(bar(B_LREADY), tok & 1, abort)) { ok = false; break; }
-            if (!mbar_wait(bar(B_PVDONE), (g + nt - 1) & 1, abort)) { ok = false; break; }
+            if (!warp_wait(bar(B_LREADY), tok & 1, abort)) { ok = false; break; }
+            if (!warp_wait(bar(B_PVDONE), (g + nt - 1) & 1, abort)) { ok = false; break; }
             fence_after();
             // whole query: out[n][h][d] = O / L; split rows: the unnormalised partial part_o[it][h][d]
             const bool whole = p.parts == 1;
@@ -1348,6 +1334,13 @@ cudaError_t launch_hd(const AttnTcArgs &a, const TcAttnParams &p, bool commit, c
                       commit ? const_cast<float *>(a.ring) : nullptr, a.raw_new, a.S, p.dp);
 }
 
+__global__ void wait_selftest_kernel(int *answers) {
+    warp_wait_selftest(
+        answers,
+        [](auto look, volatile int *abort) { return warp_bounded_wait<16>(look, abort, g_attn_wait_ns, &g_attn_tc_err); },
+        [](uint32_t bar, uint32_t parity, volatile int *abort) { return warp_wait(bar, parity, abort); });
+}
+
 }  // namespace
 
 size_t attn_tc_qsplit_bytes(int H, int D) {
@@ -1430,6 +1423,11 @@ cudaError_t launch_attention_tc(const AttnTcArgs &a, const DecodePos *dp, cudaSt
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+cudaError_t attn_tc_wait_selftest(int *answers, cudaStream_t s) {
+    wait_selftest_kernel<<<1, 32, 0, s>>>(answers);
+    return cudaGetLastError();
 }
 
 cudaError_t attn_tc_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_attn_wait_ns, &ns, sizeof ns); }

@@ -135,8 +135,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity);
 // Bounded wait of a whole warp for the completion of the phase with the given parity (CLUSTER: of arrivals
-// from both CTAs of a pair, whose writes it acquires).  (A vote on the first
-// look and then each lane for itself: 1024 x 4096 x 4096 17.8 us for 17.2, 32 rows 5.85 for 5.7.)
+// from both CTAs of a pair, whose writes it acquires).  (A vote on the first look and then each lane for itself:
+// 1024 x 4096 x 4096 17.8 us for 17.2, 32 rows 5.85 for 5.7.)
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     return warp_bounded_wait<256>([=] { return CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); }, abort,

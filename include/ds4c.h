@@ -478,7 +478,7 @@ DS4C_API ds4c_status ds4c_fma_probe(uint32_t blocks, uint32_t iters, float *out,
  * that half of the lanes never see, second at an mbarrier that nothing arrives on
  * (0 for every lane, and the kernels' error word is raised), third at one whose
  * phase is complete (1 for every lane). */
-enum { DS4C_WAITS_QUANT_MATMUL = 0, DS4C_WAITS_GEMM = 1 };
+enum { DS4C_WAITS_QUANT_MATMUL = 0, DS4C_WAITS_GEMM = 1, DS4C_WAITS_ATTENTION = 2 };
 DS4C_API ds4c_status ds4c_test_set_wait_limit(uint64_t limit_ns);
 DS4C_API ds4c_status ds4c_test_wait_timeout(uint64_t limit_ns, cudaStream_t stream);
 DS4C_API ds4c_status ds4c_test_warp_wait(uint32_t kernels, int32_t *answers, cudaStream_t stream);

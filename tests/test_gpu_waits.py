@@ -22,7 +22,7 @@ def stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-@pytest.mark.parametrize("kernels", [abi.DS4C_WAITS_QUANT_MATMUL, abi.DS4C_WAITS_GEMM])
+@pytest.mark.parametrize("kernels", [abi.DS4C_WAITS_QUANT_MATMUL, abi.DS4C_WAITS_GEMM, abi.DS4C_WAITS_ATTENTION])
 def test_lanes_that_see_different_things_get_one_answer(kernels):
     """Half of the lanes see what they wait for, the others never do: no lane may go on alone.  Then a barrier that
     nothing arrives on, and a complete one."""

@@ -181,9 +181,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // Bounded wait that ignores the abort flag: drains copies or MMAs still in
-// flight after a give-up, before the CTA frees its TMEM and exits.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-    uint64_t t0 = 0;
+// flight after a give-up, before the CTA frees its TMEM and exits.  t0: 0, or the
+// time from which the limit counts, for several drains with one limit.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t &t0) {
     for (uint32_t i = 0;; ++i) {
         uint32_t ok;
         asm volatile(
@@ -729,15 +729,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
             }
             ok = good;
         }
-        if (!ok) {
-            // after a give-up: this lane's row copies complete, and every unit issued to the ring
-            // (the last RING at most are still open) has landed before the CTA exits
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-            if (lane == 0)
-                for (uint32_t u = unit > (uint32_t)RING ? unit - RING : 0; u < unit; u++)
-                    mbar_drain(bar(B_FULL + u % RING), (u / RING) & 1);
-        }
+        // this lane's row copies complete, and every unit issued to the ring (the last RING at most are still
+        // open) has landed before the CTA exits, whichever warp gave up: the MMAs may not have waited for them
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        uint64_t drain_t0 = 0;
+        for (uint32_t u = unit > (uint32_t)RING ? unit - RING : 0; u < unit; u++)
+            mbar_drain(bar(B_FULL + u % RING), (u / RING) & 1, drain_t0);
+        __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t ID_QK = idesc(128, H, 0, 0);
@@ -877,7 +876,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap rawHi, const __grid_constant_
         // tracks all of them; bounded, given up or not)
         if (lane == 0) {
             mma_commit(bar(B_DRAIN));
-            mbar_drain(bar(B_DRAIN), 0);
+            uint64_t t0 = 0;
+            mbar_drain(bar(B_DRAIN), 0, t0);
         }
         __syncwarp();
     }

@@ -105,3 +105,36 @@ def test_projection_whose_waits_give_up(T):
     dl.compress_prefill(h, 0)
     assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
     assert torch.equal(rows, want)
+
+
+@pytest.mark.parametrize("n_seq,T,D", [(1, 700, 512), (1, 200, 128), (5, 1, 512)])
+def test_attention_whose_waits_give_up(n_seq, T, D):
+    """The tensor-core attention under the same limit: prefill queries of two head widths, a decode step."""
+    shape = configs.LayerShape(d_model=256, head_dim=D, n_rot=64, idx_head_dim=64, n_heads=64, ratio=4, top_k=300,
+                               dtype="bf16")
+    cap = 500
+    dl, _, _ = device_layer(shape, comp_cap=cap, idx_cap=cap, n_seq=n_seq, max_rows=max(T, n_seq), seed=5)
+    assert abi.ds4c_attn_uses_tensor_cores(dl.cfg) == 1
+    g = torch.Generator(device="cuda").manual_seed(D)
+    dl.raw.copy_(torch.randn(dl.raw.shape, generator=g, device="cuda"))
+    dl.attn_split.view(torch.bfloat16).copy_(torch.randn(dl.attn_split.shape, generator=g, device="cuda"))
+    n = n_seq * T
+    pos = [1200] if n_seq == 1 else [1200 + 50 * b for b in range(n_seq)]
+    q = torch.randn(n, 64, D, generator=g, device="cuda")
+    new = torch.randn(n, D, generator=g, device="cuda")
+    topk = torch.arange(300, dtype=torch.int32, device="cuda").repeat(n, 1)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    dl.attention(q, new, topk, pos, n_seq, T, want, commit_ring=False)
+    dl.sync()
+    assert torch.isfinite(want).all()
+    assert abi.ds4c_test_set_wait_limit(1) == abi.DS4C_OK
+    try:
+        for _ in range(2):
+            dl.attention(q, new, topk, pos, n_seq, T, out, commit_ring=False)
+            assert abi.ds4c_sync_status(stream()) in (abi.DS4C_OK, abi.DS4C_ERR_DEVICE)
+    finally:
+        assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
+    out.fill_(float("nan"))
+    dl.attention(q, new, topk, pos, n_seq, T, out, commit_ring=False)
+    assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
+    assert torch.equal(out, want)

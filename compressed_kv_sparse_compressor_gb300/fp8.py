@@ -6,9 +6,13 @@ with a row pitch of k rounded up to 16 bytes, scale uint8 with one E8M0 byte (2^
 per 128 values at a pitch of ceil(k / 128) rounded up to 4: [n, pitch] for rows, [ceil(n / 128),
 pitch] for weights.  ``empty`` allocates such a pair.
 
-Calls run on the current stream of the tensors' device.  A decode step's kernels take a few
-microseconds, so the checks read each tensor's attributes once and go to the stream's and the
-device's raw handles (``rmsnorm`` took 14.9 us of host time on torch's stream objects)."""
+Calls run on the current stream of the tensors' device and report what the host can see.  A product
+whose kernel gives up waiting (its waits are bounded) leaves outputs unwritten: ``sync`` waits for the
+stream and raises in that case.
+
+A decode step's kernels take a few microseconds, so the checks read each tensor's attributes once and
+go to the stream's and the device's raw handles (``rmsnorm`` took 14.9 us of host time on torch's
+stream objects)."""
 
 from __future__ import annotations
 
@@ -91,6 +95,13 @@ def run(dev, fn, *args):
         raise abi.Ds4cError(status, fn.__name__)
 
 
+def sync(device=None):
+    """Waits for the current stream of `device` (the current device if None); raises Ds4cError if a kernel launched on
+    the device since the last such check gave up, or if the stream failed."""
+    dev = _device() if device is None else torch.device(device).index
+    run(_device() if dev is None else dev, abi.ds4c_sync_status)
+
+
 def rmsnorm(x, gain=None, *, residual=None, residual_out=None, eps: float = 1e-6, q=None, scale=None, y=None):
     """RMSNorm of x [n, d] (float32 or bfloat16; rows may be strided), quantised: returns (q, scale).
 
@@ -152,7 +163,7 @@ def quantize_weight(w, q=None, scale=None) -> Fp8Weight:
 class Linear:
     """1 to 4 weight matrices of one width over the same rows: out_g = rows @ w_g.T in one launch.
 
-    Holds the weights; their addresses are read once, here."""
+    Holds the weights; their addresses are read once, here.  ``sync`` says whether a launch gave up."""
 
     def __init__(self, weights):
         self.weights = list(weights)

@@ -297,6 +297,8 @@ DS4C_API ds4c_status ds4c_quant_weight(uint32_t n, uint32_t k, uint32_t dtype, c
  * that m, k and the matrices' n fix.  The tensor cores' additions cut bits off
  * below float's last; at most 4096 values of K go through one accumulator, which
  * keeps the error near 5e-7 of the result in norm whatever k.
+ * A launch whose bounded waits give up returns with outputs unwritten or in part;
+ * ds4c_sync_status reports it (DS4C_ERR_DEVICE).
  * m <= 2^24, n and k as ds4c_quant_weight; m == 0 does nothing. */
 typedef struct {
     const uint8_t *q;       /* [n][ds4c_quant_row_bytes(k)] */

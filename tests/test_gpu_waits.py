@@ -138,3 +138,22 @@ def test_attention_whose_waits_give_up(n_seq, T, D):
     dl.attention(q, new, topk, pos, n_seq, T, out, commit_ring=False)
     assert abi.ds4c_sync_status(stream()) == abi.DS4C_OK
     assert torch.equal(out, want)
+
+
+def test_torch_calls_report_a_product_that_gave_up():
+    answers = torch.empty(96, dtype=torch.int32, device="cuda")
+    fp8.sync()
+    assert abi.ds4c_test_set_wait_limit(20000) == abi.DS4C_OK
+    try:
+        assert abi.ds4c_test_warp_wait(abi.DS4C_WAITS_QUANT_MATMUL, answers.data_ptr(), stream()) == abi.DS4C_OK
+        with pytest.raises(abi.Ds4cError) as e:
+            fp8.sync("cuda")
+        assert e.value.status == abi.DS4C_ERR_DEVICE
+    finally:
+        assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
+    fp8.sync(torch.device("cuda", 0))
+    w = fp8.quantize_weight(torch.ones(8, 256, device="cuda"))
+    q, scale = fp8.rmsnorm(torch.ones(3, 256, device="cuda"))
+    out = fp8.Linear([w])(q, scale)[0]
+    fp8.sync()
+    assert torch.equal(out, torch.full_like(out, 256.0))

@@ -84,7 +84,7 @@ class DeviceLayer:
 
     def set_weights_quant(self, attn, idx=None):
         """attn / idx = (wkv, wgate, ape, norm): the projections float tensors, quantised here on the
-        device, or fp8.Fp8Weight; ape and norm as set_weights."""
+        device, or fp8.Fp8Weight; ape and norm as set_weights.  Nothing changes if the call raises."""
         s = self.shape
 
         def lw(w, dl):
@@ -99,13 +99,12 @@ class DeviceLayer:
                 raise ValueError("ape and norm: float32")
             if kv.device_index != self.raw.get_device() or gate.device_index != self.raw.get_device():
                 raise ValueError(f"weights on cuda:{kv.device_index}, the layer on {self.raw.device}")
-            self._keep.append((kv, gate, ape, norm))
-            return abi.LaneWeightsQuant(_ptr(kv.q), _ptr(kv.scale), _ptr(gate.q), _ptr(gate.scale), _ptr(ape),
-                                        _ptr(norm))
-        if s.ratio:
-            self.attn_wq = lw(attn, s.head_dim)
-        if s.ratio == 4:
-            self.idx_wq = lw(idx, s.idx_head_dim)
+            return (kv, gate, ape, norm), abi.LaneWeightsQuant(_ptr(kv.q), _ptr(kv.scale), _ptr(gate.q),
+                                                               _ptr(gate.scale), _ptr(ape), _ptr(norm))
+        new_attn = lw(attn, s.head_dim) if s.ratio else (None, self.attn_wq)
+        new_idx = lw(idx, s.idx_head_dim) if s.ratio == 4 else (None, self.idx_wq)
+        self._keep += [new_attn[0], new_idx[0]]
+        self.attn_wq, self.idx_wq = new_attn[1], new_idx[1]
 
     # -- calls -----------------------------------------------------------------
     def state_init(self):

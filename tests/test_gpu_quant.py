@@ -536,3 +536,17 @@ def test_refusals_of_the_torch_calls():
                 lambda: fp8.Linear([w, fp8.quantize_weight(x[:, :128])])):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_layer_keeps_its_weights_when_new_ones_are_refused():
+    """A call that raises on the second lane leaves both lanes as they were, not one of each."""
+    shape, _, quant = _layers(4, 16)
+    wa, wi = (configs.lane_weights(shape, 6, 0, lane, device="cuda") for lane in ("attn", "idx"))
+    before = bytes(quant.attn_wq), bytes(quant.idx_wq)
+    for bad in (None, wa, (wi[0][:-1],) + wi[1:], wi[:2] + (wi[2].double(), wi[3])):
+        with pytest.raises((ValueError, TypeError)):
+            quant.set_weights_quant(wa, bad)
+        assert (bytes(quant.attn_wq), bytes(quant.idx_wq)) == before
+    quant.set_weights_quant(wa, wi)
+    after = bytes(quant.attn_wq), bytes(quant.idx_wq)
+    assert after[0] != before[0] and after[1] != before[1]

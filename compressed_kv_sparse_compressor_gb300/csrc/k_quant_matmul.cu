@@ -36,6 +36,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "ds4c_internal.cuh"
 
 namespace ds4c {
@@ -1017,7 +1019,7 @@ int64_t split_cost(const QuantMatmulArgs &a) {
     return (tiles * split + 151) / 152 * (300 + 37 * ((kb + split - 1) / split)) + (split > 1 ? 140 : 0);
 }
 
-constexpr int PAIRS = 76;
+constexpr int PAIRS = 76, JOINT_BT = 160;      // the widest tile whose stages are two blocks of K
 
 // Rows of a pair tile: the width with the fewest rounds over the pairs times a block's time; cost: of the
 // product, in 10 ns: 4 us and 0.115 + 0.00058 bt us a block.
@@ -1040,10 +1042,24 @@ __global__ void wait_selftest_kernel(int *answers) {
         });
 }
 
-template <typename F>
-int launch_regs(F *kernel) {
-    cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
+// Whether the warpgroups' registers after setmaxnreg fit what a launch of the pair kernel gives; where they do not, their
+// wait for them would never end.  The compiled kernel's register count is asked for until it is known: a failed query is
+// the call's error, not an answer.
+template <bool joint>
+cudaError_t pair_fits(bool &fits) {
+    static std::atomic<int> regs{0};
+    int n = regs.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaFuncAttributes attr;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, qmm_pair_kernel<joint>);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
+        regs.store(n = attr.numRegs, std::memory_order_relaxed);
+    }
+    fits = 4 * n >= 2 * REG_EPILOGUE + 2 * REG_OTHER;
+    return cudaSuccess;
 }
 
 cudaError_t launch_pair(const QuantMatmulArgs &a, int bt, cudaStream_t s) {
@@ -1051,10 +1067,7 @@ cudaError_t launch_pair(const QuantMatmulArgs &a, int bt, cudaStream_t s) {
     Params p;
     cudaError_t e = fill_params(a, 2 * BW, bt, bt / 2, p, maps);
     if (e != cudaSuccess) return e;
-    auto kernel = bt <= 160 ? qmm_pair_kernel<true> : qmm_pair_kernel<false>;
-    // the warpgroups' registers after setmaxnreg have to fit what the launch gives, or their wait for them never ends
-    static const int regs[2] = {launch_regs(qmm_pair_kernel<false>), launch_regs(qmm_pair_kernel<true>)};
-    if (regs[bt <= 160] * 4 < 2 * REG_EPILOGUE + 2 * REG_OTHER) return cudaErrorInvalidConfiguration;
+    auto kernel = bt <= JOINT_BT ? qmm_pair_kernel<true> : qmm_pair_kernel<false>;
     if ((e = ensure_dyn_smem(kernel, Pair::SMEM_BYTES)) != cudaSuccess) return e;
     const int tiles = p.tile_start[a.n_w];
     return launch_pdl(kernel, dim3((unsigned)(2 * (tiles < PAIRS ? tiles : PAIRS))), dim3(PAIR_THREADS), Pair::SMEM_BYTES, s,
@@ -1073,7 +1086,11 @@ cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s) {
     // 20.5, 1024 x 4096 8.3 and 9.8, 256 x 8192 8.1 and 15.4)
     int64_t cost;
     const int bt = pair_bt(a, cost);
-    return split_cost(a) <= cost ? launch_split<128>(a, s) : launch_pair(a, bt, s);
+    if (split_cost(a) <= cost) return launch_split<128>(a, s);
+    bool fits = false;
+    const cudaError_t e = bt <= JOINT_BT ? pair_fits<true>(fits) : pair_fits<false>(fits);
+    if (e != cudaSuccess) return e;
+    return fits ? launch_pair(a, bt, s) : launch_split<128>(a, s);
 }
 
 cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s) {

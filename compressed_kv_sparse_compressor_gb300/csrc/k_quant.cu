@@ -93,18 +93,20 @@ __device__ __forceinline__ void row_sum(float &s, float &c, float *sm) {
     }
 }
 
-// (v + lo)^-1/2 rounded once to float: CUDA's rsqrtf, then the series of (1 - e)^-1/2
+// (v + lo)^-1/2 as r + r e / 2: CUDA's rsqrtf, then the series of (1 - e)^-1/2
 // in the residual e = 1 - (v + lo) r^2, which two fused products give exactly enough.
-__device__ __forceinline__ float rsqrt_pair(float v, float lo) {
+__device__ __forceinline__ float rsqrt_pair(float v, float lo, float &half_e) {
     const float r = rsqrtf(v);
     const float t = __fmul_rn(r, r), tl = fmaf(r, r, -t);
     float e = fmaf(-v, t, 1.f);
     e = __fsub_rn(e, fmaf(v, tl, __fmul_rn(lo, t)));
-    e = fmaf(0.75f * e, e, e);
-    return fmaf(0.5f * r, e, r);
+    half_e = 0.5f * fmaf(0.75f * e, e, e);
+    return r;
 }
 
-// ((s + c) / d + eps)^-1/2, 1 / d as a sum of two floats.
+// ((s + c) / d + eps)^-1/2 rounded once to float, 1 / d as a sum of two floats.  DOWN: times 2^-80, where the result may
+// be subnormal: in 64 bits up to that one rounding.
+template <bool DOWN>
 __device__ __forceinline__ float rstd_of(float s, float c, float inv_d, float inv_d_lo, float eps) {
     const float ph = __fmul_rn(s, inv_d);
     float lo = fmaf(s, inv_d, -ph);
@@ -113,7 +115,9 @@ __device__ __forceinline__ float rstd_of(float s, float c, float inv_d, float in
     float v = ph;
     add_exact(v, lo, eps);
     const float vn = __fadd_rn(v, lo);
-    return rsqrt_pair(vn, __fsub_rn(lo, __fsub_rn(vn, v)));
+    float half_e;
+    const float r = rsqrt_pair(vn, __fsub_rn(lo, __fsub_rn(vn, v)), half_e);
+    return DOWN ? __double2float_rn(fma((double)r, (double)half_e, (double)r) * 0x1p-80) : fmaf(r, half_e, r);
 }
 
 __device__ __forceinline__ float finite_abs(float v) {
@@ -425,14 +429,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 4 : 1) rmsnorm_quant_kerne
     row_sum(s, c, sm);
     float rstd;
     if (s < 0x1p90f) {
-        rstd = rstd_of(s, c, p.inv_d, p.inv_d_lo, p.eps);
+        rstd = rstd_of<false>(s, c, p.inv_d, p.inv_d_lo, p.eps);
     } else {
         // squares near the end of float's range or past it (elements above about 1e13, infinities,
         // NaN): the sum of (h * 2^-80)^2, in which eps vanishes, and 2^-80 put back
         if (blockDim.x > 32) __syncthreads();
         sum_squares(h, 0x1p-80f, s, c);
         row_sum(s, c, sm);
-        rstd = s < INFINITY ? rstd_of(s, c, p.inv_d, p.inv_d_lo, 0.f) * 0x1p-80f : s > 0.f ? 0.f : s;
+        rstd = s < INFINITY ? rstd_of<true>(s, c, p.inv_d, p.inv_d_lo, 0.f) : s > 0.f ? 0.f : s;
     }
 
     const F2 rstd2 = f2(rstd, rstd);

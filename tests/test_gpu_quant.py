@@ -550,3 +550,22 @@ def test_layer_keeps_its_weights_when_new_ones_are_refused():
     quant.set_weights_quant(wa, wi)
     after = bytes(quant.attn_wq), bytes(quant.idx_wq)
     assert after[0] != before[0] and after[1] != before[1]
+
+
+@pytest.mark.parametrize("n,d", [(400, 256), (300, 4096), (300, 1001), (600, 2056)])
+def test_norm_whose_reciprocal_root_is_subnormal(n, d):
+    """Rows with a root mean square from 2^125 to 2^128: rstd is a subnormal float near 2^-127, rounded once."""
+    g = gen(n + d)
+    x = torch.rand(n, d, generator=g, device="cuda") + 0.5
+    x *= torch.where(torch.rand(n, d, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    x = (x * (torch.exp2(125.0 + 2.4 * torch.rand(n, 1, generator=g, device="cuda", dtype=torch.float64)))).float()
+    assert torch.isfinite(x).all()
+    q, scale, check = guarded(n, d)
+    y = torch.empty_like(x)
+    fp8.rmsnorm(x, eps=EPS, q=q, scale=scale, y=y)
+    wy = ref.rmsnorm(x, None, None, EPS)[1]
+    wq, ws = ref.quantise(wy, 1)
+    assert torch.equal(y, wy)
+    assert torch.equal(scale[:, :-(-d // 128)], ws)
+    assert torch.equal(q.view(torch.uint8), wq)
+    check()

@@ -27,10 +27,10 @@
 //     error word and the CTA winds down, freeing its tensor memory.
 //
 // What bounds it, on inputs that are not in L2: few rows, the weights' bytes and the chain
-// launch - loads - MMAs - meeting (one row through 2560 x 4096 weights 5.1 us for 1.5 us of
-// bytes, through 8192 x 8192 14.4 us, 4.7 TB/s); many rows, the ring of loads (about 3000
+// launch - loads - MMAs - meeting (one row through 2560 x 4096 weights 4.9 us for 1.5 us of
+// bytes, through 8192 x 8192 14.0 us, 4.8 TB/s); many rows, the ring of loads (about 3000
 // cycles from a stage's release to its next data) and then the tensor pipe and the power
-// limit (8192 x 8192 x 8192 308 us, 3.6 PFLOP/s; 352 us, 3.1 PFLOP/s, at 1.35 GHz when run
+// limit (8192 x 8192 x 8192 305 us, 3.6 PFLOP/s; 352-359 us, 3.1 PFLOP/s, at 1.35 GHz when run
 // for seconds).
 #include <cuda.h>
 #include <cudaTypedefs.h>

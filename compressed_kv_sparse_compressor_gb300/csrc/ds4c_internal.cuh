@@ -63,6 +63,7 @@ cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s);
 template <uint32_t LOOKS, typename Look>
 __device__ __forceinline__ bool warp_bounded_wait(Look look, volatile int *abort, const unsigned long long &limit_ns,
                                                   unsigned int *error) {
+    __syncwarp();                                        // what the lanes did apart is behind them before the first look
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
         if (__all_sync(0xffffffffu, look())) return true;

@@ -1,0 +1,361 @@
+"""Cases that measure the operators around attention over a paged cache: the rotation of heads by
+their positions (and back), the norm of each head of queries and keys with that rotation in the same
+pass, the keys going to their pages, and the attention of new tokens of several sequences over such
+pages.
+
+Layouts: a pool of pages [n_pages][page_rows][head_dim] bf16 holds rows that are key and value of
+every query head; a table [n_seq][..] names a sequence's pages, -1 behind its last.  The new tokens of
+the sequences lie one behind the other, sequence s from row start[s] on; length[s] counts a
+sequence's tokens, the new ones (whose rows are in their pages already) last.  A pool of compressed
+rows has pages and a table of its own; row c of it is visible from position (c + 1) * ratio - 1 on.
+"""
+
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-6
+
+
+def listed():
+    return [
+        # decode: one token's outputs of 64 heads turned back (the rows are values too, rotated ones)
+        {"name": "rotate_1x64x512_back_bf16", "op": "rotate", "n": 1, "h": 64, "d": 512, "rot": 64, "first": 448, "half": False,
+         "inverse": True, "dtype": "bf16", "scaling": "none", "far": 65536},
+        # a prefill chunk's outputs turned back
+        {"name": "rotate_4096x64x512_back_bf16", "op": "rotate", "n": 4096, "h": 64, "d": 512, "rot": 64, "first": 448, "half": False,
+         "inverse": True, "dtype": "bf16", "scaling": "none", "far": 131072},
+        # a ragged fp32 chunk, whole heads in halves, far positions of a scaled table
+        {"name": "rotate_437x24x128_half_f32", "op": "rotate", "n": 437, "h": 24, "d": 128, "rot": 128, "first": 0, "half": True,
+         "inverse": False, "dtype": "f32", "scaling": "yarn", "far": 1048576},
+        # decode: one token's queries and its row, normed, rotated, the row to its page
+        {"name": "norm_1x64x512_bf16", "op": "norm", "n": 1, "h": 64, "d": 512, "rot": 64, "first": 448, "half": False,
+         "dtype": "bf16", "scaling": "none", "far": 65536, "gain": True, "page": 64},
+        # a decode step of 32 sequences
+        {"name": "norm_32x64x512_bf16", "op": "norm", "n": 32, "h": 64, "d": 512, "rot": 64, "first": 448, "half": False,
+         "dtype": "bf16", "scaling": "yarn", "far": 65536, "gain": True, "page": 64},
+        # a prefill chunk
+        {"name": "norm_4096x64x512_bf16", "op": "norm", "n": 4096, "h": 64, "d": 512, "rot": 64, "first": 448, "half": False,
+         "dtype": "bf16", "scaling": "none", "far": 131072, "gain": True, "page": 128},
+        # a ragged chunk of a small fp32 layer, in halves, no gains
+        {"name": "norm_437x24x128_half_f32", "op": "norm", "n": 437, "h": 24, "d": 128, "rot": 64, "first": 64, "half": True,
+         "dtype": "f32", "scaling": "linear", "far": 65536, "gain": False, "page": 16},
+        # decode: one sequence, every earlier row
+        {"name": "attn_1@8192", "op": "attn", "h": 64, "d": 512, "seqs": "1@8192", "window": 0, "ratio": 0, "page": 64},
+        # a decode step of 32 sequences at 64K
+        {"name": "attn_32x1@65536", "op": "attn", "h": 64, "d": 512, "seqs": ",".join(f"1@{65536 + b % 4}" for b in range(32)),
+         "window": 0, "ratio": 0, "page": 64},
+        # a prefill chunk behind 8192 tokens: the largest
+        {"name": "attn_4096@12288", "op": "attn", "h": 64, "d": 512, "seqs": "4096@12288", "window": 0, "ratio": 0, "page": 128},
+        # a batch as a scheduler mixes it, on a ratio-128 layer: chunks, a whole prompt, single tokens
+        {"name": "attn_mixed_w128_r128", "op": "attn", "h": 64, "d": 512,
+         "seqs": "437@9013,1@65537,1@300,1000@1000,1@32770,65@131072,1@1,1@8191,129@16500,1@77", "window": 128, "ratio": 128,
+         "page": 64},
+        # chunks of a smaller layer, several tokens of 24 heads side by side, pages that end inside a tile
+        {"name": "attn_3_chunks_24x128", "op": "attn", "h": 24, "d": 128, "seqs": "1531@1531,700@4099,64@20000", "window": 0,
+         "ratio": 0, "page": 16},
+    ]
+
+
+def _size(rng, lo, hi, step=1):
+    """A size spread over the logarithm of lo .. hi; mostly a multiple of `step`, odd ones among them."""
+    v = int(round(lo * (hi / lo) ** rng.random()))
+    if step > 1 and rng.random() < 0.7:
+        v = max(step, v // step * step)
+    return min(max(v, lo), hi)
+
+
+def draw(rng):
+    op = rng.choice(["rotate", "norm", "norm", "attn", "attn", "attn"])
+    if op != "attn":
+        d = rng.choice([64, 128, 128, 256, 512, 512])
+        rot = rng.choice([r for r in (16, 32, 64, 128) if r <= d])
+        h = rng.choice([1, 8, 16, 24, 40, 64, 128])
+        c = {"op": op, "n": _size(rng, 1, min(4096, 4096 * 64 * 512 // (h * d))), "h": h, "d": d, "rot": rot,
+             "first": rng.choice([0, d - rot]), "half": rng.random() < 0.5, "dtype": rng.choice(["bf16", "bf16", "f32"]),
+             "scaling": rng.choice(["none", "linear", "yarn"]), "far": _size(rng, 64, 1 << 20)}
+        if c["dtype"] == "f32":
+            c["n"] = max(1, c["n"] // 2)
+        if op == "rotate":
+            c["inverse"] = rng.random() < 0.5
+        else:
+            c["gain"], c["page"] = rng.random() < 0.7, rng.choice([16, 32, 64, 128, 256])
+        return c
+    d, h = rng.choice([64, 128, 256, 512, 512]), rng.choice([8, 16, 24, 40, 64, 64, 128])
+    window, ratio = rng.choice([(0, 0), (0, 0), (128, 0), (100, 0), (128, 128), (128, 4), (64, 128)])
+    kind = rng.choice(["decode", "chunk", "mixed"])
+    while True:
+        if kind == "decode":
+            n, far = _size(rng, 1, 64), _size(rng, 64, 65536)
+            seqs = [(1, rng.randint(max(1, far // 2), far)) for _ in range(n)]
+        elif kind == "chunk":
+            new = _size(rng, 16, 4096, 64)
+            seqs = [(new, new + (0 if rng.random() < 0.3 else _size(rng, 16, 32768)))]
+        else:
+            seqs = []
+            for _ in range(rng.randint(2, 24)):
+                new = 1 if rng.random() < 0.5 else _size(rng, 2, 1024)
+                seqs.append((new, new + _size(rng, 1, 65536)))
+        c = {"op": "attn", "h": h, "d": d, "seqs": ",".join(f"{n}@{m}" for n, m in seqs), "window": window, "ratio": ratio,
+             "page": rng.choice([16, 32, 64, 128, 256])}
+        w = work(c)
+        if w["flops"] <= 4e12 and w["bytes"] <= 2e9:
+            return c
+
+
+def _type(name):
+    return torch.float32 if name == "f32" else torch.bfloat16
+
+
+def _normal(gen, *shape):
+    return torch.randn(*shape, generator=gen, device="cuda")
+
+
+SCALING = {"none": {}, "linear": {"scaling": "linear", "factor": 8.0}, "yarn": {"scaling": "yarn", "factor": 16.0, "original": 65536}}
+
+
+def _thetas(rot, scaling):
+    """Angles per position of the rot / 2 pairs, and the magnitude that a scaled table multiplies in."""
+    base = [10000.0 ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if scaling == "none":
+        return base, 1.0
+    if scaling == "linear":
+        return [t / 8.0 for t in base], 1.0
+    # by parts: pairs that turn at least 32 times within the original context stay, those that turn less
+    # than once are slowed down by the factor, a ramp over the pairs between
+    def pair(turns):
+        return rot / 2 * math.log(65536 / (2 * math.pi * turns)) / math.log(10000.0)
+    lo, hi = max(math.floor(pair(32.0)), 0), min(math.ceil(pair(1.0)), rot // 2 - 1)
+    out = []
+    for i, t in enumerate(base):
+        g = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+        out.append(t / 16.0 * g + t * (1.0 - g))
+    return out, 0.1 * math.log(16.0) + 1.0
+
+
+def _seqs(case):
+    return [tuple(int(v) for v in s.split("@")) for s in case["seqs"].split(",")]
+
+
+def _pool(gen, rows_of, page, d):
+    """A pool with the pages of sequences of rows_of[s] rows in no order, and their table."""
+    need = [-(-r // page) for r in rows_of]
+    n_pages = sum(need) + 3                                    # some pages of no sequence
+    order = torch.randperm(n_pages, generator=gen, device="cuda").to(torch.int32)
+    table = torch.full((len(need), max(max(need), 1)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for s, k in enumerate(need):
+        table[s, :k] = order[at:at + k]
+        at += k
+    return _normal(gen, n_pages, page, d).to(torch.bfloat16), table
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    s = {"case": case}
+    if own:
+        from compressed_kv_sparse_compressor_gb300 import paged, rope
+    if case["op"] == "attn":
+        seqs, h, d = _seqs(case), case["h"], case["d"]
+        n = sum(new for new, _ in seqs)
+        # queries and rows as a head's norm leaves them, the rows around a common direction that the queries know
+        lean = _normal(gen, d)
+        s["q"] = (0.8 * _normal(gen, n, h, d) + 0.15 * lean).to(torch.bfloat16)
+        s["cache"], s["pages"] = _pool(gen, [m for _, m in seqs], case["page"], d)
+        if case["ratio"]:
+            s["comp"], s["comp_pages"] = _pool(gen, [m // case["ratio"] for _, m in seqs], case["page"], d)
+        start = [0]
+        for new, _ in seqs:
+            start.append(start[-1] + new)
+        s["start"] = torch.tensor(start, dtype=torch.int32, device="cuda")
+        s["length"] = torch.tensor([m for _, m in seqs], dtype=torch.int32, device="cuda")
+        s["out"] = torch.empty_like(s["q"])
+        if own:
+            s["ws"] = paged.workspace(len(seqs), n, h, d)
+        return s
+    n, h, d, t = case["n"], case["h"], case["d"], _type(case["dtype"])
+    # a projection's outputs: channels of unequal size
+    s["x"] = (_normal(gen, n, h, d) * torch.exp(0.5 * _normal(gen, h, d))).to(t)
+    if case["n"] > 8:                                          # a chunk's positions, one behind the other
+        s["pos"] = torch.arange(max(case["far"] - n, 0), max(case["far"] - n, 0) + n, device="cuda")
+    else:
+        s["pos"] = torch.randint(0, case["far"], (n,), generator=gen, device="cuda")
+    s["out"] = torch.empty_like(s["x"])
+    if own:
+        s["table"] = rope.table(case["rot"], base=10000.0, **SCALING[case["scaling"]])
+    if case["op"] == "norm":
+        s["k"] = (_normal(gen, n, 1, d) * torch.exp(0.5 * _normal(gen, 1, d))).to(t)
+        s["q_gain"] = 1.0 + 0.1 * _normal(gen, d) if case["gain"] else None
+        s["k_gain"] = 1.0 + 0.1 * _normal(gen, d) if case["gain"] else None
+        pages = -(-n // case["page"]) + 3
+        s["cache"] = _normal(gen, pages, case["page"], d).to(t)
+        s["slots"] = torch.randperm(pages * case["page"], generator=gen, device="cuda")[:n].contiguous()
+    return s
+
+
+def _rotate(y, pos, case, inverse):
+    """y [n][h][d] in 32 bits, its pairs turned by the positions; the angles in 64."""
+    theta, magnitude = _thetas(case["rot"], case["scaling"])
+    a = pos.double()[:, None] * torch.tensor(theta, dtype=torch.float64, device=y.device)
+    c, sn = (magnitude * torch.cos(a)).float()[:, None], (magnitude * torch.sin(a)).float()[:, None]
+    if inverse:
+        sn = -sn
+    out = y.clone()
+    part = y[..., case["first"]:case["first"] + case["rot"]]
+    if case["half"]:
+        i0, i1 = slice(case["first"], case["first"] + case["rot"] // 2), slice(case["first"] + case["rot"] // 2, case["first"] + case["rot"])
+        y0, y1 = part[..., :case["rot"] // 2], part[..., case["rot"] // 2:]
+    else:
+        i0, i1 = slice(case["first"], case["first"] + case["rot"], 2), slice(case["first"] + 1, case["first"] + case["rot"], 2)
+        y0, y1 = part[..., 0::2], part[..., 1::2]
+    out[..., i0] = y0 * c - y1 * sn
+    out[..., i1] = y0 * sn + y1 * c
+    return out
+
+
+def _normed(x, gain):
+    x = x.float()
+    y = x * torch.rsqrt(x.square().mean(dim=-1, keepdim=True) + EPS)
+    return y if gain is None else y * gain
+
+
+def _rows(pool, table, n):
+    """The first n rows of a sequence, gathered from its pages."""
+    page = pool.shape[1]
+    return pool[table[:-(-n // page)].long()].reshape(-1, pool.shape[2])[:n]
+
+
+def run(state):
+    case = state["case"]
+    if own:
+        from compressed_kv_sparse_compressor_gb300 import paged, rope
+    if case["op"] == "rotate":
+        if own:
+            return rope.rotate(state["x"], state["pos"], state["table"], first=case["first"], half=case["half"],
+                               inverse=case["inverse"], out=state["out"])
+        return _rotate(state["x"].float(), state["pos"], case, case["inverse"]).to(state["x"].dtype)
+    if case["op"] == "norm":
+        if own:
+            rope.norm_rotate(state["x"], state["pos"], state["table"], gain=state["q_gain"], k=state["k"], k_gain=state["k_gain"],
+                             eps=EPS, first=case["first"], half=case["half"], out=state["out"], cache=state["cache"],
+                             slots=state["slots"])
+            return {"q": state["out"], "cache": state["cache"]}
+        q = _rotate(_normed(state["x"], state["q_gain"]), state["pos"], case, False).to(state["x"].dtype)
+        k = _rotate(_normed(state["k"], state["k_gain"]), state["pos"], case, False).to(state["x"].dtype)
+        state["cache"].view(-1, case["d"])[state["slots"]] = k[:, 0]
+        return {"q": q, "cache": state["cache"]}
+    if own:
+        return paged.attention(state["q"], state["cache"], state["pages"], state["start"], state["length"],
+                               window=case["window"], scale=case["d"] ** -0.5, comp=state.get("comp"),
+                               comp_pages=state.get("comp_pages"), ratio=case["ratio"], out=state["out"], workspace=state["ws"])
+    out = torch.empty_like(state["q"])
+    at = 0
+    for s, (new, length) in enumerate(_seqs(case)):
+        first = max(0, length - new - case["window"] + 1) if case["window"] else 0
+        x = _rows(state["cache"], state["pages"][s], length)[first:].float()
+        # where a row stands: the position of its token, or of the last token it stands for
+        born = torch.arange(first, length, device=x.device)
+        dies = born + (case["window"] if case["window"] else 1 << 30)
+        if case["ratio"]:
+            nc = length // case["ratio"]
+            x = torch.cat([x, _rows(state["comp"], state["comp_pages"][s], nc).float()])
+            cb = (torch.arange(nc, device=x.device) + 1) * case["ratio"] - 1
+            born, dies = torch.cat([born, cb]), torch.cat([dies, torch.full_like(cb, 1 << 30)])
+        step = max(1, (1 << 28) // (x.shape[0] * case["h"]))   # scores of 1 GB at a time
+        for i in range(0, new, step):
+            m = min(step, new - i)
+            t = torch.arange(length - new + i, length - new + i + m, device=x.device)[:, None]
+            p = (state["q"][at + i:at + i + m].float().reshape(m * case["h"], case["d"]) * case["d"] ** -0.5) @ x.T
+            p = p.view(m, case["h"], -1).masked_fill_(~((born <= t) & (t < dies))[:, None], -math.inf)
+            p = torch.exp(p.sub_(p.amax(dim=-1, keepdim=True)))
+            o = (p.view(m * case["h"], -1) @ x).view(m, case["h"], case["d"]) / p.sum(dim=-1, keepdim=True)
+            out[at + i:at + i + m] = o.to(out.dtype)
+        at += new
+    return out
+
+
+def _count(case):
+    """(query, row) pairs, and rows that some query sees."""
+    pairs = rows = 0
+    w, r = case["window"], case["ratio"]
+    for new, length in _seqs(case):
+        for t in range(length - new, length):
+            pairs += (min(w, t + 1) if w else t + 1) + ((t + 1) // r if r else 0)
+        rows += (min(length, new + w - 1) if w else length) + (length // r if r else 0)
+    return pairs, rows
+
+
+def work(case):
+    if case["op"] == "attn":
+        pairs, rows = _count(case)
+        n = sum(new for new, _ in _seqs(case))
+        return {"bytes": 2 * case["d"] * (2 * n * case["h"] + rows), "flops": 4 * case["h"] * case["d"] * pairs}
+    e = 4 if case["dtype"] == "f32" else 2
+    n, d = case["n"], case["d"]
+    heads = case["h"] + (1 if case["op"] == "norm" else 0)
+    b = 2 * n * heads * d * e + 8 * n
+    if case["op"] == "norm":
+        b += 8 * n + (8 * d if case["gain"] else 0)
+    return {"bytes": b, "flops": n * heads * (3 * case["rot"] + (4 * d if case["op"] == "norm" else 0))}
+
+
+def _exact_turned(z, pos, case, sign):
+    """Pairs as complex numbers, times m e^(i a)."""
+    theta, magnitude = _thetas(case["rot"], case["scaling"])
+    a = sign * torch.outer(pos.double(), torch.tensor(theta, dtype=torch.float64, device=z.device))
+    turn = torch.polar(torch.full_like(a, magnitude), a)[:, None]
+    f, r = case["first"], case["rot"]
+    out = z.clone()
+    if case["half"]:
+        w = torch.complex(z[..., f:f + r // 2].contiguous(), z[..., f + r // 2:f + r].contiguous()) * turn
+        out[..., f:f + r] = torch.cat([w.real, w.imag], dim=-1)
+    else:
+        w = torch.view_as_complex(z[..., f:f + r].contiguous().view(*z.shape[:-1], r // 2, 2)) * turn
+        out[..., f:f + r] = torch.view_as_real(w).flatten(-2)
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "rotate":
+        return _exact_turned(s["x"].double(), s["pos"], case, -1.0 if case["inverse"] else 1.0)
+    if case["op"] == "norm":
+        def one(x, gain):
+            x = x.double()
+            y = x / torch.sqrt(torch.linalg.vecdot(x, x)[..., None] / case["d"] + EPS)
+            return _exact_turned(y if gain is None else y * gain.double(), s["pos"], case, 1.0)
+        cache = s["cache"].double()
+        cache.view(-1, case["d"]).index_copy_(0, s["slots"], one(s["k"], s["k_gain"])[:, 0])
+        return {"q": one(s["x"], s["q_gain"]), "cache": cache}
+    if work(case)["flops"] > 7e12:                             # more than about ten seconds in 64 bits
+        return None
+    h, d, w, r = case["h"], case["d"], case["window"], case["ratio"]
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    at = 0
+    for i, (new, length) in enumerate(_seqs(case)):
+        keys = _rows(s["cache"], s["pages"][i], length).double()
+        ckeys = _rows(s["comp"], s["comp_pages"][i], length // r).double() if r else None
+        step = max(1, (1 << 26) // (h * length)) if not w else 64
+        for b in range(0, new, step):
+            m = min(step, new - b)
+            t0, t1 = length - new + b, length - new + b + m    # positions t0 .. t1 - 1
+            q = s["q"][at + b:at + b + m].double()
+            lo = max(0, t0 + 1 - w) if w else 0
+            t = torch.arange(t0, t1, device="cuda")
+            c = torch.arange(lo, t1, device="cuda")
+            see = c[None] <= t[:, None]
+            if w:
+                see &= c[None] > t[:, None] - w
+            logits = [torch.einsum("mhd,kd->mhk", q, keys[lo:t1]).where(see[:, None], torch.tensor(-math.inf, device="cuda").double())]
+            rows = [keys[lo:t1]]
+            if r:
+                nc = t1 // r
+                seen = torch.arange(nc, device="cuda")[None] < (t[:, None] + 1) // r
+                logits.append(torch.einsum("mhd,kd->mhk", q, ckeys[:nc]).where(seen[:, None], torch.tensor(-math.inf, device="cuda").double()))
+                rows.append(ckeys[:nc])
+            p = torch.softmax(torch.cat(logits, dim=-1) / math.sqrt(d), dim=-1)
+            out[at + b:at + b + m] = torch.einsum("mhk,kd->mhd", p, torch.cat(rows))
+        at += new
+    return out

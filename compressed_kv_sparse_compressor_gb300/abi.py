@@ -24,6 +24,9 @@ DS4C_BF16 = 1
 DS4C_WAITS_QUANT_MATMUL = 0
 DS4C_WAITS_GEMM = 1
 DS4C_WAITS_ATTENTION = 2
+DS4C_ROPE_PLAIN = 0
+DS4C_ROPE_LINEAR = 1
+DS4C_ROPE_YARN = 2
 
 EXPORTS = (
     "ds4c_workspace_bytes", "ds4c_state_init", "ds4c_compress_prefill", "ds4c_compress_decode_step",
@@ -34,6 +37,7 @@ EXPORTS = (
     "ds4c_indexer_topk_heads", "ds4c_test_set_wait_limit", "ds4c_test_wait_timeout", "ds4c_test_warp_wait",
     "ds4c_quant_row_bytes", "ds4c_quant_scale_bytes", "ds4c_rmsnorm_quant", "ds4c_quant_weight", "ds4c_quant_matmul",
     "ds4c_compress_prefill_quant", "ds4c_compress_decode_step_quant",
+    "ds4c_rope_table", "ds4c_rotate_heads",
 )
 PAYLOAD_U32_FIELDS = 13
 NOALLOC_SCORE_FLOATS = 2 * 1024 * 1024
@@ -76,6 +80,23 @@ class RmsnormArgs(C.Structure):
 class QuantMatrix(C.Structure):
     _fields_ = [("q", C.c_void_p), ("scale", C.c_void_p), ("out", C.c_void_p), ("out_ld", C.c_size_t),
                 ("n", C.c_uint32)]
+
+
+class RopeParams(C.Structure):
+    _fields_ = [("n_rot", C.c_uint32), ("scaling", C.c_uint32), ("base", C.c_double), ("factor", C.c_double),
+                ("original", C.c_double), ("beta_fast", C.c_double), ("beta_slow", C.c_double), ("magnitude", C.c_double)]
+
+
+class HeadRows(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("out", C.c_void_p), ("x_token", C.c_size_t), ("x_head", C.c_size_t),
+                ("out_token", C.c_size_t), ("out_head", C.c_size_t), ("gain", C.c_void_p), ("slots", C.c_void_p),
+                ("n_slots", C.c_uint64), ("heads", C.c_uint32), ("out_dtype", C.c_uint32)]
+
+
+class RotateArgs(C.Structure):
+    _fields_ = [("n", C.c_uint32), ("d", C.c_uint32), ("dtype", C.c_uint32), ("n_rot", C.c_uint32), ("first", C.c_uint32),
+                ("half", C.c_uint32), ("inverse", C.c_uint32), ("norm", C.c_uint32), ("eps", C.c_float),
+                ("magnitude", C.c_float), ("positions", C.c_void_p), ("turns", C.c_void_p), ("q", HeadRows), ("k", HeadRows)]
 
 
 class PayloadInfo(C.Structure):
@@ -134,6 +155,8 @@ def lib() -> C.CDLL:
         "ds4c_quant_matmul": (st, [U32, U32, P, P, C.POINTER(QuantMatrix), U32, U32, P]),
         "ds4c_compress_prefill_quant": (st, [cfgp, lqp, lqp, lsp, P, P, U32, U64, P, SZ, P]),
         "ds4c_compress_decode_step_quant": (st, [cfgp, lqp, lqp, lsp, P, P, C.POINTER(U64), U32, P, SZ, P]),
+        "ds4c_rope_table": (st, [C.POINTER(RopeParams), P, C.POINTER(C.c_float)]),
+        "ds4c_rotate_heads": (st, [C.POINTER(RotateArgs), P]),
         "ds4c_fma_probe": (st, [U32, U32, P, C.POINTER(C.c_double), P]),
         "ds4c_test_set_wait_limit": (st, [U64]),
         "ds4c_test_wait_timeout": (st, [U64, P]),
@@ -229,6 +252,16 @@ def ds4c_compress_decode_step_quant(cfg, attn_w, idx_w, state, hidden, hidden_sc
     return lib().ds4c_compress_decode_step_quant(C.byref(cfg), C.byref(attn_w) if attn_w is not None else None,
                                                  C.byref(idx_w) if idx_w is not None else None, C.byref(state),
                                                  hidden, hidden_scale, pos_h, n_seq, ws, ws_bytes, stream)
+
+
+def ds4c_rope_table(params, turns_h):
+    """turns_h: a ctypes array of params.n_rot / 2 uint64.  Returns (status, magnitude)."""
+    m = C.c_float(0.0)
+    return lib().ds4c_rope_table(params, turns_h, C.byref(m)), m.value
+
+
+def ds4c_rotate_heads(args, stream):
+    return (_lib or lib()).ds4c_rotate_heads(args, stream)
 
 
 def ds4c_indexer_topk(cfg, state, q_idx, pos_h, n_seq, n_tok, topk, scores, score_stride, ws, ws_bytes, stream):

@@ -1,0 +1,99 @@
+// extern "C" entry points of the heads' norm and rotation (include/ds4c.h): the rotary table on the
+// host, argument validation before any launch.
+#include <cmath>
+
+#include "ds4c_internal.cuh"
+
+using namespace ds4c;
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr uint32_t kMaxHeadDim = 1024, kMaxHeads = 1024, kMaxTokens = 1u << 24;
+constexpr size_t kMaxStride = (size_t)1 << 40;
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool known(uint32_t dtype) { return dtype == DS4C_F32 || dtype == DS4C_BF16; }
+size_t elem_bytes(uint32_t dtype) { return dtype == DS4C_F32 ? 4 : 2; }
+bool within(double x, double lo, double hi) { return x >= lo && x <= hi; }      // false for NaN
+
+// `outer` steps of so and `inner` steps of si, each of d elements: no two rows share an element.
+bool apart(size_t n_outer, size_t so, size_t n_inner, size_t si, size_t d) {
+    return (n_inner <= 1 || si >= d) && (n_outer <= 1 || so >= (n_inner - 1) * si + d);
+}
+
+ds4c_status check_side(const ds4c_rotate_args &a, const ds4c_head_rows &r) {
+    if (!r.x || !r.out) return DS4C_ERR_NULL;
+    if (!known(r.out_dtype) || !aligned(r.x, elem_bytes(a.dtype)) || !aligned(r.out, elem_bytes(r.out_dtype))) return DS4C_ERR_SHAPE;
+    if (!aligned(r.gain, 4) || !aligned(r.slots, 8)) return DS4C_ERR_SHAPE;
+    if (r.x_token > kMaxStride || r.x_head > kMaxStride || r.out_token > kMaxStride || r.out_head > kMaxStride) return DS4C_ERR_SHAPE;
+    if (r.slots) {
+        if (r.n_slots > (uint64_t)1 << 40 || r.out == r.x) return DS4C_ERR_SHAPE;
+        if (!apart(2, r.out_token, r.heads, r.out_head, a.d)) return DS4C_ERR_SHAPE;
+    } else {
+        if (!apart(a.n, r.out_token, r.heads, r.out_head, a.d) && !apart(r.heads, r.out_head, a.n, r.out_token, a.d)) return DS4C_ERR_SHAPE;
+        if (r.out == r.x && (r.out_dtype != a.dtype || (a.n > 1 && r.out_token != r.x_token) || (r.heads > 1 && r.out_head != r.x_head)))
+            return DS4C_ERR_SHAPE;
+    }
+    return DS4C_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ds4c_status ds4c_rope_table(const ds4c_rope_params *params, uint64_t *turns_h, float *magnitude_h) {
+    if (!params || !turns_h || !magnitude_h) return DS4C_ERR_NULL;
+    const ds4c_rope_params &p = *params;
+    if (p.n_rot < 2 || p.n_rot > kMaxHeadDim || p.n_rot % 2 || p.scaling > DS4C_ROPE_YARN) return DS4C_ERR_SHAPE;
+    if (!(p.base > 1.0) || !(p.base <= 1e12) || !within(p.magnitude, 0.0, 1e6)) return DS4C_ERR_SHAPE;
+    const int pairs = (int)p.n_rot / 2;
+    double factor = 1.0, lo = 0.0, hi = 0.0, magnitude = 1.0;
+    if (p.scaling != DS4C_ROPE_PLAIN) {
+        if (!within(p.factor, 1.0, 1e6)) return DS4C_ERR_SHAPE;
+        factor = p.factor;
+    }
+    if (p.scaling == DS4C_ROPE_YARN) {
+        if (!within(p.original, 1.0, 1099511627776.0) || !(p.beta_slow > 0.0) || !(p.beta_slow <= p.beta_fast) || !(p.beta_fast <= 1e6))
+            return DS4C_ERR_SHAPE;
+        auto pair = [&](double turns) { return pairs * std::log(p.original / (kTwoPi * turns)) / std::log(p.base); };
+        lo = std::fmax(std::floor(pair(p.beta_fast)), 0.0);
+        hi = std::fmin(std::ceil(pair(p.beta_slow)), pairs - 1.0);
+        magnitude = 0.1 * std::log(factor) + 1.0;
+    }
+    for (int j = 0; j < pairs; j++) {
+        const double theta = std::pow(p.base, -2.0 * j / p.n_rot);
+        double t = theta / factor;
+        if (p.scaling == DS4C_ROPE_YARN) {
+            const double g = std::fmin(std::fmax((j - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            t = theta * (1.0 - g) + theta / factor * g;
+        }
+        turns_h[j] = (uint64_t)std::llround(std::ldexp(t / kTwoPi, 64));      // below 2^62: t <= 1
+    }
+    *magnitude_h = (float)(p.magnitude > 0.0 ? p.magnitude : magnitude);
+    return DS4C_OK;
+}
+
+ds4c_status ds4c_rotate_heads(const ds4c_rotate_args *args, cudaStream_t stream) {
+    if (!args) return DS4C_ERR_NULL;
+    const ds4c_rotate_args &a = *args;
+    if (a.d == 0 || a.d > kMaxHeadDim || !known(a.dtype) || a.n > kMaxTokens) return DS4C_ERR_SHAPE;
+    if (a.n_rot % 2 || a.first > a.d || a.n_rot > a.d - a.first) return DS4C_ERR_SHAPE;
+    if (a.norm && !within(a.eps, 1e-12f, 1.0f)) return DS4C_ERR_SHAPE;
+    if (a.q.heads > kMaxHeads || a.k.heads > kMaxHeads) return DS4C_ERR_SHAPE;
+    const uint32_t heads = a.q.heads + a.k.heads;
+    if (heads == 0 || heads > kMaxHeads || (uint64_t)a.n * heads > 0x7fffffffull) return DS4C_ERR_SHAPE;
+    if (a.n == 0) return DS4C_OK;
+    if (a.n_rot) {
+        if (!a.positions || !a.turns) return DS4C_ERR_NULL;
+        if (!aligned(a.positions, 8) || !aligned(a.turns, 8) || !within(a.magnitude, 0.0, 1e6)) return DS4C_ERR_SHAPE;
+    }
+    for (const ds4c_head_rows *r : {&a.q, &a.k}) {
+        if (r->heads == 0) continue;
+        const ds4c_status s = check_side(a, *r);
+        if (s != DS4C_OK) return s;
+    }
+    return cuda_status(launch_rotate_heads(a, stream));
+}
+
+}  // extern "C"

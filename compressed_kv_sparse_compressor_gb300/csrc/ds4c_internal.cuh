@@ -284,6 +284,12 @@ cudaError_t launch_quant_matmul(const QuantMatmulArgs &a, cudaStream_t s);
 unsigned int qmm_read_clear_error();
 
 // ----------------------------------------------------------------------------
+// Heads: norm and rotation (arguments checked by the caller)
+// ----------------------------------------------------------------------------
+cudaError_t launch_rotate_heads(const ds4c_rotate_args &a, cudaStream_t s);
+unsigned int heads_read_clear_error();
+
+// ----------------------------------------------------------------------------
 // Compressor (store + APE, pool, RMSNorm, tail RoPE, FP8, append, frontier).
 // ----------------------------------------------------------------------------
 struct RopeTable { float inv_freq[kMaxRot / 2]; };

@@ -1,0 +1,339 @@
+// Norm and rotation of heads: for every token i and head h a row x of d values becomes
+//   y = x * rstd * gain,  rstd = (sum x^2 / d + eps)^-1/2      (NORM; y = x without)
+//   pairs (a, b) of y's rotated part -> m (a cos t - b sin t, a sin t + b cos t),  t = pos_i theta_j
+// in one pass: the row in registers, one rounding at the end.  Pairs are neighbours or lie half the
+// rotated part apart.
+//
+// Angles: theta_j comes as a whole number of 2^-64 turns, so pos * theta_j modulo one turn is one wrapping
+// 64-bit product, exact for every position; a quarter turn is split off in whole numbers too, and only the
+// rest (at most 1/8 turn) is rounded to float.  (A float product of position and angle is off by 0.03 rad
+// at a position of 10^6.)
+//
+// What bounds it: HBM for many tokens, launch and one chain load - sum - store for few.  A block takes one
+// token, so that its sines are computed once for all heads, in shared memory; a warp takes a row of 256
+// values and more, 8 or 16 lanes a shorter one, 16 bytes a lane and access, and loads its next row before
+// it works on this one.
+#include <cuda_bf16.h>
+
+#include "ds4c_internal.cuh"
+
+namespace ds4c {
+
+__device__ unsigned int g_heads_err;
+
+namespace {
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+
+struct Side {
+    const void *x;
+    void *out;
+    const float *gain;
+    const int64_t *slots;
+    int64_t x_token, x_head, out_token, out_head, n_slots;
+    int heads, out_f32;
+};
+struct Params {
+    Side side[2];
+    const int64_t *pos;
+    const unsigned long long *turns;
+    float magnitude, eps, inv_d;
+    int d, n_rot, first, half, inverse;
+    int chunks, chunk;                       // blocks to a token, heads to a block
+};
+
+// cos and sin of t / 2^64 turns.
+__device__ __forceinline__ float2 cos_sin_turns(unsigned long long t) {
+    const int quarter = (int)((t + (1ull << 61)) >> 62) & 3;
+    const float x = (float)(long long)(t - ((unsigned long long)quarter << 62)) * 0x1p-63f;   // half turns, |x| <= 1/4
+    float s, c;
+    sincospif(x, &s, &c);
+    const float a = (quarter & 1) ? s : c, b = (quarter & 1) ? c : s;
+    return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter >= 2 ? -b : b);
+}
+
+template <typename TI, int V>
+struct Vec {
+    TI v[V];
+};
+template <typename TI, int V>
+__device__ __forceinline__ void load_vec(Vec<TI, V> &r, const TI *p) {
+    if constexpr (V * sizeof(TI) >= 16) {
+#pragma unroll
+        for (int i = 0; i < (int)(V * sizeof(TI) / 16); i++)
+            reinterpret_cast<uint4 *>(r.v)[i] = reinterpret_cast<const uint4 *>(p)[i];
+    } else {
+        r.v[0] = *p;
+    }
+}
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <int V>
+__device__ __forceinline__ void store_vec(void *out, int64_t at, const float (&y)[V], int f32) {
+    if (f32) {
+        float *p = static_cast<float *>(out) + at;
+        if constexpr (V == 8) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+            *p = y[0];
+        }
+    } else {
+        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(out) + at;
+        if constexpr (V == 8) {
+            __nv_bfloat162 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) b[i] = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(b);
+        } else {
+            *p = __float2bfloat16_rn(y[0]);
+        }
+    }
+}
+
+// T lanes to a row, G vectors of V values to a lane (value e of the row in vector e / V, vector v in lane v % T).
+// V = 8 needs 16-byte aligned rows, d a multiple of 8 and pairs inside a vector or in the same place of two vectors;
+// V = 1 takes anything.
+template <typename TI, int V, int T, int G, bool NORM>
+__global__ void __launch_bounds__(THREADS) heads_kernel(const Params p) {
+    extern __shared__ float4 smem4[];
+    float2 *cs = reinterpret_cast<float2 *>(smem4);                       // [n_rot / 2]: magnitude * (cos, sin)
+    constexpr int ROWS = 32 / T;                                          // rows a warp works on at a time
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = lane % T;
+    const int token = blockIdx.x / p.chunks, h0 = (blockIdx.x % p.chunks) * p.chunk;
+    const int h_end = min(h0 + p.chunk, p.side[0].heads + p.side[1].heads);
+    // the warps' rows of the rotated part, where pairs lie in different lanes
+    float *buf = reinterpret_cast<float *>(smem4) + ((p.n_rot + 3) & ~3) + (warp * ROWS + lane / T) * p.n_rot;
+    const bool exchange = V == 1 || p.half;
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    Vec<TI, V> x[G];
+    auto load = [&](int h) {
+        if (h >= h_end) return;
+        const Side &s = p.side[h >= p.side[0].heads];
+        const int hh = h >= p.side[0].heads ? h - p.side[0].heads : h;
+        const TI *row = static_cast<const TI *>(s.x) + token * s.x_token + hh * s.x_head;
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            const int e = (g * T + t) * V;
+            if (e < p.d) load_vec<TI, V>(x[g], row + e);
+        }
+    };
+    int h = h0 + warp * ROWS + lane / T;
+    load(h);
+    if ((int)threadIdx.x < p.n_rot / 2) {
+        const unsigned long long pos = (unsigned long long)p.pos[token];
+        for (int j = threadIdx.x; j < p.n_rot / 2; j += THREADS) {
+            const float2 v = cos_sin_turns(pos * p.turns[j]);
+            cs[j] = make_float2(p.magnitude * v.x, p.inverse ? -p.magnitude * v.y : p.magnitude * v.y);
+        }
+    }
+    __syncthreads();
+
+    // whole warps go round together: some of a warp's rows may be past the end
+    for (int hw = h0 + warp * ROWS; hw < h_end; hw += WARPS * ROWS, h += WARPS * ROWS) {
+        const bool live = h < h_end;
+        const Side &s = p.side[live && h >= p.side[0].heads];
+        const int hh = h >= p.side[0].heads ? h - p.side[0].heads : h;
+        float y[G][V];
+        float ss = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            const bool in = live && (g * T + t) * V < p.d;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                y[g][j] = in ? to_float(x[g].v[j]) : 0.f;
+                if (NORM) ss = fmaf(y[g][j], y[g][j], ss);
+            }
+        }
+        load(h + WARPS * ROWS);
+        if (NORM) {
+#pragma unroll
+            for (int o = T / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            float rstd = 1.0f / sqrtf(fmaf(ss, p.inv_d, p.eps));
+            if (__any_sync(0xffffffffu, ss > 3.0e38f)) {                 // squares past float's range: those rows at 2^-80
+                const float down = ss > 3.0e38f ? 0x1p-80f : 1.0f;
+                float s2 = 0.f;
+#pragma unroll
+                for (int g = 0; g < G; g++)
+#pragma unroll
+                    for (int j = 0; j < V; j++) {
+                        y[g][j] *= down;
+                        s2 = fmaf(y[g][j], y[g][j], s2);
+                    }
+#pragma unroll
+                for (int o = T / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+                if (ss > 3.0e38f) rstd = 1.0f / sqrtf(s2 * p.inv_d);     // eps <= 1 is nothing beside such squares
+            }
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const int e = (g * T + t) * V;
+#pragma unroll
+                for (int j = 0; j < V; j++) y[g][j] *= rstd;
+                if (s.gain && e < p.d) {
+                    if constexpr (V == 8) {
+                        const float4 a = reinterpret_cast<const float4 *>(s.gain + e)[0], b = reinterpret_cast<const float4 *>(s.gain + e)[1];
+                        y[g][0] *= a.x; y[g][1] *= a.y; y[g][2] *= a.z; y[g][3] *= a.w;
+                        y[g][4] *= b.x; y[g][5] *= b.y; y[g][6] *= b.z; y[g][7] *= b.w;
+                    } else {
+                        y[g][0] *= s.gain[e];
+                    }
+                }
+            }
+        }
+        if (exchange && p.n_rot > 0) {
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const int r = (g * T + t) * V - p.first;
+                if (r >= 0 && r < p.n_rot) {
+                    if constexpr (V == 8) {
+                        reinterpret_cast<float4 *>(buf + r)[0] = make_float4(y[g][0], y[g][1], y[g][2], y[g][3]);
+                        reinterpret_cast<float4 *>(buf + r)[1] = make_float4(y[g][4], y[g][5], y[g][6], y[g][7]);
+                    } else {
+                        buf[r] = y[g][0];
+                    }
+                }
+            }
+            __syncwarp();
+            const int hr = p.n_rot / 2;
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const int r = (g * T + t) * V - p.first;
+                if (r >= 0 && r < p.n_rot) {
+                    const bool second = p.half ? r >= hr : (r & 1) != 0;     // the pair's b
+                    const int other = p.half ? (second ? r - hr : r + hr) : r ^ 1;
+                    const int pair = p.half ? (second ? r - hr : r) : r >> 1;
+                    if constexpr (V == 8) {
+                        const float4 u = reinterpret_cast<const float4 *>(buf + other)[0], w = reinterpret_cast<const float4 *>(buf + other)[1];
+                        const float o[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            const float4 c = *reinterpret_cast<const float4 *>(cs + pair + j);
+                            y[g][j] = second ? fmaf(o[j], c.y, y[g][j] * c.x) : fmaf(-o[j], c.y, y[g][j] * c.x);
+                            y[g][j + 1] = second ? fmaf(o[j + 1], c.w, y[g][j + 1] * c.z) : fmaf(-o[j + 1], c.w, y[g][j + 1] * c.z);
+                        }
+                    } else {
+                        const float o = buf[other];
+                        const float2 c = cs[pair];
+                        y[g][0] = second ? fmaf(o, c.y, y[g][0] * c.x) : fmaf(-o, c.y, y[g][0] * c.x);
+                    }
+                }
+            }
+        } else if constexpr (V == 8) {
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const int r = (g * T + t) * V - p.first;                     // even
+                if (r > -V && r < p.n_rot) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        if (r + j < 0 || r + j >= p.n_rot) continue;
+                        const float2 c = cs[(r + j) >> 1];
+                        const float a = y[g][j], b = y[g][j + 1];
+                        y[g][j] = fmaf(-b, c.y, a * c.x);
+                        y[g][j + 1] = fmaf(b, c.x, a * c.y);
+                    }
+                }
+            }
+        }
+        int64_t row = token;
+        bool keep = live;
+        if (live && s.slots) {
+            row = s.slots[token];
+            keep = row >= 0 && row < s.n_slots;
+            if (row >= s.n_slots && t == 0) atomicOr(&g_heads_err, 1u);
+        }
+        if (keep) {
+            const int64_t at = row * s.out_token + hh * s.out_head;
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const int e = (g * T + t) * V;
+                if (e < p.d) store_vec<V>(s.out, at + e, y[g], s.out_f32);
+            }
+        }
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+template <typename TI, int V, int T, int G>
+cudaError_t launch_form(Params p, uint32_t n, bool norm, cudaStream_t s) {
+    constexpr int ROWS = WARPS * (32 / T);                     // rows a block works on at a time
+    const int heads = p.side[0].heads + p.side[1].heads, most = (heads + ROWS - 1) / ROWS;
+    // A block takes all heads of its token once there are tokens for four blocks to an SM; fewer tokens are cut
+    // into as many blocks as the heads allow.
+    const int64_t want = 4ll * sm_count();
+    int chunks = (int)((want + n - 1) / n);
+    chunks = chunks < most ? chunks : most;
+    p.chunk = (most + chunks - 1) / chunks * ROWS;
+    p.chunks = (heads + p.chunk - 1) / p.chunk;
+    size_t smem = (size_t)((p.n_rot + 3) & ~3) * 4;
+    if (V == 1 || p.half) smem += (size_t)ROWS * p.n_rot * 4;
+    const dim3 grid((unsigned)((uint64_t)n * p.chunks));
+    auto run = [&](auto kernel) {
+        const cudaError_t e = ensure_dyn_smem(kernel, smem);
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(THREADS), smem, s, p);
+    };
+    return norm ? run(heads_kernel<TI, V, T, G, true>) : run(heads_kernel<TI, V, T, G, false>);
+}
+
+template <typename TI>
+cudaError_t launch_type(const Params &p, uint32_t n, bool norm, bool vec, cudaStream_t s) {
+    if (!vec) return p.d <= 256 ? launch_form<TI, 1, 32, 8>(p, n, norm, s) : launch_form<TI, 1, 32, 32>(p, n, norm, s);
+    if (p.d <= 64) return launch_form<TI, 8, 8, 1>(p, n, norm, s);
+    if (p.d <= 128) return launch_form<TI, 8, 16, 1>(p, n, norm, s);
+    if (p.d <= 256) return launch_form<TI, 8, 32, 1>(p, n, norm, s);
+    if (p.d <= 512) return launch_form<TI, 8, 32, 2>(p, n, norm, s);
+    return launch_form<TI, 8, 32, 4>(p, n, norm, s);
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+}  // namespace
+
+cudaError_t launch_rotate_heads(const ds4c_rotate_args &a, cudaStream_t s) {
+    Params p{};
+    bool vec = a.d % 8 == 0 && (a.half ? a.first % 8 == 0 && a.n_rot % 16 == 0 : a.first % 2 == 0);
+    const ds4c_head_rows *side[2] = {&a.q, &a.k};
+    const size_t in_bytes = a.dtype == DS4C_F32 ? 4 : 2;
+    for (int i = 0; i < 2; i++) {
+        const ds4c_head_rows &r = *side[i];
+        Side &o = p.side[i];
+        if (r.heads == 0) continue;
+        const size_t out_bytes = r.out_dtype == DS4C_F32 ? 4 : 2;
+        o.x = r.x; o.out = r.out; o.gain = r.gain; o.slots = r.slots;
+        o.x_token = (int64_t)r.x_token; o.x_head = (int64_t)r.x_head;
+        o.out_token = (int64_t)r.out_token; o.out_head = (int64_t)r.out_head;
+        o.n_slots = (int64_t)r.n_slots;
+        o.heads = (int)r.heads;
+        o.out_f32 = r.out_dtype == DS4C_F32;
+        vec = vec && aligned16(r.x) && aligned16(r.out) && aligned16(r.gain) && r.x_token * in_bytes % 16 == 0 &&
+              r.x_head * in_bytes % 16 == 0 && r.out_token * out_bytes % 16 == 0 && r.out_head * out_bytes % 16 == 0;
+    }
+    p.pos = a.positions;
+    p.turns = reinterpret_cast<const unsigned long long *>(a.turns);
+    p.magnitude = a.magnitude;
+    p.eps = a.eps;
+    p.inv_d = 1.0f / (float)a.d;
+    p.d = (int)a.d; p.n_rot = (int)a.n_rot; p.first = (int)a.first;
+    p.half = a.half != 0; p.inverse = a.inverse != 0;
+    return a.dtype == DS4C_F32 ? launch_type<float>(p, a.n, a.norm != 0, vec, s)
+                               : launch_type<__nv_bfloat16>(p, a.n, a.norm != 0, vec, s);
+}
+
+unsigned int heads_read_clear_error() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_heads_err, sizeof v) != cudaSuccess) return 0;
+    if (v) cudaMemcpyToSymbol(g_heads_err, &z, sizeof z);
+    return v;
+}
+
+}  // namespace ds4c

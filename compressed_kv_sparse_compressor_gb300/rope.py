@@ -1,0 +1,178 @@
+"""Rotary positions of heads on torch tensors over the C ABI: tables (plain or scaled for long contexts),
+the rotation and its inverse, and the norm of each head of queries and keys with the rotation in the
+same pass, keys to the pages of a cache.  Marshalling only.
+
+Rows are heads [n tokens, heads, d] (or [n, d]: one head), float32 or bfloat16, the d values of a row
+contiguous, any strides between rows.  Of the d values, table.n_rot from `first` on are rotated (None:
+the last ones): neighbours in pairs, or with half=True value j with value j + n_rot / 2.
+
+Calls run on the current stream of the tensors' device.  A slot behind the cache writes nothing;
+``fp8.sync`` reports it."""
+
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import abi
+from .fp8 import run
+
+_DTYPES = {torch.float32: abi.DS4C_F32, torch.bfloat16: abi.DS4C_BF16}
+_SCALINGS = {None: abi.DS4C_ROPE_PLAIN, "linear": abi.DS4C_ROPE_LINEAR, "yarn": abi.DS4C_ROPE_YARN}
+
+
+class Table:
+    """theta_j of n_rot / 2 pairs as whole numbers of 2^-64 turns (int64 on the device), and the magnitude that cosine
+    and sine are multiplied by."""
+
+    def __init__(self, turns, magnitude: float = 1.0):
+        if turns.dim() != 1 or turns.dtype != torch.int64 or turns.get_device() < 0 or not turns.is_contiguous():
+            raise ValueError(f"turns: {turns.dtype} {tuple(turns.shape)} on {turns.device}, expected contiguous int64 (pairs,) on "
+                             "a CUDA device")
+        self.turns, self.magnitude = turns, float(magnitude)
+        self.n_rot = 2 * turns.shape[0]
+        self.device_index = turns.get_device()
+        self._ptr = turns.data_ptr()
+
+
+def turns(n_rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0,
+          beta_slow: float = 1.0, magnitude: float = 0.0):
+    """(turns as a host int64 tensor, magnitude) of a table, by the header's formulas."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling {scaling!r}: None, 'linear' or 'yarn'")
+    if not 2 <= n_rot <= 1024:
+        raise ValueError(f"n_rot {n_rot}: even, 2 to 1024")
+    host = (C.c_uint64 * (n_rot // 2))()
+    status, m = abi.ds4c_rope_table(abi.RopeParams(n_rot, _SCALINGS[scaling], base, factor, original, beta_fast, beta_slow,
+                                                   magnitude), host)
+    abi.check(status, "ds4c_rope_table")
+    return torch.tensor(list(host), dtype=torch.int64), m
+
+
+def table(n_rot: int, base: float = 10000.0, *, scaling=None, factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0,
+          beta_slow: float = 1.0, magnitude: float = 0.0, device="cuda") -> Table:
+    """A rotary table: theta_j = base^(-2j / n_rot), with scaling "linear" divided by `factor`, with "yarn" only the
+    slow pairs (`original`: the context the model was trained on).  magnitude 0: the scaling's own."""
+    t, m = turns(n_rot, base, scaling, factor, original, beta_fast, beta_slow, magnitude)
+    return Table(t.to(device), m)
+
+
+def _rows(t, what):
+    """(n, heads, d, token stride, head stride) of rows of heads; a stride that no step uses is 0."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        n, heads, d = shape
+        st, sh, sd = stride
+    elif len(shape) == 2:
+        (n, d), (st, sd), heads, sh = shape, stride, 1, 0
+    else:
+        raise ValueError(f"{what}: {tuple(shape)}, expected (tokens, heads, d) or (tokens, d)")
+    if sd != 1 and d > 1:
+        raise ValueError(f"{what}: the rows' elements must be contiguous")
+    return n, heads, d, st if n > 1 else 0, sh if heads > 1 else 0
+
+
+def _side(x, out, gain, n, d, dev, what):
+    """HeadRows of x -> out (the same shape, float32 or bfloat16)."""
+    xn, heads, xd, xt, xh = _rows(x, what)
+    if xn != n or xd != d or x.get_device() != dev:
+        raise ValueError(f"{what}: {tuple(x.shape)} on {x.device}, expected {n} tokens of {d} values on cuda:{dev}")
+    if out is not x:
+        if out.shape != x.shape or out.get_device() != dev or out.dtype not in _DTYPES:
+            raise ValueError(f"{what}'s output: {out.dtype} {tuple(out.shape)} on {out.device}, expected float32 or bfloat16 "
+                             f"{tuple(x.shape)} on cuda:{dev}")
+        _, _, _, ot, oh = _rows(out, f"{what}'s output")
+    else:
+        ot, oh = xt, xh
+    return abi.HeadRows(x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, _gain(gain, d, dev, what), None, 0, heads, _DTYPES[out.dtype])
+
+
+def _gain(gain, d, dev, what):
+    if gain is None:
+        return None
+    if gain.shape != (d,) or gain.dtype != torch.float32 or gain.get_device() != dev or not gain.is_contiguous():
+        raise ValueError(f"gain of {what}: {gain.dtype} {tuple(gain.shape)} on {gain.device}, expected contiguous float32 {(d,)} on "
+                         f"cuda:{dev}")
+    return gain.data_ptr()
+
+
+def _index(t, n, dev, what):
+    if t.shape != (n,) or t.dtype != torch.int64 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous int64 {(n,)} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _args(x, positions, table, first, half, inverse, norm, eps):
+    """RotateArgs without its rows."""
+    dt, dev, shape = _DTYPES.get(x.dtype), x.get_device(), x.shape
+    if dt is None or dev < 0:
+        raise ValueError(f"rows: {x.dtype} on {x.device}, expected float32 or bfloat16 on a CUDA device")
+    n, d = shape[0], shape[-1]
+    n_rot, turns, magnitude, pos = 0, None, 1.0, None
+    if table is not None:
+        if table.device_index != dev:
+            raise ValueError(f"table on cuda:{table.device_index}, rows on {x.device}")
+        n_rot, turns, magnitude = table.n_rot, table._ptr, table.magnitude
+        pos = _index(positions, n, dev, "positions")
+    if first is None:
+        first = d - n_rot
+    if first < 0 or first + n_rot > d:
+        raise ValueError(f"values {first} .. {first + n_rot - 1} of rows of {d}")
+    return abi.RotateArgs(n, d, dt, n_rot, first, half, inverse, norm, eps, magnitude, pos, turns), n, d, dev
+
+
+def rotate(x, positions, table: Table, *, first=None, half: bool = False, inverse: bool = False, out=None):
+    """x [n, heads, d] with its rotated part turned by positions [n] (int64), by the negative positions if `inverse` (which
+    undoes a rotation of magnitude 1 and is the gradient of any).  out: x's shape, float32 or bfloat16, x itself
+    allowed; allocated in x's type if None."""
+    a, n, d, dev = _args(x, positions, table, first, half, inverse, 0, 0.0)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a.q = _side(x, out, None, n, d, dev, "x")
+    run(dev, abi.ds4c_rotate_heads, a)
+    return out
+
+
+def norm_rotate(q, positions, table: Table | None, *, gain=None, k=None, k_gain=None, eps: float = 1e-6, first=None,
+                half: bool = False, out=None, k_out=None, cache=None, slots=None):
+    """RMSNorm of each head of q [n, heads, d], with gain [d] float32 or None (ones), and the rotation by positions
+    [n] (table None: no rotation), in one pass.  Returns q's result in `out` (allocated in q's type if None).
+
+    k [n, k heads, d] (or [n, d]) of q's type takes the same with k_gain, in the same launch.  Its result goes to k_out
+    (k's shape, k itself allowed), or to a cache [pages, page rows, d] (one head) or [pages, page rows, k heads, d]:
+    token i's rows to slot slots[i] = page * page rows + row (int64; below 0: nowhere)."""
+    a, n, d, dev = _args(q, positions, table, first, half, False, 1, eps)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    a.q = _side(q, out, gain, n, d, dev, "q")
+    if k is None:
+        if k_out is not None or cache is not None or slots is not None or k_gain is not None:
+            raise ValueError("k's output, gain or slots without k")
+    else:
+        if k.dtype != q.dtype:
+            raise ValueError(f"k: {k.dtype}, expected q's {q.dtype}")
+        if (k_out is None) == (cache is None) or (cache is None) != (slots is None):
+            raise ValueError("k needs k_out, or cache and slots")
+        if cache is None:
+            a.k = _side(k, k_out, k_gain, n, d, dev, "k")
+        else:
+            a.k = _cached(k, cache, slots, k_gain, n, d, dev)
+    run(dev, abi.ds4c_rotate_heads, a)
+    return out
+
+
+def _cached(k, cache, slots, k_gain, n, d, dev):
+    """HeadRows of k -> slots of a cache of pages."""
+    kn, heads, kd, kt, kh = _rows(k, "k")
+    shape, stride = cache.shape, cache.stride()
+    if kn != n or kd != d or k.get_device() != dev:
+        raise ValueError(f"k: {tuple(k.shape)} on {k.device}, expected {n} tokens of {d} values on cuda:{dev}")
+    if len(shape) not in (3, 4) or shape[-1] != d or (shape[2] if len(shape) == 4 else 1) != heads or cache.dtype not in _DTYPES or \
+            cache.get_device() != dev:
+        raise ValueError(f"cache: {cache.dtype} {tuple(shape)} on {cache.device}, expected float32 or bfloat16 (pages, page rows, "
+                         f"{'' if heads == 1 else f'{heads}, '}{d}) on cuda:{dev}")
+    if not cache.is_contiguous():
+        raise ValueError(f"cache: stride {stride}, expected contiguous pages")
+    return abi.HeadRows(k.data_ptr(), cache.data_ptr(), kt, kh, heads * d, d, _gain(k_gain, d, dev, "k"),
+                        _index(slots, n, dev, "slots"), shape[0] * shape[1], heads, _DTYPES[cache.dtype])

@@ -334,6 +334,64 @@ DS4C_API ds4c_status ds4c_compress_decode_step_quant(const ds4c_layer_cfg *cfg, 
                                                      const uint64_t *pos_h, uint32_t n_seq, void *ws, size_t ws_bytes,
                                                      cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Heads: norm of each head of queries and keys, rotary positions.
+ *
+ * A rotary table is theta_j, the angle by which pair j of n_rot / 2 turns per position, as whole
+ * numbers of 2^-64 turns (round(theta_j / 2 pi * 2^64)), so that pos * theta_j modulo a turn is exact
+ * for every position, and a magnitude that multiplies cosine and sine.  ds4c_rope_table fills a host
+ * array of n_rot / 2 with theta_j = base^(-2 j / n_rot), scaled for long contexts:
+ *   DS4C_ROPE_LINEAR  theta_j / factor;
+ *   DS4C_ROPE_YARN    theta_j (1 - g) + theta_j / factor * g, g = clamp((j - lo) / (hi - lo), 0, 1) with
+ *                     lo = floor(pair(beta_fast)) and hi = ceil(pair(beta_slow)) in 0 .. n_rot / 2 - 1, pair(b) =
+ *                     n_rot / 2 * ln(original / (2 pi b)) / ln(base) the pair that turns b times within the
+ *                     original context.
+ * magnitude: as given, or where 0 is given 0.1 ln(factor) + 1 (DS4C_ROPE_YARN) and 1 (the others).
+ * n_rot even, 2 .. 1024; 1 < base <= 1e12; 1 <= factor <= 1e6; YaRN: 1 <= original <= 2^40, 0 < beta_slow <= beta_fast <=
+ * 1e6; 0 <= magnitude <= 1e6 (else DS4C_ERR_SHAPE).  Host only.  (The compressor rotates its rows by a float product of
+ * position and plain theta_j; an indexer or attention lane's rows and these may differ in the last bits at far positions.) */
+enum { DS4C_ROPE_PLAIN = 0, DS4C_ROPE_LINEAR = 1, DS4C_ROPE_YARN = 2 };
+typedef struct {
+    uint32_t n_rot, scaling;
+    double base, factor, original, beta_fast, beta_slow, magnitude;
+} ds4c_rope_params;
+DS4C_API ds4c_status ds4c_rope_table(const ds4c_rope_params *params, uint64_t *turns_h, float *magnitude_h);
+
+/* Norm and rotation of the heads of n tokens, queries (q) and keys (k, one launch with the queries; k.heads 0:
+ * none), rows of d values:
+ *   y = x, or with norm != 0: y = x * rstd * gain, rstd = (sum x^2 / d + eps)^-1/2 (gain NULL: ones), in float;
+ *   the pairs of y's values first .. first + n_rot - 1, (2j, 2j+1) of them or with half != 0 (j, j + n_rot / 2),
+ *   become (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t), t = positions[i] * theta_j, or with inverse
+ *   != 0 t = -positions[i] * theta_j (with magnitude 1 what undoes the rotation, with any its gradient);
+ *   rounded once to out_dtype.
+ * Row (i, h) is read at x + i * x_token + h * x_head (elements; input rows may coincide) and written at out +
+ * i * out_token + h * out_head, or with slots at out + slots[i] * out_token + h * out_head: a slot below 0 writes
+ * nothing, one of n_slots or more writes nothing and raises the device error word, the same slot twice leaves
+ * either token's row.  Output rows must not overlap each other (DS4C_ERR_SHAPE), nor any input but in place: out ==
+ * x with the same strides and type, without slots.
+ * d <= 1024, n_rot even, first + n_rot <= d, heads of q and k together 1 .. 1024, n <= 2^24, n * heads <= 2^31 - 1, 1e-12
+ * <= eps <= 1 with norm.  n_rot 0: no rotation (positions and turns may be NULL).  positions, slots and turns: 8-byte
+ * aligned device arrays.  n == 0 does nothing.  Rows of 16-byte aligned addresses and strides, d a multiple of 8 and pairs that a
+ * group of 8 values does not cut are read 16 bytes at a time, others value by value. */
+typedef struct {
+    const void *x;              /* rows of the call's dtype */
+    void *out;
+    size_t x_token, x_head, out_token, out_head;    /* strides, elements */
+    const float *gain;          /* [d] or NULL */
+    const int64_t *slots;       /* [n] or NULL */
+    uint64_t n_slots;
+    uint32_t heads, out_dtype;
+} ds4c_head_rows;
+typedef struct {
+    uint32_t n, d, dtype;
+    uint32_t n_rot, first, half, inverse, norm;
+    float eps, magnitude;
+    const int64_t *positions;   /* [n] */
+    const uint64_t *turns;      /* [n_rot / 2], device */
+    ds4c_head_rows q, k;
+} ds4c_rotate_args;
+DS4C_API ds4c_status ds4c_rotate_heads(const ds4c_rotate_args *args, cudaStream_t stream);
+
 /* Score capacity of ds4c_indexer_topk_noalloc: 2M floats (8 MiB). */
 #define DS4C_NOALLOC_SCORE_FLOATS (2u * 1024u * 1024u)
 

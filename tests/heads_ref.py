@@ -1,0 +1,55 @@
+"""Plain 64-bit implementation of the heads' norm and rotation, and how far a result may be from it."""
+
+import math
+
+import torch
+
+U = 2.0 ** -24
+
+
+def thetas(n_rot, base=10000.0, scaling=None, factor=1.0, original=0.0, beta_fast=32.0, beta_slow=1.0):
+    """Angles per position (64 bits), from the header's formulas."""
+    j = torch.arange(n_rot // 2, dtype=torch.float64)
+    t = torch.exp(-2.0 * j / n_rot * math.log(base))
+    if scaling == "linear":
+        return t / factor
+    if scaling == "yarn":
+        lo = math.floor(n_rot / 2 * math.log(original / (2 * math.pi * beta_fast)) / math.log(base))
+        hi = math.ceil(n_rot / 2 * math.log(original / (2 * math.pi * beta_slow)) / math.log(base))
+        lo, hi = max(lo, 0), min(hi, n_rot // 2 - 1)
+        g = ((j - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        return t * (1 - g) + t / factor * g
+    return t
+
+
+def turned(y, pos, theta, first, half, inverse=False, magnitude=1.0):
+    """(rotated y, sum of the magnitudes that met in each value): y [n, h, d] in 64 bits."""
+    n_rot = 2 * theta.shape[0]
+    out, size = y.clone(), y.abs()
+    if n_rot == 0:
+        return out, size
+    a = pos.double()[:, None] * theta.to(y.device)
+    c, s = magnitude * torch.cos(a)[:, None], magnitude * torch.sin(a)[:, None] * (-1.0 if inverse else 1.0)
+    i0 = torch.arange(n_rot // 2, device=y.device) * (1 if half else 2) + first
+    i1 = i0 + (n_rot // 2 if half else 1)
+    y0, y1 = y[..., i0], y[..., i1]
+    out[..., i0], out[..., i1] = y0 * c - y1 * s, y0 * s + y1 * c
+    size[..., i0] = size[..., i1] = magnitude * (y0.abs() + y1.abs())
+    return out, size
+
+
+def normed(x, gain, eps):
+    x = x.double()
+    y = x / torch.sqrt((x * x).sum(-1, keepdim=True) / x.shape[-1] + eps)
+    return y if gain is None else y * gain.double()
+
+
+def assert_close(got, want, size):
+    """got, rounded once from float arithmetic, against want in 64 bits.  Float arithmetic: the sum of squares in one
+    lane's 32 fused products and 5 additions, halved by the root, 22 steps with the root's own; gain and scale 2; the
+    rotation's cosine and sine 4, its two roundings 2; 32 steps of 2^-24 of the magnitudes that meet cover them (rows of
+    1024 values included).  Then half a step of the output's type."""
+    half_step = torch.finfo(got.dtype).eps / 2
+    tol = 32 * U * size + half_step * want.abs() + 2.0 ** -126
+    bad = ~((got.double() - want).abs() <= tol) & ~(got.isnan() & want.isnan())
+    assert not bad.any(), (int(bad.sum()), float(((got.double() - want).abs() / tol)[bad].max()))

@@ -1,0 +1,221 @@
+"""Norm and rotation of heads on the GPU (-m gpu) against a plain implementation in 64 bits."""
+
+import pytest
+import torch
+
+import heads_ref as ref
+from compressed_kv_sparse_compressor_gb300 import abi, fp8, rope
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+SCALINGS = {"plain": {}, "linear": dict(scaling="linear", factor=4.0), "yarn": dict(scaling="yarn", factor=16.0, original=4096.0)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def positions(g, n, far):
+    return torch.randint(0, far, (n,), generator=g, device="cuda")
+
+
+# rows of 16-byte vectors (every number of lanes and vectors), rows value by value, pairs that a vector cuts
+SHAPES = [(1, 1, 64, 64, 0), (3, 8, 128, 64, 64), (2, 65, 512, 64, 448), (5, 24, 256, 256, 0), (300, 3, 64, 16, 48),
+          (700, 65, 512, 64, 448), (9, 2, 1024, 128, 256), (4, 5, 768, 512, 128), (7, 3, 40, 8, 16), (6, 4, 96, 32, 10),
+          (5, 2, 65, 64, 1), (3, 3, 7, 2, 5), (4, 1, 1, 0, 0), (2, 2, 1023, 1022, 1), (3, 130, 72, 24, 3), (2, 4, 128, 48, 64),
+          (2, 1, 2, 2, 0), (160, 9, 257, 64, 193)]
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,h,d,rot,first", SHAPES)
+def test_norm_and_rotation(n, h, d, rot, first, dtype, half):
+    g = gen(n + h + d + rot)
+    kh = 1 + h % 3
+    q = (randn(g, n, h, d) * torch.exp(randn(g, d))).to(dtype)
+    k = (randn(g, n, kh, d) * torch.exp(randn(g, d))).to(dtype)
+    gq, gk = 1 + 0.1 * randn(g, d), (None if h % 2 else 1 + 0.1 * randn(g, d))
+    pos = positions(g, n, 1 << 20)
+    kw = SCALINGS[("plain", "linear", "yarn")[(n + d) % 3]]
+    table = rope.table(rot, base=5000.0, **kw) if rot else None
+    theta, m = ref.thetas(rot, 5000.0, **kw), table.magnitude if rot else 1.0
+    k_out = torch.empty(k.shape, dtype=torch.float32, device="cuda")
+    out = rope.norm_rotate(q, pos, table, gain=gq, k=k, k_gain=gk, eps=EPS, first=first, half=half, k_out=k_out)
+    assert out.dtype == dtype
+    ref.assert_close(out, *ref.turned(ref.normed(q, gq, EPS), pos, theta, first, half, magnitude=m))
+    ref.assert_close(k_out, *ref.turned(ref.normed(k, gk, EPS), pos, theta, first, half, magnitude=m))
+    if rot:
+        for inverse in (False, True):
+            got = rope.rotate(q, pos, table, first=first, half=half, inverse=inverse)
+            ref.assert_close(got, *ref.turned(q.double(), pos, theta, first, half, inverse, m))
+    fp8.sync()
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_far_positions_are_exact(half):
+    """Whole numbers of turns: positions past float's and past 32 bits, and negative ones (64-bit angles of the reference
+    hold 2^40 * theta to 2^-12 of a radian only, so the reference is in whole numbers too)."""
+    g = gen(3)
+    x = randn(g, 6, 4, 64)
+    turns, _ = rope.turns(64)
+    t = rope.Table(turns.cuda())
+    at = [0, 1, (1 << 24) + 1, (1 << 40) + 12345, -1, -(1 << 33) - 7]
+    pos = torch.tensor(at, device="cuda")
+    frac = torch.tensor([[float(((p * int(w)) % (1 << 64))) / 2.0 ** 64 for w in turns] for p in at], dtype=torch.float64, device="cuda")
+    got = rope.rotate(x, pos, t, half=half)
+    # the angle's fraction of a turn as theta, at position 1
+    for i in range(len(at)):
+        want = ref.turned(x[i:i + 1].double(), torch.ones(1, device="cuda"), 2 * torch.pi * frac[i].cpu(), 0, half)
+        ref.assert_close(got[i:i + 1], *want)
+
+
+def test_rotation_and_its_inverse_and_gradient():
+    g = gen(4)
+    n, h, d = 33, 5, 128
+    x, w = randn(g, n, h, d), randn(g, n, h, d)
+    pos = positions(g, n, 100000)
+    for kw in SCALINGS.values():
+        t = rope.table(64, **kw)
+        for half in (False, True):
+            y = rope.rotate(x, pos, t, half=half)
+            gx = rope.rotate(w, pos, t, half=half, inverse=True)
+            # <w, R x> = <R^T w, x>, row by row, and against differences: R is linear, so a step of any size does
+            a, b = (w.double() * y.double()).sum(-1), (gx.double() * x.double()).sum(-1)
+            scale = w.double().norm(dim=-1) * x.double().norm(dim=-1) * t.magnitude
+            assert ((a - b).abs() <= 64 * ref.U * scale).all()
+            step = rope.rotate(x + w, pos, t, half=half)
+            dy = rope.rotate(w, pos, t, half=half)
+            assert ((step.double() - y.double() - dy.double()).abs() <= 16 * ref.U * t.magnitude * 2 * (x.abs() + w.abs()).max()).all()
+            if t.magnitude == 1.0:
+                back = rope.rotate(y, pos, t, half=half, inverse=True)
+                assert (back - x).abs().max() <= 32 * ref.U * 2 * x.abs().max()
+
+
+def test_strides_and_in_place():
+    g = gen(5)
+    n, hq, hk, d = 77, 6, 2, 96
+    t, theta = rope.table(32), ref.thetas(32)
+    pos = positions(g, n, 5000)
+    for off in (0, 1, 3):                                         # a fused projection's output, aligned and not
+        fused = randn(g, n, (hq + hk) * d + 40 + off).bfloat16()
+        q = fused[:, off:off + hq * d].view(n, hq, d)
+        k = fused[:, off + hq * d:off + (hq + hk) * d].view(n, hk, d)
+        wq = ref.turned(ref.normed(q, None, EPS), pos, theta, d - 32, False)
+        wk = ref.turned(ref.normed(k, None, EPS), pos, theta, d - 32, False)
+        rest = fused.clone()
+        # heads before tokens on the way out
+        out = torch.empty(hq, n, d, device="cuda").transpose(0, 1)
+        rope.norm_rotate(q, pos, t, out=out, k=k, k_out=k)
+        ref.assert_close(out, *wq)
+        ref.assert_close(k, *wk)
+        rest[:, off + hq * d:off + (hq + hk) * d] = k.reshape(n, hk * d)
+        assert torch.equal(fused, rest)
+    x = randn(g, n, d)                                            # two dimensions, in place
+    want = ref.turned(x.double()[:, None], pos, theta, 0, True)
+    assert rope.rotate(x, pos, t, first=0, half=True, out=x) is x
+    ref.assert_close(x[:, None], *want)
+    one = randn(g, 1, 1, d)                                       # one row read for all tokens and heads
+    got = rope.rotate(one.expand(n, 3, d), pos, t)
+    ref.assert_close(got, *ref.turned(one.expand(n, 3, d).double(), pos, theta, d - 32, False))
+    assert rope.rotate(x[:0], pos[:0], t).shape == (0, d)
+    fp8.sync()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("heads", [1, 3])
+def test_keys_to_slots(dtype, heads):
+    g = gen(6)
+    n, d, page, pages = 41, 128, 16, 9
+    q, k = randn(g, n, 4, d), randn(g, n, heads, d)
+    t, theta = rope.table(64), ref.thetas(64)
+    pos = positions(g, n, 70000)
+    cache = randn(g, pages, page, heads, d).to(dtype)
+    if heads == 1:
+        cache = cache[:, :, 0].contiguous()
+    before = cache.clone()
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:n].contiguous()
+    slots[0], slots[1] = pages * page - 1, 0
+    slots[2:] = torch.where((slots[2:] == 0) | (slots[2:] == pages * page - 1), -5, slots[2:])
+    slots[7] = -1
+    slots[8] = -(1 << 62)
+    rope.norm_rotate(q, pos, t, k=k, cache=cache, slots=slots)
+    want, size = ref.turned(ref.normed(k, None, EPS), pos, theta, d - 64, False)
+    live = slots >= 0
+    flat = cache.view(pages * page, heads, d)
+    ref.assert_close(flat[slots[live]], want[live], size[live])
+    others = torch.ones(pages * page, dtype=torch.bool, device="cuda")
+    others[slots[live]] = False
+    assert torch.equal(flat[others], before.view(pages * page, heads, d)[others])
+    fp8.sync()
+    # slots behind the cache: nothing written, reported once
+    bad = torch.full((n,), pages * page, device="cuda")
+    bad[1] = 1 << 62
+    now = cache.clone()
+    rope.norm_rotate(q, pos, t, k=k, cache=cache, slots=bad)
+    with pytest.raises(abi.Ds4cError) as e:
+        fp8.sync()
+    assert e.value.status == abi.DS4C_ERR_DEVICE
+    assert torch.equal(cache, now)
+    fp8.sync()
+
+
+def test_extreme_rows():
+    g = gen(7)
+    for dtype in (torch.bfloat16, torch.float32):
+        for d in (64, 512, 1000, 33):
+            x = randn(g, 9, 2, d)
+            x[0] = 0
+            x[1] *= 1e30
+            x[2] *= 1e38
+            x[2].clamp_(-3e38, 3e38)
+            x[3] *= 1e-30
+            x[4, 0, 1] = float("nan")
+            x[5, 1, 0] = 3e38
+            x = x.to(dtype)
+            got = rope.norm_rotate(x, torch.zeros(9, dtype=torch.int64, device="cuda"), None)
+            want = ref.normed(x, None, EPS)
+            ref.assert_close(got, want, want.abs())
+            assert got[4, 0].isnan().all() and not got[4, 1].isnan().any()
+            x[6, 0, 0] = float("inf")                             # no finite norm: what the formula gives in float
+            got = rope.norm_rotate(x, torch.zeros(9, dtype=torch.int64, device="cuda"), None)
+            assert got[6, 0, 0].isnan() and (got[6, 0, 1:] == 0).all() and not got[6, 1].isnan().any()
+
+
+def test_streams_and_graphs():
+    g = gen(8)
+    n, h, d = 50, 8, 512
+    t, theta = rope.table(64), ref.thetas(64)
+    q, k = randn(g, n, h, d).bfloat16(), randn(g, n, d).bfloat16()
+    pos, slots = positions(g, n, 9000), torch.randperm(64, generator=g, device="cuda")[:n].contiguous()
+    cache, out = torch.zeros(4, 16, d, dtype=torch.bfloat16, device="cuda"), torch.empty_like(q)
+    want = ref.turned(ref.normed(q, None, EPS), pos, theta, d - 64, False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        rope.norm_rotate(q, pos, t, k=k, cache=cache, slots=slots, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    ref.assert_close(out, *want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rope.norm_rotate(q, pos, t, k=k, cache=cache, slots=slots, out=out)
+        back = rope.rotate(out, pos, t, inverse=True)
+    q.copy_(randn(g, n, h, d))
+    pos.add_(17)
+    graph.replay()
+    want = ref.turned(ref.normed(q, None, EPS), pos, theta, d - 64, False)
+    ref.assert_close(out, *want)
+    ref.assert_close(back, *ref.turned(out.double(), pos, theta, d - 64, False, True))
+    wk = ref.turned(ref.normed(k[:, None], None, EPS), pos, theta, d - 64, False)
+    ref.assert_close(cache.view(64, 1, d)[slots], *wk)

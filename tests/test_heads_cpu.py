@@ -1,0 +1,102 @@
+"""Rotary tables, and host validation of the heads' norm and rotation: bad arguments refused before any launch."""
+
+import ctypes as C
+import math
+
+import pytest
+import torch
+
+import heads_ref as ref
+from compressed_kv_sparse_compressor_gb300 import abi, rope
+from compressed_kv_sparse_compressor_gb300 import build as build_mod
+
+FAKE = 1 << 20          # an aligned non-NULL address that is never dereferenced
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build_mod.build()
+    abi.lib()
+
+
+@pytest.mark.parametrize("n_rot,base,kw,magnitude", [
+    (64, 10000.0, {}, 1.0), (2, 5.0, {}, 1.0), (1024, 1e6, {}, 1.0), (128, 500000.0, dict(scaling="linear", factor=8.0), 1.0),
+    (64, 10000.0, dict(scaling="yarn", factor=16.0, original=65536.0), 0.1 * math.log(16.0) + 1.0),
+    (128, 1e6, dict(scaling="yarn", factor=40.0, original=4096.0, beta_fast=20.0, beta_slow=2.0), 0.1 * math.log(40.0) + 1.0),
+    (16, 10000.0, dict(scaling="yarn", factor=4.0, original=2.0), 0.1 * math.log(4.0) + 1.0),     # every pair slow
+    (64, 10000.0, dict(scaling="yarn", factor=4.0, original=1e12), 0.1 * math.log(4.0) + 1.0)])   # every pair fast
+def test_tables(n_rot, base, kw, magnitude):
+    turns, m = rope.turns(n_rot, base, **kw)
+    want = ref.thetas(n_rot, base, **kw) / (2 * math.pi)
+    got = torch.tensor([int(t) / 2.0 ** 64 for t in turns], dtype=torch.float64)
+    assert turns.shape == (n_rot // 2,) and (turns > 0).all()
+    assert ((got - want).abs() <= 2.0 ** -48 * want + 2.0 ** -65).all()    # pow, quotient and exp: a few steps of 2^-53 of 700
+    assert m == pytest.approx(magnitude, rel=2.0 ** -23)
+    assert rope.turns(n_rot, base, magnitude=1.5, **kw)[1] == 1.5
+
+
+def test_table_refusals():
+    def call(out=True, **kw):
+        f = dict(n_rot=64, scaling=0, base=10000.0, factor=1.0, original=4096.0, beta_fast=32.0, beta_slow=1.0, magnitude=0.0)
+        f.update(kw)
+        return abi.ds4c_rope_table(abi.RopeParams(**f), (C.c_uint64 * 512)() if out else None)[0]
+    assert call() == abi.DS4C_OK
+    assert call(out=False) == abi.DS4C_ERR_NULL
+    nan, inf = float("nan"), float("inf")
+    for kw in (dict(n_rot=0), dict(n_rot=63), dict(n_rot=1026), dict(scaling=3), dict(base=1.0), dict(base=nan), dict(base=inf),
+               dict(magnitude=-1.0), dict(magnitude=nan), dict(scaling=1, factor=0.5), dict(scaling=1, factor=nan),
+               dict(scaling=2, factor=2.0, original=0.0), dict(scaling=2, factor=2.0, beta_slow=0.0),
+               dict(scaling=2, factor=2.0, beta_slow=33.0), dict(scaling=2, factor=inf), dict(scaling=2, original=nan)):
+        assert call(**kw) == abi.DS4C_ERR_SHAPE, kw
+    for bad in (dict(scaling="ntk"), dict(n_rot=2048)):
+        with pytest.raises(ValueError):
+            rope.turns(**{"n_rot": 64, **bad})
+    with pytest.raises(abi.Ds4cError):
+        rope.turns(63)
+    with pytest.raises(ValueError):
+        rope.Table(torch.zeros(4, dtype=torch.int64))             # not on a GPU
+
+
+def rows(**kw):
+    f = dict(x=FAKE, out=2 * FAKE, x_token=1024, x_head=128, out_token=1024, out_head=128, gain=None, slots=None, n_slots=0, heads=8,
+             out_dtype=abi.DS4C_BF16)
+    f.update(kw)
+    return abi.HeadRows(**f)
+
+
+def call(q=None, k=None, **kw):
+    f = dict(n=4, d=128, dtype=abi.DS4C_BF16, n_rot=64, first=64, half=0, inverse=0, norm=1, eps=1e-6, magnitude=1.0,
+             positions=FAKE, turns=FAKE)
+    f.update(kw)
+    return abi.ds4c_rotate_heads(abi.RotateArgs(**f, q=rows(**(q or {})), k=abi.HeadRows() if k is None else rows(**k)), None)
+
+
+def test_rotation_refusals():
+    nan = float("nan")
+    assert abi.lib().ds4c_rotate_heads(None, None) == abi.DS4C_ERR_NULL
+    assert call(n=0) == abi.DS4C_OK
+    for q in (dict(x=None), dict(out=None)):
+        assert call(q) == abi.DS4C_ERR_NULL, q
+        assert call(k=q) == abi.DS4C_ERR_NULL, q
+    assert call(positions=None) == call(turns=None) == abi.DS4C_ERR_NULL
+    for kw in (dict(d=0), dict(d=1025), dict(dtype=2), dict(n=(1 << 24) + 1), dict(n_rot=63), dict(first=65), dict(first=1 << 31),
+               dict(first=129, n_rot=0), dict(eps=0.0), dict(eps=nan), dict(eps=2.0), dict(positions=FAKE + 4), dict(turns=FAKE + 4),
+               dict(magnitude=nan), dict(magnitude=-1.0)):
+        assert call(**kw) == abi.DS4C_ERR_SHAPE, kw
+    for q in (dict(heads=0), dict(heads=1025), dict(x=FAKE + 1), dict(out=FAKE + 1), dict(out_dtype=2), dict(out_head=127),
+              dict(out_token=1023), dict(out_token=0), dict(gain=FAKE + 2), dict(slots=FAKE + 4, n_slots=9), dict(x_token=1 << 41),
+              dict(out=FAKE, out_token=2048), dict(out=FAKE, out_dtype=abi.DS4C_F32), dict(out=FAKE, slots=FAKE, n_slots=9),
+              dict(slots=FAKE, n_slots=9, out_token=1023), dict(slots=FAKE, n_slots=9, out_token=128, out_head=4 * 128)):
+        assert call(q) == abi.DS4C_ERR_SHAPE, q
+        if "heads" not in q:
+            assert call(k=q) == abi.DS4C_ERR_SHAPE, q
+    assert call(k=dict(heads=1020)) == abi.DS4C_ERR_SHAPE         # 1028 heads
+    assert call(dict(heads=1000, x_head=0, out_head=128, out_token=128000), n=1 << 22) == abi.DS4C_ERR_SHAPE
+
+
+def test_python_refusals():
+    x = torch.zeros(4, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        rope.rotate(x, torch.arange(4), None)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        rope.norm_rotate(x.half(), torch.arange(4), None)

@@ -9,4 +9,4 @@ torch tensors; ``configs`` and ``synth`` describe the synthetic workloads.
 
 from . import configs, synth  # noqa: F401
 
-__all__ = ["configs", "synth", "abi", "layer", "fp8", "rope", "build"]
+__all__ = ["configs", "synth", "abi", "layer", "fp8", "rope", "paged", "build"]

@@ -37,7 +37,7 @@ EXPORTS = (
     "ds4c_indexer_topk_heads", "ds4c_test_set_wait_limit", "ds4c_test_wait_timeout", "ds4c_test_warp_wait",
     "ds4c_quant_row_bytes", "ds4c_quant_scale_bytes", "ds4c_rmsnorm_quant", "ds4c_quant_weight", "ds4c_quant_matmul",
     "ds4c_compress_prefill_quant", "ds4c_compress_decode_step_quant",
-    "ds4c_rope_table", "ds4c_rotate_heads",
+    "ds4c_rope_table", "ds4c_rotate_heads", "ds4c_paged_attn_workspace_bytes", "ds4c_paged_attn",
 )
 PAYLOAD_U32_FIELDS = 13
 NOALLOC_SCORE_FLOATS = 2 * 1024 * 1024
@@ -99,6 +99,18 @@ class RotateArgs(C.Structure):
                 ("magnitude", C.c_float), ("positions", C.c_void_p), ("turns", C.c_void_p), ("q", HeadRows), ("k", HeadRows)]
 
 
+class PagePool(C.Structure):
+    _fields_ = [("rows", C.c_void_p), ("pages", C.c_void_p), ("pages_ld", C.c_size_t), ("n_pages", C.c_uint32),
+                ("page_rows", C.c_uint32), ("max_pages", C.c_uint32)]
+
+
+class PagedAttnArgs(C.Structure):
+    _fields_ = [("n_seq", C.c_uint32), ("n_tok", C.c_uint32), ("n_heads", C.c_uint32), ("head_dim", C.c_uint32),
+                ("window", C.c_uint32), ("ratio", C.c_uint32), ("scale", C.c_float), ("q", C.c_void_p), ("out", C.c_void_p),
+                ("q_token", C.c_size_t), ("q_head", C.c_size_t), ("out_token", C.c_size_t), ("out_head", C.c_size_t),
+                ("start", C.c_void_p), ("length", C.c_void_p), ("raw", PagePool), ("comp", PagePool)]
+
+
 class PayloadInfo(C.Structure):
     _fields_ = [(n, C.c_uint32) for n in ("ctx_size", "prefill_chunk", "raw_cap", "raw_window", "comp_cap",
                                            "token_count", "layer_count", "head_dim", "idx_head_dim", "vocab_size",
@@ -157,6 +169,8 @@ def lib() -> C.CDLL:
         "ds4c_compress_decode_step_quant": (st, [cfgp, lqp, lqp, lsp, P, P, C.POINTER(U64), U32, P, SZ, P]),
         "ds4c_rope_table": (st, [C.POINTER(RopeParams), P, C.POINTER(C.c_float)]),
         "ds4c_rotate_heads": (st, [C.POINTER(RotateArgs), P]),
+        "ds4c_paged_attn_workspace_bytes": (SZ, [U32, U32, U32, U32]),
+        "ds4c_paged_attn": (st, [C.POINTER(PagedAttnArgs), P, SZ, P]),
         "ds4c_fma_probe": (st, [U32, U32, P, C.POINTER(C.c_double), P]),
         "ds4c_test_set_wait_limit": (st, [U64]),
         "ds4c_test_wait_timeout": (st, [U64, P]),
@@ -262,6 +276,14 @@ def ds4c_rope_table(params, turns_h):
 
 def ds4c_rotate_heads(args, stream):
     return (_lib or lib()).ds4c_rotate_heads(args, stream)
+
+
+def ds4c_paged_attn_workspace_bytes(n_seq, n_tok, n_heads, head_dim):
+    return (_lib or lib()).ds4c_paged_attn_workspace_bytes(n_seq, n_tok, n_heads, head_dim)
+
+
+def ds4c_paged_attn(args, ws, ws_bytes, stream):
+    return (_lib or lib()).ds4c_paged_attn(args, ws, ws_bytes, stream)
 
 
 def ds4c_indexer_topk(cfg, state, q_idx, pos_h, n_seq, n_tok, topk, scores, score_stride, ws, ws_bytes, stream):

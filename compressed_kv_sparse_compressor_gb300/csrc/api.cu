@@ -807,8 +807,8 @@ ds4c_status ds4c_sync_status(cudaStream_t stream) {
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_status(e);
     const unsigned int e1 = gemm_tc_read_clear_error(), e2 = attn_tc_read_clear_error(), e3 = idx_read_clear_error(),
-                       e4 = qmm_read_clear_error(), e5 = heads_read_clear_error();
-    if (e1 != 0 || e2 != 0 || e3 != 0 || e4 != 0 || e5 != 0) return DS4C_ERR_DEVICE;
+                       e4 = qmm_read_clear_error(), e5 = heads_read_clear_error(), e6 = paged_attn_read_clear_error();
+    if (e1 != 0 || e2 != 0 || e3 != 0 || e4 != 0 || e5 != 0 || e6 != 0) return DS4C_ERR_DEVICE;
     return DS4C_OK;
 }
 

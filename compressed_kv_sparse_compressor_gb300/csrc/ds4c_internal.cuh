@@ -290,6 +290,13 @@ cudaError_t launch_rotate_heads(const ds4c_rotate_args &a, cudaStream_t s);
 unsigned int heads_read_clear_error();
 
 // ----------------------------------------------------------------------------
+// Attention over a paged cache (arguments checked by the caller)
+// ----------------------------------------------------------------------------
+size_t paged_attn_ws_bytes(uint32_t n_seq, uint32_t n_tok, uint32_t n_heads, uint32_t head_dim);
+cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStream_t s);
+unsigned int paged_attn_read_clear_error();
+
+// ----------------------------------------------------------------------------
 // Compressor (store + APE, pool, RMSNorm, tail RoPE, FP8, append, frontier).
 // ----------------------------------------------------------------------------
 struct RopeTable { float inv_freq[kMaxRot / 2]; };

@@ -1,0 +1,88 @@
+"""Attention of new tokens of several sequences over a paged cache, on torch tensors over the C ABI.
+Marshalling only.
+
+A cache is a tensor [pages, page rows, d] bfloat16 of rows that are key and value of every head; a table
+[sequences, entries] int32 names each sequence's pages in order (-1: none).  ``rope.norm_rotate`` writes rows to
+such pages.
+
+Calls run on the current stream of the tensors' device.  What only the device can see (a page outside the cache where a
+token looks, starts that fall, a kernel that gave up waiting) is reported by ``fp8.sync``."""
+
+from __future__ import annotations
+
+import torch
+
+from . import abi
+from .fp8 import run
+
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def workspace(n_seq: int, n_tok: int, n_heads: int, head_dim: int, device="cuda"):
+    """A workspace for calls of up to these sizes.  It belongs to one call at a time: calls that may overlap (on other
+    streams, in graphs replayed beside each other) take one each."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        size = abi.ds4c_paged_attn_workspace_bytes(n_seq, n_tok, n_heads, head_dim)
+    if size == 0:
+        raise abi.Ds4cError(abi.DS4C_ERR_SHAPE, "ds4c_paged_attn_workspace_bytes")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _pool(cache, pages, n_seq, d, dev, what):
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] != d or cache.dtype != _BF16 or cache.get_device() != dev or not cache.is_contiguous():
+        raise ValueError(f"{what}: {cache.dtype} {tuple(shape)} on {cache.device}, expected contiguous bfloat16 (pages, page rows, "
+                         f"{d}) on cuda:{dev}")
+    ps = pages.shape
+    if len(ps) != 2 or ps[0] != n_seq or pages.dtype != _I32 or pages.get_device() != dev:
+        raise ValueError(f"{what}'s table: {pages.dtype} {tuple(ps)} on {pages.device}, expected int32 ({n_seq}, entries) on "
+                         f"cuda:{dev}")
+    ld, col = pages.stride()
+    if col != 1 and ps[1] > 1:
+        raise ValueError(f"{what}'s table: the entries of a sequence must be contiguous")
+    return abi.PagePool(cache.data_ptr(), pages.data_ptr(), ld if n_seq > 1 else ps[1], shape[0], shape[1], ps[1])
+
+
+def _ints(t, n, dev, what):
+    if t.shape != (n,) or t.dtype != _I32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous int32 {(n,)} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def attention(q, cache, pages, start, length, *, window: int = 0, scale=None, comp=None, comp_pages=None, ratio: int = 0,
+              out=None, workspace=None):
+    """q [n_tok, heads, d] bfloat16 (strides in multiples of 8): tokens start[s] .. start[s + 1] - 1 are the new ones of
+    sequence s, which has length[s] tokens with them (start, length: int32 on the device); their rows are in the cache.  Token
+    at position t sees raw rows max(0, t + 1 - window) .. t (window 0: all) and, with ratio > 0, the rows c of `comp` with
+    (c + 1) * ratio <= t + 1, in one softmax of scale * q . row (scale None: d^-1/2).  Tokens of no sequence are left as
+    they are.  workspace: from ``workspace``, of this call alone; allocated if None."""
+    dev, shape = q.get_device(), q.shape
+    if len(shape) != 3 or q.dtype != _BF16 or dev < 0:
+        raise ValueError(f"q: {q.dtype} {tuple(shape)} on {q.device}, expected bfloat16 (tokens, heads, d) on a CUDA device")
+    n, h, d = shape
+    qt, qh, qd = q.stride()
+    if qd != 1:
+        raise ValueError("q: the rows' elements must be contiguous")
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    if out.shape != shape or out.dtype != _BF16 or out.get_device() != dev:
+        raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, expected bfloat16 {tuple(shape)} on cuda:{dev}")
+    ot, oh, od = out.stride()
+    if od != 1:
+        raise ValueError("out: the rows' elements must be contiguous")
+    n_seq = length.shape[0] if length.dim() == 1 else -1
+    a = abi.PagedAttnArgs(n_seq if n_seq > 0 else 0, n, h, d, window, ratio, d ** -0.5 if scale is None else scale, q.data_ptr(),
+                          out.data_ptr(), qt if n > 1 else 0, qh if h > 1 else 0, ot if n > 1 else 0, oh if h > 1 else 0,
+                          _ints(start, n_seq + 1, dev, "start"), _ints(length, n_seq, dev, "length"),
+                          _pool(cache, pages, n_seq, d, dev, "cache"))
+    if (comp is None) != (ratio == 0) or (comp is None) != (comp_pages is None):
+        raise ValueError("comp, comp_pages and ratio: all or none")
+    if comp is not None:
+        a.comp = _pool(comp, comp_pages, n_seq, d, dev, "comp")
+    if workspace is None:
+        workspace = globals()["workspace"](n_seq, n, h, d, q.device)
+    elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected contiguous uint8 on cuda:{dev}")
+    run(dev, abi.ds4c_paged_attn, a, workspace.data_ptr(), workspace.numel())
+    return out

@@ -392,6 +392,54 @@ typedef struct {
 } ds4c_rotate_args;
 DS4C_API ds4c_status ds4c_rotate_heads(const ds4c_rotate_args *args, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention of new tokens of several sequences over a paged cache.
+ *
+ * A pool holds rows of head_dim bfloat16 values, key and value of every query head at once, in pages of
+ * page_rows rows: rows [n_pages][page_rows][head_dim], 16-byte aligned.  Row c of sequence s lies in page
+ * pages[s * pages_ld + c / page_rows] at row c % page_rows; each sequence has max_pages entries.  page_rows is a power of
+ * two, 16 to 1024.
+ *
+ * Tokens start[s] .. start[s + 1] - 1 of q are the new tokens of sequence s, length[s] the sequence's tokens with
+ * them (start and length: device arrays of 32-bit values; a sequence may have no new token).  The new token i of
+ * start[s + 1] - start[s] = n sits at position t = length[s] - n + i; its own row and those before it are in their pages
+ * already.  It sees the raw rows c with max(0, t + 1 - window) <= c <= t (window 0: all up to t) and, with
+ * ratio > 0, every compressed row c with (c + 1) * ratio <= t + 1, in one softmax over both:
+ *   out[i][h] = sum over rows of softmax(scale * q[i][h] . row) * row,
+ * accumulated in float with probabilities rounded to bfloat16 on the way into the second product; a token that sees no
+ * row (t < 0) gives zeros.  q, out: [n_tok] tokens of n_heads heads at strides of elements (multiples of 8, 16-byte aligned,
+ * output rows apart); out may not overlap q or a pool.  Tokens outside every sequence (in front of start[0], behind
+ * start[n_seq]) are left as they are.
+ *
+ * Only rows that some token of the call sees are waited for to hold numbers: pages behind a sequence's end or before its
+ * windows may hold anything and need not be listed (-1).  A row that is no number somewhere makes NaN the outputs of the tokens that
+ * see it, and of no other.  A page outside 0 .. n_pages - 1 or past max_pages where a visible row should be, and a
+ * start that falls or leaves 0 .. n_tok, raise the device error word; such rows and tokens count as not there.
+ *
+ * n_heads 1 .. 128, head_dim 64, 128, 256 or 512, n_seq <= 65536, n_tok <= 2^20, n_pages * page_rows <= 2^31 - 1, 0 < scale <= 1e4.
+ * The workspace (ds4c_paged_attn_workspace_bytes, of the device the call runs on; 256-byte aligned) belongs to one call
+ * at a time: calls that may overlap, captured ones among them, take one each.  Equal calls give equal bits. */
+typedef struct {
+    const void *rows;
+    const int32_t *pages;
+    size_t pages_ld;
+    uint32_t n_pages, page_rows, max_pages;
+} ds4c_page_pool;
+typedef struct {
+    uint32_t n_seq, n_tok, n_heads, head_dim;
+    uint32_t window, ratio;
+    float scale;
+    const void *q;
+    void *out;
+    size_t q_token, q_head, out_token, out_head;
+    const int32_t *start;       /* [n_seq + 1] */
+    const int32_t *length;      /* [n_seq] */
+    ds4c_page_pool raw, comp;   /* comp: read with ratio > 0 */
+} ds4c_paged_attn_args;
+/* 0 for sizes that the call refuses. */
+DS4C_API size_t ds4c_paged_attn_workspace_bytes(uint32_t n_seq, uint32_t n_tok, uint32_t n_heads, uint32_t head_dim);
+DS4C_API ds4c_status ds4c_paged_attn(const ds4c_paged_attn_args *args, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Score capacity of ds4c_indexer_topk_noalloc: 2M floats (8 MiB). */
 #define DS4C_NOALLOC_SCORE_FLOATS (2u * 1024u * 1024u)
 

@@ -1,0 +1,313 @@
+"""Attention over a paged cache on the GPU (-m gpu) against a plain implementation in 64 bits."""
+
+import math
+
+import pytest
+import torch
+
+import heads_ref
+import paged_ref as ref
+from compressed_kv_sparse_compressor_gb300 import abi, fp8, paged, rope
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def setup(g, h, d, page, seqs, window=0, ratio=0, tail=0, fill=math.nan):
+    """Inputs of a call: what no token sees is `fill`; `tail` tokens of no sequence behind the last."""
+    first = [max(0, m - n + 1 - window) if window and n else 0 for n, m in seqs]
+    a = dict(zip(("cache", "pages"), ref.pool(g, [max(m, 0) if n else 0 for n, m in seqs], page, d, [f if n else 0 for f, (n, _) in zip(first, seqs)], fill=fill)))
+    if ratio:
+        a["comp"], a["comp_pages"] = ref.pool(g, [max(m, 0) // ratio for _, m in seqs], page, d, fill=fill)
+        a["ratio"] = ratio
+    a["start"], a["length"] = ref.starts(seqs)
+    n = sum(n for n, _ in seqs)
+    return randn(g, n + tail, h, d).bfloat16(), a, dict(window=window)
+
+
+def check(q, a, kw, seqs, **more):
+    out = torch.full_like(q, 7.0)
+    got = paged.attention(q, out=out, **a, **kw, **more)
+    assert got is out
+    fp8.sync()
+    rest = {k: v for k, v in a.items() if k not in ("start", "length")}
+    want, size = ref.attention(q, seqs=seqs, **rest, **kw, **more)
+    n = sum(n for n, _ in seqs)
+    ref.assert_close(out[:n], want[:n], size[:n])
+    assert (out[n:] == 7.0).all()
+    return out
+
+
+ONE = [(1, 1)]
+MIXED = [(1, 300), (37, 40), (0, 77), (1, 1), (130, 130), (3, 515), (1, 128), (1, 129), (2, 1025), (0, 0), (64, 200)]
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("h,d", [(64, 512), (8, 128), (128, 512), (24, 256), (3, 64), (67, 64), (1, 512), (128, 128), (40, 64),
+                                 (96, 256)])
+@pytest.mark.parametrize("window,ratio", [(0, 0), (128, 0), (50, 4), (128, 128)])
+def test_mixed_batch(h, d, page, window, ratio):
+    g = gen(h + d + page + window)
+    seqs = MIXED if page == 64 else MIXED[:6]
+    check(*setup(g, h, d, page, seqs, window, ratio, tail=3), seqs)
+
+
+@pytest.mark.parametrize("h,d,seqs,window,ratio", [
+    (64, 512, ONE, 0, 0), (64, 512, [(1, 5000)], 0, 0), (64, 512, [(1, 5000 + 100 * b) for b in range(40)], 0, 128),
+    (64, 512, [(700, 2000)], 0, 0), (64, 512, [(700, 2000)], 128, 128), (64, 512, [(513, 513)], 1, 0),
+    (16, 128, [(1000, 3001)], 0, 0), (16, 128, [(1, 20000)], 0, 0), (128, 256, [(260, 700)], 300, 4),
+    (8, 64, [(515, 900), (1, 9000)], 0, 0), (64, 512, [(1, 70000)], 0, 0), (5, 512, [(9, 4000)], 1000, 0),
+    (64, 128, [(1, m) for m in range(1, 260, 7)], 0, 0), (20, 256, [(129, 129)] * 7, 0, 1), (64, 512, [(1, 131072)], 128, 128),
+])
+def test_shapes(h, d, seqs, window, ratio):
+    g = gen(h + d + len(seqs))
+    check(*setup(g, h, d, 64, seqs, window, ratio), seqs)
+
+
+def test_many_tiles_of_work():
+    """More work items than CTAs, long and short ones in any order."""
+    g = gen(11)
+    seqs = [(int(torch.randint(0, 90, (1,), generator=g, device="cuda")) * (b % 3), 0) for b in range(200)]
+    seqs = [(n, n + int(torch.randint(0, 3000, (1,), generator=g, device="cuda"))) for n, _ in seqs]
+    check(*setup(g, 8, 128, 32, seqs), seqs)
+
+
+def test_tokens_that_see_nothing():
+    g = gen(12)
+    # more new tokens than the sequence has, no length at all, a ratio that nothing has reached yet and no raw rows
+    seqs = [(5, 3), (4, 0), (2, 2), (3, -7), (1, 1)]
+    q, a, kw = setup(g, 16, 128, 16, seqs, window=2)
+    out = check(q, a, kw, seqs)
+    assert (out[:2] == 0).all() and (out[5:9] == 0).all() and (out[11:14] == 0).all()
+    # tokens in front of the first sequence and behind the last are left alone
+    a["start"], a["length"] = ref.starts([(5, 3)], 4)
+    a["pages"] = a["pages"][:1]
+    out = torch.full_like(q, 7.0)
+    paged.attention(q, out=out, **a, **kw)
+    fp8.sync()
+    want, size = ref.attention(q, a["cache"], a["pages"], [(5, 3)], start0=4, **kw)
+    ref.assert_close(out[4:9], want[4:9], size[4:9])
+    assert (out[:4] == 7.0).all() and (out[9:] == 7.0).all()
+    # no sequences, no tokens
+    empty = dict(cache=a["cache"], pages=a["pages"][:0], start=a["start"][:1], length=a["length"][:0])
+    assert (paged.attention(q, out=torch.full_like(q, 7.0), **empty) == 7.0).all()
+    assert paged.attention(q[:0], **{**empty, "pages": a["pages"], "start": torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                     "length": a["length"]}).shape == (0, 16, 128)
+
+
+@pytest.mark.parametrize("h,d", [(64, 512), (8, 128), (40, 256), (3, 64)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_rows_that_are_no_numbers(h, d, value):
+    """A row with a NaN or an infinity poisons the tokens that see it, and no other."""
+    g = gen(13)
+    seqs = [(70, 300), (40, 40)]
+    for window, ratio in ((0, 0), (20, 0), (0, 8)):
+        q, a, kw = setup(g, h, d, 32, seqs, window, ratio)
+        t = 261                                                  # of sequence 0: token 31
+        a["cache"][a["pages"][0, t // 32].long(), t % 32, 5] = value
+        got = paged.attention(q, **a, **kw)
+        fp8.sync()
+        rest = {k: v for k, v in a.items() if k not in ("start", "length")}
+        want, size = ref.attention(q, seqs=seqs, **rest, **kw)
+        sees = torch.zeros(110, dtype=torch.bool, device="cuda")
+        sees[31:(31 + window if window else 70)] = True
+        assert got[sees][..., 5].isnan().all()
+        ref.assert_close(got[~sees], want[~sees], size[~sees])
+
+
+@pytest.mark.parametrize("h,d", [(64, 512), (16, 128), (8, 64)])
+def test_logits_far_apart(h, d):
+    """Logits of some thousands, that rise, fall, or are all equal along the sequence: one row takes all the weight, or
+    all rows share it."""
+    g = gen(14)
+    seqs = [(20, 1500), (1, 2000)]
+    q, a, kw = setup(g, h, d, 64, seqs)
+    lean = torch.sign(randn(g, d))
+    for ramp in (torch.linspace(0, 4, 2000, device="cuda"), torch.linspace(4, 0, 2000, device="cuda"), torch.ones(2000, device="cuda")):
+        for s, (_, m) in enumerate(seqs):
+            rows = (ramp[:m, None] * lean).bfloat16()
+            ids = a["pages"][s, :-(-m // 64)].long()
+            flat = a["cache"][ids].view(-1, d)
+            flat[:m] = rows
+            a["cache"][ids] = flat.view(-1, 64, d)
+        for sign in (1.0, -1.0):
+            q[:] = (sign * lean * (1 + 0.1 * randn(g, 21, h, 1))).bfloat16()
+            check(q, a, kw, seqs, scale=2.0)
+            check(q, a, kw, seqs, scale=1e-4)
+
+
+def test_strides():
+    g = gen(15)
+    seqs = MIXED
+    q, a, kw = setup(g, 24, 128, 64, seqs)
+    n = q.shape[0]
+    wide = randn(g, n, 30, 256).bfloat16()
+    wide[:, 2:26, 64:192] = q
+    out = torch.zeros(24, n, 128, dtype=torch.bfloat16, device="cuda")
+    want = paged.attention(q, **a, **kw)
+    got = paged.attention(wide[:, 2:26, 64:192], out=out.transpose(0, 1), **a, **kw)
+    assert torch.equal(got, want) and torch.equal(out.transpose(0, 1), want)
+    table = torch.full((len(seqs), a["pages"].shape[1] + 5), -9, dtype=torch.int32, device="cuda")
+    table[:, :a["pages"].shape[1]] = a["pages"]
+    assert torch.equal(paged.attention(q, **{**a, "pages": table[:, :a["pages"].shape[1]]}, **kw), want)
+    with pytest.raises(abi.Ds4cError) as e:
+        paged.attention(wide[:, 2:26, 1:129], **a, **kw)          # rows that are not 16-byte aligned
+    assert e.value.status == abi.DS4C_ERR_SHAPE
+
+
+def test_bad_pages_and_starts_are_reported():
+    g = gen(16)
+    seqs = [(40, 200), (1, 90), (3, 77)]
+    q, a, kw = setup(g, 16, 128, 16, seqs)
+    good = paged.attention(q, **a, **kw)
+    fp8.sync()
+
+    def reported(change, same):
+        out = torch.full_like(q, 7.0)
+        paged.attention(q, out=out, **{**a, **change}, **kw)
+        with pytest.raises(abi.Ds4cError) as e:
+            fp8.sync()
+        assert e.value.status == abi.DS4C_ERR_DEVICE
+        assert torch.equal(out[same], good[same])
+        fp8.sync()
+        return out
+    for page in (-1, a["cache"].shape[0], 1 << 30, -(1 << 31)):
+        table = a["pages"].clone()
+        table[1, 2] = page
+        out = reported({"pages": table}, torch.tensor([i for i in range(44) if i != 40], device="cuda"))
+        # such rows count as not there
+        kept = torch.cat([ref.rows_of(a["cache"], a["pages"][1], 90)[:32], ref.rows_of(a["cache"], a["pages"][1], 90)[48:]])
+        p = torch.softmax(q[40].double() @ kept.T * 128 ** -0.5, dim=-1)
+        ref.assert_close(out[40], p @ kept, p @ kept.abs())
+    reported({"pages": a["pages"][:, :5].contiguous()}, slice(41, 41))   # a table that ends before the sequences
+    t = torch.tensor
+    for bad in ([0, 40, 41, 45], [0, 40, 30, 44], [-3, 40, 41, 44], [0, 40, 41, 1 << 30]):
+        start = t(bad, dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 7.0)
+        paged.attention(q, out=out, **{**a, "start": start}, **kw)
+        with pytest.raises(abi.Ds4cError):
+            fp8.sync()
+
+
+def test_streams_graphs_and_equal_bits():
+    g = gen(17)
+    seqs = [(1, 3000), (300, 1200), (1, 70)]
+    q, a, kw = setup(g, 64, 512, 64, seqs, 0, 8)
+    want = check(q, a, kw, seqs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        outs = [paged.attention(q, **a, **kw) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    # two graphs that run beside each other, each with a workspace of its own, lengths that change between replays
+    graphs = []
+    for _ in range(2):
+        out, ws = torch.empty_like(q), paged.workspace(3, q.shape[0], 64, 512)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            paged.attention(q, out=out, workspace=ws, **a, **kw)
+        graphs.append((graph, out, ws, torch.cuda.Stream()))
+    for lengths in ([3000, 1200, 70], [2000, 400, 1], [1, 300, 64]):
+        a["length"].copy_(torch.tensor(lengths, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for graph, _, _, s in graphs:
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        want = check(q, a, kw, [(n, m) for (n, _), m in zip(seqs, lengths)])
+        for _, out, _, _ in graphs:
+            assert torch.equal(out, want)
+    small = paged.workspace(1, 1, 64, 512)
+    if small.numel() < paged.workspace(3, q.shape[0], 64, 512).numel():
+        with pytest.raises(abi.Ds4cError) as e:
+            paged.attention(q, workspace=small, **a, **kw)
+        assert e.value.status == abi.DS4C_ERR_WORKSPACE
+
+
+def test_pages_past_32_bits():
+    """A pool of 6 GB: rows beyond 2^31 elements and 2^32 bytes."""
+    g = gen(18)
+    d, page, pages = 512, 128, 48 * 1024
+    cache = torch.empty(pages, page, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[pages - 1, 0, pages - 2, pages // 2 + 1], [5, pages - 7, -1, -1]], dtype=torch.int32, device="cuda")
+    for i in table.flatten().tolist():
+        if i >= 0:
+            cache[i] = randn(g, page, d).bfloat16()
+    seqs = [(90, 500), (1, 256)]
+    q = randn(g, 91, 64, d).bfloat16()
+    start, length = ref.starts(seqs)
+    out = paged.attention(q, cache, table, start, length)
+    fp8.sync()
+    small = torch.stack([cache[i] for i in (pages - 1, 0, pages - 2, pages // 2 + 1, 5, pages - 7)])
+    ids = torch.tensor([[0, 1, 2, 3], [4, 5, -1, -1]], dtype=torch.int32, device="cuda")
+    ref.assert_close(out, *ref.attention(q, small, ids, seqs))
+
+
+def test_rows_written_read_and_turned_back():
+    """The operators as a layer uses them: rows normed, rotated and written to pages chunk by chunk for three sequences,
+    queries the same way, attention over all pages, outputs turned back; in a graph for the last step too."""
+    g = gen(19)
+    h, d, page, rot, base = 16, 128, 16, 64, 10000.0
+    t, theta = rope.table(rot, base), heads_ref.thetas(rot, base)
+    gq, gk = 1 + 0.1 * randn(g, d), 1 + 0.1 * randn(g, d)
+    total = [150, 33, 90]
+    steps = [[100, 0, 1], [37, 32, 60], [13, 1, 29]]
+    cache = torch.full((40, page, d), math.nan, dtype=torch.bfloat16, device="cuda")
+    order = torch.randperm(40, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((3, 10), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for s, m in enumerate(total):
+        table[s, :-(-m // page)] = order[at:at - (-m // page)]
+        at += -(-m // page)
+    x = [randn(g, m, h, d).bfloat16() for m in total]
+    k = [randn(g, m, d).bfloat16() for m in total]
+    # in 64 bits, from the stored queries and rows (bfloat16 after the rotation)
+    done = [0, 0, 0]
+    for step in steps:
+        seqs = [(n, b + n) for n, b in zip(step, done)]
+        pos = torch.cat([torch.arange(m - n, m, device="cuda") for n, m in seqs])
+        rows = torch.cat([torch.arange(m - n, m, device="cuda") + 1000 * s for s, (n, m) in enumerate(seqs)])
+        slots = table[rows // 1000, rows % 1000 // page].long() * page + rows % page
+        q = torch.cat([x[s][m - n:m] for s, (n, m) in enumerate(seqs)])
+        kk = torch.cat([k[s][m - n:m] for s, (n, m) in enumerate(seqs)])
+        start, length = ref.starts(seqs)
+        ws = paged.workspace(3, q.shape[0], h, d)
+
+        def layer():
+            turned = rope.norm_rotate(q, pos, t, gain=gq, k=kk, k_gain=gk, cache=cache, slots=slots)
+            o = paged.attention(turned, cache, table, start, length, workspace=ws)
+            return turned, o, rope.rotate(o, pos, t, inverse=True)
+        if step is steps[-1]:
+            graph = torch.cuda.CUDAGraph()
+            before = cache.clone()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                outs = layer()
+            assert torch.equal(cache.view(torch.int16), before.view(torch.int16))
+            graph.replay()
+        else:
+            outs = layer()
+        fp8.sync()
+        turned, o, back = outs
+        heads_ref.assert_close(turned, *heads_ref.turned(heads_ref.normed(q, gq, 1e-6), pos, theta, d - rot, False))
+        wk, size = heads_ref.turned(heads_ref.normed(kk[:, None], gk, 1e-6), pos, theta, d - rot, False)
+        heads_ref.assert_close(cache.view(-1, d)[slots][:, None], wk, size)
+        ref.assert_close(o, *ref.attention(turned, cache, table, seqs))
+        heads_ref.assert_close(back, *heads_ref.turned(o.double(), pos, theta, d - rot, False, True))
+        done = [m for _, m in seqs]
+    assert done == total

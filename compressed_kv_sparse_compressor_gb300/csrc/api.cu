@@ -787,6 +787,7 @@ ds4c_status ds4c_test_set_wait_limit(uint64_t limit_ns) {
     if (e == cudaSuccess) e = attn_tc_set_wait_ns(ns);
     if (e == cudaSuccess) e = idx_set_wait_ns(ns);
     if (e == cudaSuccess) e = qmm_set_wait_ns(ns);
+    if (e == cudaSuccess) e = paged_attn_set_wait_ns(ns);
     return cuda_status(e);
 }
 

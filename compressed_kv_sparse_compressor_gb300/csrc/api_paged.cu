@@ -6,8 +6,8 @@ using namespace ds4c;
 
 namespace {
 
-constexpr uint32_t kMaxSeq = 65536, kMaxTokens = 1u << 20, kMaxHeads = 128;
-constexpr size_t kMaxStride = (size_t)1 << 40;
+constexpr uint32_t kMaxSeq = 4096, kMaxTokens = 1u << 20, kMaxHeads = 128;
+constexpr size_t kMaxStride = (size_t)1 << 39;
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -26,7 +26,8 @@ ds4c_status check_pool(const ds4c_page_pool &p) {
 
 // Strides of [n][h] rows of d: multiples of 16 bytes, below the limit.
 bool strides_ok(const ds4c_paged_attn_args &a, size_t token, size_t head) {
-    return (a.n_tok <= 1 || (token % 8 == 0 && token <= kMaxStride)) && (a.n_heads <= 1 || (head % 8 == 0 && head <= kMaxStride));
+    return (a.n_tok <= 1 || (token % 8 == 0 && token > 0 && token < kMaxStride)) &&
+           (a.n_heads <= 1 || (head % 8 == 0 && head > 0 && head < kMaxStride));
 }
 bool apart(size_t n_outer, size_t so, size_t n_inner, size_t si, size_t d) {
     return (n_inner <= 1 || si >= d) && (n_outer <= 1 || so >= (n_inner - 1) * si + d);

@@ -295,6 +295,7 @@ unsigned int heads_read_clear_error();
 size_t paged_attn_ws_bytes(uint32_t n_seq, uint32_t n_tok, uint32_t n_heads, uint32_t head_dim);
 cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStream_t s);
 unsigned int paged_attn_read_clear_error();
+cudaError_t paged_attn_set_wait_ns(unsigned long long ns);
 
 // ----------------------------------------------------------------------------
 // Compressor (store + APE, pool, RMSNorm, tail RoPE, FP8, append, frontier).

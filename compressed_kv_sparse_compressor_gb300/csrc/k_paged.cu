@@ -1,106 +1,1063 @@
-// Attention of new tokens over a paged cache: a warp per token and head, one row after the other, online
-// softmax.
+// Attention of new tokens of several sequences over a paged cache, on the 5th-generation tensor cores:
+//   o[i][h] = sum_k p_k x_k / sum_k p_k,  p_k = 2^(scale_log2 q[i][h] . x_k - m),  m a running reference
+// over the rows x_k that the token sees (raw rows of a window, compressed rows), K = V = the row.
+//
+// A work item is a sequence's next tokens whose heads fill the N columns of the MMAs (64 at head_dim 512, 128
+// below: one token of 64 heads, or several tokens of fewer heads, or a group of a wide layer's heads).  For
+// each tile of 128 rows, rows on the TMEM lanes, (token, head) columns side by side:
+//   S^T[row][col] = sum_d X[row][d] Q[col][d]         M = 128 rows, K = head_dim
+//   O^T[d][col]  += sum_row X[row][d] P[row][col]     M = 128 of d, K = 128 rows
+// The tile is loaded once: its [128 rows][64 d] chunks in the 128-byte swizzle are the K-major operand of the first
+// product and, two chunks side by side, the MN-major operand of the second.  At head_dim 512 one tile
+// fills the ring, and the next one's chunks follow as the second product frees theirs.
+//
+// Work is cut evenly: the tiles of all items in a row (each item one tile longer, for its queries and output),
+// divided by the number of CTAs; an item that a cut divides leaves parts (sum, reference, denominator), which
+// a second kernel joins in the order of the CTAs.  Items of few tiles are not divided.  A one-block
+// kernel in front makes the items and cuts on the device, so that lengths are the device's own
+// and a captured call follows them.
+//
+// Softmax: a thread holds one row's logits for half of the columns (two warpgroups), the denominators as its own
+// partial sums, which meet at the end of the item.  The reference moves only when a logit exceeds it by
+// more than 2^8, so p <= 256, and O is rescaled in tensor memory only then; P is rounded to bfloat16, an error of 2^-9
+// of each weight that the output's own rounding is as large as.
+// Rows that no column sees take no part; a row that is no number somewhere (stale or poisoned) would spoil columns
+// that do not see it through 0 * NaN, so where a tile is masked and all of a row's logits are not finite, the row
+// is set to zero in shared memory and the columns that see it get NaN weights.
+//
+// Warps: 0 loads (queries and tiles by TMA, a box per page), 1 issues the MMAs, 4-7 and 8-11 softmax and output.
+// Every wait is bounded; after one gave up the warps go on through their loops without waiting, so that the
+// barriers of a warpgroup stay matched, and nothing more is loaded, multiplied or stored.
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
 
 #include "ds4c_internal.cuh"
 
 namespace ds4c {
 
 __device__ unsigned int g_paged_err;
+__device__ unsigned long long g_paged_wait_ns = kWaitNsDefault;
 
 namespace {
 
-struct Pool {
-    const __nv_bfloat16 *rows;
-    const int32_t *pages;
-    int64_t ld;
-    int n_pages, page_rows, max_pages;
-};
-struct Params {
-    const __nv_bfloat16 *q;
-    __nv_bfloat16 *out;
-    int64_t q_token, q_head, out_token, out_head;
-    const int32_t *start, *length;
-    Pool raw, comp;
-    int n_seq, n_tok, n_heads, window, ratio;
-    float scale_log2;
-};
+constexpr int ROWS = 128, CHUNK = ROWS * 128, SLOT = 2 * CHUNK;      // bytes of a [128][64] chunk, of a ring slot
+constexpr int THREADS = 384;
+// registers of a thread of the loading and MMA warps and of the softmax warps (setmaxnreg at entry): their sum over
+// three warpgroups fits the launch's, which the host checks
+constexpr int REG_LOW = 72, REG_SOFT = 216;
+constexpr int MASKS = 8;                                            // tiles whose unlisted pages are remembered
+constexpr float TAU = 8.0f;
+constexpr float NONE = -3.0e38f;                                    // reference of a column that saw nothing yet
+constexpr int PLAN_THREADS = 1024;
+constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
+constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
+constexpr int MIN_COST = 2;                                         // a CTA's share, in tiles, where there is little work
 
 template <int D>
-__global__ void paged_attn_kernel(const Params p) {
+struct Shape {
+    static constexpr int N = D == 512 ? 64 : 128;                   // columns
+    static constexpr int C = N / 2;                                 // columns of a softmax warpgroup
+    static constexpr int DC = D / 64, DB = (D + 127) / 128, SLOTS_TILE = DB;
+    static constexpr int RING = D == 512 || D == 256 ? 4 : 5;       // slots
+    static constexpr bool AHEAD = RING >= 2 * SLOTS_TILE;           // the next tile's S in front of this one's O
+    static constexpr int OFF_Q = 0, Q_CHUNK = N * 128, OFF_P = DC * Q_CHUNK, OFF_X = OFF_P + ROWS * N * 2;
+    static constexpr int OFF_RED = OFF_X + RING * SLOT;             // [2][4][C] floats
+    static constexpr int OFF_REF = OFF_RED + 8 * C * 4;             // [N]
+    static constexpr int OFF_MASK = OFF_REF + 4 * N;
+    static constexpr int OFF_BAR = OFF_MASK + 4 * MASKS;
+    static constexpr int N_BAR = 2 * RING + 10;
+    static constexpr int SMEM = OFF_BAR + 8 * N_BAR + 16;
+    static constexpr int T_S = 0, T_O = 2 * N;
+    static_assert(T_O + DB * N <= 512, "tensor memory");
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(OFF_X % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0 && OFF_RED % 16 == 0 && OFF_REF % 16 == 0, "alignment");
+    static_assert(RING / SLOTS_TILE < MASKS, "a tile's mask is read before its slot is loaded again");
+};
+// barriers behind the ring's
+enum { B_QFULL, B_QEMPTY, B_SFULL, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PVDONE, B_OFREE, B_DRAIN };
+
+struct Pool {
+    const int32_t *pages;
+    int64_t ld;
+    int n_pages, page_log, max_pages;
+};
+struct Item {
+    int seq, tok0, n_tok, head0;
+    int t0, raw_tile0, raw_tiles, comp_tiles;
+};
+struct Start { int item, y; };
+// Workspace: counts, each CTA's first item and place in it, the boundaries that start a divided item, the items,
+// the parts.
+struct Plan {
+    int *counts;               // [0] items, [1] divided items, [2] CTAs with work
+    Start *start;              // [grid + 1]
+    int *split;                // [grid]
+    Item *items;
+    float *part_o;             // [2 grid][N][D]
+    float *part_ml;            // [2 grid][2][N]
+};
+struct Params {
+    __nv_bfloat16 *out;
+    int64_t out_token, out_head;
+    const int32_t *start, *length;
+    Pool raw, comp;
+    int raw_rows, comp_rows;   // rows of the pools: the first row past the end, which TMA fills with zeros
+    int n_seq, n_tok, n_heads, window, ratio;
+    int hg, tt, groups;        // heads and tokens of an item, head groups
+    float scale_log2;
+    Plan plan;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint64_t globaltimer() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One look, suspended for up to 1 us: waiting warps leave the issue slots to the others.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return warp_bounded_wait<16>([=] { return mbar_try(bar, parity); }, abort, g_paged_wait_ns, &g_paged_err);
+}
+// Bounded wait that ignores the abort flag: what is in flight lands before the CTA exits.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t &t0) {
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try(bar, parity)) return;
+        if ((i & 15u) == 15u) {
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kDrainNs) return;
+        }
+    }
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Shared-memory matrix descriptor without its start address (adding address >> 4 fills it in): leading and
+// stride byte offsets, 128-byte swizzle.
+__host__ __device__ constexpr uint64_t desc(uint32_t lbo, uint32_t sbo) {
+    return ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor: bf16 operands, float accumulation, M = 128.
+__host__ __device__ constexpr uint32_t idesc(int n, int a_mn, int b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+// By a converged warp, the leading lane issues.
+__device__ __forceinline__ void mma_w(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_w(uint32_t bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's TMEM lane, without the wait for them.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
+    const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+// Barriers of a softmax warpgroup's 128 threads (id 1 or 2).
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+// Reduction of C values per lane over a warp by a transposing butterfly: lane l ends with the results
+// of values l * C / 32 .. (C / 32 of them) in r.
+template <bool MAX, int C>
+__device__ __forceinline__ void reduce_columns(const float (&v)[C], float (&r)[C / 32]) {
+    const int lane = threadIdx.x % 32;
+    float m[C];
+#pragma unroll
+    for (int k = 0; k < C; k++) m[k] = v[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = (lane & o) != 0;
+        const int half = o * C / 32;
+#pragma unroll
+        for (int k = 0; k < half; k++) {
+            const float send = up ? m[k] : m[k + half], keep = up ? m[k + half] : m[k];
+            const float x = __shfl_xor_sync(0xffffffffu, send, o);
+            m[k] = MAX ? fmaxf(keep, x) : keep + x;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < C / 32; k++) r[k] = m[k];
+}
+
+// Tiles of an item in front of place y (0: its start, 1 + t: tile t) of the cuts.
+__device__ __forceinline__ int tiles_before(int y, int tiles) {
+    if (tiles <= SHORT) return y > 0 ? tiles : 0;
+    return y > 0 ? y - 1 : 0;
+}
+
+// ---- items and cuts ----------------------------------------------------------------------------
+
+template <typename T>
+__device__ T block_scan(T v, T *sums, T &total) {              // inclusive, over PLAN_THREADS threads
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        T s = sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const T u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        sums[lane] = s;
+    }
+    __syncthreads();
+    total = sums[31];
+    return warp > 0 ? v + sums[warp - 1] : v;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const Params p, int grid) {
+    extern __shared__ int first_item[];                        // [n_seq + 1]
+    __shared__ long long prefix[PLAN_THREADS + 1];
+    __shared__ long long sums_l[32];
+    __shared__ int sums_i[32];
+    __shared__ int n_split;
+    const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int E = D / 32;
-    const int warp = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int token = warp / p.n_heads, h = warp % p.n_heads;
-    if (token >= p.n_tok) return;
-    for (int s = 0; s < p.n_seq; s++) {
-        int b = p.start[s], e = p.start[s + 1];
-        if (b < 0 || e < b || e > p.n_tok) {
-            if (lane == 0) atomicOr(&g_paged_err, 2u);
-            continue;
+
+    // items of the sequences before each
+    int carry = 0;
+    if (tid == 0) n_split = 0;
+    for (int s0 = 0; s0 < p.n_seq; s0 += PLAN_THREADS) {
+        const int s = s0 + tid;
+        int k = 0;
+        if (s < p.n_seq) {
+            const int b = p.start[s], e = p.start[s + 1];
+            if (b < 0 || e < b || e > p.n_tok) atomicOr(&g_paged_err, 2u);
+            else k = (e - b + p.tt - 1) / p.tt * p.groups;
         }
-        if (token < b || token >= e) continue;
-        const int64_t t = (int64_t)p.length[s] - (e - b) + (token - b);
-        float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-        for (int i = 0; i < E; i++) q[i] = __bfloat162float(p.q[token * p.q_token + h * p.q_head + lane + 32 * i]);
-        for (int side = 0; side < 2; side++) {
-            const Pool &pool = side ? p.comp : p.raw;
-            int64_t lo = 0, hi = t + 1;
-            if (side == 0 && p.window) lo = max((int64_t)0, t + 1 - p.window);
-            if (side) hi = p.ratio && t >= 0 ? (t + 1) / p.ratio : 0;
-            for (int64_t c = lo; c < hi; c++) {
-                const int64_t k = c / pool.page_rows;
-                const int page = k < pool.max_pages ? pool.pages[s * pool.ld + k] : -1;
-                if (page < 0 || page >= pool.n_pages) {
-                    if (lane == 0) atomicOr(&g_paged_err, 4u);
-                    continue;
-                }
-                const __nv_bfloat16 *row = pool.rows + ((int64_t)page * pool.page_rows + c % pool.page_rows) * D;
-                float x[E], dot = 0.f;
-                for (int i = 0; i < E; i++) {
-                    x[i] = __bfloat162float(row[lane + 32 * i]);
-                    dot = fmaf(q[i], x[i], dot);
-                }
-                for (int w = 16; w; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
-                dot *= p.scale_log2;
-                const float mn = fmaxf(m, dot), f = exp2f(m - mn), pr = exp2f(dot - mn);
-                for (int i = 0; i < E; i++) o[i] = fmaf(pr, x[i], o[i] * f);
-                l = l * f + pr;
-                m = mn;
+        int total;
+        const int incl = block_scan<int>(k, sums_i, total);
+        if (s < p.n_seq) first_item[s] = carry + incl - k;
+        carry += total;
+    }
+    // starts that overlap could make more items than there is room for
+    const int most = p.n_tok * p.groups;
+    if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
+    const int n_items = min(carry, most);
+    if (tid == 0) first_item[p.n_seq] = carry;
+    __syncthreads();
+
+    auto make = [&](int i) -> int {                            // writes item i; its cost
+        int lo = 0, hi = p.n_seq;                              // the last sequence with first_item <= i (it has items)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (first_item[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int b = p.start[lo], n = p.start[lo + 1] - b, k = i - first_item[lo];
+        Item it;
+        it.seq = lo;
+        const int j = k / p.groups * p.tt;
+        it.tok0 = b + j;
+        it.n_tok = min(p.tt, n - j);
+        it.head0 = k % p.groups * p.hg;
+        const long long t0 = (long long)p.length[lo] - n + j, end = t0 + it.n_tok;   // positions t0 .. end - 1
+        it.t0 = (int)max(t0, -(1ll << 30));                    // a token before 0 sees nothing wherever it is
+        it.raw_tile0 = it.raw_tiles = it.comp_tiles = 0;
+        if (end > 0) {
+            const long long from = p.window ? max(0ll, t0 + 1 - p.window) : 0;
+            it.raw_tile0 = (int)(from / ROWS);
+            it.raw_tiles = (int)((end + ROWS - 1) / ROWS) - it.raw_tile0;
+            if (p.ratio) it.comp_tiles = (int)((end / p.ratio + ROWS - 1) / ROWS);
+        }
+        p.plan.items[i] = it;
+        return it.raw_tiles + it.comp_tiles + 1;
+    };
+    // the whole cost, then the cuts by each stretch of items that they fall into
+    long long all = 0;
+    int cost = 0;
+    for (int i0 = 0; i0 < n_items; i0 += PLAN_THREADS) {
+        cost = i0 + tid < n_items ? make(i0 + tid) : 0;
+        long long total;
+        block_scan<long long>(cost, sums_l, total);
+        all += total;
+    }
+    const int ctas = (int)max(1ll, min((long long)grid, all / MIN_COST));
+    long long before = 0;
+    for (int i0 = 0; i0 < n_items; i0 += PLAN_THREADS) {
+        if (n_items > PLAN_THREADS) {
+            cost = 0;
+            if (i0 + tid < n_items) {
+                const Item &it = p.plan.items[i0 + tid];
+                cost = it.raw_tiles + it.comp_tiles + 1;
             }
         }
-        for (int i = 0; i < E; i++)
-            p.out[token * p.out_token + h * p.out_head + lane + 32 * i] = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] / l);
-        return;
+        long long total;
+        const long long incl = block_scan<long long>(cost, sums_l, total);
+        prefix[tid + 1] = before + incl;
+        if (tid == 0) prefix[0] = before;
+        __syncthreads();
+        for (int c = tid; c < ctas; c += PLAN_THREADS) {
+            const long long at = all * c / ctas;
+            if (at >= before && at < before + total) {
+                int lo = 0, hi = min(PLAN_THREADS, n_items - i0);
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (prefix[mid] <= at) lo = mid;
+                    else hi = mid;
+                }
+                p.plan.start[c] = {i0 + lo, (int)(at - prefix[lo])};
+            }
+        }
+        before += total;
+        __syncthreads();
+    }
+    for (int c = (n_items ? ctas : 0) + tid; c <= grid; c += PLAN_THREADS) p.plan.start[c] = {n_items, 0};
+    __threadfence_block();
+    __syncthreads();
+    // the cuts inside an item whose predecessor is not: one for each divided item
+    auto inside = [&](int c) {
+        const Start s = p.plan.start[c];
+        if (s.item >= n_items) return false;
+        const Item &it = p.plan.items[s.item];
+        const int tiles = it.raw_tiles + it.comp_tiles, f = tiles_before(s.y, tiles);
+        return f > 0 && f < tiles;
+    };
+    for (int c = 1 + tid; c < ctas; c += PLAN_THREADS)
+        if (n_items && inside(c) && !(p.plan.start[c - 1].item == p.plan.start[c].item && inside(c - 1)))
+            p.plan.split[atomicAdd(&n_split, 1)] = c;
+    __syncthreads();
+    if (tid == 0) {
+        p.plan.counts[0] = n_items;
+        p.plan.counts[1] = n_split;
+        p.plan.counts[2] = n_items ? ctas : 0;
     }
 }
 
+// ---- attention ---------------------------------------------------------------------------------
+
+// The items of this CTA, one after the other, with the tiles [tb, te) of each.
+struct Work {
+    const Params &p;
+    Start from, to;
+    int i;
+    Item it;
+    int tiles, tb, te;
+    __device__ Work(const Params &p_) : p(p_) {
+        from = p.plan.start[blockIdx.x];
+        to = p.plan.start[blockIdx.x + 1];
+        i = from.item - 1;
+    }
+    __device__ __forceinline__ bool next() {                    // the next item that this CTA has something of
+        for (;;) {
+            i++;
+            if (i > to.item || (i == to.item && to.y == 0)) return false;
+            it = p.plan.items[i];
+            tiles = it.raw_tiles + it.comp_tiles;
+            tb = i == from.item ? tiles_before(from.y, tiles) : 0;
+            te = i == to.item ? tiles_before(to.y, tiles) : tiles;
+            if (tb < te || (tiles == 0 && !(i == from.item && from.y > 0))) return true;
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap raw_map,
+                  const __grid_constant__ CUtensorMap comp_map, const __grid_constant__ Params p) {
+    using S = Shape<D>;
+    constexpr int N = S::N, C = S::C, RING = S::RING;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    if ((smem_u32(sm) & 1023u) != 0) {                          // the layout has no room to realign
+        pdl_wait();
+        if (threadIdx.x == 0) atomicOr(&g_paged_err, 8u);
+        return;
+    }
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + S::N_BAR);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *ref = reinterpret_cast<float *>(sm + S::OFF_REF);
+    volatile uint32_t *masks = reinterpret_cast<volatile uint32_t *>(sm + S::OFF_MASK);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](uint32_t u) { return bar0 + 8 * (u % RING); };
+    auto empty = [&](uint32_t u) { return bar0 + 8 * (RING + u % RING); };
+    auto bar = [&](int b) { return bar0 + 8 * (2 * RING + b); };
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RING; i++) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        mbar_init(bar(B_QFULL), 1);
+        mbar_init(bar(B_QEMPTY), 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(bar(B_SFULL + i), 1);
+            mbar_init(bar(B_SFREE + i), 8);
+        }
+        mbar_init(bar(B_PFULL), 8);
+        mbar_init(bar(B_PVDONE), 1);
+        mbar_init(bar(B_OFREE), 8);
+        mbar_init(bar(B_DRAIN), 1);
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (D == 64) {                                              // the second chunk of a slot is never loaded
+        for (int i = threadIdx.x; i < RING * CHUNK / 16; i += THREADS)
+            *reinterpret_cast<uint4 *>(sm + S::OFF_X + i / (CHUNK / 16) * SLOT + CHUNK + i % (CHUNK / 16) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    fence_proxy_async();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+    Work w(p);
+    bool ok = true;
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        uint32_t unit = 0, g = 0, n_q = 0;
+        while (w.next()) {
+            if (w.tiles == 0) continue;
+            // the item's queries, once the last S of the item before has read its own
+            if (ok && n_q > 0) ok = warp_wait(bar(B_QEMPTY), (n_q - 1) & 1, abort);
+            if (ok) {
+                if (lane == 0) {
+                    mbar_expect_tx(bar(B_QFULL), S::DC * p.hg * p.tt * 128);
+                    for (int c = 0; c < S::DC; c++)
+                        tma_3d(smem_u32(sm + S::OFF_Q + c * S::Q_CHUNK), &q_map, 64 * c, w.it.head0, w.it.tok0, bar(B_QFULL));
+                }
+                n_q++;
+                __syncwarp();
+            }
+            const long long t0 = w.it.t0, end = t0 + w.it.n_tok;
+            for (int j = w.tb; j < w.te; j++, g++) {
+                const bool raw = j < w.it.raw_tiles;
+                const Pool &pool = raw ? p.raw : p.comp;
+                // this lane's box: a page's rows, or a tile's of a larger page
+                const int box = min(1 << pool.page_log, ROWS), boxes = ROWS / box;
+                const long long row = (long long)(raw ? w.it.raw_tile0 + j : j - w.it.raw_tiles) * ROWS + lane * box;
+                const long long lo = raw && p.window ? t0 + 1 - p.window : 0, hi = raw ? end : end / p.ratio;
+                int y = raw ? p.raw_rows : p.comp_rows;
+                bool missing = false;
+                if (lane < boxes && row + box > lo && row < hi) {
+                    const long long k = row >> pool.page_log;
+                    const int page = k < pool.max_pages ? pool.pages[w.it.seq * pool.ld + k] : -1;
+                    missing = page < 0 || page >= pool.n_pages;
+                    if (!missing) y = (page << pool.page_log) + (int)(row & ((1 << pool.page_log) - 1));
+                }
+                const uint32_t miss = __ballot_sync(0xffffffffu, missing);
+                if (miss && lane == 0) atomicOr(&g_paged_err, 4u);
+                if (lane == 0) masks[g % MASKS] = miss;         // the slots' previous tile is done with its own
+                const CUtensorMap *map = raw ? &raw_map : &comp_map;
+                for (int b = 0; b < S::DB; b++) {
+                    if (ok) ok = warp_wait(empty(unit), ((unit / RING) & 1) ^ 1, abort);
+                    if (!ok) continue;
+                    const uint32_t dst = smem_u32(sm + S::OFF_X) + unit % RING * SLOT + lane * box * 128, fb = full(unit);
+                    if (lane == 0) mbar_expect_tx(fb, D == 64 ? CHUNK : SLOT);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        tma_2d(dst, map, 128 * b, y, fb);
+                        if (D != 64) tma_2d(dst + CHUNK, map, 128 * b + 64, y, fb);
+                    }
+                    unit++;
+                }
+            }
+        }
+        // what was issued lands before the CTA exits, whichever warp gave up
+        uint64_t t0 = 0;
+        __syncwarp();
+        for (uint32_t u = unit > (uint32_t)RING ? unit - RING : 0; u < unit; u++) mbar_drain(full(u), (u / RING) & 1, t0);
+        if (n_q > 0) mbar_drain(bar(B_QFULL), (n_q - 1) & 1, t0);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t ID_S = idesc(N, 0, 0), ID_O = idesc(N, 1, 1);
+        constexpr uint64_t DK = desc(16, 1024), DM = desc(CHUNK, 1024);
+        const uint32_t q0 = smem_u32(sm + S::OFF_Q) >> 4, p0 = smem_u32(sm + S::OFF_P) >> 4, x0 = smem_u32(sm + S::OFF_X);
+        const uint32_t leader = lane == 0;
+        uint32_t g = 0, unit_s = 0, unit_o = 0, items = 0;
+        auto do_s = [&](bool first, bool last) {
+            if (first && ok) ok = warp_wait(bar(B_QFULL), items & 1, abort);
+            if (ok && g >= 2) ok = warp_wait(bar(B_SFREE + (g & 1)), ((g >> 1) - 1) & 1, abort);
+            const uint32_t d = tmem + S::T_S + (g & 1) * N;
+            for (int b = 0; b < S::DB; b++, unit_s++) {
+                if (ok) ok = warp_wait(full(unit_s), (unit_s / RING) & 1, abort);
+                if (!ok) continue;
+                fence_after();
+                const uint32_t x = (x0 + unit_s % RING * SLOT) >> 4;
+#pragma unroll
+                for (int c = 0; c < (D == 64 ? 1 : 2); c++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_w(d, DK + x + c * (CHUNK >> 4) + 2 * k, DK + q0 + (2 * b + c) * (S::Q_CHUNK >> 4) + 2 * k, ID_S,
+                              b + c + k > 0 ? 1u : 0u, leader);
+            }
+            if (ok) {
+                commit_w(bar(B_SFULL + (g & 1)), leader);
+                if (last) commit_w(bar(B_QEMPTY), leader);
+            }
+            g++;
+        };
+        auto do_o = [&](uint32_t go, bool first) {
+            if (ok) ok = warp_wait(bar(B_PFULL), go & 1, abort);
+            if (first && ok && items > 0) ok = warp_wait(bar(B_OFREE), (items - 1) & 1, abort);
+            if (ok) fence_after();
+            for (int b = 0; b < S::DB; b++, unit_o++) {
+                if (!ok) continue;
+                const uint32_t x = (x0 + unit_o % RING * SLOT) >> 4, d = tmem + S::T_O + b * N;
+#pragma unroll
+                for (int k = 0; k < 8; k++) mma_w(d, DM + x + k * 128, DM + p0 + k * 128, ID_O, first && k == 0 ? 0u : 1u, leader);
+                commit_w(empty(unit_o), leader);
+            }
+            if (ok) commit_w(bar(B_PVDONE), leader);
+        };
+        while (w.next()) {
+            const int n = w.te - w.tb;
+            if (n == 0) continue;
+            do_s(true, n == 1);
+            for (int j = 0; j < n; j++) {
+                if (S::AHEAD && j + 1 < n) do_s(false, j + 2 == n);
+                do_o(S::AHEAD && j + 1 < n ? g - 2 : g - 1, j == 0);
+                if (!S::AHEAD && j + 1 < n) do_s(false, j + 2 == n);
+            }
+            items++;
+        }
+        // every MMA issued completes before the TMEM is freed
+        commit_w(bar(B_DRAIN), leader);
+        uint64_t t0 = 0;
+        mbar_drain(bar(B_DRAIN), 0, t0);
+        __syncwarp();
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
+        Work w(p);
+        bool ok = true;
+        // ------------------------------------------------------------ softmax, output
+        const int grp = (warp - 4) / 4, q4 = warp % 4, id = 1 + grp, col0 = grp * C;
+        const int r = q4 * 32 + lane, tid = threadIdx.x - 128 - 128 * grp;
+        const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
+        float *red = reinterpret_cast<float *>(sm + S::OFF_RED) + grp * 4 * C;
+        float *gref = ref + col0;
+        uint8_t *prow = sm + S::OFF_P + (C == 64 ? grp * CHUNK : 0) + r * 128;
+        const int u0 = C == 64 ? 0 : grp * 4;                   // first 16-byte unit of the group's columns
+        uint32_t g = 0, items = 0;
+        while (w.next()) {
+            const int n_cols = w.it.n_tok * p.hg, mine = min(max(n_cols - col0, 0), C);   // this group's columns in use
+            const long long t0 = w.it.t0;
+            float l[C];
+#pragma unroll
+            for (int c = 0; c < C; c++) l[c] = 0.f;
+            // columns out of use: a reference that no logit exceeds
+            if (tid < C) gref[tid] = tid < mine ? NONE : INFINITY;
+            group_sync(id);
+            for (int j = w.tb; j < w.te; j++, g++) {
+                const int sb = g & 1;
+                if (ok) ok = warp_wait(bar(B_SFULL + sb), (g >> 1) & 1, abort);
+                fence_after();
+                // columns [ca, cb) see this thread's row; full: all of the tile's rows by all columns
+                const bool raw = j < w.it.raw_tiles;
+                const long long base = (long long)(raw ? w.it.raw_tile0 + j : j - w.it.raw_tiles) * ROWS, row = base + r;
+                const uint32_t miss = masks[g % MASKS];
+                bool is_full;
+                int ca, cb;
+                {
+                    long long a, b = w.it.n_tok;
+                    if (raw) {
+                        a = row - t0;
+                        if (p.window) b = min(b, row + p.window - t0);
+                        is_full = base + ROWS - 1 <= t0 && (!p.window || base + p.window >= t0 + w.it.n_tok);
+                    } else {
+                        a = (row + 1) * p.ratio - 1 - t0;
+                        is_full = (base + ROWS) * p.ratio - 1 <= t0;
+                    }
+                    a = min(max(a, 0ll), (long long)w.it.n_tok);
+                    b = max(b, 0ll);
+                    const Pool &pool = raw ? p.raw : p.comp;
+                    if ((miss >> (r >> min(pool.page_log, 7))) & 1) b = 0;
+                    is_full = is_full && miss == 0;
+                    ca = (int)a * p.hg - col0;
+                    cb = (int)b * p.hg - col0;
+                }
+                float s[C];
+                auto load_s = [&]() {
+#pragma unroll
+                    for (int c = 0; c < C; c += 32) tmem_ld32(lane_base + S::T_S + sb * N + col0 + c, s + c);
+                    ld_wait();
+                };
+                auto mask = [&]() {
+                    bool finite = false;
+#pragma unroll
+                    for (int c = 0; c < C; c++) finite |= c < mine && fabsf(s[c]) <= 3.4028235e38f;
+                    const float seen = finite ? 0.f : __int_as_float(0x7fc00000);
+#pragma unroll
+                    for (int c = 0; c < C; c++) s[c] = c >= ca && c < cb ? s[c] + seen : -INFINITY;
+                    return finite;
+                };
+                load_s();
+                bool finite = true;
+                if (!is_full) finite = mask();
+                bool need = false;
+#pragma unroll
+                for (int c = 0; c < C; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(gref + c);
+                    s[c] = fmaf(s[c], p.scale_log2, -m.x);
+                    s[c + 1] = fmaf(s[c + 1], p.scale_log2, -m.y);
+                    s[c + 2] = fmaf(s[c + 2], p.scale_log2, -m.z);
+                    s[c + 3] = fmaf(s[c + 3], p.scale_log2, -m.w);
+                    need |= s[c] > TAU || s[c + 1] > TAU || s[c + 2] > TAU || s[c + 3] > TAU;
+                }
+                const bool moves = group_any(id, need);
+                if (moves) {
+                    // the tile's largest logit of each column, the new references and the factors 2^(old - new)
+                    load_s();
+                    if (!is_full) mask();
+                    float m[C / 32];
+#pragma unroll
+                    for (int c = 0; c < C; c++) s[c] *= p.scale_log2;
+                    reduce_columns<true, C>(s, m);
+#pragma unroll
+                    for (int k = 0; k < C / 32; k++) red[q4 * C + lane * (C / 32) + k] = m[k];
+                    group_sync(id);
+                    if (tid < C) {
+                        const float old = gref[tid], now = fmaxf(old, fmaxf(fmaxf(red[tid], red[C + tid]), fmaxf(red[2 * C + tid], red[3 * C + tid])));
+                        gref[tid] = now;
+                        red[tid] = ex2(old - now);
+                    }
+                    group_sync(id);
+#pragma unroll
+                    for (int c = 0; c < C; c++) {
+                        s[c] -= gref[c];
+                        l[c] *= red[c];
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SFREE + sb));
+                // the second product of the tile before is done with P, and with O
+                if (ok && g > 0) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
+                if (moves && j > w.tb) {
+                    fence_after();
+#pragma unroll 1
+                    for (int b = 0; b < S::DB; b++)
+#pragma unroll
+                        for (int c = 0; c < C; c += 32) {
+                            float v[32];
+                            const uint32_t at = lane_base + S::T_O + b * N + col0 + c;
+                            tmem_ld32(at, v);
+                            ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; e++) v[e] *= red[c + e];
+                            tmem_st32(at, v);
+                        }
+                    st_wait();
+                }
+                if (mine > 0) {
+#pragma unroll
+                    for (int c = 0; c < C; c++) {
+                        s[c] = ex2(s[c]);
+                        l[c] += s[c];
+                    }
+#pragma unroll
+                    for (int u = 0; u < C / 8; u++)
+                        *reinterpret_cast<uint4 *>(prow + (((u0 + u) ^ (r & 7)) * 16)) =
+                            make_uint4(pack(s[8 * u], s[8 * u + 1]), pack(s[8 * u + 2], s[8 * u + 3]), pack(s[8 * u + 4], s[8 * u + 5]),
+                                       pack(s[8 * u + 6], s[8 * u + 7]));
+                }
+                if (grp == 0 && !finite && ok) {
+                    // no logit of this row is a number: if the row is none, it takes no part (its columns got NaN weights)
+                    const uint32_t unit = g * S::DB;
+                    bool bad = false;
+                    for (int b = 0; b < S::DB; b++)
+                        for (int c = 0; c < (D == 64 ? 1 : 2); c++)
+                            for (int u = 0; u < 8; u++) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(sm + S::OFF_X + (unit + b) % RING * SLOT + c * CHUNK + r * 128 + ((u + lane) & 7) * 16);
+                                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                                for (int e = 0; e < 4; e++) bad |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+                            }
+                    if (bad)
+                        for (int b = 0; b < S::DB; b++)
+                            for (int c = 0; c < (D == 64 ? 1 : 2); c++)
+                                for (int u = 0; u < 8; u++)
+                                    *reinterpret_cast<uint4 *>(sm + S::OFF_X + (unit + b) % RING * SLOT + c * CHUNK + r * 128 + ((u + lane) & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                }
+                fence_before();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PFULL));
+            }
+            // denominators: the lanes' and warps' sums
+            float sum[C / 32];
+            reduce_columns<false, C>(l, sum);
+            group_sync(id);                                     // the factors in red have been read
+#pragma unroll
+            for (int k = 0; k < C / 32; k++) red[q4 * C + lane * (C / 32) + k] = sum[k];
+            group_sync(id);
+            const bool whole = w.tb == 0 && w.te == w.tiles;
+            const int64_t part = (int64_t)2 * blockIdx.x + (w.tb == 0 ? 1 : 0);
+            if (tid < C) {
+                const float d = (red[tid] + red[C + tid]) + (red[2 * C + tid] + red[3 * C + tid]);
+                if (!whole && ok) {
+                    p.plan.part_ml[part * 2 * N + col0 + tid] = gref[tid];
+                    p.plan.part_ml[part * 2 * N + N + col0 + tid] = d;
+                }
+                red[tid] = d == 0.f ? 0.f : 1.0f / d;           // no row seen: zeros
+            }
+            group_sync(id);
+            if (w.tiles > 0) {
+                if (ok) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
+                fence_after();
+            }
+#pragma unroll 1
+            for (int b = 0; b < S::DB; b++) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < C; c0 += 32) {
+                    if (c0 >= mine) break;
+                    float v[32];
+                    if (w.tiles > 0) {
+                        tmem_ld32(lane_base + S::T_O + b * N + col0 + c0, v);
+                        ld_wait();
+                    }
+                    if (!ok) continue;
+                    const int d = 128 * b + r;
+                    if (!whole) {
+                        float *dst = p.plan.part_o + (part * N + col0 + c0) * D + d;
+                        if (D > 64 || r < 64) {
+#pragma unroll
+                            for (int c = 0; c < 32; c++)
+                                if (c0 + c < mine) dst[c * D] = v[c];
+                        }
+                    } else {
+                        // two lanes trade so that each stores two neighbouring values: the even one of column c, the
+                        // odd one of column c + 1
+                        int tok = (col0 + c0) / p.hg, h = (col0 + c0) % p.hg;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float a = red[c0 + c] == 0.f ? 0.f : v[c] * red[c0 + c], e = red[c0 + c + 1] == 0.f ? 0.f : v[c + 1] * red[c0 + c + 1];
+                            const float x = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : e, 1);
+                            const uint32_t two = lane & 1 ? pack(x, e) : pack(a, x);
+                            int tok1 = tok, h1 = h + 1;
+                            if (h1 == p.hg) { h1 = 0; tok1++; }
+                            const int mt = lane & 1 ? tok1 : tok, mh = w.it.head0 + (lane & 1 ? h1 : h);
+                            if (c0 + c + (lane & 1) < mine && mh < p.n_heads && (D > 64 || r < 64))
+                                *reinterpret_cast<uint32_t *>(p.out + (w.it.tok0 + mt) * p.out_token + mh * p.out_head + (d & ~1)) = two;
+                            tok = tok1;
+                            h = h1 + 1;
+                            if (h == p.hg) { h = 0; tok++; }
+                        }
+                    }
+                }
+            }
+            if (w.tiles > 0) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_OFREE));
+                items++;
+            }
+            group_sync(id);                                     // red and ref are free for the next item
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// Joins the parts of the divided items: a block per item and column.
+template <int D>
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
+    constexpr int N = Shape<D>::N, PER = 4, LANES = D / PER, GROUPS = JOIN_THREADS / LANES;   // values of a thread, threads of a part
+    constexpr int AT_ONCE = 4;
+    __shared__ float weight[MAX_GRID], denom[MAX_GRID];
+    __shared__ int slot[MAX_GRID];
+    __shared__ __align__(16) float sums[GROUPS][D];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int col = blockIdx.x % N;
+    if ((int)(blockIdx.x / N) >= p.plan.counts[1]) return;
+    const int c0 = p.plan.split[blockIdx.x / N], ctas = p.plan.counts[2];
+    const int item = p.plan.start[c0].item;
+    const Item it = p.plan.items[item];
+    const int tiles = it.raw_tiles + it.comp_tiles;
+    if (col >= it.n_tok * p.hg || it.head0 + col % p.hg >= p.n_heads) return;
+    // parts: the CTA in front of the first cut, then every CTA that starts inside the item
+    int n = 1;
+    for (int c = c0; c < ctas; c += JOIN_THREADS) {
+        const int cc = c + threadIdx.x;
+        bool in = false;
+        if (cc < ctas && p.plan.start[cc].item == item) {
+            const int f = tiles_before(p.plan.start[cc].y, tiles);
+            in = f > 0 && f < tiles;
+        }
+        const int k = __syncthreads_count(in);
+        n += k;
+        if (k < JOIN_THREADS) break;
+    }
+    float m = NONE;
+    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
+        slot[i] = i == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + i - 1);
+        weight[i] = p.plan.part_ml[(int64_t)slot[i] * 2 * N + col];
+        denom[i] = p.plan.part_ml[(int64_t)slot[i] * 2 * N + N + col];
+    }
+    __syncthreads();
+    for (int i = 0; i < n; i++) m = fmaxf(m, weight[i]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
+        weight[i] = ex2(weight[i] - m);
+        denom[i] *= weight[i];
+    }
+    __syncthreads();
+    float den = 0.f;
+    for (int i = 0; i < n; i++) den += denom[i];
+    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *src = p.plan.part_o + (int64_t)col * D + PER * lane;
+#pragma unroll AT_ONCE
+    for (int i = grp; i < n; i += GROUPS) {
+        const float4 v = *reinterpret_cast<const float4 *>(src + slot[i] * (int64_t)(N * D));
+        const float f = weight[i];
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+    }
+    *reinterpret_cast<float4 *>(&sums[grp][PER * lane]) = acc;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int k = 1; k < GROUPS; k++) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sums[k][PER * lane]);
+        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    const float inv = den == 0.f ? 0.f : 1.0f / den;
+    if (den == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t at = (it.tok0 + col / p.hg) * p.out_token + (it.head0 + col % p.hg) * p.out_head + PER * lane;
+    *reinterpret_cast<uint2 *>(p.out + at) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
+}
+
+// ---- host --------------------------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_relaxed);
+    if (!f) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+        fn.store(f, std::memory_order_relaxed);
+    }
+    return f;
+}
+bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    const auto fn = encode_fn();
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool pool_map(CUtensorMap *m, const ds4c_page_pool &a, uint32_t d) {
+    const cuuint64_t dims[2] = {d, (cuuint64_t)a.n_pages * a.page_rows}, strides[1] = {(cuuint64_t)d * 2};
+    const cuuint32_t box[2] = {64, a.page_rows < ROWS ? a.page_rows : ROWS};
+    return make_map(m, a.rows, 2, dims, strides, box);
+}
 Pool pool_of(const ds4c_page_pool &a) {
-    return {static_cast<const __nv_bfloat16 *>(a.rows), a.pages, (int64_t)a.pages_ld, (int)a.n_pages, (int)a.page_rows, (int)a.max_pages};
+    int log = 0;
+    while ((1u << log) < a.page_rows) log++;
+    return {a.pages, (int64_t)a.pages_ld, (int)a.n_pages, log, (int)a.max_pages};
+}
+int sm_count() {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+struct Split { int n, hg, groups, tt; };
+Split split_of(uint32_t n_heads, uint32_t d) {
+    const int n = d == 512 ? 64 : 128, h = (int)n_heads, groups = (h + n - 1) / n, hg = (h + groups - 1) / groups;
+    return {n, hg, groups, n / hg};
+}
+// The workspace's regions; returns its size.
+size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_heads, uint32_t d) {
+    const Split c = split_of(n_heads, d);
+    size_t at = 0;
+    auto region = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes, 256);
+        return ws + here;
+    };
+    Plan o;
+    o.counts = reinterpret_cast<int *>(region(16));
+    o.start = reinterpret_cast<Start *>(region(sizeof(Start) * (grid + 1)));
+    o.split = reinterpret_cast<int *>(region(4 * (size_t)grid));
+    o.items = reinterpret_cast<Item *>(region(sizeof(Item) * (size_t)n_tok * c.groups));
+    o.part_ml = reinterpret_cast<float *>(region((size_t)2 * grid * 2 * c.n * 4));
+    o.part_o = reinterpret_cast<float *>(region((size_t)2 * grid * c.n * d * 4));
+    if (plan) *plan = o;
+    return at;
+}
+
+template <int D>
+cudaError_t launch(const ds4c_paged_attn_args &a, const Params &p, int grid, cudaStream_t s) {
+    using S = Shape<D>;
+    CUtensorMap qm, rm, cm;
+    {
+        const cuuint64_t dims[3] = {D, a.n_heads, a.n_tok};
+        const cuuint64_t strides[2] = {a.n_heads > 1 ? (cuuint64_t)a.q_head * 2 : D * 2, a.n_tok > 1 ? (cuuint64_t)a.q_token * 2 : D * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)p.hg, (cuuint32_t)p.tt};
+        if (!make_map(&qm, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    if (!pool_map(&rm, a.raw, D) || !pool_map(&cm, a.ratio ? a.comp : a.raw, D)) return cudaErrorInvalidValue;
+    cudaError_t e = ensure_dyn_smem(paged_attn_kernel<D>, S::SMEM);
+    if (e != cudaSuccess) return e;
+    // a register split above the launch's total would wait for ever
+    static std::atomic<int> regs{0};
+    int have = regs.load(std::memory_order_relaxed);
+    if (have == 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, paged_attn_kernel<D>);
+        if (e != cudaSuccess) return e;
+        regs.store(have = fa.numRegs, std::memory_order_relaxed);
+    }
+    if (128 * (REG_LOW + 2 * REG_SOFT) > THREADS * have) return cudaErrorNotSupported;
+    e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), (a.n_seq + 1) * sizeof(int), s, p, grid);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(paged_attn_kernel<D>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
+    if (e != cudaSuccess) return e;
+    // every divided item holds a cut
+    const uint64_t items = (uint64_t)a.n_tok * p.groups, joins = items < (uint64_t)grid - 1 ? items : (uint64_t)grid - 1;
+    return joins ? launch_pdl(paged_join_kernel<D>, dim3((unsigned)joins * S::N), dim3(JOIN_THREADS), 0, s, p) : cudaSuccess;
 }
 
 }  // namespace
 
-size_t paged_attn_ws_bytes(uint32_t, uint32_t, uint32_t, uint32_t) { return 256; }
+size_t paged_attn_ws_bytes(uint32_t, uint32_t n_tok, uint32_t n_heads, uint32_t head_dim) {
+    return lay_out(nullptr, nullptr, sm_count(), n_tok, n_heads, head_dim);
+}
 
-cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *, cudaStream_t s) {
+cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStream_t s) {
+    const int grid = sm_count();
+    if (grid > MAX_GRID) return cudaErrorNotSupported;
     Params p{};
-    p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.out = static_cast<__nv_bfloat16 *>(a.out);
-    p.q_token = (int64_t)a.q_token; p.q_head = (int64_t)a.q_head;
     p.out_token = (int64_t)a.out_token; p.out_head = (int64_t)a.out_head;
     p.start = a.start; p.length = a.length;
     p.raw = pool_of(a.raw);
-    if (a.ratio) p.comp = pool_of(a.comp);
+    p.raw_rows = (int)(a.raw.n_pages * a.raw.page_rows);
+    if (a.ratio) {
+        p.comp = pool_of(a.comp);
+        p.comp_rows = (int)(a.comp.n_pages * a.comp.page_rows);
+    }
     p.n_seq = (int)a.n_seq; p.n_tok = (int)a.n_tok; p.n_heads = (int)a.n_heads;
     p.window = (int)a.window; p.ratio = (int)a.ratio;
+    const Split c = split_of(a.n_heads, a.head_dim);
+    p.hg = c.hg; p.groups = c.groups; p.tt = c.tt;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    const dim3 grid((unsigned)(((uint64_t)a.n_tok * a.n_heads + 3) / 4));
-    auto run = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(128), 0, s, p); };
-    return a.head_dim == 64 ? run(paged_attn_kernel<64>) : a.head_dim == 128 ? run(paged_attn_kernel<128>)
-         : a.head_dim == 256 ? run(paged_attn_kernel<256>) : run(paged_attn_kernel<512>);
+    lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.n_heads, a.head_dim);
+    return a.head_dim == 64 ? launch<64>(a, p, grid, s) : a.head_dim == 128 ? launch<128>(a, p, grid, s)
+         : a.head_dim == 256 ? launch<256>(a, p, grid, s) : launch<512>(a, p, grid, s);
 }
+
+cudaError_t paged_attn_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_paged_wait_ns, &ns, sizeof ns); }
 
 unsigned int paged_attn_read_clear_error() {
     unsigned int v = 0, z = 0;

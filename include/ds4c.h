@@ -416,7 +416,7 @@ DS4C_API ds4c_status ds4c_rotate_heads(const ds4c_rotate_args *args, cudaStream_
  * see it, and of no other.  A page outside 0 .. n_pages - 1 or past max_pages where a visible row should be, and a
  * start that falls or leaves 0 .. n_tok, raise the device error word; such rows and tokens count as not there.
  *
- * n_heads 1 .. 128, head_dim 64, 128, 256 or 512, n_seq <= 65536, n_tok <= 2^20, n_pages * page_rows <= 2^31 - 1, 0 < scale <= 1e4.
+ * n_heads 1 .. 128, head_dim 64, 128, 256 or 512, n_seq <= 4096, n_tok <= 2^20, n_pages * page_rows <= 2^31 - 1, 0 < scale <= 1e4.
  * The workspace (ds4c_paged_attn_workspace_bytes, of the device the call runs on; 256-byte aligned) belongs to one call
  * at a time: calls that may overlap, captured ones among them, take one each.  Equal calls give equal bits. */
 typedef struct {

@@ -38,7 +38,7 @@ def test_refusals():
     for kw in (dict(q=None), dict(out=None), dict(start=None), dict(length=None), dict(raw=dict(rows=None)), dict(raw=dict(pages=None)),
                dict(ratio=4, comp=dict(rows=None)), dict(ratio=4, comp=dict(pages=None))):
         assert call(**kw) == abi.DS4C_ERR_NULL, kw
-    for kw in (dict(n_seq=65537), dict(n_tok=(1 << 20) + 1), dict(n_heads=0), dict(n_heads=129), dict(head_dim=96), dict(head_dim=0),
+    for kw in (dict(n_seq=4097), dict(n_tok=(1 << 20) + 1), dict(n_heads=0), dict(n_heads=129), dict(head_dim=96), dict(head_dim=0),
                dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=1e5), dict(window=1 << 31), dict(ratio=1 << 31),
                dict(q=FAKE + 8), dict(out=FAKE + 8), dict(start=FAKE + 2), dict(length=FAKE + 2), dict(q_token=64 * 512 + 4),
                dict(q_head=516), dict(out_token=64 * 512 + 4), dict(out_head=516), dict(out_head=504), dict(out_token=63 * 512),
@@ -51,7 +51,7 @@ def test_refusals():
     need = abi.ds4c_paged_attn_workspace_bytes(3, 10, 64, 512)
     for kw in (dict(ws=None), dict(ws=FAKE + 128), dict(ws_bytes=need - 1)):
         assert call(**kw) == abi.DS4C_ERR_WORKSPACE, kw
-    for bad in ((65537, 1, 64, 512), (1, (1 << 20) + 1, 64, 512), (1, 1, 0, 512), (1, 1, 129, 512), (1, 1, 64, 500)):
+    for bad in ((4097, 1, 64, 512), (1, (1 << 20) + 1, 64, 512), (1, 1, 0, 512), (1, 1, 129, 512), (1, 1, 64, 500)):
         assert abi.ds4c_paged_attn_workspace_bytes(*bad) == 0
     assert abi.ds4c_paged_attn_workspace_bytes(0, 0, 1, 64) > 0
 

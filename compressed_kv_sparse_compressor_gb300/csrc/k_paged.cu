@@ -174,23 +174,26 @@ __host__ __device__ constexpr uint32_t idesc(int n, int a_mn, int b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
-// By a converged warp, the leading lane issues.
-__device__ __forceinline__ void mma_w(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t leader) {
+// One lane of a converged warp: what it issues lies in uniform registers.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(leader)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void commit_w(uint32_t bar, uint32_t leader) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "setp.ne.b32 e, %1, 0;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(leader)
-        : "memory");
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -570,8 +573,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t ID_S = idesc(N, 0, 0), ID_O = idesc(N, 1, 1);
         constexpr uint64_t DK = desc(16, 1024), DM = desc(CHUNK, 1024);
-        const uint32_t q0 = smem_u32(sm + S::OFF_Q) >> 4, p0 = smem_u32(sm + S::OFF_P) >> 4, x0 = smem_u32(sm + S::OFF_X);
-        const uint32_t leader = lane == 0;
+        const uint64_t qk = DK + (smem_u32(sm + S::OFF_Q) >> 4), xk = DK + (smem_u32(sm + S::OFF_X) >> 4),
+                       pm = DM + (smem_u32(sm + S::OFF_P) >> 4), xm = DM + (smem_u32(sm + S::OFF_X) >> 4);
         uint32_t g = 0, unit_s = 0, unit_o = 0, items = 0;
         auto do_s = [&](bool first, bool last) {
             if (first && ok) ok = warp_wait(bar(B_QFULL), items & 1, abort);
@@ -581,17 +584,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 if (ok) ok = warp_wait(full(unit_s), (unit_s / RING) & 1, abort);
                 if (!ok) continue;
                 fence_after();
-                const uint32_t x = (x0 + unit_s % RING * SLOT) >> 4;
+                const uint64_t x = xk + unit_s % RING * (SLOT >> 4), q = qk + 2 * b * (S::Q_CHUNK >> 4);
+                const uint32_t acc = b > 0 ? 1u : 0u;
+                if (elect()) {
 #pragma unroll
-                for (int c = 0; c < (D == 64 ? 1 : 2); c++)
+                    for (int c = 0; c < (D == 64 ? 1 : 2); c++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_w(d, DK + x + c * (CHUNK >> 4) + 2 * k, DK + q0 + (2 * b + c) * (S::Q_CHUNK >> 4) + 2 * k, ID_S,
-                              b + c + k > 0 ? 1u : 0u, leader);
-            }
-            if (ok) {
-                commit_w(bar(B_SFULL + (g & 1)), leader);
-                if (last) commit_w(bar(B_QEMPTY), leader);
+                        for (int k = 0; k < 4; k++)
+                            mma(d, x + c * (CHUNK >> 4) + 2 * k, q + c * (S::Q_CHUNK >> 4) + 2 * k, ID_S, c + k > 0 ? 1u : acc);
+                    if (b == S::DB - 1) {
+                        commit(bar(B_SFULL + (g & 1)));
+                        if (last) commit(bar(B_QEMPTY));
+                    }
+                }
+                __syncwarp();
             }
             g++;
         };
@@ -601,12 +607,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             if (ok) fence_after();
             for (int b = 0; b < S::DB; b++, unit_o++) {
                 if (!ok) continue;
-                const uint32_t x = (x0 + unit_o % RING * SLOT) >> 4, d = tmem + S::T_O + b * N;
+                const uint64_t x = xm + unit_o % RING * (SLOT >> 4);
+                const uint32_t d = tmem + S::T_O + b * N, acc = first ? 0u : 1u;
+                if (elect()) {
 #pragma unroll
-                for (int k = 0; k < 8; k++) mma_w(d, DM + x + k * 128, DM + p0 + k * 128, ID_O, first && k == 0 ? 0u : 1u, leader);
-                commit_w(empty(unit_o), leader);
+                    for (int k = 0; k < 8; k++) mma(d, x + k * 128, pm + k * 128, ID_O, k > 0 ? 1u : acc);
+                    commit(empty(unit_o));
+                    if (b == S::DB - 1) commit(bar(B_PVDONE));
+                }
+                __syncwarp();
             }
-            if (ok) commit_w(bar(B_PVDONE), leader);
         };
         while (w.next()) {
             const int n = w.te - w.tb;
@@ -620,7 +630,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             items++;
         }
         // every MMA issued completes before the TMEM is freed
-        commit_w(bar(B_DRAIN), leader);
+        if (elect()) commit(bar(B_DRAIN));
+        __syncwarp();
         uint64_t t0 = 0;
         mbar_drain(bar(B_DRAIN), 0, t0);
         __syncwarp();

@@ -660,31 +660,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             group_sync(id);
             for (int j = w.tb; j < w.te; j++, g++) {
                 const int sb = g & 1;
-                if (ok) ok = warp_wait(bar(B_SFULL + sb), (g >> 1) & 1, abort);
-                fence_after();
-                // columns [ca, cb) see this thread's row; full: all of the tile's rows by all columns
+                // columns [ca, cb) see this thread's row; is_full: all of the tile's rows by all columns
                 const bool raw = j < w.it.raw_tiles;
                 const long long base = (long long)(raw ? w.it.raw_tile0 + j : j - w.it.raw_tiles) * ROWS, row = base + r;
+                bool is_full = raw ? base + ROWS - 1 <= t0 && (!p.window || base + p.window >= t0 + w.it.n_tok)
+                                   : (base + ROWS) * p.ratio - 1 <= t0;
+                int ca = -col0, cb = n_cols - col0;
+                if (!is_full) {
+                    const long long a = raw ? row - t0 : (row + 1) * p.ratio - 1 - t0, n = w.it.n_tok;
+                    const long long e = raw && p.window ? min(n, row + p.window - t0) : n;
+                    ca = (int)min(max(a, 0ll), n) * p.hg - col0;
+                    cb = (int)max(e, 0ll) * p.hg - col0;
+                }
+                if (ok) ok = warp_wait(bar(B_SFULL + sb), (g >> 1) & 1, abort);
+                fence_after();
                 const uint32_t miss = masks[g % MASKS];
-                bool is_full;
-                int ca, cb;
-                {
-                    long long a, b = w.it.n_tok;
-                    if (raw) {
-                        a = row - t0;
-                        if (p.window) b = min(b, row + p.window - t0);
-                        is_full = base + ROWS - 1 <= t0 && (!p.window || base + p.window >= t0 + w.it.n_tok);
-                    } else {
-                        a = (row + 1) * p.ratio - 1 - t0;
-                        is_full = (base + ROWS) * p.ratio - 1 <= t0;
-                    }
-                    a = min(max(a, 0ll), (long long)w.it.n_tok);
-                    b = max(b, 0ll);
-                    const Pool &pool = raw ? p.raw : p.comp;
-                    if ((miss >> (r >> min(pool.page_log, 7))) & 1) b = 0;
-                    is_full = is_full && miss == 0;
-                    ca = (int)a * p.hg - col0;
-                    cb = (int)b * p.hg - col0;
+                if (miss) {
+                    is_full = false;
+                    if ((miss >> (r >> min((raw ? p.raw : p.comp).page_log, 7))) & 1) cb = ca;
                 }
                 float s[C];
                 auto load_s = [&]() {
@@ -692,19 +685,32 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     for (int c = 0; c < C; c += 32) tmem_ld32(lane_base + S::T_S + sb * N + col0 + c, s + c);
                     ld_wait();
                 };
+                // logits that are not seen to -infinity; those of a row without a finite logit to NaN
                 auto mask = [&]() {
-                    bool finite = false;
+                    float least = INFINITY;                     // fminf passes NaN over
+                    if (mine == C) {
 #pragma unroll
-                    for (int c = 0; c < C; c++) finite |= c < mine && fabsf(s[c]) <= 3.4028235e38f;
+                        for (int c = 0; c < C; c++) least = fminf(least, fabsf(s[c]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C; c++) least = c < mine ? fminf(least, fabsf(s[c])) : least;
+                    }
+                    const bool finite = least < INFINITY;
                     const float seen = finite ? 0.f : __int_as_float(0x7fc00000);
+                    const uint32_t span = max(cb - ca, 0);
+                    if (ca <= 0 && cb >= C) {
 #pragma unroll
-                    for (int c = 0; c < C; c++) s[c] = c >= ca && c < cb ? s[c] + seen : -INFINITY;
+                        for (int c = 0; c < C; c++) s[c] += seen;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C; c++) s[c] = (uint32_t)(c - ca) < span ? s[c] + seen : -INFINITY;
+                    }
                     return finite;
                 };
                 load_s();
                 bool finite = true;
                 if (!is_full) finite = mask();
-                bool need = false;
+                float most = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < C; c += 4) {
                     const float4 m = *reinterpret_cast<const float4 *>(gref + c);
@@ -712,8 +718,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     s[c + 1] = fmaf(s[c + 1], p.scale_log2, -m.y);
                     s[c + 2] = fmaf(s[c + 2], p.scale_log2, -m.z);
                     s[c + 3] = fmaf(s[c + 3], p.scale_log2, -m.w);
-                    need |= s[c] > TAU || s[c + 1] > TAU || s[c + 2] > TAU || s[c + 3] > TAU;
+                    most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
+                    most = fmaxf(fmaxf(most, s[c + 2]), s[c + 3]);
                 }
+                const bool need = most > TAU;
                 const bool moves = group_any(id, need);
                 if (moves) {
                     // the tile's largest logit of each column, the new references and the factors 2^(old - new)
@@ -741,8 +749,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SFREE + sb));
-                // the second product of the tile before is done with P, and with O
-                if (ok && g > 0) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
+                // the second product of the tile before is done with P, and with O: where it was issued in front of this
+                // tile's first, the wait for that was the wait for both
+                if (S::AHEAD && ok && g > 0) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
                 if (moves && j > w.tb) {
                     fence_after();
 #pragma unroll 1
@@ -816,42 +825,58 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 if (ok) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
                 fence_after();
             }
+            // Whole items: two lanes trade so that each stores two neighbouring values, the even one of column c, the odd one
+            // of column c + 1; this lane's columns c0 + 2 i + (lane & 1) lie `at` and a step of out_head further each, or a
+            // token further.  What is read from shared memory is read ahead of the stores, which it may not pass.
 #pragma unroll 1
-            for (int b = 0; b < S::DB; b++) {
+            for (int c0 = 0; c0 < C && c0 < mine; c0 += 32) {
+                const int my = c0 + (lane & 1);
+                const int first_h = (col0 + my) % p.hg;
+                __nv_bfloat16 *first = p.out + (w.it.tok0 + (col0 + my) / p.hg) * p.out_token + (w.it.head0 + first_h) * p.out_head + (r & ~1);
+                float inv[32];
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) *reinterpret_cast<float4 *>(inv + c) = *reinterpret_cast<const float4 *>(red + c0 + c);
 #pragma unroll 1
-                for (int c0 = 0; c0 < C; c0 += 32) {
-                    if (c0 >= mine) break;
+                for (int b = 0; b < S::DB; b++) {
                     float v[32];
                     if (w.tiles > 0) {
                         tmem_ld32(lane_base + S::T_O + b * N + col0 + c0, v);
                         ld_wait();
                     }
                     if (!ok) continue;
-                    const int d = 128 * b + r;
                     if (!whole) {
-                        float *dst = p.plan.part_o + (part * N + col0 + c0) * D + d;
+                        float *dst = p.plan.part_o + (part * N + col0 + c0) * D + 128 * b + r;
                         if (D > 64 || r < 64) {
+                            if (c0 + 32 <= mine) {
 #pragma unroll
-                            for (int c = 0; c < 32; c++)
-                                if (c0 + c < mine) dst[c * D] = v[c];
+                                for (int c = 0; c < 32; c++) dst[c * D] = v[c];
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 32; c++)
+                                    if (c0 + c < mine) dst[c * D] = v[c];
+                            }
                         }
-                    } else {
-                        // two lanes trade so that each stores two neighbouring values: the even one of column c, the
-                        // odd one of column c + 1
-                        int tok = (col0 + c0) / p.hg, h = (col0 + c0) % p.hg;
+                        continue;
+                    }
+                    uint32_t two[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float a = red[c0 + c] == 0.f ? 0.f : v[c] * red[c0 + c], e = red[c0 + c + 1] == 0.f ? 0.f : v[c + 1] * red[c0 + c + 1];
-                            const float x = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : e, 1);
-                            const uint32_t two = lane & 1 ? pack(x, e) : pack(a, x);
-                            int tok1 = tok, h1 = h + 1;
-                            if (h1 == p.hg) { h1 = 0; tok1++; }
-                            const int mt = lane & 1 ? tok1 : tok, mh = w.it.head0 + (lane & 1 ? h1 : h);
-                            if (c0 + c + (lane & 1) < mine && mh < p.n_heads && (D > 64 || r < 64))
-                                *reinterpret_cast<uint32_t *>(p.out + (w.it.tok0 + mt) * p.out_token + mh * p.out_head + (d & ~1)) = two;
-                            tok = tok1;
-                            h = h1 + 1;
-                            if (h == p.hg) { h = 0; tok++; }
+                    for (int c = 0; c < 32; c += 2) {
+                        const float a = inv[c] == 0.f ? 0.f : v[c] * inv[c], e = inv[c + 1] == 0.f ? 0.f : v[c + 1] * inv[c + 1];
+                        const float x = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : e, 1);
+                        two[c / 2] = lane & 1 ? pack(x, e) : pack(a, x);
+                    }
+                    if (D > 64 || r < 64) {
+                        __nv_bfloat16 *dst = first + 128 * b;
+                        int h = first_h;
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            if (my + 2 * i < mine && w.it.head0 + h < p.n_heads) *reinterpret_cast<uint32_t *>(dst) = two[i];
+                            h += 2;
+                            dst += 2 * p.out_head;
+                            while (h >= p.hg) {
+                                h -= p.hg;
+                                dst += p.out_token - p.hg * p.out_head;
+                            }
                         }
                     }
                 }

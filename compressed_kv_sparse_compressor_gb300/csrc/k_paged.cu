@@ -61,14 +61,15 @@ struct Shape {
     static constexpr int N = D == 512 ? 64 : 128;                   // columns
     static constexpr int C = N / 2;                                 // columns of a softmax warpgroup
     static constexpr int DC = D / 64, DB = (D + 127) / 128, SLOTS_TILE = DB;
-    static constexpr int RING = D == 512 || D == 256 ? 4 : 5;       // slots
+    static constexpr int RING = 4;                                  // slots
+    static constexpr int NP = D <= 128 ? 2 : 1;                     // buffers of P
     static constexpr bool AHEAD = RING >= 2 * SLOTS_TILE;           // the next tile's S in front of this one's O
-    static constexpr int OFF_Q = 0, Q_CHUNK = N * 128, OFF_P = DC * Q_CHUNK, OFF_X = OFF_P + ROWS * N * 2;
+    static constexpr int OFF_Q = 0, Q_CHUNK = N * 128, OFF_P = DC * Q_CHUNK, P_BYTES = ROWS * N * 2, OFF_X = OFF_P + NP * P_BYTES;
     static constexpr int OFF_RED = OFF_X + RING * SLOT;             // [2][4][C] floats
     static constexpr int OFF_REF = OFF_RED + 8 * C * 4;             // [N]
     static constexpr int OFF_MASK = OFF_REF + 4 * N;
     static constexpr int OFF_BAR = OFF_MASK + 4 * MASKS;
-    static constexpr int N_BAR = 2 * RING + 10;
+    static constexpr int N_BAR = 2 * RING + 12;
     static constexpr int SMEM = OFF_BAR + 8 * N_BAR + 16;
     static constexpr int T_S = 0, T_O = 2 * N;
     static_assert(T_O + DB * N <= 512, "tensor memory");
@@ -77,7 +78,8 @@ struct Shape {
     static_assert(RING / SLOTS_TILE < MASKS, "a tile's mask is read before its slot is loaded again");
 };
 // barriers behind the ring's
-enum { B_QFULL, B_QEMPTY, B_SFULL, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PVDONE, B_OFREE, B_DRAIN };
+// (P's two are one for each buffer: with one for both, a wait for a tile's phase could find the next one's complete too)
+enum { B_QFULL, B_QEMPTY, B_SFULL, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PVDONE = B_PFULL + 2, B_OFREE = B_PVDONE + 2, B_DRAIN };
 
 struct Pool {
     const int32_t *pages;
@@ -249,10 +251,15 @@ __device__ __forceinline__ bool group_any(int id, bool v) {
         : "memory");
     return r != 0;
 }
-// Reduction of C values per lane over a warp by a transposing butterfly: lane l ends with the results
-// of values l * C / 32 .. (C / 32 of them) in r.
-template <bool MAX, int C>
-__device__ __forceinline__ void reduce_columns(const float (&v)[C], float (&r)[C / 32]) {
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Sums of C values per lane over a warp by a transposing butterfly: lane l ends with those of values l * C / 32 ..
+// (C / 32 of them) in r.
+template <int C>
+__device__ __forceinline__ void sum_columns(const float (&v)[C], float (&r)[C / 32]) {
     const int lane = threadIdx.x % 32;
     float m[C];
 #pragma unroll
@@ -265,7 +272,7 @@ __device__ __forceinline__ void reduce_columns(const float (&v)[C], float (&r)[C
         for (int k = 0; k < half; k++) {
             const float send = up ? m[k] : m[k + half], keep = up ? m[k + half] : m[k];
             const float x = __shfl_xor_sync(0xffffffffu, send, o);
-            m[k] = MAX ? fmaxf(keep, x) : keep + x;
+            m[k] = keep + x;
         }
     }
 #pragma unroll
@@ -486,8 +493,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             mbar_init(bar(B_SFULL + i), 1);
             mbar_init(bar(B_SFREE + i), 8);
         }
-        mbar_init(bar(B_PFULL), 8);
-        mbar_init(bar(B_PVDONE), 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(bar(B_PFULL + i), 8);
+            mbar_init(bar(B_PVDONE + i), 1);
+        }
         mbar_init(bar(B_OFREE), 8);
         mbar_init(bar(B_DRAIN), 1);
         *abort = 0;
@@ -602,18 +611,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             g++;
         };
         auto do_o = [&](uint32_t go, bool first) {
-            if (ok) ok = warp_wait(bar(B_PFULL), go & 1, abort);
+            if (ok) ok = warp_wait(bar(B_PFULL + go % S::NP), go / S::NP & 1, abort);
             if (first && ok && items > 0) ok = warp_wait(bar(B_OFREE), (items - 1) & 1, abort);
             if (ok) fence_after();
             for (int b = 0; b < S::DB; b++, unit_o++) {
                 if (!ok) continue;
-                const uint64_t x = xm + unit_o % RING * (SLOT >> 4);
+                const uint64_t x = xm + unit_o % RING * (SLOT >> 4), pr = pm + go % S::NP * (S::P_BYTES >> 4);
                 const uint32_t d = tmem + S::T_O + b * N, acc = first ? 0u : 1u;
                 if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < 8; k++) mma(d, x + k * 128, pm + k * 128, ID_O, k > 0 ? 1u : acc);
+                    for (int k = 0; k < 8; k++) mma(d, x + k * 128, pr + k * 128, ID_O, k > 0 ? 1u : acc);
                     commit(empty(unit_o));
-                    if (b == S::DB - 1) commit(bar(B_PVDONE));
+                    if (b == S::DB - 1) commit(bar(B_PVDONE + go % S::NP));
                 }
                 __syncwarp();
             }
@@ -729,10 +738,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     if (!is_full) mask();
                     float m[C / 32];
 #pragma unroll
-                    for (int c = 0; c < C; c++) s[c] *= p.scale_log2;
-                    reduce_columns<true, C>(s, m);
+                    for (int c = 0; c < C; c++) {
+                        s[c] *= p.scale_log2;
+                        const float x = warp_max(s[c]);
+                        m[c / 32] = lane == c % 32 ? x : m[c / 32];
+                    }
 #pragma unroll
-                    for (int k = 0; k < C / 32; k++) red[q4 * C + lane * (C / 32) + k] = m[k];
+                    for (int k = 0; k < C / 32; k++) red[q4 * C + 32 * k + lane] = m[k];
                     group_sync(id);
                     if (tid < C) {
                         const float old = gref[tid], now = fmaxf(old, fmaxf(fmaxf(red[tid], red[C + tid]), fmaxf(red[2 * C + tid], red[3 * C + tid])));
@@ -741,9 +753,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     }
                     group_sync(id);
 #pragma unroll
-                    for (int c = 0; c < C; c++) {
-                        s[c] -= gref[c];
-                        l[c] *= red[c];
+                    for (int c = 0; c < C; c += 4) {
+                        const float4 now = *reinterpret_cast<const float4 *>(gref + c), f = *reinterpret_cast<const float4 *>(red + c);
+                        s[c] -= now.x; s[c + 1] -= now.y; s[c + 2] -= now.z; s[c + 3] -= now.w;
+                        l[c] *= f.x; l[c + 1] *= f.y; l[c + 2] *= f.z; l[c + 3] *= f.w;
                     }
                 }
                 fence_before();
@@ -751,8 +764,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 if (lane == 0) mbar_arrive(bar(B_SFREE + sb));
                 // the second product of the tile before is done with P, and with O: where it was issued in front of this
                 // tile's first, the wait for that was the wait for both
-                if (S::AHEAD && ok && g > 0) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
+                if (S::AHEAD && ok && g >= S::NP) ok = warp_wait(bar(B_PVDONE + g % S::NP), (g / S::NP - 1) & 1, abort);
                 if (moves && j > w.tb) {
+                    if (S::AHEAD && S::NP > 1 && ok) ok = warp_wait(bar(B_PVDONE + (g - 1) % S::NP), (g - 1) / S::NP & 1, abort);
                     fence_after();
 #pragma unroll 1
                     for (int b = 0; b < S::DB; b++)
@@ -776,7 +790,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     }
 #pragma unroll
                     for (int u = 0; u < C / 8; u++)
-                        *reinterpret_cast<uint4 *>(prow + (((u0 + u) ^ (r & 7)) * 16)) =
+                        *reinterpret_cast<uint4 *>(prow + g % S::NP * S::P_BYTES + (((u0 + u) ^ (r & 7)) * 16)) =
                             make_uint4(pack(s[8 * u], s[8 * u + 1]), pack(s[8 * u + 2], s[8 * u + 3]), pack(s[8 * u + 4], s[8 * u + 5]),
                                        pack(s[8 * u + 6], s[8 * u + 7]));
                 }
@@ -801,11 +815,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 fence_before();
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_PFULL));
+                if (lane == 0) mbar_arrive(bar(B_PFULL + g % S::NP));
             }
             // denominators: the lanes' and warps' sums
             float sum[C / 32];
-            reduce_columns<false, C>(l, sum);
+            sum_columns<C>(l, sum);
             group_sync(id);                                     // the factors in red have been read
 #pragma unroll
             for (int k = 0; k < C / 32; k++) red[q4 * C + lane * (C / 32) + k] = sum[k];
@@ -822,7 +836,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             }
             group_sync(id);
             if (w.tiles > 0) {
-                if (ok) ok = warp_wait(bar(B_PVDONE), (g - 1) & 1, abort);
+                if (ok) ok = warp_wait(bar(B_PVDONE + (g - 1) % S::NP), (g - 1) / S::NP & 1, abort);
                 fence_after();
             }
             // Whole items: two lanes trade so that each stores two neighbouring values, the even one of column c, the odd one
@@ -832,6 +846,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             for (int c0 = 0; c0 < C && c0 < mine; c0 += 32) {
                 const int my = c0 + (lane & 1);
                 const int first_h = (col0 + my) % p.hg;
+                const int h0 = (col0 + c0) % p.hg;              // 32 heads of one token?
+                const bool one_token = c0 + 32 <= mine && h0 + 32 <= p.hg && w.it.head0 + h0 + 32 <= p.n_heads;
                 __nv_bfloat16 *first = p.out + (w.it.tok0 + (col0 + my) / p.hg) * p.out_token + (w.it.head0 + first_h) * p.out_head + (r & ~1);
                 float inv[32];
 #pragma unroll
@@ -842,6 +858,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     if (w.tiles > 0) {
                         tmem_ld32(lane_base + S::T_O + b * N + col0 + c0, v);
                         ld_wait();
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c++) v[c] = 0.f;
                     }
                     if (!ok) continue;
                     if (!whole) {
@@ -861,21 +880,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     uint32_t two[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float a = inv[c] == 0.f ? 0.f : v[c] * inv[c], e = inv[c + 1] == 0.f ? 0.f : v[c + 1] * inv[c + 1];
+                        const float a = v[c] * inv[c], e = v[c + 1] * inv[c + 1];
                         const float x = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : e, 1);
                         two[c / 2] = lane & 1 ? pack(x, e) : pack(a, x);
                     }
                     if (D > 64 || r < 64) {
                         __nv_bfloat16 *dst = first + 128 * b;
-                        int h = first_h;
+                        if (one_token) {
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            if (my + 2 * i < mine && w.it.head0 + h < p.n_heads) *reinterpret_cast<uint32_t *>(dst) = two[i];
-                            h += 2;
-                            dst += 2 * p.out_head;
-                            while (h >= p.hg) {
-                                h -= p.hg;
-                                dst += p.out_token - p.hg * p.out_head;
+                            for (int i = 0; i < 16; i++, dst += 2 * p.out_head) *reinterpret_cast<uint32_t *>(dst) = two[i];
+                        } else {
+                            int h = first_h;
+#pragma unroll
+                            for (int i = 0; i < 16; i++) {
+                                if (my + 2 * i < mine && w.it.head0 + h < p.n_heads) *reinterpret_cast<uint32_t *>(dst) = two[i];
+                                h += 2;
+                                dst += 2 * p.out_head;
+                                while (h >= p.hg) {
+                                    h -= p.hg;
+                                    dst += p.out_token - p.hg * p.out_head;
+                                }
                             }
                         }
                     }

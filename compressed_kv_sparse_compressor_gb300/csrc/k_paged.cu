@@ -52,7 +52,9 @@ constexpr int MASKS = 8;                                            // tiles who
 constexpr float TAU = 8.0f;
 constexpr float NONE = -3.0e38f;                                    // reference of a column that saw nothing yet
 constexpr int PLAN_THREADS = 1024;
+constexpr int SMALL = THREADS;                                      // items and sequences that each CTA cuts for itself
 constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
+constexpr int FEW_ITEMS = 64;                                       // joined by a block for each column
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
 constexpr int MIN_COST = 2;                                         // a CTA's share, in tiles, where there is little work
 
@@ -72,6 +74,7 @@ struct Shape {
     static constexpr int N_BAR = 2 * RING + 12;
     static constexpr int SMEM = OFF_BAR + 8 * N_BAR + 16;
     static constexpr int T_S = 0, T_O = 2 * N;
+    static constexpr int OVER = D == 512 ? 1 : D == 256 ? 2 : 3;    // an item's start and end, in tiles
     static_assert(T_O + DB * N <= 512, "tensor memory");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(OFF_X % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0 && OFF_RED % 16 == 0 && OFF_REF % 16 == 0, "alignment");
@@ -91,12 +94,15 @@ struct Item {
     int t0, raw_tile0, raw_tiles, comp_tiles;
 };
 struct Start { int item, y; };
-// Workspace: counts, each CTA's first item and place in it, the boundaries that start a divided item, the items,
-// the parts.
+// The parts of a divided item: the second of CTA `cta`, then the first of the n - 1 CTAs behind it.
+struct Parts { int item, cta, n; };
+struct Totals { long long cost; int items, ctas; };
+// Workspace: totals, each CTA's first item and place in it, the parts of an item (by item where each CTA cuts for
+// itself, else by the CTA that starts it), the items, the parts.
 struct Plan {
-    int *counts;               // [0] items, [1] divided items, [2] CTAs with work
+    Totals *totals;
     Start *start;              // [grid + 1]
-    int *split;                // [grid]
+    Parts *parts;              // [max(grid, SMALL)]
     Item *items;
     float *part_o;             // [2 grid][N][D]
     float *part_ml;            // [2 grid][2][N]
@@ -109,6 +115,8 @@ struct Params {
     int raw_rows, comp_rows;   // rows of the pools: the first row past the end, which TMA fills with zeros
     int n_seq, n_tok, n_heads, window, ratio;
     int hg, tt, groups;        // heads and tokens of an item, head groups
+    int over;                  // an item's start and end, in tiles
+    int small;                 // each CTA cuts for itself
     float scale_log2;
     Plan plan;
 };
@@ -279,16 +287,62 @@ __device__ __forceinline__ void sum_columns(const float (&v)[C], float (&r)[C / 
     for (int k = 0; k < C / 32; k++) r[k] = m[k];
 }
 
-// Tiles of an item in front of place y (0: its start, 1 + t: tile t) of the cuts.
-__device__ __forceinline__ int tiles_before(int y, int tiles) {
+// ---- items and cuts ----------------------------------------------------------------------------
+// The items lie one behind the other, each `over` places and then a place for each tile long; `ctas` cuts divide
+// the whole evenly.
+
+// Tiles of an item in front of its place y.
+__device__ __forceinline__ int tiles_before(int y, int tiles, int over) {
     if (tiles <= SHORT) return y > 0 ? tiles : 0;
-    return y > 0 ? y - 1 : 0;
+    return max(y - over, 0);
+}
+__device__ __forceinline__ int tiles_of(const Item &it) { return it.raw_tiles + it.comp_tiles; }
+
+// Item k of a sequence of n new tokens from token b on, `length` long with them.
+__device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n, int length, int k) {
+    Item it;
+    const int j = k / p.groups * p.tt;
+    it.seq = seq;
+    it.tok0 = b + j;
+    it.n_tok = min(p.tt, n - j);
+    it.head0 = k % p.groups * p.hg;
+    // positions t0 .. end - 1; a token before 0 sees nothing wherever it is
+    it.t0 = max(length, -(1 << 30)) - n + j;
+    const int end = it.t0 + it.n_tok;
+    it.raw_tile0 = it.raw_tiles = it.comp_tiles = 0;
+    if (end > 0) {
+        it.raw_tile0 = (p.window && it.t0 >= p.window ? it.t0 + 1 - p.window : 0) / ROWS;
+        it.raw_tiles = (int)(((unsigned)end + ROWS - 1) / ROWS) - it.raw_tile0;
+        if (p.ratio) it.comp_tiles = (int)(((unsigned)(end / p.ratio) + ROWS - 1) / ROWS);
+    }
+    return it;
+}
+// Items of sequence s (start b, end e); reports starts that fall or leave the tokens.
+__device__ __forceinline__ int items_of(const Params &p, int b, int e, bool report) {
+    if (b < 0 || e < b || e > p.n_tok) {
+        if (report) atomicOr(&g_paged_err, 2u);
+        return 0;
+    }
+    return (e - b + p.tt - 1) / p.tt * p.groups;
+}
+// The last of n ascending values v that is <= x.
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T *v, int n, T x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (v[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+__device__ __forceinline__ int ctas_of(long long cost, int grid) {
+    return (int)max(1ll, min((long long)grid, cost / MIN_COST));
 }
 
-// ---- items and cuts ----------------------------------------------------------------------------
-
-template <typename T>
-__device__ T block_scan(T v, T *sums, T &total) {              // inclusive, over PLAN_THREADS threads
+// Sum over the block's threads before this one and its own; sums: a value for each warp.
+template <int BLOCK, typename T>
+__device__ __forceinline__ T block_scan(T v, T *sums, T &total) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -298,138 +352,138 @@ __device__ T block_scan(T v, T *sums, T &total) {              // inclusive, ove
     __syncthreads();
     if (lane == 31) sums[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        T s = sums[lane];
+    T before = 0, all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const T u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
-        }
-        sums[lane] = s;
+    for (int w = 0; w < BLOCK / 32; w++) {
+        const T u = sums[w];
+        if (w < warp) before += u;
+        all += u;
     }
-    __syncthreads();
-    total = sums[31];
-    return warp > 0 ? v + sums[warp - 1] : v;
+    total = all;
+    return before + v;
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const Params p, int grid) {
-    extern __shared__ int first_item[];                        // [n_seq + 1]
-    __shared__ long long prefix[PLAN_THREADS + 1];
-    __shared__ long long sums_l[32];
-    __shared__ int sums_i[32];
-    __shared__ int n_split;
+// Many items: one block makes them and the cuts.
+__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ Params p, int grid) {
+    extern __shared__ int seq_info[];                          // [n_seq] first item, start, length
+    __shared__ long long before[PLAN_THREADS];                 // cost in front of each thread's items
+    __shared__ long long sums_l[PLAN_THREADS / 32];
+    __shared__ int sums_i[PLAN_THREADS / 32];
+    int *first = seq_info, *begin = seq_info + p.n_seq, *length = begin + p.n_seq + 1;
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch_dependents();
-
-    // items of the sequences before each
     int carry = 0;
-    if (tid == 0) n_split = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += PLAN_THREADS) {
         const int s = s0 + tid;
         int k = 0;
         if (s < p.n_seq) {
             const int b = p.start[s], e = p.start[s + 1];
-            if (b < 0 || e < b || e > p.n_tok) atomicOr(&g_paged_err, 2u);
-            else k = (e - b + p.tt - 1) / p.tt * p.groups;
+            length[s] = p.length[s];
+            begin[s] = b;
+            if (s == p.n_seq - 1) begin[s + 1] = e;
+            k = items_of(p, b, e, true);
         }
         int total;
-        const int incl = block_scan<int>(k, sums_i, total);
-        if (s < p.n_seq) first_item[s] = carry + incl - k;
+        const int incl = block_scan<PLAN_THREADS, int>(k, sums_i, total);
+        if (s < p.n_seq) first[s] = carry + incl - k;
         carry += total;
     }
+    __syncthreads();
     // starts that overlap could make more items than there is room for
-    const int most = p.n_tok * p.groups;
+    const int most = p.n_tok * p.groups, n_items = min(carry, most);
     if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
-    const int n_items = min(carry, most);
-    if (tid == 0) first_item[p.n_seq] = carry;
-    __syncthreads();
-
-    auto make = [&](int i) -> int {                            // writes item i; its cost
-        int lo = 0, hi = p.n_seq;                              // the last sequence with first_item <= i (it has items)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (first_item[mid] <= i) lo = mid;
-            else hi = mid;
+    // each thread's items, one behind the other
+    const int each = (n_items + PLAN_THREADS - 1) / PLAN_THREADS;
+    auto walk = [&](int thread, auto visit) {                  // visit(item number, item) until it returns false
+        const int from = min(thread * each, n_items), to = min(from + each, n_items);
+        if (from >= to) return;
+        int s = last_at_most(first, p.n_seq, from);
+        for (int i = from; i < to; i++) {
+            while (s + 1 < p.n_seq && first[s + 1] <= i) s++;
+            if (!visit(i, make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], i - first[s]))) return;
         }
-        const int b = p.start[lo], n = p.start[lo + 1] - b, k = i - first_item[lo];
-        Item it;
-        it.seq = lo;
-        const int j = k / p.groups * p.tt;
-        it.tok0 = b + j;
-        it.n_tok = min(p.tt, n - j);
-        it.head0 = k % p.groups * p.hg;
-        const long long t0 = (long long)p.length[lo] - n + j, end = t0 + it.n_tok;   // positions t0 .. end - 1
-        it.t0 = (int)max(t0, -(1ll << 30));                    // a token before 0 sees nothing wherever it is
-        it.raw_tile0 = it.raw_tiles = it.comp_tiles = 0;
-        if (end > 0) {
-            const long long from = p.window ? max(0ll, t0 + 1 - p.window) : 0;
-            it.raw_tile0 = (int)(from / ROWS);
-            it.raw_tiles = (int)((end + ROWS - 1) / ROWS) - it.raw_tile0;
-            if (p.ratio) it.comp_tiles = (int)((end / p.ratio + ROWS - 1) / ROWS);
-        }
+    };
+    long long cost = 0;
+    walk(tid, [&](int i, const Item &it) {
         p.plan.items[i] = it;
-        return it.raw_tiles + it.comp_tiles + 1;
-    };
-    // the whole cost, then the cuts by each stretch of items that they fall into
-    long long all = 0;
+        cost += p.over + tiles_of(it);
+        return true;
+    });
+    long long all;
+    before[tid] = block_scan<PLAN_THREADS, long long>(cost, sums_l, all) - cost;
+    __syncthreads();
+    const int ctas = n_items ? ctas_of(all, grid) : 0;
+    if (tid < ctas) {                                          // grid <= MAX_GRID <= PLAN_THREADS
+        const long long at = all * tid / ctas;
+        const int thread = last_at_most(before, (n_items + each - 1) / each, at);
+        long long here = before[thread];
+        walk(thread, [&](int i, const Item &it) {
+            const int c = p.over + tiles_of(it);
+            if (at < here + c) {
+                p.plan.start[tid] = {i, (int)(at - here)};
+                return false;
+            }
+            here += c;
+            return true;
+        });
+    } else if (tid <= grid) {
+        p.plan.start[tid] = {n_items, 0};
+    }
+    if (tid == 0) *p.plan.totals = {all, n_items, ctas};
+}
+
+// Few items: every CTA makes them all, one to a thread, and finds its own cuts.  Writes the items that it has
+// something of.  scratch: SMALL_SCRATCH bytes of shared memory, 16-byte aligned.
+constexpr int SMALL_SCRATCH = 3 * 4 * (SMALL + 4) + 16 * (SMALL / 32) + 64;
+struct Cuts { Start from, to; Totals t; };
+__device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
+    Cuts *out = reinterpret_cast<Cuts *>(scratch);
+    static_assert(sizeof(Cuts) <= 32, "scratch");
+    long long *sums_l = reinterpret_cast<long long *>(scratch + 32);
+    int *sums_i = reinterpret_cast<int *>(sums_l + SMALL / 32);
+    int *first = sums_i + SMALL / 32, *begin = first + SMALL, *length = begin + SMALL + 1;
+    const int tid = threadIdx.x, grid = gridDim.x, cta = blockIdx.x;
+    int k = 0;
+    if (tid < p.n_seq) {
+        const int b = p.start[tid], e = p.start[tid + 1];
+        length[tid] = p.length[tid];
+        begin[tid] = b;
+        if (tid == p.n_seq - 1) begin[tid + 1] = e;
+        k = items_of(p, b, e, cta == 0);
+    }
+    int carry;
+    const int incl = block_scan<SMALL, int>(k, sums_i, carry);
+    first[tid] = tid < p.n_seq ? incl - k : 0x7fffffff;
+    __syncthreads();
+    const int most = p.n_tok * p.groups, n_items = min(carry, most);
+    if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
+    Item it{};
     int cost = 0;
-    for (int i0 = 0; i0 < n_items; i0 += PLAN_THREADS) {
-        cost = i0 + tid < n_items ? make(i0 + tid) : 0;
-        long long total;
-        block_scan<long long>(cost, sums_l, total);
-        all += total;
+    if (tid < n_items) {
+        const int s = last_at_most(first, p.n_seq, tid);
+        it = make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], tid - first[s]);
+        cost = p.over + tiles_of(it);
     }
-    const int ctas = (int)max(1ll, min((long long)grid, all / MIN_COST));
-    long long before = 0;
-    for (int i0 = 0; i0 < n_items; i0 += PLAN_THREADS) {
-        if (n_items > PLAN_THREADS) {
-            cost = 0;
-            if (i0 + tid < n_items) {
-                const Item &it = p.plan.items[i0 + tid];
-                cost = it.raw_tiles + it.comp_tiles + 1;
-            }
-        }
-        long long total;
-        const long long incl = block_scan<long long>(cost, sums_l, total);
-        prefix[tid + 1] = before + incl;
-        if (tid == 0) prefix[0] = before;
-        __syncthreads();
-        for (int c = tid; c < ctas; c += PLAN_THREADS) {
-            const long long at = all * c / ctas;
-            if (at >= before && at < before + total) {
-                int lo = 0, hi = min(PLAN_THREADS, n_items - i0);
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    if (prefix[mid] <= at) lo = mid;
-                    else hi = mid;
-                }
-                p.plan.start[c] = {i0 + lo, (int)(at - prefix[lo])};
-            }
-        }
-        before += total;
-        __syncthreads();
-    }
-    for (int c = (n_items ? ctas : 0) + tid; c <= grid; c += PLAN_THREADS) p.plan.start[c] = {n_items, 0};
-    __threadfence_block();
+    long long all;
+    const long long end = block_scan<SMALL, long long>(cost, sums_l, all), here = end - cost;
+    const int ctas = n_items ? ctas_of(all, grid) : 0;
+    if (tid == 0) *out = {{n_items, 0}, {n_items, 0}, {all, n_items, ctas}};
     __syncthreads();
-    // the cuts inside an item whose predecessor is not: one for each divided item
-    auto inside = [&](int c) {
-        const Start s = p.plan.start[c];
-        if (s.item >= n_items) return false;
-        const Item &it = p.plan.items[s.item];
-        const int tiles = it.raw_tiles + it.comp_tiles, f = tiles_before(s.y, tiles);
-        return f > 0 && f < tiles;
-    };
-    for (int c = 1 + tid; c < ctas; c += PLAN_THREADS)
-        if (n_items && inside(c) && !(p.plan.start[c - 1].item == p.plan.start[c].item && inside(c - 1)))
-            p.plan.split[atomicAdd(&n_split, 1)] = c;
-    __syncthreads();
-    if (tid == 0) {
-        p.plan.counts[0] = n_items;
-        p.plan.counts[1] = n_split;
-        p.plan.counts[2] = n_items ? ctas : 0;
+    if (tid < n_items && cta < ctas) {
+        const long long a = all * cta / ctas, b = all * (cta + 1) / ctas;
+        if (here <= a && a < end) out->from = {tid, (int)(a - here)};
+        if (cta + 1 < ctas && here <= b && b < end) out->to = {tid, (int)(b - here)};
+        if (a < end && b > here) p.plan.items[tid] = it;
+        // the CTA that has the item's first tile says who has the others
+        const int tiles = tiles_of(it), tb = a > here ? tiles_before((int)(a - here), tiles, p.over) : 0,
+                  te = b < end ? tiles_before((int)max(b - here, 0ll), tiles, p.over) : tiles;
+        if (a < end && b > here && tb == 0 && (te > 0 || tiles == 0))
+            p.plan.parts[tid] = {tid, cta, te < tiles ? (int)((end * ctas - 1) / all) - cta + 1 : 1};
     }
+    if (cta == 0 && tid == 0) *p.plan.totals = out->t;
+    __syncthreads();
+    return *out;
 }
 
 // ---- attention ---------------------------------------------------------------------------------
@@ -441,19 +495,15 @@ struct Work {
     int i;
     Item it;
     int tiles, tb, te;
-    __device__ Work(const Params &p_) : p(p_) {
-        from = p.plan.start[blockIdx.x];
-        to = p.plan.start[blockIdx.x + 1];
-        i = from.item - 1;
-    }
+    __device__ Work(const Params &p_, const Start &from_, const Start &to_) : p(p_), from(from_), to(to_), i(from_.item - 1) {}
     __device__ __forceinline__ bool next() {                    // the next item that this CTA has something of
         for (;;) {
             i++;
             if (i > to.item || (i == to.item && to.y == 0)) return false;
             it = p.plan.items[i];
-            tiles = it.raw_tiles + it.comp_tiles;
-            tb = i == from.item ? tiles_before(from.y, tiles) : 0;
-            te = i == to.item ? tiles_before(to.y, tiles) : tiles;
+            tiles = tiles_of(it);
+            tb = i == from.item ? tiles_before(from.y, tiles, p.over) : 0;
+            te = i == to.item ? tiles_before(to.y, tiles, p.over) : tiles;
             if (tb < te || (tiles == 0 && !(i == from.item && from.y > 0))) return true;
         }
     }
@@ -517,10 +567,34 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_launch_dependents();
+    static_assert(SMALL_SCRATCH <= S::P_BYTES, "the cuts' scratch lies where P will");
+    Start from, to;
+    if (p.small) {
+        const Cuts c = plan_small(p, sm + S::OFF_P);
+        from = c.from;
+        to = c.to;
+        __syncthreads();
+    } else {
+        from = p.plan.start[blockIdx.x];
+        to = p.plan.start[blockIdx.x + 1];
+        if (threadIdx.x == 0) {
+            Parts parts{0, (int)blockIdx.x, 0};
+            const Totals t = *p.plan.totals;
+            if (to.y > 0) {
+                const int tiles = tiles_of(p.plan.items[to.item]), te = tiles_before(to.y, tiles, p.over);
+                if (te > 0 && te < tiles && !(from.item == to.item && tiles_before(from.y, tiles, p.over) > 0)) {
+                    const long long end = t.cost * (blockIdx.x + 1) / t.ctas - to.y + p.over + tiles;
+                    parts.item = to.item;
+                    parts.n = (int)((end * t.ctas - 1) / t.cost) - (int)blockIdx.x + 1;
+                }
+            }
+            p.plan.parts[blockIdx.x] = parts;
+        }
+    }
 
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
-    Work w(p);
+    Work w(p, from, to);
     bool ok = true;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -647,7 +721,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
-        Work w(p);
+        Work w(p, from, to);
         bool ok = true;
         // ------------------------------------------------------------ softmax, output
         const int grp = (warp - 4) / 4, q4 = warp % 4, id = 1 + grp, col0 = grp * C;
@@ -921,74 +995,71 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
 }
 
-// Joins the parts of the divided items: a block per item and column.
-template <int D>
+// Joins the parts of the divided items.  Few items (FEW), perhaps many parts: a block for each item and column, whose
+// threads share the parts; else, mostly two or three parts: a thread takes all parts of its values.
+template <int D, bool FEW>
 __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
-    constexpr int N = Shape<D>::N, PER = 4, LANES = D / PER, GROUPS = JOIN_THREADS / LANES;   // values of a thread, threads of a part
-    constexpr int AT_ONCE = 4;
-    __shared__ float weight[MAX_GRID], denom[MAX_GRID];
-    __shared__ int slot[MAX_GRID];
-    __shared__ __align__(16) float sums[GROUPS][D];
+    constexpr int N = Shape<D>::N, LANES = D / 4;              // threads of a column, four values each
+    constexpr int COLS = FEW ? 1 : JOIN_THREADS / LANES, GROUPS = JOIN_THREADS / LANES / COLS;
+    __shared__ float weight[FEW ? MAX_GRID : 1], denom[FEW ? MAX_GRID : 1];
+    __shared__ __align__(16) float sums[FEW ? GROUPS : 1][D];
     pdl_wait();
     pdl_launch_dependents();
-    const int col = blockIdx.x % N;
-    if ((int)(blockIdx.x / N) >= p.plan.counts[1]) return;
-    const int c0 = p.plan.split[blockIdx.x / N], ctas = p.plan.counts[2];
-    const int item = p.plan.start[c0].item;
-    const Item it = p.plan.items[item];
-    const int tiles = it.raw_tiles + it.comp_tiles;
+    const int entry = blockIdx.x / (N / COLS), lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    if (p.small && entry >= p.plan.totals->items) return;
+    const Parts parts = p.plan.parts[entry];
+    const int n = parts.n;
+    if (n < 2) return;
+    const Item it = p.plan.items[parts.item];
+    const int col = blockIdx.x % (N / COLS) * COLS + (FEW ? 0 : grp);
     if (col >= it.n_tok * p.hg || it.head0 + col % p.hg >= p.n_heads) return;
-    // parts: the CTA in front of the first cut, then every CTA that starts inside the item
-    int n = 1;
-    for (int c = c0; c < ctas; c += JOIN_THREADS) {
-        const int cc = c + threadIdx.x;
-        bool in = false;
-        if (cc < ctas && p.plan.start[cc].item == item) {
-            const int f = tiles_before(p.plan.start[cc].y, tiles);
-            in = f > 0 && f < tiles;
-        }
-        const int k = __syncthreads_count(in);
-        n += k;
-        if (k < JOIN_THREADS) break;
-    }
-    float m = NONE;
-    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
-        slot[i] = i == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + i - 1);
-        weight[i] = p.plan.part_ml[(int64_t)slot[i] * 2 * N + col];
-        denom[i] = p.plan.part_ml[(int64_t)slot[i] * 2 * N + N + col];
-    }
-    __syncthreads();
-    for (int i = 0; i < n; i++) m = fmaxf(m, weight[i]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
-        weight[i] = ex2(weight[i] - m);
-        denom[i] *= weight[i];
-    }
-    __syncthreads();
-    float den = 0.f;
-    for (int i = 0; i < n; i++) den += denom[i];
-    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+    // part 0 lies alone, the others every second place behind it
+    const int64_t slot0 = 2 * parts.cta + 1, slot1 = 2 * parts.cta + 2;
+    const float *ml = p.plan.part_ml + col, *o = p.plan.part_o + (int64_t)col * D + 4 * lane;
+    auto m_of = [&](int i) { return ml[(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * 2 * N]; };
+    auto l_of = [&](int i) { return ml[(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * 2 * N + N]; };
+    float m = NONE, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *src = p.plan.part_o + (int64_t)col * D + PER * lane;
-#pragma unroll AT_ONCE
-    for (int i = grp; i < n; i += GROUPS) {
-        const float4 v = *reinterpret_cast<const float4 *>(src + slot[i] * (int64_t)(N * D));
-        const float f = weight[i];
+    auto add = [&](const float *src, float f) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
-    }
-    *reinterpret_cast<float4 *>(&sums[grp][PER * lane]) = acc;
-    __syncthreads();
-    if (grp > 0) return;
-    for (int k = 1; k < GROUPS; k++) {
-        const float4 v = *reinterpret_cast<const float4 *>(&sums[k][PER * lane]);
-        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    };
+    if (FEW) {
+        for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
+            weight[i] = m_of(i);
+            denom[i] = l_of(i);
+        }
+        __syncthreads();
+        for (int i = 0; i < n; i++) m = fmaxf(m, weight[i]);
+        for (int i = 0; i < n; i++) den = fmaf(ex2(weight[i] - m), denom[i], den);
+        if (grp == 0) add(o + slot0 * N * D, ex2(weight[0] - m));
+        const float *src = o + (slot1 + 2 * grp) * N * D;
+#pragma unroll 4
+        for (int i = 1 + grp; i < n; i += GROUPS, src += (int64_t)2 * GROUPS * N * D) add(src, ex2(weight[i] - m));
+        *reinterpret_cast<float4 *>(&sums[grp][4 * lane]) = acc;
+        __syncthreads();
+        if (grp > 0) return;
+        for (int k = 1; k < GROUPS; k++) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sums[k][4 * lane]);
+            acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+        }
+    } else {
+        for (int i = 0; i < n; i++) m = fmaxf(m, m_of(i));
+        const float *src = o + slot1 * N * D;
+        add(o + slot0 * N * D, ex2(m_of(0) - m));
+        den = ex2(m_of(0) - m) * l_of(0);
+        for (int i = 1; i < n; i++, src += (int64_t)2 * N * D) {
+            const float f = ex2(m_of(i) - m);
+            add(src, f);
+            den = fmaf(f, l_of(i), den);
+        }
     }
     const float inv = den == 0.f ? 0.f : 1.0f / den;
     if (den == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t at = (it.tok0 + col / p.hg) * p.out_token + (it.head0 + col % p.hg) * p.out_head + PER * lane;
+    const int64_t at = (it.tok0 + col / p.hg) * p.out_token + (it.head0 + col % p.hg) * p.out_head + 4 * lane;
     *reinterpret_cast<uint2 *>(p.out + at) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
 }
 
@@ -1046,9 +1117,9 @@ size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_hea
         return ws + here;
     };
     Plan o;
-    o.counts = reinterpret_cast<int *>(region(16));
+    o.totals = reinterpret_cast<Totals *>(region(sizeof(Totals)));
     o.start = reinterpret_cast<Start *>(region(sizeof(Start) * (grid + 1)));
-    o.split = reinterpret_cast<int *>(region(4 * (size_t)grid));
+    o.parts = reinterpret_cast<Parts *>(region(sizeof(Parts) * (grid > SMALL ? grid : SMALL)));
     o.items = reinterpret_cast<Item *>(region(sizeof(Item) * (size_t)n_tok * c.groups));
     o.part_ml = reinterpret_cast<float *>(region((size_t)2 * grid * 2 * c.n * 4));
     o.part_o = reinterpret_cast<float *>(region((size_t)2 * grid * c.n * d * 4));
@@ -1057,8 +1128,10 @@ size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_hea
 }
 
 template <int D>
-cudaError_t launch(const ds4c_paged_attn_args &a, const Params &p, int grid, cudaStream_t s) {
+cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream_t s) {
     using S = Shape<D>;
+    p.over = S::OVER;
+    p.small = a.n_seq <= SMALL && (uint64_t)a.n_tok * p.groups <= SMALL;
     CUtensorMap qm, rm, cm;
     {
         const cuuint64_t dims[3] = {D, a.n_heads, a.n_tok};
@@ -1079,13 +1152,17 @@ cudaError_t launch(const ds4c_paged_attn_args &a, const Params &p, int grid, cud
         regs.store(have = fa.numRegs, std::memory_order_relaxed);
     }
     if (128 * (REG_LOW + 2 * REG_SOFT) > THREADS * have) return cudaErrorNotSupported;
-    e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), (a.n_seq + 1) * sizeof(int), s, p, grid);
-    if (e != cudaSuccess) return e;
+    if (!p.small) {
+        const size_t info = (3 * (size_t)a.n_seq + 1) * sizeof(int);
+        e = ensure_dyn_smem(paged_plan_kernel, info);
+        if (e == cudaSuccess) e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), info, s, p, grid);
+        if (e != cudaSuccess) return e;
+    }
     e = launch_pdl(paged_attn_kernel<D>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
     if (e != cudaSuccess) return e;
-    // every divided item holds a cut
-    const uint64_t items = (uint64_t)a.n_tok * p.groups, joins = items < (uint64_t)grid - 1 ? items : (uint64_t)grid - 1;
-    return joins ? launch_pdl(paged_join_kernel<D>, dim3((unsigned)joins * S::N), dim3(JOIN_THREADS), 0, s, p) : cudaSuccess;
+    const int entries = p.small ? (int)a.n_tok * p.groups : grid;
+    if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, true>, dim3(entries * S::N), dim3(JOIN_THREADS), 0, s, p);
+    return launch_pdl(paged_join_kernel<D, false>, dim3(entries * (S::N / (JOIN_THREADS / (D / 4)))), dim3(JOIN_THREADS), 0, s, p);
 }
 
 }  // namespace

@@ -56,33 +56,43 @@ constexpr int SMALL = THREADS;                                      // items and
 constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
 constexpr int FEW_ITEMS = 64;                                       // joined by a block for each column
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
+constexpr uint32_t WIDE_TOKENS = 4;                                 // new tokens a sequence, from which items are wide
 constexpr int MIN_COST = 2;                                         // a CTA's share, in tiles, where there is little work
 
-template <int D>
+// WIDE: 128 columns at head_dim 512.  O then has 512 columns of its own, all that TMEM has, so the first 128 of d
+// are kept in the softmax warps' registers: S and that block of the second product take turns in the same 128
+// columns of TMEM.  The queries (128 KB) are streamed beside the rows, tile after tile.
+template <int D, bool WIDE_ = false>
 struct Shape {
-    static constexpr int N = D == 512 ? 64 : 128;                   // columns
+    static constexpr bool WIDE = WIDE_;
+    static_assert(!WIDE || D == 512, "wide items are for head_dim 512");
+    static constexpr int N = D == 512 && !WIDE ? 64 : 128;          // columns
     static constexpr int C = N / 2;                                 // columns of a softmax warpgroup
-    static constexpr int DC = D / 64, DB = (D + 127) / 128, SLOTS_TILE = DB;
+    static constexpr int DC = D / 64, DB = (D + 127) / 128;
     static constexpr int RING = 4;                                  // slots
     static constexpr int NP = D <= 128 ? 2 : 1;                     // buffers of P
-    static constexpr bool AHEAD = RING >= 2 * SLOTS_TILE;           // the next tile's S in front of this one's O
-    static constexpr int OFF_Q = 0, Q_CHUNK = N * 128, OFF_P = DC * Q_CHUNK, P_BYTES = ROWS * N * 2, OFF_X = OFF_P + NP * P_BYTES;
+    static constexpr int NS = WIDE ? 1 : 2;                         // buffers of S
+    static constexpr bool AHEAD = RING >= 2 * DB;                   // the next tile's S in front of this one's O
+    static constexpr int Q_CHUNK = N * 128, NQ = WIDE ? 2 : 1;      // buffers of queries, WIDE: of two chunks each
+    static constexpr int OFF_Q = 0, OFF_P = (WIDE ? 2 * NQ : DC) * Q_CHUNK, P_BYTES = ROWS * N * 2, OFF_X = OFF_P + NP * P_BYTES;
     static constexpr int OFF_RED = OFF_X + RING * SLOT;             // [2][4][C] floats
     static constexpr int OFF_REF = OFF_RED + 8 * C * 4;             // [N]
     static constexpr int OFF_MASK = OFF_REF + 4 * N;
     static constexpr int OFF_BAR = OFF_MASK + 4 * MASKS;
-    static constexpr int N_BAR = 2 * RING + 12;
+    static constexpr int N_BAR = 2 * RING + 15;
     static constexpr int SMEM = OFF_BAR + 8 * N_BAR + 16;
-    static constexpr int T_S = 0, T_O = 2 * N;
+    static constexpr int HELD = WIDE ? 1 : 0;                       // d-blocks of O in registers
+    static constexpr int T_S = 0, T_O = NS * N - HELD * N;          // d-block b at T_O + b * N
     static constexpr int OVER = D == 512 ? 1 : D == 256 ? 2 : 3;    // an item's start and end, in tiles
     static_assert(T_O + DB * N <= 512, "tensor memory");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(OFF_X % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0 && OFF_RED % 16 == 0 && OFF_REF % 16 == 0, "alignment");
-    static_assert(RING / SLOTS_TILE < MASKS, "a tile's mask is read before its slot is loaded again");
+    static_assert(RING / DB < MASKS, "a tile's mask is read before its slot is loaded again");
 };
 // barriers behind the ring's
-// (P's two are one for each buffer: with one for both, a wait for a tile's phase could find the next one's complete too)
-enum { B_QFULL, B_QEMPTY, B_SFULL, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PVDONE = B_PFULL + 2, B_OFREE = B_PVDONE + 2, B_DRAIN };
+// (one for each buffer: with one for both, a wait for a tile's phase could find the next one's complete too)
+enum { B_QFULL, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PVDONE = B_PFULL + 2,
+       B_OFREE = B_PVDONE + 2, B_HELD, B_DRAIN };
 
 struct Pool {
     const int32_t *pages;
@@ -516,11 +526,11 @@ struct Work {
     }
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap raw_map,
                   const __grid_constant__ CUtensorMap comp_map, const __grid_constant__ Params p) {
-    using S = Shape<D>;
+    using S = Shape<D, WIDE>;
     constexpr int N = S::N, C = S::C, RING = S::RING;
     extern __shared__ __align__(1024) uint8_t sm[];
     if ((smem_u32(sm) & 1023u) != 0) {                          // the layout has no room to realign
@@ -544,9 +554,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
         }
-        mbar_init(bar(B_QFULL), 1);
-        mbar_init(bar(B_QEMPTY), 1);
         for (int i = 0; i < 2; i++) {
+            mbar_init(bar(B_QFULL + i), 1);
+            mbar_init(bar(B_QEMPTY + i), 1);
             mbar_init(bar(B_SFULL + i), 1);
             mbar_init(bar(B_SFREE + i), 8);
         }
@@ -555,6 +565,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             mbar_init(bar(B_PVDONE + i), 1);
         }
         mbar_init(bar(B_OFREE), 8);
+        mbar_init(bar(B_HELD), 1);
         mbar_init(bar(B_DRAIN), 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -608,17 +619,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         uint32_t unit = 0, g = 0, n_q = 0;
         while (w.next()) {
             if (w.tiles == 0) continue;
-            // the item's queries, once the last S of the item before has read its own
-            if (ok && n_q > 0) ok = warp_wait(bar(B_QEMPTY), (n_q - 1) & 1, abort);
-            if (ok) {
-                if (lane == 0) {
-                    mbar_expect_tx(bar(B_QFULL), S::DC * p.hg * p.tt * 128);
-                    for (int c = 0; c < S::DC; c++)
-                        tma_3d(smem_u32(sm + S::OFF_Q + c * S::Q_CHUNK), &q_map, 64 * c, w.it.head0, w.it.tok0, bar(B_QFULL));
+            // queries: `chunks` chunks from chunk c0 on into the next buffer, once the S that read its last ones is done
+            auto load_q = [&](int c0, int chunks) {
+                const uint32_t i = n_q % S::NQ, fb = bar(B_QFULL) + 8 * i;
+                if (ok && n_q >= (uint32_t)S::NQ) ok = warp_wait(bar(B_QEMPTY) + 8 * i, (n_q / S::NQ - 1) & 1, abort);
+                if (!ok) return;
+                if (elect()) {
+                    mbar_expect_tx(fb, chunks * p.hg * p.tt * 128);
+                    for (int c = 0; c < chunks; c++)
+                        tma_3d(smem_u32(sm + S::OFF_Q + (i * 2 + c) * S::Q_CHUNK), &q_map, 64 * (c0 + c), w.it.head0, w.it.tok0, fb);
                 }
                 n_q++;
                 __syncwarp();
-            }
+            };
+            if (!S::WIDE) load_q(0, S::DC);
             const long long t0 = w.it.t0, end = t0 + w.it.n_tok;
             // this lane's box of tile j, a page's rows or a tile's of a larger page: its first row in the pool, or that
             // past the pool's end, which reads as zeros, where no token sees it or no page is listed
@@ -659,6 +673,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 if (miss && lane == 0) atomicOr(&g_paged_err, 4u);
                 if (lane == 0) masks[g % MASKS] = miss;         // the slots' previous tile is done with its own
                 for (int b = 0; b < S::DB; b++) {
+                    if (S::WIDE) load_q(2 * b, 2);
                     if (ok) ok = warp_wait(empty(unit), ((unit / RING) & 1) ^ 1, abort);
                     if (!ok) continue;
                     const uint32_t dst = smem_u32(sm + S::OFF_X) + unit % RING * SLOT + lane * box * 128, fb = full(unit);
@@ -677,7 +692,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         uint64_t t0 = 0;
         __syncwarp();
         for (uint32_t u = unit > (uint32_t)RING ? unit - RING : 0; u < unit; u++) mbar_drain(full(u), (u / RING) & 1, t0);
-        if (n_q > 0) mbar_drain(bar(B_QFULL), (n_q - 1) & 1, t0);
+        for (uint32_t i = n_q > (uint32_t)S::NQ ? n_q - S::NQ : 0; i < n_q; i++) mbar_drain(bar(B_QFULL) + 8 * (i % S::NQ), (i / S::NQ) & 1, t0);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
@@ -685,16 +700,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         constexpr uint64_t DK = desc(16, 1024), DM = desc(CHUNK, 1024);
         const uint64_t qk = DK + (smem_u32(sm + S::OFF_Q) >> 4), xk = DK + (smem_u32(sm + S::OFF_X) >> 4),
                        pm = DM + (smem_u32(sm + S::OFF_P) >> 4), xm = DM + (smem_u32(sm + S::OFF_X) >> 4);
-        uint32_t g = 0, unit_s = 0, unit_o = 0, items = 0;
+        uint32_t g = 0, unit_s = 0, unit_o = 0, items = 0, q_seen = 0;
         auto do_s = [&](bool first, bool last) {
-            if (first && ok) ok = warp_wait(bar(B_QFULL), items & 1, abort);
-            if (ok && g >= 2) ok = warp_wait(bar(B_SFREE + (g & 1)), ((g >> 1) - 1) & 1, abort);
-            const uint32_t d = tmem + S::T_S + (g & 1) * N;
+            if (ok && g >= (uint32_t)S::NS) ok = warp_wait(bar(B_SFREE + g % S::NS), (g / S::NS - 1) & 1, abort);
+            const uint32_t d = tmem + S::T_S + g % S::NS * N;
             for (int b = 0; b < S::DB; b++, unit_s++) {
+                const uint32_t i = q_seen % S::NQ;
+                if (S::WIDE || (first && b == 0)) {
+                    if (ok) ok = warp_wait(bar(B_QFULL) + 8 * i, (q_seen / S::NQ) & 1, abort);
+                    if (S::WIDE) q_seen++;
+                }
                 if (ok) ok = warp_wait(full(unit_s), (unit_s / RING) & 1, abort);
                 if (!ok) continue;
                 fence_after();
-                const uint64_t x = xk + unit_s % RING * (SLOT >> 4), q = qk + 2 * b * (S::Q_CHUNK >> 4);
+                const uint64_t x = xk + unit_s % RING * (SLOT >> 4), q = qk + (S::WIDE ? i : b) * 2 * (S::Q_CHUNK >> 4);
                 const uint32_t acc = b > 0 ? 1u : 0u;
                 if (elect()) {
 #pragma unroll
@@ -702,13 +721,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 #pragma unroll
                         for (int k = 0; k < 4; k++)
                             mma(d, x + c * (CHUNK >> 4) + 2 * k, q + c * (S::Q_CHUNK >> 4) + 2 * k, ID_S, c + k > 0 ? 1u : acc);
+                    if (S::WIDE) commit(bar(B_QEMPTY) + 8 * i);
                     if (b == S::DB - 1) {
-                        commit(bar(B_SFULL + (g & 1)));
-                        if (last) commit(bar(B_QEMPTY));
+                        commit(bar(B_SFULL + g % S::NS));
+                        if (!S::WIDE && last) commit(bar(B_QEMPTY));
                     }
                 }
                 __syncwarp();
             }
+            if (!S::WIDE && last) q_seen++;
             g++;
         };
         auto do_o = [&](uint32_t go, bool first) {
@@ -718,11 +739,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             for (int b = 0; b < S::DB; b++, unit_o++) {
                 if (!ok) continue;
                 const uint64_t x = xm + unit_o % RING * (SLOT >> 4), pr = pm + go % S::NP * (S::P_BYTES >> 4);
-                const uint32_t d = tmem + S::T_O + b * N, acc = first ? 0u : 1u;
+                const bool held = b < S::HELD;                  // into the columns of S, which the softmax warps have read
+                const uint32_t d = held ? tmem + S::T_S : tmem + S::T_O + b * N, acc = first || held ? 0u : 1u;
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < 8; k++) mma(d, x + k * 128, pr + k * 128, ID_O, k > 0 ? 1u : acc);
                     commit(empty(unit_o));
+                    if (held) commit(bar(B_HELD));
                     if (b == S::DB - 1) commit(bar(B_PVDONE + go % S::NP));
                 }
                 __syncwarp();
@@ -762,14 +785,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         while (w.next()) {
             const int n_cols = w.it.n_tok * p.hg, mine = min(max(n_cols - col0, 0), C);   // this group's columns in use
             const long long t0 = w.it.t0;
-            float l[C];
+            float l[C], held[S::HELD ? C : 1];                  // denominators of this row, the first d-block of O
 #pragma unroll
             for (int c = 0; c < C; c++) l[c] = 0.f;
+            if constexpr (S::HELD > 0) {
+#pragma unroll
+                for (int c = 0; c < C; c++) held[c] = 0.f;
+            }
             // columns out of use: a reference that no logit exceeds
             if (tid < C) gref[tid] = tid < mine ? NONE : INFINITY;
             group_sync(id);
             for (int j = w.tb; j < w.te; j++, g++) {
-                const int sb = g & 1;
+                const uint32_t sb = g % S::NS;
                 // columns [ca, cb) see this thread's row; is_full: all of the tile's rows by all columns
                 const bool raw = j < w.it.raw_tiles;
                 const long long base = (long long)(raw ? w.it.raw_tile0 + j : j - w.it.raw_tiles) * ROWS, row = base + r;
@@ -782,70 +809,72 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     ca = (int)min(max(a, 0ll), n) * p.hg - col0;
                     cb = (int)max(e, 0ll) * p.hg - col0;
                 }
-                if (ok) ok = warp_wait(bar(B_SFULL + sb), (g >> 1) & 1, abort);
+                if (ok) ok = warp_wait(bar(B_SFULL + sb), (g / S::NS) & 1, abort);
                 fence_after();
                 const uint32_t miss = masks[g % MASKS];
                 if (miss) {
                     is_full = false;
                     if ((miss >> (r >> min((raw ? p.raw : p.comp).page_log, 7))) & 1) cb = ca;
                 }
-                float s[C];
-                auto load_s = [&]() {
-#pragma unroll
-                    for (int c = 0; c < C; c += 32) tmem_ld32(lane_base + S::T_S + sb * N + col0 + c, s + c);
+                // 32 columns at a time: their logits from TMEM, those that are not seen to -infinity
+                float s[32];
+                auto load = [&](int c0) {
+                    tmem_ld32(lane_base + S::T_S + sb * N + col0 + c0, s);
                     ld_wait();
                 };
-                // logits that are not seen to -infinity; those of a row without a finite logit to NaN
-                auto mask = [&]() {
-                    float least = INFINITY;                     // fminf passes NaN over
-                    if (mine == C) {
+                const uint32_t span = max(cb - ca, 0);
+                auto mask = [&](int c0) {
+                    if (ca > c0 || cb < c0 + 32) {
 #pragma unroll
-                        for (int c = 0; c < C; c++) least = fminf(least, fabsf(s[c]));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < C; c++) least = c < mine ? fminf(least, fabsf(s[c])) : least;
+                        for (int c = 0; c < 32; c++) s[c] = (uint32_t)(c0 + c - ca) < span ? s[c] : -INFINITY;
                     }
-                    const bool finite = least < INFINITY;
-                    const float seen = finite ? 0.f : __int_as_float(0x7fc00000);
-                    const uint32_t span = max(cb - ca, 0);
-                    if (ca <= 0 && cb >= C) {
-#pragma unroll
-                        for (int c = 0; c < C; c++) s[c] += seen;
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < C; c++) s[c] = (uint32_t)(c - ca) < span ? s[c] + seen : -INFINITY;
-                    }
-                    return finite;
                 };
-                load_s();
-                bool finite = true;
-                if (!is_full) finite = mask();
-                float most = -INFINITY;
+                auto scale = [&](int c0) {                      // s * scale - reference
 #pragma unroll
-                for (int c = 0; c < C; c += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(gref + c);
-                    s[c] = fmaf(s[c], p.scale_log2, -m.x);
-                    s[c + 1] = fmaf(s[c + 1], p.scale_log2, -m.y);
-                    s[c + 2] = fmaf(s[c + 2], p.scale_log2, -m.z);
-                    s[c + 3] = fmaf(s[c + 3], p.scale_log2, -m.w);
-                    most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
-                    most = fmaxf(fmaxf(most, s[c + 2]), s[c + 3]);
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(gref + c0 + c);
+                        s[c] = fmaf(s[c], p.scale_log2, -m.x);
+                        s[c + 1] = fmaf(s[c + 1], p.scale_log2, -m.y);
+                        s[c + 2] = fmaf(s[c + 2], p.scale_log2, -m.z);
+                        s[c + 3] = fmaf(s[c + 3], p.scale_log2, -m.w);
+                    }
+                };
+                float most = -INFINITY, least = is_full ? 0.f : INFINITY;   // fmaxf and fminf pass NaN over
+#pragma unroll
+                for (int c0 = 0; c0 < C; c0 += 32) {
+                    if (c0 >= mine) break;
+                    load(c0);
+                    if (!is_full) {
+                        if (c0 + 32 <= mine) {
+#pragma unroll
+                            for (int c = 0; c < 32; c++) least = fminf(least, fabsf(s[c]));
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; c++) least = c0 + c < mine ? fminf(least, fabsf(s[c])) : least;
+                        }
+                        mask(c0);
+                    }
+                    scale(c0);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
                 }
-                const bool need = most > TAU;
-                const bool moves = group_any(id, need);
+                const bool finite = least < INFINITY;           // some logit of the row is a number
+                const bool moves = group_any(id, most > TAU);
                 if (moves) {
                     // the tile's largest logit of each column, the new references and the factors 2^(old - new)
-                    load_s();
-                    if (!is_full) mask();
-                    float m[C / 32];
 #pragma unroll
-                    for (int c = 0; c < C; c++) {
-                        s[c] *= p.scale_log2;
-                        const float x = warp_max(s[c]);
-                        m[c / 32] = lane == c % 32 ? x : m[c / 32];
+                    for (int c0 = 0; c0 < C; c0 += 32) {
+                        if (c0 >= mine) break;
+                        load(c0);
+                        if (!is_full) mask(c0);
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            const float x = warp_max(s[c] * p.scale_log2);
+                            m = lane == c ? x : m;
+                        }
+                        red[q4 * C + c0 + lane] = m;
                     }
-#pragma unroll
-                    for (int k = 0; k < C / 32; k++) red[q4 * C + 32 * k + lane] = m[k];
                     group_sync(id);
                     if (tid < C) {
                         const float old = gref[tid], now = fmaxf(old, fmaxf(fmaxf(red[tid], red[C + tid]), fmaxf(red[2 * C + tid], red[3 * C + tid])));
@@ -855,14 +884,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     group_sync(id);
 #pragma unroll
                     for (int c = 0; c < C; c += 4) {
-                        const float4 now = *reinterpret_cast<const float4 *>(gref + c), f = *reinterpret_cast<const float4 *>(red + c);
-                        s[c] -= now.x; s[c + 1] -= now.y; s[c + 2] -= now.z; s[c + 3] -= now.w;
+                        const float4 f = *reinterpret_cast<const float4 *>(red + c);
                         l[c] *= f.x; l[c + 1] *= f.y; l[c + 2] *= f.z; l[c + 3] *= f.w;
+                        if constexpr (S::HELD > 0) {
+                            held[c] *= f.x; held[c + 1] *= f.y; held[c + 2] *= f.z; held[c + 3] *= f.w;
+                        }
                     }
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_SFREE + sb));
                 // the second product of the tile before is done with P, and with O: where it was issued in front of this
                 // tile's first, the wait for that was the wait for both
                 if (S::AHEAD && ok && g >= S::NP) ok = warp_wait(bar(B_PVDONE + g % S::NP), (g / S::NP - 1) & 1, abort);
@@ -870,28 +898,41 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     if (S::AHEAD && S::NP > 1 && ok) ok = warp_wait(bar(B_PVDONE + (g - 1) % S::NP), (g - 1) / S::NP & 1, abort);
                     fence_after();
 #pragma unroll 1
-                    for (int b = 0; b < S::DB; b++)
-#pragma unroll
+                    for (int b = S::HELD; b < S::DB; b++)
+#pragma unroll 1
                         for (int c = 0; c < C; c += 32) {
-                            float v[32];
                             const uint32_t at = lane_base + S::T_O + b * N + col0 + c;
-                            tmem_ld32(at, v);
+                            tmem_ld32(at, s);
                             ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; e++) v[e] *= red[c + e];
-                            tmem_st32(at, v);
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(red + c + e);
+                                s[e] *= f.x; s[e + 1] *= f.y; s[e + 2] *= f.z; s[e + 3] *= f.w;
+                            }
+                            tmem_st32(at, s);
                         }
                     st_wait();
                 }
-                if (mine > 0) {
 #pragma unroll
-                    for (int c = 0; c < C; c++) {
-                        s[c] = ex2(s[c]);
-                        l[c] += s[c];
+                for (int c0 = 0; c0 < C; c0 += 32) {
+                    if (c0 >= mine) break;
+                    if (C > 32 || moves) {
+                        load(c0);
+                        if (!is_full) mask(c0);
+                        scale(c0);
+                    }
+                    if (!finite) {                              // NaN to the columns that see the row
+#pragma unroll
+                        for (int c = 0; c < 32; c++) s[c] = (uint32_t)(c0 + c - ca) < span ? __int_as_float(0x7fc00000) : -INFINITY;
                     }
 #pragma unroll
-                    for (int u = 0; u < C / 8; u++)
-                        *reinterpret_cast<uint4 *>(prow + g % S::NP * S::P_BYTES + (((u0 + u) ^ (r & 7)) * 16)) =
+                    for (int c = 0; c < 32; c++) {
+                        s[c] = ex2(s[c]);
+                        l[c0 + c] += s[c];
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; u++)
+                        *reinterpret_cast<uint4 *>(prow + g % S::NP * S::P_BYTES + (((u0 + c0 / 8 + u) ^ (r & 7)) * 16)) =
                             make_uint4(pack(s[8 * u], s[8 * u + 1]), pack(s[8 * u + 2], s[8 * u + 3]), pack(s[8 * u + 4], s[8 * u + 5]),
                                        pack(s[8 * u + 6], s[8 * u + 7]));
                 }
@@ -916,7 +957,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 fence_before();
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_PFULL + g % S::NP));
+                if (lane == 0) {
+                    if (!S::HELD) mbar_arrive(bar(B_SFREE + sb));
+                    mbar_arrive(bar(B_PFULL + g % S::NP));
+                }
+                if constexpr (S::HELD > 0) {                    // the tile's share of the first d-block
+                    if (ok) ok = warp_wait(bar(B_HELD), g & 1, abort);
+                    fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < C; c0 += 32) {
+                        if (c0 >= mine) break;
+                        load(c0);
+#pragma unroll
+                        for (int c = 0; c < 32; c++) held[c0 + c] += s[c];
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SFREE));
+                }
             }
             // denominators: the lanes' and warps' sums
             float sum[C / 32];
@@ -943,8 +1001,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             // Whole items: two lanes trade so that each stores two neighbouring values, the even one of column c, the odd one
             // of column c + 1; this lane's columns c0 + 2 i + (lane & 1) lie `at` and a step of out_head further each, or a
             // token further.  What is read from shared memory is read ahead of the stores, which it may not pass.
-#pragma unroll 1
-            for (int c0 = 0; c0 < C && c0 < mine; c0 += 32) {
+#pragma unroll
+            for (int c0 = 0; c0 < C; c0 += 32) {
+                if (c0 >= mine) break;
                 const int my = c0 + (lane & 1);
                 const int first_h = (col0 + my) % p.hg;
                 const int h0 = (col0 + c0) % p.hg;              // 32 heads of one token?
@@ -956,7 +1015,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 #pragma unroll 1
                 for (int b = 0; b < S::DB; b++) {
                     float v[32];
-                    if (w.tiles > 0) {
+                    if (b < S::HELD) {
+                        if constexpr (S::HELD > 0) {
+#pragma unroll
+                            for (int c = 0; c < 32; c++) v[c] = held[c0 + c];
+                        }
+                    } else if (w.tiles > 0) {
                         tmem_ld32(lane_base + S::T_O + b * N + col0 + c0, v);
                         ld_wait();
                     } else {
@@ -1024,9 +1088,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 
 // Joins the parts of the divided items.  Few items (FEW), perhaps many parts: a block for each item and column, whose
 // threads share the parts; else, mostly two or three parts: a thread takes all parts of its values.
-template <int D, bool FEW>
+template <int D, bool WIDE, bool FEW>
 __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
-    constexpr int N = Shape<D>::N, LANES = D / 4;              // threads of a column, four values each
+    constexpr int N = Shape<D, WIDE>::N, LANES = D / 4;              // threads of a column, four values each
     constexpr int COLS = FEW ? 1 : JOIN_THREADS / LANES, GROUPS = JOIN_THREADS / LANES / COLS;
     __shared__ float weight[FEW ? MAX_GRID : 1], denom[FEW ? MAX_GRID : 1];
     __shared__ __align__(16) float sums[FEW ? GROUPS : 1][D];
@@ -1130,13 +1194,13 @@ int sm_count() {
 }
 
 struct Split { int n, hg, groups, tt; };
-Split split_of(uint32_t n_heads, uint32_t d) {
-    const int n = d == 512 ? 64 : 128, h = (int)n_heads, groups = (h + n - 1) / n, hg = (h + groups - 1) / groups;
+Split split_of(uint32_t n_heads, uint32_t d, bool wide) {
+    const int n = d == 512 && !wide ? 64 : 128, h = (int)n_heads, groups = (h + n - 1) / n, hg = (h + groups - 1) / groups;
     return {n, hg, groups, n / hg};
 }
 // The workspace's regions; returns its size.
-size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_heads, uint32_t d) {
-    const Split c = split_of(n_heads, d);
+size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_heads, uint32_t d, bool wide) {
+    const Split c = split_of(n_heads, d, wide);
     size_t at = 0;
     auto region = [&](size_t bytes) {
         const size_t here = at;
@@ -1154,9 +1218,9 @@ size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_hea
     return at;
 }
 
-template <int D>
+template <int D, bool WIDE = false>
 cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream_t s) {
-    using S = Shape<D>;
+    using S = Shape<D, WIDE>;
     p.over = S::OVER;
     p.small = a.n_seq <= SMALL && (uint64_t)a.n_tok * p.groups <= SMALL;
     CUtensorMap qm, rm, cm;
@@ -1167,14 +1231,14 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
         if (!make_map(&qm, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
     if (!pool_map(&rm, a.raw, D) || !pool_map(&cm, a.ratio ? a.comp : a.raw, D)) return cudaErrorInvalidValue;
-    cudaError_t e = ensure_dyn_smem(paged_attn_kernel<D>, S::SMEM);
+    cudaError_t e = ensure_dyn_smem(paged_attn_kernel<D, WIDE>, S::SMEM);
     if (e != cudaSuccess) return e;
     // a register split above the launch's total would wait for ever
     static std::atomic<int> regs{0};
     int have = regs.load(std::memory_order_relaxed);
     if (have == 0) {
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, paged_attn_kernel<D>);
+        e = cudaFuncGetAttributes(&fa, paged_attn_kernel<D, WIDE>);
         if (e != cudaSuccess) return e;
         regs.store(have = fa.numRegs, std::memory_order_relaxed);
     }
@@ -1185,17 +1249,20 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
         if (e == cudaSuccess) e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), info, s, p, grid);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(paged_attn_kernel<D>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
+    e = launch_pdl(paged_attn_kernel<D, WIDE>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
     if (e != cudaSuccess) return e;
     const int entries = p.small ? (int)a.n_tok * p.groups : grid;
-    if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, true>, dim3(entries * S::N), dim3(JOIN_THREADS), 0, s, p);
-    return launch_pdl(paged_join_kernel<D, false>, dim3(entries * (S::N / (JOIN_THREADS / (D / 4)))), dim3(JOIN_THREADS), 0, s, p);
+    if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N), dim3(JOIN_THREADS), 0, s, p);
+    return launch_pdl(paged_join_kernel<D, WIDE, false>, dim3(entries * (S::N / (JOIN_THREADS / (D / 4)))), dim3(JOIN_THREADS), 0, s, p);
 }
 
 }  // namespace
 
 size_t paged_attn_ws_bytes(uint32_t, uint32_t n_tok, uint32_t n_heads, uint32_t head_dim) {
-    return lay_out(nullptr, nullptr, sm_count(), n_tok, n_heads, head_dim);
+    const int grid = sm_count();
+    const size_t a = lay_out(nullptr, nullptr, grid, n_tok, n_heads, head_dim, false);
+    const size_t b = lay_out(nullptr, nullptr, grid, n_tok, n_heads, head_dim, true);
+    return a > b ? a : b;
 }
 
 cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStream_t s) {
@@ -1213,12 +1280,13 @@ cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStrea
     }
     p.n_seq = (int)a.n_seq; p.n_tok = (int)a.n_tok; p.n_heads = (int)a.n_heads;
     p.window = (int)a.window; p.ratio = (int)a.ratio;
-    const Split c = split_of(a.n_heads, a.head_dim);
+    const bool wide = a.head_dim == 512 && (a.n_heads > 64 || a.n_tok >= WIDE_TOKENS * a.n_seq);
+    const Split c = split_of(a.n_heads, a.head_dim, wide);
     p.hg = c.hg; p.groups = c.groups; p.tt = c.tt;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.n_heads, a.head_dim);
+    lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.n_heads, a.head_dim, wide);
     return a.head_dim == 64 ? launch<64>(a, p, grid, s) : a.head_dim == 128 ? launch<128>(a, p, grid, s)
-         : a.head_dim == 256 ? launch<256>(a, p, grid, s) : launch<512>(a, p, grid, s);
+         : a.head_dim == 256 ? launch<256>(a, p, grid, s) : wide ? launch<512, true>(a, p, grid, s) : launch<512>(a, p, grid, s);
 }
 
 cudaError_t paged_attn_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_paged_wait_ns, &ns, sizeof ns); }

@@ -45,9 +45,6 @@ namespace {
 
 constexpr int ROWS = 128, CHUNK = ROWS * 128, SLOT = 2 * CHUNK;      // bytes of a [128][64] chunk, of a ring slot
 constexpr int THREADS = 384;
-// registers of a thread of the loading and MMA warps and of the softmax warps (setmaxnreg at entry): their sum over
-// three warpgroups fits the launch's, which the host checks
-constexpr int REG_LOW = 72, REG_SOFT = 216;
 constexpr int MASKS = 8;                                            // tiles whose unlisted pages are remembered
 constexpr float TAU = 8.0f;
 constexpr float NONE = -3.0e38f;                                    // reference of a column that saw nothing yet
@@ -81,6 +78,9 @@ struct Shape {
     static constexpr int OFF_BAR = OFF_MASK + 4 * MASKS;
     static constexpr int N_BAR = 2 * RING + 15;
     static constexpr int SMEM = OFF_BAR + 8 * N_BAR + 16;
+    // registers of a thread of the loading and MMA warps and of the softmax warps (setmaxnreg at entry): their sum over
+    // three warpgroups fits the launch's, which the host checks
+    static constexpr int REG_LOW = WIDE ? 72 : C == 64 ? 88 : 120, REG_SOFT = WIDE ? 216 : C == 64 ? 208 : 192;
     static constexpr int HELD = WIDE ? 1 : 0;                       // d-blocks of O in registers
     static constexpr int T_S = 0, T_O = NS * N - HELD * N;          // d-block b at T_O + b * N
     static constexpr int OVER = D == 512 ? 1 : D == 256 ? 2 : 3;    // an item's start and end, in tiles
@@ -611,7 +611,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REG_LOW));
     Work w(p, from, to);
     bool ok = true;
     if (warp == 0) {
@@ -770,7 +770,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         __syncwarp();
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REG_SOFT));
         Work w(p, from, to);
         bool ok = true;
         // ------------------------------------------------------------ softmax, output
@@ -816,22 +816,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     is_full = false;
                     if ((miss >> (r >> min((raw ? p.raw : p.comp).page_log, 7))) & 1) cb = ca;
                 }
-                // 32 columns at a time: their logits from TMEM, those that are not seen to -infinity
-                float s[32];
+                // BL columns at a time: their logits from TMEM, those that are not seen to -infinity.  All columns at once
+                // where the registers are not needed for O: the logits then stay in them for the second pass.
+                constexpr int BL = S::HELD ? 32 : C;
+                float s[BL];
                 auto load = [&](int c0) {
-                    tmem_ld32(lane_base + S::T_S + sb * N + col0 + c0, s);
+#pragma unroll
+                    for (int k = 0; k < BL; k += 32) tmem_ld32(lane_base + S::T_S + sb * N + col0 + c0 + k, s + k);
                     ld_wait();
                 };
                 const uint32_t span = max(cb - ca, 0);
                 auto mask = [&](int c0) {
-                    if (ca > c0 || cb < c0 + 32) {
+                    if (ca > c0 || cb < c0 + BL) {
 #pragma unroll
-                        for (int c = 0; c < 32; c++) s[c] = (uint32_t)(c0 + c - ca) < span ? s[c] : -INFINITY;
+                        for (int c = 0; c < BL; c++) s[c] = (uint32_t)(c0 + c - ca) < span ? s[c] : -INFINITY;
                     }
                 };
                 auto scale = [&](int c0) {                      // s * scale - reference
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
+                    for (int c = 0; c < BL; c += 4) {
                         const float4 m = *reinterpret_cast<const float4 *>(gref + c0 + c);
                         s[c] = fmaf(s[c], p.scale_log2, -m.x);
                         s[c + 1] = fmaf(s[c + 1], p.scale_log2, -m.y);
@@ -841,39 +844,40 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 };
                 float most = -INFINITY, least = is_full ? 0.f : INFINITY;   // fmaxf and fminf pass NaN over
 #pragma unroll
-                for (int c0 = 0; c0 < C; c0 += 32) {
+                for (int c0 = 0; c0 < C; c0 += BL) {
                     if (c0 >= mine) break;
                     load(c0);
                     if (!is_full) {
-                        if (c0 + 32 <= mine) {
+                        if (c0 + BL <= mine) {
 #pragma unroll
-                            for (int c = 0; c < 32; c++) least = fminf(least, fabsf(s[c]));
+                            for (int c = 0; c < BL; c++) least = fminf(least, fabsf(s[c]));
                         } else {
 #pragma unroll
-                            for (int c = 0; c < 32; c++) least = c0 + c < mine ? fminf(least, fabsf(s[c])) : least;
+                            for (int c = 0; c < BL; c++) least = c0 + c < mine ? fminf(least, fabsf(s[c])) : least;
                         }
                         mask(c0);
                     }
                     scale(c0);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
+                    for (int c = 0; c < BL; c += 2) most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
                 }
                 const bool finite = least < INFINITY;           // some logit of the row is a number
                 const bool moves = group_any(id, most > TAU);
                 if (moves) {
                     // the tile's largest logit of each column, the new references and the factors 2^(old - new)
 #pragma unroll
-                    for (int c0 = 0; c0 < C; c0 += 32) {
+                    for (int c0 = 0; c0 < C; c0 += BL) {
                         if (c0 >= mine) break;
                         load(c0);
                         if (!is_full) mask(c0);
-                        float m = -INFINITY;
+                        float m[BL / 32];
 #pragma unroll
-                        for (int c = 0; c < 32; c++) {
+                        for (int c = 0; c < BL; c++) {
                             const float x = warp_max(s[c] * p.scale_log2);
-                            m = lane == c ? x : m;
+                            m[c / 32] = lane == c % 32 ? x : m[c / 32];
                         }
-                        red[q4 * C + c0 + lane] = m;
+#pragma unroll
+                        for (int k = 0; k < BL / 32; k++) red[q4 * C + c0 + 32 * k + lane] = m[k];
                     }
                     group_sync(id);
                     if (tid < C) {
@@ -882,6 +886,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         red[tid] = ex2(old - now);
                     }
                     group_sync(id);
+                    if (!S::HELD) scale(0);
 #pragma unroll
                     for (int c = 0; c < C; c += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(red + c);
@@ -901,37 +906,39 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     for (int b = S::HELD; b < S::DB; b++)
 #pragma unroll 1
                         for (int c = 0; c < C; c += 32) {
-                            const uint32_t at = lane_base + S::T_O + b * N + col0 + c;
-                            tmem_ld32(at, s);
+                            const uint32_t o = lane_base + S::T_O + b * N + col0 + c;
+                            float v[32];
+                            tmem_ld32(o, v);
                             ld_wait();
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
                                 const float4 f = *reinterpret_cast<const float4 *>(red + c + e);
-                                s[e] *= f.x; s[e + 1] *= f.y; s[e + 2] *= f.z; s[e + 3] *= f.w;
+                                v[e] *= f.x; v[e + 1] *= f.y; v[e + 2] *= f.z; v[e + 3] *= f.w;
                             }
-                            tmem_st32(at, s);
+                            tmem_st32(o, v);
                         }
                     st_wait();
                 }
 #pragma unroll
-                for (int c0 = 0; c0 < C; c0 += 32) {
+                for (int c0 = 0; c0 < C; c0 += BL) {
                     if (c0 >= mine) break;
-                    if (C > 32 || moves) {
+                    if (S::HELD) {
                         load(c0);
                         if (!is_full) mask(c0);
                         scale(c0);
                     }
-                    if (!finite) {                              // NaN to the columns that see the row
+                    if (!is_full && __any_sync(0xffffffffu, !finite)) {   // NaN to the columns that see the row
 #pragma unroll
-                        for (int c = 0; c < 32; c++) s[c] = (uint32_t)(c0 + c - ca) < span ? __int_as_float(0x7fc00000) : -INFINITY;
+                        for (int c = 0; c < BL; c++)
+                            s[c] = finite ? s[c] : (uint32_t)(c0 + c - ca) < span ? __int_as_float(0x7fc00000) : -INFINITY;
                     }
 #pragma unroll
-                    for (int c = 0; c < 32; c++) {
+                    for (int c = 0; c < BL; c++) {
                         s[c] = ex2(s[c]);
                         l[c0 + c] += s[c];
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; u++)
+                    for (int u = 0; u < BL / 8; u++)
                         *reinterpret_cast<uint4 *>(prow + g % S::NP * S::P_BYTES + (((u0 + c0 / 8 + u) ^ (r & 7)) * 16)) =
                             make_uint4(pack(s[8 * u], s[8 * u + 1]), pack(s[8 * u + 2], s[8 * u + 3]), pack(s[8 * u + 4], s[8 * u + 5]),
                                        pack(s[8 * u + 6], s[8 * u + 7]));
@@ -965,11 +972,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     if (ok) ok = warp_wait(bar(B_HELD), g & 1, abort);
                     fence_after();
 #pragma unroll
-                    for (int c0 = 0; c0 < C; c0 += 32) {
+                    for (int c0 = 0; c0 < C; c0 += BL) {
                         if (c0 >= mine) break;
                         load(c0);
 #pragma unroll
-                        for (int c = 0; c < 32; c++) held[c0 + c] += s[c];
+                        for (int c = 0; c < BL; c++) held[c0 + c] += s[c];
                     }
                     fence_before();
                     __syncwarp();
@@ -1242,7 +1249,7 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
         if (e != cudaSuccess) return e;
         regs.store(have = fa.numRegs, std::memory_order_relaxed);
     }
-    if (128 * (REG_LOW + 2 * REG_SOFT) > THREADS * have) return cudaErrorNotSupported;
+    if (128 * (S::REG_LOW + 2 * S::REG_SOFT) > THREADS * have) return cudaErrorNotSupported;
     if (!p.small) {
         const size_t info = (3 * (size_t)a.n_seq + 1) * sizeof(int);
         e = ensure_dyn_smem(paged_plan_kernel, info);

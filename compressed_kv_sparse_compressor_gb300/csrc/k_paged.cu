@@ -72,7 +72,10 @@ struct Shape {
     static constexpr bool AHEAD = RING >= 2 * DB;                   // the next tile's S in front of this one's O
     static constexpr int Q_CHUNK = N * 128, NQ = WIDE ? 2 : 1;      // buffers of queries, WIDE: of two chunks each
     static constexpr int OFF_Q = 0, OFF_P = (WIDE ? 2 * NQ : DC) * Q_CHUNK, P_BYTES = ROWS * N * 2, OFF_X = OFF_P + NP * P_BYTES;
-    static constexpr int OFF_RED = OFF_X + RING * SLOT;             // [2][4][C] floats
+    // 2 KB for each softmax warp, where its outputs are turned: a group's own half of P, if P's columns lie in halves
+    static constexpr bool OWN_TURN = N == 64;
+    static constexpr int OFF_TURN = OWN_TURN ? OFF_X + RING * SLOT : OFF_P;
+    static constexpr int OFF_RED = OFF_X + RING * SLOT + (OWN_TURN ? 8 * 2048 : 0);   // [2][4][C] floats
     static constexpr int OFF_REF = OFF_RED + 8 * C * 4;             // [N]
     static constexpr int OFF_MASK = OFF_REF + 4 * N;
     static constexpr int OFF_BAR = OFF_MASK + 4 * MASKS;
@@ -251,6 +254,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
         "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
         "r"(r[31])
         : "memory");
+}
+// A warp's 16 lanes from taddr's on, 32 columns: value 4 i + 2 h + e of lane t is that of TMEM lane t / 4 + 8 h, column
+// 8 i + 2 (t % 4) + e (two neighbouring columns to a pair, as stmatrix takes them).  Without the wait.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit values, transposed; lane t gives the address of row t % 8 of matrix t / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -785,7 +803,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         while (w.next()) {
             const int n_cols = w.it.n_tok * p.hg, mine = min(max(n_cols - col0, 0), C);   // this group's columns in use
             const long long t0 = w.it.t0;
-            float l[C], held[S::HELD ? C : 1];                  // denominators of this row, the first d-block of O
+            // denominators of this row; the first d-block of O, as tmem_ld_16x32 gives it, the warp's lower 16 rows first
+            float l[C], held[S::HELD ? C : 1];
 #pragma unroll
             for (int c = 0; c < C; c++) l[c] = 0.f;
             if constexpr (S::HELD > 0) {
@@ -891,8 +910,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     for (int c = 0; c < C; c += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(red + c);
                         l[c] *= f.x; l[c + 1] *= f.y; l[c + 2] *= f.z; l[c + 3] *= f.w;
-                        if constexpr (S::HELD > 0) {
-                            held[c] *= f.x; held[c + 1] *= f.y; held[c + 2] *= f.z; held[c + 3] *= f.w;
+                    }
+                    if constexpr (S::HELD > 0) {
+#pragma unroll
+                        for (int i = 0; i < C / 8; i++) {
+                            const float2 f = *reinterpret_cast<const float2 *>(red + 8 * i + 2 * (lane % 4));
+#pragma unroll
+                            for (int k = 0; k < 4; k++) held[4 * i + k] *= k % 2 ? f.y : f.x, held[C / 2 + 4 * i + k] *= k % 2 ? f.y : f.x;
                         }
                     }
                 }
@@ -972,11 +996,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     if (ok) ok = warp_wait(bar(B_HELD), g & 1, abort);
                     fence_after();
 #pragma unroll
-                    for (int c0 = 0; c0 < C; c0 += BL) {
+                    for (int c0 = 0; c0 < C; c0 += 32) {
                         if (c0 >= mine) break;
-                        load(c0);
+                        tmem_ld_16x32(lane_base + S::T_S + col0 + c0, s);
+                        tmem_ld_16x32(lane_base + (16u << 16) + S::T_S + col0 + c0, s + 16);
+                        ld_wait();
 #pragma unroll
-                        for (int c = 0; c < BL; c++) held[c0 + c] += s[c];
+                        for (int c = 0; c < 16; c++) held[c0 / 2 + c] += s[c], held[C / 2 + c0 / 2 + c] += s[16 + c];
                     }
                     fence_before();
                     __syncwarp();
@@ -1005,76 +1031,72 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 if (ok) ok = warp_wait(bar(B_PVDONE + (g - 1) % S::NP), (g - 1) / S::NP & 1, abort);
                 fence_after();
             }
-            // Whole items: two lanes trade so that each stores two neighbouring values, the even one of column c, the odd one
-            // of column c + 1; this lane's columns c0 + 2 i + (lane & 1) lie `at` and a step of out_head further each, or a
-            // token further.  What is read from shared memory is read ahead of the stores, which it may not pass.
+            // Output, 32 columns of a d-block at a time: pairs of columns from TMEM, whole items scaled, rounded and turned
+            // through 2 KB of shared memory (16-byte units of a row swapped by its number, so that no bank meets twice), so that
+            // four lanes store 64 bytes of a head; divided items as they are.
+            const uint32_t turn = smem_u32(sm + S::OFF_TURN) + (S::OWN_TURN ? grp * 8192 : grp * CHUNK) + q4 * 2048;
+            const uint8_t *turned = sm + S::OFF_TURN + (S::OWN_TURN ? grp * 8192 : grp * CHUNK) + q4 * 2048;
 #pragma unroll
             for (int c0 = 0; c0 < C; c0 += 32) {
-                if (c0 >= mine) break;
-                const int my = c0 + (lane & 1);
-                const int first_h = (col0 + my) % p.hg;
-                const int h0 = (col0 + c0) % p.hg;              // 32 heads of one token?
-                const bool one_token = c0 + 32 <= mine && h0 + 32 <= p.hg && w.it.head0 + h0 + 32 <= p.n_heads;
-                __nv_bfloat16 *first = p.out + (w.it.tok0 + (col0 + my) / p.hg) * p.out_token + (w.it.head0 + first_h) * p.out_head + (r & ~1);
-                float inv[32];
+                if (c0 >= mine || !ok || (D == 64 && q4 >= 2)) break;
+                float2 inv[4];                                  // of columns c0 + 8 i + 2 (lane % 4) and the next
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) *reinterpret_cast<float4 *>(inv + c) = *reinterpret_cast<const float4 *>(red + c0 + c);
-#pragma unroll 1
-                for (int b = 0; b < S::DB; b++) {
-                    float v[32];
-                    if (b < S::HELD) {
-                        if constexpr (S::HELD > 0) {
+                for (int i = 0; i < 4; i++) inv[i] = *reinterpret_cast<const float2 *>(red + c0 + 8 * i + 2 * (lane % 4));
+                __nv_bfloat16 *dst[4];                          // rows 8 k + lane / 4, null out of use
 #pragma unroll
-                            for (int c = 0; c < 32; c++) v[c] = held[c0 + c];
+                for (int k = 0; k < 4; k++) {
+                    const int c = col0 + c0 + 8 * k + lane / 4, h = w.it.head0 + c % p.hg;
+                    dst[k] = c0 + 8 * k + lane / 4 < mine && h < p.n_heads
+                                 ? p.out + (w.it.tok0 + c / p.hg) * p.out_token + h * p.out_head + 32 * q4 + 8 * (lane % 4) : nullptr;
+                }
+                auto put = [&](const float *v, int b) {         // v: 16 values of the lower 16 rows, 16 of the upper
+                    if (!whole) {
+                        float *o = p.plan.part_o + (part * N + col0 + c0) * D + 128 * b + 32 * q4 + lane / 4;
+#pragma unroll
+                        for (int half = 0; half < 2; half++)
+#pragma unroll
+                            for (int i = 0; i < 16; i++) {
+                                const int c = 8 * (i / 4) + 2 * (lane % 4) + i % 2;
+                                if (c0 + c < mine) o[c * D + 16 * half + 8 * (i / 2 % 2)] = v[16 * half + i];
+                            }
+                        return;
+                    }
+                    __syncwarp();                               // the rows before have been read
+#pragma unroll
+                    for (int half = 0; half < 2; half++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            uint32_t m[4];
+#pragma unroll
+                            for (int i = 0; i < 4; i++) m[i] = pack(v[16 * half + 4 * i + 2 * h] * inv[i].x, v[16 * half + 4 * i + 2 * h + 1] * inv[i].y);
+                            store_transposed(turn + lane * 64 + (((2 * half + h) ^ (lane / 2 % 4)) * 16), m[0], m[1], m[2], m[3]);
                         }
-                    } else if (w.tiles > 0) {
-                        tmem_ld32(lane_base + S::T_O + b * N + col0 + c0, v);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const int row = 8 * k + lane / 4;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(turned + row * 64 + ((lane % 4) ^ (row / 2 % 4)) * 16);
+                        if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + 128 * b) = x;
+                    }
+                };
+                float v[32];
+                if constexpr (S::HELD > 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++) v[i] = held[c0 / 2 + i], v[16 + i] = held[C / 2 + c0 / 2 + i];
+                    put(v, 0);
+                }
+#pragma unroll 1
+                for (int b = S::HELD; b < S::DB; b++) {
+                    if (w.tiles > 0) {
+                        const uint32_t o = lane_base + S::T_O + b * N + col0 + c0;
+                        tmem_ld_16x32(o, v);
+                        tmem_ld_16x32(o + (16u << 16), v + 16);
                         ld_wait();
                     } else {
 #pragma unroll
                         for (int c = 0; c < 32; c++) v[c] = 0.f;
                     }
-                    if (!ok) continue;
-                    if (!whole) {
-                        float *dst = p.plan.part_o + (part * N + col0 + c0) * D + 128 * b + r;
-                        if (D > 64 || r < 64) {
-                            if (c0 + 32 <= mine) {
-#pragma unroll
-                                for (int c = 0; c < 32; c++) dst[c * D] = v[c];
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < 32; c++)
-                                    if (c0 + c < mine) dst[c * D] = v[c];
-                            }
-                        }
-                        continue;
-                    }
-                    uint32_t two[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float a = v[c] * inv[c], e = v[c + 1] * inv[c + 1];
-                        const float x = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : e, 1);
-                        two[c / 2] = lane & 1 ? pack(x, e) : pack(a, x);
-                    }
-                    if (D > 64 || r < 64) {
-                        __nv_bfloat16 *dst = first + 128 * b;
-                        if (one_token) {
-#pragma unroll
-                            for (int i = 0; i < 16; i++, dst += 2 * p.out_head) *reinterpret_cast<uint32_t *>(dst) = two[i];
-                        } else {
-                            int h = first_h;
-#pragma unroll
-                            for (int i = 0; i < 16; i++) {
-                                if (my + 2 * i < mine && w.it.head0 + h < p.n_heads) *reinterpret_cast<uint32_t *>(dst) = two[i];
-                                h += 2;
-                                dst += 2 * p.out_head;
-                                while (h >= p.hg) {
-                                    h -= p.hg;
-                                    dst += p.out_token - p.hg * p.out_head;
-                                }
-                            }
-                        }
-                    }
+                    put(v, b);
                 }
             }
             if (w.tiles > 0) {

@@ -33,6 +33,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ds4c_internal.cuh"
 
@@ -104,7 +105,7 @@ struct Pool {
 };
 struct Item {
     int seq, tok0, n_tok, head0;
-    int t0, raw_tile0, raw_tiles, comp_tiles;
+    int t0, raw0, raws, comps; // position of its first token, first raw row, 16-row pieces of raw and of compressed rows
     int alone;                 // the sequence's only item (or the first group of its heads): its rows come from memory
 };
 struct Start { int item, y; };
@@ -330,7 +331,9 @@ __device__ __forceinline__ int tiles_before(int y, int tiles, int over) {
     if (tiles <= SHORT) return y > 0 ? tiles : 0;
     return max(y - over, 0);
 }
-__device__ __forceinline__ int tiles_of(const Item &it) { return it.raw_tiles + it.comp_tiles; }
+constexpr int MAX_LENGTH = 1 << 30;
+constexpr int PIECE = 16, PIECES = ROWS / PIECE;               // a tile is 8 pieces of 16 rows, one K step of the second product each
+__device__ __forceinline__ int tiles_of(const Item &it) { return (it.raws + it.comps + PIECES - 1) / PIECES; }
 
 // Item k of a sequence of n new tokens from token b on, `length` long with them.
 __device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n, int length, int k) {
@@ -342,19 +345,22 @@ __device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n
     it.head0 = k % p.groups * p.hg;
     it.alone = n <= p.tt && k == 0;
     // positions t0 .. end - 1; a token before 0 sees nothing wherever it is
-    it.t0 = max(length, -(1 << 30)) - n + j;
+    it.t0 = max(length, 0) - n + j;
     const int end = it.t0 + it.n_tok;
-    it.raw_tile0 = it.raw_tiles = it.comp_tiles = 0;
+    // With a window its raw pieces are those it touches, the compressed ones right behind them (a window of 128 rows and
+    // up to 112 compressed ones are two tiles); without one tiles start at multiples of 128 rows, whole pages to a load.
+    it.raw0 = it.raws = it.comps = 0;
     if (end > 0) {
-        it.raw_tile0 = (p.window && it.t0 >= p.window ? it.t0 + 1 - p.window : 0) / ROWS;
-        it.raw_tiles = (int)(((unsigned)end + ROWS - 1) / ROWS) - it.raw_tile0;
-        if (p.ratio) it.comp_tiles = (int)(((unsigned)(end / p.ratio) + ROWS - 1) / ROWS);
+        const int step = p.window ? PIECE : ROWS;
+        if (p.window && it.t0 >= p.window) it.raw0 = (it.t0 + 1 - p.window) / PIECE * PIECE;
+        it.raws = (end - it.raw0 + step - 1) / step * (step / PIECE);
+        if (p.ratio) it.comps = (end / p.ratio + PIECE - 1) / PIECE;
     }
     return it;
 }
-// Items of sequence s (start b, end e); reports starts that fall or leave the tokens.
-__device__ __forceinline__ int items_of(const Params &p, int b, int e, bool report) {
-    if (b < 0 || e < b || e > p.n_tok) {
+// Items of a sequence of tokens b .. e - 1; reports starts that fall or leave the tokens, and lengths past the limit.
+__device__ __forceinline__ int items_of(const Params &p, int b, int e, int length, bool report) {
+    if (b < 0 || e < b || e > p.n_tok || length > MAX_LENGTH) {
         if (report) atomicOr(&g_paged_err, 2u);
         return 0;
     }
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             length[s] = p.length[s];
             begin[s] = b;
             if (s == p.n_seq - 1) begin[s + 1] = e;
-            k = items_of(p, b, e, true);
+            k = items_of(p, b, e, length[s], true);
         }
         int total;
         const int incl = block_scan<PLAN_THREADS, int>(k, sums_i, total);
@@ -485,7 +491,7 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
         length[tid] = p.length[tid];
         begin[tid] = b;
         if (tid == p.n_seq - 1) begin[tid + 1] = e;
-        k = items_of(p, b, e, cta == 0);
+        k = items_of(p, b, e, length[tid], cta == 0);
     }
     int carry;
     const int incl = block_scan<SMALL, int>(k, sums_i, carry);
@@ -544,7 +550,8 @@ struct Work {
     }
 };
 
-template <int D, bool WIDE>
+// WIN: with a window, tiles of pieces.
+template <int D, bool WIDE, bool WIN>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap raw_map,
                   const __grid_constant__ CUtensorMap comp_map, const __grid_constant__ Params p) {
@@ -651,59 +658,55 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 __syncwarp();
             };
             if (!S::WIDE) load_q(0, S::DC);
-            const long long t0 = w.it.t0, end = t0 + w.it.n_tok;
-            // this lane's box of tile j, a page's rows or a tile's of a larger page: its first row in the pool, or that
-            // past the pool's end, which reads as zeros, where no token sees it or no page is listed
-            auto box_of = [&](int j, bool &missing) -> int {
-                const bool raw = j < w.it.raw_tiles;
+            const int t0 = w.it.t0, end = t0 + w.it.n_tok;
+            // This lane's box of tile j: a piece with a window, else a page's rows, or a tile's of a larger page.  `y`: its
+            // first row in the pool, or that past the pool's end, which reads as zeros, where no token sees it or no page is
+            // listed.
+            const int comp_end = p.ratio ? end / p.ratio : 0;
+            struct Box { const CUtensorMap *map; int y, rows; bool there, missing; };
+            auto box_of = [&](int j) -> Box {
+                const int q0 = j * PIECES;
+                const bool raw = WIN ? q0 + lane < w.it.raws : q0 < w.it.raws;
                 const Pool &pool = raw ? p.raw : p.comp;
-                const int box = min(1 << pool.page_log, ROWS);
-                const long long row = (long long)(raw ? w.it.raw_tile0 + j : j - w.it.raw_tiles) * ROWS + lane * box;
-                const long long lo = raw && p.window ? t0 + 1 - p.window : 0, hi = raw ? end : end / p.ratio;
-                missing = false;
-                if (lane < ROWS / box && row + box > lo && row < hi) {
-                    const long long k = row >> pool.page_log;
+                Box b{raw ? &raw_map : &comp_map, raw ? p.raw_rows : p.comp_rows, WIN ? PIECE : min(1 << pool.page_log, ROWS), false, false};
+                const int row = (raw ? w.it.raw0 + PIECE * q0 : PIECE * (q0 - w.it.raws)) + lane * b.rows;
+                const int lo = WIN && raw ? t0 + 1 - p.window : 0, hi = raw ? end : comp_end;
+                b.there = WIN ? lane < min(w.it.raws + w.it.comps - q0, PIECES) : lane < ROWS / b.rows;
+                if (b.there && row + b.rows > lo && row < hi) {
+                    const int k = row >> pool.page_log;
                     const int page = k < pool.max_pages ? pool.pages[w.it.seq * pool.ld + k] : -1;
-                    missing = page < 0 || page >= pool.n_pages;
-                    if (!missing) return (page << pool.page_log) + (int)(row & ((1 << pool.page_log) - 1));
+                    b.missing = page < 0 || page >= pool.n_pages;
+                    if (!b.missing) b.y = (page << pool.page_log) + (row & ((1 << pool.page_log) - 1));
                 }
-                return raw ? p.raw_rows : p.comp_rows;
+                return b;
             };
-            bool missing = false, missing_next = false;
-            int y_next = box_of(w.tb, missing_next);
+            Box next = box_of(w.tb);
             for (int j = w.tb; j < w.te; j++, g++) {
-                const bool raw = j < w.it.raw_tiles;
-                const CUtensorMap *map = raw ? &raw_map : &comp_map;
-                const int box = min(1 << (raw ? p.raw : p.comp).page_log, ROWS), boxes = ROWS / box;
-                const int y = y_next;
-                missing = missing_next;
+                const Box box = next;
                 // rows that nobody else reads are brought to L2 a tile ahead (the ring holds hardly more than a tile: 32
                 // sequences at 64K 407 us without, 382 with)
                 if (w.it.alone && j + 1 < w.te) {
-                    y_next = box_of(j + 1, missing_next);
-                    const bool raw_next = j + 1 < w.it.raw_tiles;
-                    if (ok && lane < ROWS / min(1 << (raw_next ? p.raw : p.comp).page_log, ROWS)) {
-                        const CUtensorMap *m = raw_next ? &raw_map : &comp_map;
-                        for (int c = 0; c < S::DC; c++) prefetch_2d(m, 64 * c, y_next);
-                    }
+                    next = box_of(j + 1);
+                    if (ok && next.there)
+                        for (int c = 0; c < S::DC; c++) prefetch_2d(next.map, 64 * c, next.y);
                 }
-                const uint32_t miss = __ballot_sync(0xffffffffu, missing);
+                const uint32_t miss = __ballot_sync(0xffffffffu, box.missing), boxes = __popc(__ballot_sync(0xffffffffu, box.there));
                 if (miss && lane == 0) atomicOr(&g_paged_err, 4u);
                 if (lane == 0) masks[g % MASKS] = miss;         // the slots' previous tile is done with its own
                 for (int b = 0; b < S::DB; b++) {
                     if (S::WIDE) load_q(2 * b, 2);
                     if (ok) ok = warp_wait(empty(unit), ((unit / RING) & 1) ^ 1, abort);
                     if (!ok) continue;
-                    const uint32_t dst = smem_u32(sm + S::OFF_X) + unit % RING * SLOT + lane * box * 128, fb = full(unit);
-                    if (lane == 0) mbar_expect_tx(fb, D == 64 ? CHUNK : SLOT);
+                    const uint32_t dst = smem_u32(sm + S::OFF_X) + unit % RING * SLOT + lane * box.rows * 128, fb = full(unit);
+                    if (lane == 0) mbar_expect_tx(fb, boxes * box.rows * (D == 64 ? 128 : 256));
                     __syncwarp();
-                    if (lane < boxes) {
-                        tma_2d(dst, map, 128 * b, y, fb);
-                        if (D != 64) tma_2d(dst + CHUNK, map, 128 * b + 64, y, fb);
+                    if (box.there) {
+                        tma_2d(dst, box.map, 128 * b, box.y, fb);
+                        if (D != 64) tma_2d(dst + CHUNK, box.map, 128 * b + 64, box.y, fb);
                     }
                     unit++;
                 }
-                if (!w.it.alone && j + 1 < w.te) y_next = box_of(j + 1, missing_next);
+                if (!w.it.alone && j + 1 < w.te) next = box_of(j + 1);
             }
         }
         // what was issued lands before the CTA exits, whichever warp gave up
@@ -750,7 +753,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             if (!S::WIDE && last) q_seen++;
             g++;
         };
-        auto do_o = [&](uint32_t go, bool first) {
+        auto do_o = [&](uint32_t go, int tile, bool first) {
+            const int steps = WIN ? min(w.it.raws + w.it.comps - tile * PIECES, PIECES) : PIECES;   // pieces of the tile
             if (ok) ok = warp_wait(bar(B_PFULL + go % S::NP), go / S::NP & 1, abort);
             if (first && ok && items > 0) ok = warp_wait(bar(B_OFREE), (items - 1) & 1, abort);
             if (ok) fence_after();
@@ -761,7 +765,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 const uint32_t d = held ? tmem + S::T_S : tmem + S::T_O + b * N, acc = first || held ? 0u : 1u;
                 if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < 8; k++) mma(d, x + k * 128, pr + k * 128, ID_O, k > 0 ? 1u : acc);
+                    for (int k = 0; k < PIECES; k++)
+                        if (!WIN || k < steps) mma(d, x + k * 128, pr + k * 128, ID_O, k > 0 ? 1u : acc);
                     commit(empty(unit_o));
                     if (held) commit(bar(B_HELD));
                     if (b == S::DB - 1) commit(bar(B_PVDONE + go % S::NP));
@@ -775,7 +780,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             do_s(true, n == 1);
             for (int j = 0; j < n; j++) {
                 if (S::AHEAD && j + 1 < n) do_s(false, j + 2 == n);
-                do_o(S::AHEAD && j + 1 < n ? g - 2 : g - 1, j == 0);
+                do_o(S::AHEAD && j + 1 < n ? g - 2 : g - 1, w.tb + j, j == 0);
                 if (!S::AHEAD && j + 1 < n) do_s(false, j + 2 == n);
             }
             items++;
@@ -802,7 +807,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         uint32_t g = 0, items = 0;
         while (w.next()) {
             const int n_cols = w.it.n_tok * p.hg, mine = min(max(n_cols - col0, 0), C);   // this group's columns in use
-            const long long t0 = w.it.t0;
+            const int t0 = w.it.t0;
+            // compressed rows that all, and that some of its tokens see
+            const int comp_all = p.ratio && t0 >= 0 ? (t0 + 1) / p.ratio : 0, comp_some = p.ratio ? max(t0 + w.it.n_tok, 0) / p.ratio : 0;
             // denominators of this row; the first d-block of O, as tmem_ld_16x32 gives it, the warp's lower 16 rows first
             float l[C], held[S::HELD ? C : 1];
 #pragma unroll
@@ -817,23 +824,32 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             for (int j = w.tb; j < w.te; j++, g++) {
                 const uint32_t sb = g % S::NS;
                 // columns [ca, cb) see this thread's row; is_full: all of the tile's rows by all columns
-                const bool raw = j < w.it.raw_tiles;
-                const long long base = (long long)(raw ? w.it.raw_tile0 + j : j - w.it.raw_tiles) * ROWS, row = base + r;
-                bool is_full = raw ? base + ROWS - 1 <= t0 && (!p.window || base + p.window >= t0 + w.it.n_tok)
-                                   : (base + ROWS) * p.ratio - 1 <= t0;
+                const int q0 = j * PIECES, q = q0 + r / PIECE;
+                const bool raw = WIN ? q < w.it.raws : q0 < w.it.raws;
+                const int row = (raw ? w.it.raw0 + PIECE * q0 : PIECE * (q0 - w.it.raws)) + r;
+                bool is_full;
+                if (WIN) {
+                    const int raw_base = w.it.raw0 + PIECE * q0;
+                    is_full = q0 + PIECES <= w.it.raws ? raw_base + ROWS - 1 <= t0 && raw_base + p.window >= t0 + w.it.n_tok
+                                                       : q0 >= w.it.raws && PIECE * (q0 + PIECES - w.it.raws) <= comp_all;
+                } else {
+                    is_full = raw ? PIECE * q0 + ROWS - 1 <= t0 : PIECE * (q0 + PIECES - w.it.raws) <= comp_all;
+                }
                 int ca = -col0, cb = n_cols - col0;
                 if (!is_full) {
-                    const long long a = raw ? row - t0 : (row + 1) * p.ratio - 1 - t0, n = w.it.n_tok;
-                    const long long e = raw && p.window ? min(n, row + p.window - t0) : n;
-                    ca = (int)min(max(a, 0ll), n) * p.hg - col0;
-                    cb = (int)max(e, 0ll) * p.hg - col0;
+                    // the first and the last token + 1 that see the row
+                    const int n = w.it.n_tok;
+                    const int from = raw ? max(row - t0, 0) : row < comp_all ? 0 : row < comp_some ? (int)((long long)(row + 1) * p.ratio - 1 - t0) : n;
+                    const int to = WIN && raw ? min(n, row - t0 + p.window) : n;
+                    ca = min(from, n) * p.hg - col0;
+                    cb = !WIN || q < w.it.raws + w.it.comps ? max(to, 0) * p.hg - col0 : ca;
                 }
                 if (ok) ok = warp_wait(bar(B_SFULL + sb), (g / S::NS) & 1, abort);
                 fence_after();
                 const uint32_t miss = masks[g % MASKS];
                 if (miss) {
                     is_full = false;
-                    if ((miss >> (r >> min((raw ? p.raw : p.comp).page_log, 7))) & 1) cb = ca;
+                    if ((miss >> (r >> (WIN ? 4 : min((raw ? p.raw : p.comp).page_log, 7)))) & 1) cb = ca;
                 }
                 // BL columns at a time: their logits from TMEM, those that are not seen to -infinity.  All columns at once
                 // where the registers are not needed for O: the logits then stay in them for the second pass.
@@ -1205,9 +1221,9 @@ bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool pool_map(CUtensorMap *m, const ds4c_page_pool &a, uint32_t d) {
+bool pool_map(CUtensorMap *m, const ds4c_page_pool &a, uint32_t d, bool pieces) {
     const cuuint64_t dims[2] = {d, (cuuint64_t)a.n_pages * a.page_rows}, strides[1] = {(cuuint64_t)d * 2};
-    const cuuint32_t box[2] = {64, a.page_rows < ROWS ? a.page_rows : ROWS};
+    const cuuint32_t box[2] = {64, pieces ? (cuuint32_t)PIECE : a.page_rows < ROWS ? a.page_rows : ROWS};
     return make_map(m, a.rows, 2, dims, strides, box);
 }
 Pool pool_of(const ds4c_page_pool &a) {
@@ -1247,7 +1263,7 @@ size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_hea
     return at;
 }
 
-template <int D, bool WIDE = false>
+template <int D, bool WIDE, bool WIN>
 cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream_t s) {
     using S = Shape<D, WIDE>;
     p.over = S::OVER;
@@ -1259,15 +1275,15 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
         const cuuint32_t box[3] = {64, (cuuint32_t)p.hg, (cuuint32_t)p.tt};
         if (!make_map(&qm, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    if (!pool_map(&rm, a.raw, D) || !pool_map(&cm, a.ratio ? a.comp : a.raw, D)) return cudaErrorInvalidValue;
-    cudaError_t e = ensure_dyn_smem(paged_attn_kernel<D, WIDE>, S::SMEM);
+    if (!pool_map(&rm, a.raw, D, WIN) || !pool_map(&cm, a.ratio ? a.comp : a.raw, D, WIN)) return cudaErrorInvalidValue;
+    cudaError_t e = ensure_dyn_smem(paged_attn_kernel<D, WIDE, WIN>, S::SMEM);
     if (e != cudaSuccess) return e;
     // a register split above the launch's total would wait for ever
     static std::atomic<int> regs{0};
     int have = regs.load(std::memory_order_relaxed);
     if (have == 0) {
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, paged_attn_kernel<D, WIDE>);
+        e = cudaFuncGetAttributes(&fa, paged_attn_kernel<D, WIDE, WIN>);
         if (e != cudaSuccess) return e;
         regs.store(have = fa.numRegs, std::memory_order_relaxed);
     }
@@ -1278,7 +1294,7 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
         if (e == cudaSuccess) e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), info, s, p, grid);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl(paged_attn_kernel<D, WIDE>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
+    e = launch_pdl(paged_attn_kernel<D, WIDE, WIN>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
     if (e != cudaSuccess) return e;
     const int entries = p.small ? (int)a.n_tok * p.groups : grid;
     if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N), dim3(JOIN_THREADS), 0, s, p);
@@ -1308,14 +1324,20 @@ cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStrea
         p.comp_rows = (int)(a.comp.n_pages * a.comp.page_rows);
     }
     p.n_seq = (int)a.n_seq; p.n_tok = (int)a.n_tok; p.n_heads = (int)a.n_heads;
-    p.window = (int)a.window; p.ratio = (int)a.ratio;
+    p.window = a.window >= (uint32_t)MAX_LENGTH ? 0 : (int)a.window;   // as long as any sequence: none
+    p.ratio = (int)a.ratio;
     const bool wide = a.head_dim == 512 && (a.n_heads > 64 || a.n_tok >= WIDE_TOKENS * a.n_seq);
     const Split c = split_of(a.n_heads, a.head_dim, wide);
     p.hg = c.hg; p.groups = c.groups; p.tt = c.tt;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.n_heads, a.head_dim, wide);
-    return a.head_dim == 64 ? launch<64>(a, p, grid, s) : a.head_dim == 128 ? launch<128>(a, p, grid, s)
-         : a.head_dim == 256 ? launch<256>(a, p, grid, s) : wide ? launch<512, true>(a, p, grid, s) : launch<512>(a, p, grid, s);
+    auto run = [&](auto win) {
+        constexpr bool WIN = decltype(win)::value;
+        return a.head_dim == 64 ? launch<64, false, WIN>(a, p, grid, s) : a.head_dim == 128 ? launch<128, false, WIN>(a, p, grid, s)
+             : a.head_dim == 256 ? launch<256, false, WIN>(a, p, grid, s)
+             : wide ? launch<512, true, WIN>(a, p, grid, s) : launch<512, false, WIN>(a, p, grid, s);
+    };
+    return p.window ? run(std::true_type{}) : run(std::false_type{});
 }
 
 cudaError_t paged_attn_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_paged_wait_ns, &ns, sizeof ns); }

@@ -414,7 +414,8 @@ DS4C_API ds4c_status ds4c_rotate_heads(const ds4c_rotate_args *args, cudaStream_
  * Only rows that some token of the call sees are waited for to hold numbers: pages behind a sequence's end or before its
  * windows may hold anything and need not be listed (-1).  A row that is no number somewhere makes NaN the outputs of the tokens that
  * see it, and of no other.  A page outside 0 .. n_pages - 1 or past max_pages where a visible row should be, and a
- * start that falls or leaves 0 .. n_tok, raise the device error word; such rows and tokens count as not there.
+ * start that falls or leaves 0 .. n_tok, or a length above 2^30, raise the device error word; such rows, and the tokens of
+ * such sequences, count as not there.
  *
  * n_heads 1 .. 128, head_dim 64, 128, 256 or 512, n_seq <= 4096, n_tok <= 2^20, n_pages * page_rows <= 2^31 - 1, 0 < scale <= 1e4.
  * The workspace (ds4c_paged_attn_workspace_bytes, of the device the call runs on; 256-byte aligned) belongs to one call

@@ -55,7 +55,7 @@ constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
 constexpr int FEW_ITEMS = 64;                                       // joined by a block for each column
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
 constexpr uint32_t WIDE_TOKENS = 4;                                 // new tokens a sequence, from which items are wide
-constexpr int MIN_COST = 2;                                         // a CTA's share, in tiles, where there is little work
+constexpr int MIN_COST = 1;                                         // a CTA's share, in tiles, where there is little work
 
 // WIDE: 128 columns at head_dim 512.  O then has 512 columns of its own, all that TMEM has, so the first 128 of d
 // are kept in the softmax warps' registers: S and that block of the second product take turns in the same 128
@@ -110,7 +110,7 @@ struct Item {
 };
 struct Start { int item, y; };
 // The parts of a divided item: the second of CTA `cta`, then the first of the n - 1 CTAs behind it.
-struct Parts { int item, cta, n; };
+struct Parts { int cta, n, tok0, cols, head0; };
 struct Totals { long long cost; int items, ctas; };
 // Workspace: totals, each CTA's first item and place in it, the parts of an item (by item where each CTA cuts for
 // itself, else by the CTA that starts it), the items, the parts.
@@ -520,9 +520,10 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
         const int tiles = tiles_of(it), tb = a > here ? tiles_before((int)(a - here), tiles, p.over) : 0,
                   te = b < end ? tiles_before((int)max(b - here, 0ll), tiles, p.over) : tiles;
         if (a < end && b > here && tb == 0 && (te > 0 || tiles == 0))
-            p.plan.parts[tid] = {tid, cta, te < tiles ? (int)((end * ctas - 1) / all) - cta + 1 : 1};
+            p.plan.parts[tid] = {cta, te < tiles ? (int)((end * ctas - 1) / all) - cta + 1 : 1, it.tok0, it.n_tok * p.hg, it.head0};
     }
-    if (cta == 0 && tid == 0) *p.plan.totals = out->t;
+    // entries that no item has are joined from nothing
+    if (cta == 0 && tid >= n_items && tid < most) p.plan.parts[tid] = {0, 0, 0, 0, 0};
     __syncthreads();
     return *out;
 }
@@ -621,14 +622,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         from = p.plan.start[blockIdx.x];
         to = p.plan.start[blockIdx.x + 1];
         if (threadIdx.x == 0) {
-            Parts parts{0, (int)blockIdx.x, 0};
+            Parts parts{(int)blockIdx.x, 0, 0, 0, 0};
             const Totals t = *p.plan.totals;
             if (to.y > 0) {
-                const int tiles = tiles_of(p.plan.items[to.item]), te = tiles_before(to.y, tiles, p.over);
+                const Item it = p.plan.items[to.item];
+                const int tiles = tiles_of(it), te = tiles_before(to.y, tiles, p.over);
                 if (te > 0 && te < tiles && !(from.item == to.item && tiles_before(from.y, tiles, p.over) > 0)) {
                     const long long end = t.cost * (blockIdx.x + 1) / t.ctas - to.y + p.over + tiles;
-                    parts.item = to.item;
-                    parts.n = (int)((end * t.ctas - 1) / t.cost) - (int)blockIdx.x + 1;
+                    parts = {(int)blockIdx.x, (int)((end * t.ctas - 1) / t.cost) - (int)blockIdx.x + 1, it.tok0, it.n_tok * p.hg, it.head0};
                 }
             }
             p.plan.parts[blockIdx.x] = parts;
@@ -1049,7 +1050,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             }
             // Output, 32 columns of a d-block at a time: pairs of columns from TMEM, whole items scaled, rounded and turned
             // through 2 KB of shared memory (16-byte units of a row swapped by its number, so that no bank meets twice), so that
-            // four lanes store 64 bytes of a head; divided items as they are.
+            // four lanes store 64 bytes of a head.
             const uint32_t turn = smem_u32(sm + S::OFF_TURN) + (S::OWN_TURN ? grp * 8192 : grp * CHUNK) + q4 * 2048;
             const uint8_t *turned = sm + S::OFF_TURN + (S::OWN_TURN ? grp * 8192 : grp * CHUNK) + q4 * 2048;
 #pragma unroll
@@ -1065,18 +1066,30 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     dst[k] = c0 + 8 * k + lane / 4 < mine && h < p.n_heads
                                  ? p.out + (w.it.tok0 + c / p.hg) * p.out_token + h * p.out_head + 32 * q4 + 8 * (lane % 4) : nullptr;
                 }
-                auto put = [&](const float *v, int b) {         // v: 16 values of the lower 16 rows, 16 of the upper
-                    if (!whole) {
-                        float *o = p.plan.part_o + (part * N + col0 + c0) * D + 128 * b + 32 * q4 + lane / 4;
+                if (!whole) {                                   // as they are, a line of a column's d to a store
+                    float *o = p.plan.part_o + (part * N + col0 + c0) * D + 32 * q4;
+                    if constexpr (S::HELD > 0) {
 #pragma unroll
                         for (int half = 0; half < 2; half++)
 #pragma unroll
                             for (int i = 0; i < 16; i++) {
                                 const int c = 8 * (i / 4) + 2 * (lane % 4) + i % 2;
-                                if (c0 + c < mine) o[c * D + 16 * half + 8 * (i / 2 % 2)] = v[16 * half + i];
+                                if (c0 + c < mine) o[c * D + 16 * half + 8 * (i / 2 % 2) + lane / 4] = held[half * (C / 2) + c0 / 2 + i];
                             }
-                        return;
                     }
+#pragma unroll 1
+                    for (int b = S::HELD; b < S::DB; b++) {
+                        float v[32];
+                        tmem_ld32(lane_base + S::T_O + b * N + col0 + c0, v);
+                        ld_wait();
+                        float *x = o + 128 * b + lane;
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (c0 + c < mine) x[c * D] = v[c];
+                    }
+                    continue;
+                }
+                auto put = [&](const float *v, int b) {         // v: 16 values of the lower 16 rows, 16 of the upper
                     __syncwarp();                               // the rows before have been read
 #pragma unroll
                     for (int half = 0; half < 2; half++)
@@ -1131,39 +1144,39 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
 }
 
-// Joins the parts of the divided items.  Few items (FEW), perhaps many parts: a block for each item and column, whose
-// threads share the parts; else, mostly two or three parts: a thread takes all parts of its values.
+// Joins the parts of the divided items.  Few items (FEW), perhaps many parts: a block for each item, column and 128 of
+// d, whose threads share the parts; else, mostly two or three parts: a thread takes all parts of its values.
 template <int D, bool WIDE, bool FEW>
 __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
-    constexpr int N = Shape<D, WIDE>::N, LANES = D / 4;              // threads of a column, four values each
+    constexpr int N = Shape<D, WIDE>::N, SLICE = FEW && D > 128 ? 128 : D, SLICES = D / SLICE;
+    constexpr int LANES = SLICE / 4;                           // threads of a column, four values each
     constexpr int COLS = FEW ? 1 : JOIN_THREADS / LANES, GROUPS = JOIN_THREADS / LANES / COLS;
     __shared__ float weight[FEW ? MAX_GRID : 1], denom[FEW ? MAX_GRID : 1];
-    __shared__ __align__(16) float sums[FEW ? GROUPS : 1][D];
+    __shared__ __align__(16) float sums[FEW ? GROUPS : 1][SLICE];
     pdl_wait();
     pdl_launch_dependents();
-    const int entry = blockIdx.x / (N / COLS), lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-    if (p.small && entry >= p.plan.totals->items) return;
-    const Parts parts = p.plan.parts[entry];
-    const int n = parts.n;
-    if (n < 2) return;
-    const Item it = p.plan.items[parts.item];
-    const int col = blockIdx.x % (N / COLS) * COLS + (FEW ? 0 : grp);
-    if (col >= it.n_tok * p.hg || it.head0 + col % p.hg >= p.n_heads) return;
+    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, slice = blockIdx.x % SLICES, at = blockIdx.x / SLICES;
+    const Parts parts = p.plan.parts[at / (N / COLS)];
+    const int n = parts.n, col = at % (N / COLS) * COLS + (FEW ? 0 : grp);
+    if (n < 2 || col >= parts.cols || parts.head0 + col % p.hg >= p.n_heads) return;
     // part 0 lies alone, the others every second place behind it
     const int64_t slot0 = 2 * parts.cta + 1, slot1 = 2 * parts.cta + 2;
-    const float *ml = p.plan.part_ml + col, *o = p.plan.part_o + (int64_t)col * D + 4 * lane;
+    const float *ml = p.plan.part_ml + col, *o = p.plan.part_o + (int64_t)col * D + slice * SLICE + 4 * lane;
     auto m_of = [&](int i) { return ml[(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * 2 * N]; };
     auto l_of = [&](int i) { return ml[(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * 2 * N + N]; };
     float m = NONE, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float *src, float f) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
+    auto add = [&](const float4 &v, float f) {
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
         acc.w = fmaf(f, v.w, acc.w);
     };
     if (FEW) {
+        // the first parts' values are on their way while the weights are formed
+        const float *src = o + (grp == 0 ? slot0 : slot1 + 2 * (grp - 1)) * N * D;
+        float4 first = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (grp < n) first = *reinterpret_cast<const float4 *>(src);
         for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
             weight[i] = m_of(i);
             denom[i] = l_of(i);
@@ -1171,10 +1184,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
         __syncthreads();
         for (int i = 0; i < n; i++) m = fmaxf(m, weight[i]);
         for (int i = 0; i < n; i++) den = fmaf(ex2(weight[i] - m), denom[i], den);
-        if (grp == 0) add(o + slot0 * N * D, ex2(weight[0] - m));
-        const float *src = o + (slot1 + 2 * grp) * N * D;
+        if (grp < n) add(first, ex2(weight[grp] - m));
+        src = o + (slot1 + 2 * (grp + GROUPS - 1)) * N * D;
 #pragma unroll 4
-        for (int i = 1 + grp; i < n; i += GROUPS, src += (int64_t)2 * GROUPS * N * D) add(src, ex2(weight[i] - m));
+        for (int i = grp + GROUPS; i < n; i += GROUPS, src += (int64_t)2 * GROUPS * N * D)
+            add(*reinterpret_cast<const float4 *>(src), ex2(weight[i] - m));
         *reinterpret_cast<float4 *>(&sums[grp][4 * lane]) = acc;
         __syncthreads();
         if (grp > 0) return;
@@ -1185,18 +1199,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
     } else {
         for (int i = 0; i < n; i++) m = fmaxf(m, m_of(i));
         const float *src = o + slot1 * N * D;
-        add(o + slot0 * N * D, ex2(m_of(0) - m));
+        add(*reinterpret_cast<const float4 *>(o + slot0 * N * D), ex2(m_of(0) - m));
         den = ex2(m_of(0) - m) * l_of(0);
         for (int i = 1; i < n; i++, src += (int64_t)2 * N * D) {
             const float f = ex2(m_of(i) - m);
-            add(src, f);
+            add(*reinterpret_cast<const float4 *>(src), f);
             den = fmaf(f, l_of(i), den);
         }
     }
     const float inv = den == 0.f ? 0.f : 1.0f / den;
     if (den == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t at = (it.tok0 + col / p.hg) * p.out_token + (it.head0 + col % p.hg) * p.out_head + 4 * lane;
-    *reinterpret_cast<uint2 *>(p.out + at) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
+    const int64_t to = (parts.tok0 + col / p.hg) * p.out_token + (parts.head0 + col % p.hg) * p.out_head + slice * SLICE + 4 * lane;
+    *reinterpret_cast<uint2 *>(p.out + to) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
 }
 
 // ---- host --------------------------------------------------------------------------------------
@@ -1297,7 +1311,7 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
     e = launch_pdl(paged_attn_kernel<D, WIDE, WIN>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
     if (e != cudaSuccess) return e;
     const int entries = p.small ? (int)a.n_tok * p.groups : grid;
-    if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N), dim3(JOIN_THREADS), 0, s, p);
+    if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N * (D > 128 ? D / 128 : 1)), dim3(JOIN_THREADS), 0, s, p);
     return launch_pdl(paged_join_kernel<D, WIDE, false>, dim3(entries * (S::N / (JOIN_THREADS / (D / 4)))), dim3(JOIN_THREADS), 0, s, p);
 }
 

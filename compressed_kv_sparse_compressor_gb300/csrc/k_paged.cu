@@ -50,7 +50,8 @@ constexpr int MASKS = 8;                                            // tiles who
 constexpr float TAU = 8.0f;
 constexpr float NONE = -3.0e38f;                                    // reference of a column that saw nothing yet
 constexpr int PLAN_THREADS = 1024;
-constexpr int SMALL = THREADS;                                      // items and sequences that each CTA cuts for itself
+constexpr int SMALL = THREADS;                                      // sequences up to which each CTA cuts for itself,
+constexpr int SMALL_ITEMS = 8 * SMALL;                              // and items
 constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
 constexpr int FEW_ITEMS = 64;                                       // joined by a block for each column
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
@@ -112,12 +113,12 @@ struct Start { int item, y; };
 // The parts of a divided item: the second of CTA `cta`, then the first of the n - 1 CTAs behind it.
 struct Parts { int cta, n, tok0, cols, head0; };
 struct Totals { long long cost; int items, ctas; };
-// Workspace: totals, each CTA's first item and place in it, the parts of an item (by item where each CTA cuts for
-// itself, else by the CTA that starts it), the items, the parts.
+// Workspace: totals, each CTA's first item and place in it, the parts of an item (by item if there are few, else by the
+// CTA that has its first tile), the items, the parts.
 struct Plan {
     Totals *totals;
     Start *start;              // [grid + 1]
-    Parts *parts;              // [max(grid, SMALL)]
+    Parts *parts;              // [max(grid, FEW_ITEMS)]
     Item *items;
     float *part_o;             // [2 grid][N][D]
     float *part_ml;            // [2 grid][2][N]
@@ -131,7 +132,7 @@ struct Params {
     int n_seq, n_tok, n_heads, window, ratio;
     int hg, tt, groups;        // heads and tokens of an item, head groups
     int over;                  // an item's start and end, in tiles
-    int small;                 // each CTA cuts for itself
+    int small, by_item;        // each CTA cuts for itself; parts lie by items
     float scale_log2;
     Plan plan;
 };
@@ -335,15 +336,14 @@ constexpr int MAX_LENGTH = 1 << 30;
 constexpr int PIECE = 16, PIECES = ROWS / PIECE;               // a tile is 8 pieces of 16 rows, one K step of the second product each
 __device__ __forceinline__ int tiles_of(const Item &it) { return (it.raws + it.comps + PIECES - 1) / PIECES; }
 
-// Item k of a sequence of n new tokens from token b on, `length` long with them.
-__device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n, int length, int k) {
+// The item of tokens j .. and head group g of a sequence of n new tokens from token b on, `length` long with them.
+__device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n, int length, int j, int g) {
     Item it;
-    const int j = k / p.groups * p.tt;
     it.seq = seq;
     it.tok0 = b + j;
     it.n_tok = min(p.tt, n - j);
-    it.head0 = k % p.groups * p.hg;
-    it.alone = n <= p.tt && k == 0;
+    it.head0 = g * p.hg;
+    it.alone = n <= p.tt && g == 0;
     // positions t0 .. end - 1; a token before 0 sees nothing wherever it is
     it.t0 = max(length, 0) - n + j;
     const int end = it.t0 + it.n_tok;
@@ -379,6 +379,24 @@ __device__ __forceinline__ int last_at_most(const T *v, int n, T x) {
 }
 __device__ __forceinline__ int ctas_of(long long cost, int grid) {
     return (int)max(1ll, min((long long)grid, cost / MIN_COST));
+}
+// Items from `from` on, one behind the other; first, begin, length: the sequences' first item, start (and the end) and
+// length.  visit(number, item) until it returns false or `to` is reached.
+template <typename Visit>
+__device__ __forceinline__ void walk_items(const Params &p, const int *first, const int *begin, const int *length, int from, int to, Visit visit) {
+    if (from >= to) return;
+    int s = last_at_most(first, p.n_seq, from), k = from - first[s];
+    int j = k / p.groups * p.tt, g = k % p.groups;
+    for (int i = from; i < to; i++) {
+        if (!visit(i, make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], j, g))) return;
+        if (++g < p.groups) continue;
+        g = 0;
+        j += p.tt;
+        if (s + 1 < p.n_seq && first[s + 1] <= i + 1) {
+            j = 0;
+            while (s + 1 < p.n_seq && first[s + 1] <= i + 1) s++;
+        }
+    }
 }
 
 // Sum over the block's threads before this one and its own; sums: a value for each warp.
@@ -436,15 +454,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
     // each thread's items, one behind the other
     const int each = (n_items + PLAN_THREADS - 1) / PLAN_THREADS;
-    auto walk = [&](int thread, auto visit) {                  // visit(item number, item) until it returns false
-        const int from = min(thread * each, n_items), to = min(from + each, n_items);
-        if (from >= to) return;
-        int s = last_at_most(first, p.n_seq, from);
-        for (int i = from; i < to; i++) {
-            while (s + 1 < p.n_seq && first[s + 1] <= i) s++;
-            if (!visit(i, make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], i - first[s]))) return;
-        }
-    };
+    auto walk = [&](int thread, auto visit) { walk_items(p, first, begin, length, thread * each, min(thread * each + each, n_items), visit); };
     long long cost = 0;
     walk(tid, [&](int i, const Item &it) {
         p.plan.items[i] = it;
@@ -474,13 +484,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     if (tid == 0) *p.plan.totals = {all, n_items, ctas};
 }
 
-// Few items: every CTA makes them all, one to a thread, and finds its own cuts.  Writes the items that it has
-// something of.  scratch: SMALL_SCRATCH bytes of shared memory, 16-byte aligned.
+// Few items: every CTA weighs them all and finds its own cuts.  Writes the items that it has something of, and who has the
+// parts of those it starts.  scratch: SMALL_SCRATCH bytes of shared memory, 16-byte aligned.
 constexpr int SMALL_SCRATCH = 3 * 4 * (SMALL + 4) + 16 * (SMALL / 32) + 64;
-struct Cuts { Start from, to; Totals t; };
+struct Cuts { Start from, to; };
 __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
     Cuts *out = reinterpret_cast<Cuts *>(scratch);
-    static_assert(sizeof(Cuts) <= 32, "scratch");
     long long *sums_l = reinterpret_cast<long long *>(scratch + 32);
     int *sums_i = reinterpret_cast<int *>(sums_l + SMALL / 32);
     int *first = sums_i + SMALL / 32, *begin = first + SMALL, *length = begin + SMALL + 1;
@@ -495,35 +504,49 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
     }
     int carry;
     const int incl = block_scan<SMALL, int>(k, sums_i, carry);
-    first[tid] = tid < p.n_seq ? incl - k : 0x7fffffff;
+    if (tid < p.n_seq) first[tid] = incl - k;
     __syncthreads();
     const int most = p.n_tok * p.groups, n_items = min(carry, most);
     if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
-    Item it{};
-    int cost = 0;
-    if (tid < n_items) {
-        const int s = last_at_most(first, p.n_seq, tid);
-        it = make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], tid - first[s]);
-        cost = p.over + tiles_of(it);
-    }
+    const int each = (n_items + SMALL - 1) / SMALL, i0 = tid * each, i1 = min(i0 + each, n_items);
+    long long cost = 0;
+    walk_items(p, first, begin, length, i0, i1, [&](int, const Item &it) {
+        cost += p.over + tiles_of(it);
+        return true;
+    });
     long long all;
     const long long end = block_scan<SMALL, long long>(cost, sums_l, all), here = end - cost;
     const int ctas = n_items ? ctas_of(all, grid) : 0;
-    if (tid == 0) *out = {{n_items, 0}, {n_items, 0}, {all, n_items, ctas}};
+    if (tid == 0) *out = {{n_items, 0}, {n_items, 0}};
+    if (!p.by_item && tid == 0) p.plan.parts[cta] = {cta, 0, 0, 0, 0};
+    if (p.by_item && cta == 0 && tid >= n_items && tid < most) p.plan.parts[tid] = {0, 0, 0, 0, 0};   // entries of no item
     __syncthreads();
-    if (tid < n_items && cta < ctas) {
-        const long long a = all * cta / ctas, b = all * (cta + 1) / ctas;
-        if (here <= a && a < end) out->from = {tid, (int)(a - here)};
-        if (cta + 1 < ctas && here <= b && b < end) out->to = {tid, (int)(b - here)};
-        if (a < end && b > here) p.plan.items[tid] = it;
-        // the CTA that has the item's first tile says who has the others
-        const int tiles = tiles_of(it), tb = a > here ? tiles_before((int)(a - here), tiles, p.over) : 0,
-                  te = b < end ? tiles_before((int)max(b - here, 0ll), tiles, p.over) : tiles;
-        if (a < end && b > here && tb == 0 && (te > 0 || tiles == 0))
-            p.plan.parts[tid] = {cta, te < tiles ? (int)((end * ctas - 1) / all) - cta + 1 : 1, it.tok0, it.n_tok * p.hg, it.head0};
+    if (cta < ctas) {
+        const long long a = all * cta / ctas, b = all * (cta + 1) / ctas;      // this CTA's share: the places a .. b - 1
+        if (a < end && b > here) {
+            long long at = here;
+            walk_items(p, first, begin, length, i0, i1, [&](int i, const Item &it) {
+                const int tiles = tiles_of(it);
+                const long long next = at + p.over + tiles;
+                if (a >= at && a < next) out->from = {i, (int)(a - at)};
+                if (b >= at && b < next) out->to = {i, (int)(b - at)};
+                if (a < next && b > at) {
+                    p.plan.items[i] = it;
+                    // the CTA that has the item's first tile says who has the others
+                    const int tb = a > at ? tiles_before((int)(a - at), tiles, p.over) : 0;
+                    const int te = b < next ? tiles_before((int)(b - at), tiles, p.over) : tiles;
+                    const bool divided = tb == 0 && te > 0 && te < tiles;
+                    if (divided || (p.by_item && tb == 0 && (te > 0 || tiles == 0)))
+                        p.plan.parts[p.by_item ? i : cta] = {cta, divided ? (int)((next * ctas - 1) / all) - cta + 1 : 1, it.tok0,
+                                                             it.n_tok * p.hg, it.head0};
+                }
+                at = next;
+                return at <= b;                                 // the item that starts at b too
+            });
+        }
+        // a cut at the very start of the next thread's items is that item's place 0
+        if (b == end && b < all && i1 > i0) out->to = {i1, 0};
     }
-    // entries that no item has are joined from nothing
-    if (cta == 0 && tid >= n_items && tid < most) p.plan.parts[tid] = {0, 0, 0, 0, 0};
     __syncthreads();
     return *out;
 }
@@ -1269,7 +1292,7 @@ size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_hea
     Plan o;
     o.totals = reinterpret_cast<Totals *>(region(sizeof(Totals)));
     o.start = reinterpret_cast<Start *>(region(sizeof(Start) * (grid + 1)));
-    o.parts = reinterpret_cast<Parts *>(region(sizeof(Parts) * (grid > SMALL ? grid : SMALL)));
+    o.parts = reinterpret_cast<Parts *>(region(sizeof(Parts) * (grid > FEW_ITEMS ? grid : FEW_ITEMS)));
     o.items = reinterpret_cast<Item *>(region(sizeof(Item) * (size_t)n_tok * c.groups));
     o.part_ml = reinterpret_cast<float *>(region((size_t)2 * grid * 2 * c.n * 4));
     o.part_o = reinterpret_cast<float *>(region((size_t)2 * grid * c.n * d * 4));
@@ -1281,7 +1304,10 @@ template <int D, bool WIDE, bool WIN>
 cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream_t s) {
     using S = Shape<D, WIDE>;
     p.over = S::OVER;
-    p.small = a.n_seq <= SMALL && (uint64_t)a.n_tok * p.groups <= SMALL;
+    const uint64_t whole = a.n_tok / (uint32_t)p.tt + a.n_seq;    // items of a head group, at most; none is without a token
+    const uint64_t items = (whole < a.n_tok ? whole : a.n_tok) * p.groups;
+    p.small = a.n_seq <= SMALL && items <= SMALL_ITEMS;
+    p.by_item = p.small && items <= FEW_ITEMS;
     CUtensorMap qm, rm, cm;
     {
         const cuuint64_t dims[3] = {D, a.n_heads, a.n_tok};
@@ -1310,8 +1336,8 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
     }
     e = launch_pdl(paged_attn_kernel<D, WIDE, WIN>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
     if (e != cudaSuccess) return e;
-    const int entries = p.small ? (int)a.n_tok * p.groups : grid;
-    if (entries <= FEW_ITEMS) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N * (D > 128 ? D / 128 : 1)), dim3(JOIN_THREADS), 0, s, p);
+    const int entries = p.by_item ? (int)items : grid;
+    if (p.by_item) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N * (D > 128 ? D / 128 : 1)), dim3(JOIN_THREADS), 0, s, p);
     return launch_pdl(paged_join_kernel<D, WIDE, false>, dim3(entries * (S::N / (JOIN_THREADS / (D / 4)))), dim3(JOIN_THREADS), 0, s, p);
 }
 

@@ -311,3 +311,31 @@ def test_rows_written_read_and_turned_back():
         heads_ref.assert_close(back, *heads_ref.turned(o.double(), pos, theta, d - rot, False, True))
         done = [m for _, m in seqs]
     assert done == total
+
+
+@pytest.mark.parametrize("h,d", [(64, 512), (128, 512), (8, 128)])
+def test_many_sequences_and_many_items(h, d):
+    """Batches whose items one block makes for all CTAs: more sequences, and more items, than a CTA weighs for itself."""
+    g = gen(20)
+    seqs = [(b % 3 if b % 7 else 5, 0) for b in range(450)]
+    seqs = [(n, n + int(torch.randint(0, 400, (1,), generator=g, device="cuda"))) for n, _ in seqs]
+    check(*setup(g, h, d, 32, seqs, 64 if h == 128 else 0, 4 if h == 64 else 0, tail=2), seqs)
+    seqs = [(1700, 1900), (1, 3000)] if h == 128 else [(7000, 7100), (3, 900)] if h == 64 else [(30000, 30000)]
+    q, a, kw = setup(g, h, d, 128, seqs, 100)
+    out = paged.attention(q, **a, **kw)
+    fp8.sync()
+    rest = {k: v for k, v in a.items() if k not in ("start", "length")}
+    n = seqs[0][0]
+    for i in (0, 1, n // 2, n - 1):                              # single tokens of the long one, as a sequence that ends there
+        t = seqs[0][1] - n + i
+        want, size = ref.attention(q[i:i + 1], rest["cache"], rest["pages"][:1], [(1, t + 1)], **kw)
+        ref.assert_close(out[i:i + 1], want, size)
+
+
+def test_few_tokens_each():
+    """Sequences of one to three new tokens: items of 64 columns at head_dim 512, several tokens in one with few heads."""
+    for h in (8, 24, 32, 33, 64):
+        g = gen(21 + h)
+        seqs = [(1 + b % 3, 3 + 97 * b) for b in range(12)]
+        check(*setup(g, h, 512, 64, seqs, 0, 16), seqs)
+        check(*setup(g, h, 512, 64, seqs, 130, 0), seqs)

@@ -12,6 +12,7 @@ Calls run on the current stream of the tensors' device.  A slot behind the cache
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 import torch
 
@@ -47,7 +48,7 @@ def turns(n_rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, 
     status, m = abi.ds4c_rope_table(abi.RopeParams(n_rot, _SCALINGS[scaling], base, factor, original, beta_fast, beta_slow,
                                                    magnitude), host)
     abi.check(status, "ds4c_rope_table")
-    return torch.tensor(list(host), dtype=torch.int64), m
+    return torch.frombuffer(host, dtype=torch.int64).clone(), m
 
 
 def table(n_rot: int, base: float = 10000.0, *, scaling=None, factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0,
@@ -58,14 +59,23 @@ def table(n_rot: int, base: float = 10000.0, *, scaling=None, factor: float = 1.
     return Table(t.to(device), m)
 
 
+# A call's arguments as the ABI's struct lays them out: packed at once they take a quarter of the time of its fields
+# set one by one.
+_pack = struct.Struct("8I2f2P" + 2 * "2P4N2PQ2I").pack
+_NO_ROWS = (0,) * 11
+
+
 def _rows(t, what):
     """(n, heads, d, token stride, head stride) of rows of heads; a stride that no step uses is 0."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) == 3:
         n, heads, d = shape
-        st, sh, sd = stride
+        st, sh, sd = t.stride()
     elif len(shape) == 2:
-        (n, d), (st, sd), heads, sh = shape, stride, 1, 0
+        n, d = shape
+        st, sd = t.stride()
+        heads = 1
+        sh = 0
     else:
         raise ValueError(f"{what}: {tuple(shape)}, expected (tokens, heads, d) or (tokens, d)")
     if sd != 1 and d > 1:
@@ -74,43 +84,40 @@ def _rows(t, what):
 
 
 def _side(x, out, gain, n, d, dev, what):
-    """HeadRows of x -> out (the same shape, float32 or bfloat16)."""
+    """The struct's fields for x -> out (the same shape, float32 or bfloat16)."""
     xn, heads, xd, xt, xh = _rows(x, what)
     if xn != n or xd != d or x.get_device() != dev:
         raise ValueError(f"{what}: {tuple(x.shape)} on {x.device}, expected {n} tokens of {d} values on cuda:{dev}")
-    if out is not x:
-        if out.shape != x.shape or out.get_device() != dev or out.dtype not in _DTYPES:
+    dt = _DTYPES.get(out.dtype)
+    if out is x:
+        ot, oh = xt, xh
+    else:
+        if out.shape != x.shape or out.get_device() != dev or dt is None:
             raise ValueError(f"{what}'s output: {out.dtype} {tuple(out.shape)} on {out.device}, expected float32 or bfloat16 "
                              f"{tuple(x.shape)} on cuda:{dev}")
         _, _, _, ot, oh = _rows(out, f"{what}'s output")
-    else:
-        ot, oh = xt, xh
-    return abi.HeadRows(x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, _gain(gain, d, dev, what), None, 0, heads, _DTYPES[out.dtype])
+    return x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, 0 if gain is None else _gain(gain, d, dev, what), 0, 0, heads, dt
 
 
 def _gain(gain, d, dev, what):
-    if gain is None:
-        return None
-    if gain.shape != (d,) or gain.dtype != torch.float32 or gain.get_device() != dev or not gain.is_contiguous():
+    if gain.dtype != torch.float32 or gain.get_device() != dev or gain.shape != (d,) or not gain.is_contiguous():
         raise ValueError(f"gain of {what}: {gain.dtype} {tuple(gain.shape)} on {gain.device}, expected contiguous float32 {(d,)} on "
                          f"cuda:{dev}")
     return gain.data_ptr()
 
 
 def _index(t, n, dev, what):
-    if t.shape != (n,) or t.dtype != torch.int64 or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype != torch.int64 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous int64 {(n,)} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _args(x, positions, table, first, half, inverse, norm, eps):
-    """RotateArgs without its rows."""
-    dt, dev, shape = _DTYPES.get(x.dtype), x.get_device(), x.shape
-    if dt is None or dev < 0:
-        raise ValueError(f"rows: {x.dtype} on {x.device}, expected float32 or bfloat16 on a CUDA device")
-    n, d = shape[0], shape[-1]
-    n_rot, turns, magnitude, pos = 0, None, 1.0, None
-    if table is not None:
+def _run(x, positions, table, first, half, inverse, norm, eps, n, d, dev, q, k):
+    """The call with rows q and k (fields of the struct)."""
+    if table is None:
+        n_rot = turns = pos = 0
+        magnitude = 1.0
+    else:
         if table.device_index != dev:
             raise ValueError(f"table on cuda:{table.device_index}, rows on {x.device}")
         n_rot, turns, magnitude = table.n_rot, table._ptr, table.magnitude
@@ -119,18 +126,26 @@ def _args(x, positions, table, first, half, inverse, norm, eps):
         first = d - n_rot
     if first < 0 or first + n_rot > d:
         raise ValueError(f"values {first} .. {first + n_rot - 1} of rows of {d}")
-    return abi.RotateArgs(n, d, dt, n_rot, first, half, inverse, norm, eps, magnitude, pos, turns), n, d, dev
+    args = abi.RotateArgs.from_buffer_copy(_pack(n, d, _DTYPES[x.dtype], n_rot, first, half, inverse, norm, eps, magnitude, pos, turns, *q, *k))
+    run(dev, abi.ds4c_rotate_heads, args)
+
+
+def _check(x, what):
+    """(tokens, d, device) of rows of heads."""
+    dev, shape = x.get_device(), x.shape
+    if x.dtype not in _DTYPES or dev < 0:
+        raise ValueError(f"{what}: {x.dtype} on {x.device}, expected float32 or bfloat16 on a CUDA device")
+    return shape[0], shape[-1], dev
 
 
 def rotate(x, positions, table: Table, *, first=None, half: bool = False, inverse: bool = False, out=None):
     """x [n, heads, d] with its rotated part turned by positions [n] (int64), by the negative positions if `inverse` (which
     undoes a rotation of magnitude 1 and is the gradient of any).  out: x's shape, float32 or bfloat16, x itself
     allowed; allocated in x's type if None."""
-    a, n, d, dev = _args(x, positions, table, first, half, inverse, 0, 0.0)
+    n, d, dev = _check(x, "x")
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.q = _side(x, out, None, n, d, dev, "x")
-    run(dev, abi.ds4c_rotate_heads, a)
+    _run(x, positions, table, first, half, inverse, 0, 0.0, n, d, dev, _side(x, out, None, n, d, dev, "x"), _NO_ROWS)
     return out
 
 
@@ -142,37 +157,38 @@ def norm_rotate(q, positions, table: Table | None, *, gain=None, k=None, k_gain=
     k [n, k heads, d] (or [n, d]) of q's type takes the same with k_gain, in the same launch.  Its result goes to k_out
     (k's shape, k itself allowed), or to a cache [pages, page rows, d] (one head) or [pages, page rows, k heads, d]:
     token i's rows to slot slots[i] = page * page rows + row (int64; below 0: nowhere)."""
-    a, n, d, dev = _args(q, positions, table, first, half, False, 1, eps)
+    n, d, dev = _check(q, "q")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    a.q = _side(q, out, gain, n, d, dev, "q")
     if k is None:
         if k_out is not None or cache is not None or slots is not None or k_gain is not None:
             raise ValueError("k's output, gain or slots without k")
+        kr = _NO_ROWS
     else:
         if k.dtype != q.dtype:
             raise ValueError(f"k: {k.dtype}, expected q's {q.dtype}")
         if (k_out is None) == (cache is None) or (cache is None) != (slots is None):
             raise ValueError("k needs k_out, or cache and slots")
-        if cache is None:
-            a.k = _side(k, k_out, k_gain, n, d, dev, "k")
-        else:
-            a.k = _cached(k, cache, slots, k_gain, n, d, dev)
-    run(dev, abi.ds4c_rotate_heads, a)
+        kr = _side(k, k_out, k_gain, n, d, dev, "k") if cache is None else _cached(k, cache, slots, k_gain, n, d, dev)
+    _run(q, positions, table, first, half, False, 1, eps, n, d, dev, _side(q, out, gain, n, d, dev, "q"), kr)
     return out
 
 
 def _cached(k, cache, slots, k_gain, n, d, dev):
-    """HeadRows of k -> slots of a cache of pages."""
+    """The struct's fields for k -> slots of a cache of pages."""
     kn, heads, kd, kt, kh = _rows(k, "k")
-    shape, stride = cache.shape, cache.stride()
     if kn != n or kd != d or k.get_device() != dev:
         raise ValueError(f"k: {tuple(k.shape)} on {k.device}, expected {n} tokens of {d} values on cuda:{dev}")
-    if len(shape) not in (3, 4) or shape[-1] != d or (shape[2] if len(shape) == 4 else 1) != heads or cache.dtype not in _DTYPES or \
-            cache.get_device() != dev:
+    shape, dt = cache.shape, _DTYPES.get(cache.dtype)
+    if len(shape) == 3:
+        pages, page, cd = shape
+        ch = 1
+    else:
+        pages, page, ch, cd = shape if len(shape) == 4 else (0, 0, -1, 0)
+    if cd != d or ch != heads or dt is None or cache.get_device() != dev:
         raise ValueError(f"cache: {cache.dtype} {tuple(shape)} on {cache.device}, expected float32 or bfloat16 (pages, page rows, "
                          f"{'' if heads == 1 else f'{heads}, '}{d}) on cuda:{dev}")
     if not cache.is_contiguous():
-        raise ValueError(f"cache: stride {stride}, expected contiguous pages")
-    return abi.HeadRows(k.data_ptr(), cache.data_ptr(), kt, kh, heads * d, d, _gain(k_gain, d, dev, "k"),
-                        _index(slots, n, dev, "slots"), shape[0] * shape[1], heads, _DTYPES[cache.dtype])
+        raise ValueError(f"cache: stride {cache.stride()}, expected contiguous pages")
+    return (k.data_ptr(), cache.data_ptr(), kt, kh, heads * d, d, 0 if k_gain is None else _gain(k_gain, d, dev, "k"),
+            _index(slots, n, dev, "slots"), pages * page, heads, dt)

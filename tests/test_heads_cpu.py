@@ -100,3 +100,10 @@ def test_python_refusals():
         rope.rotate(x, torch.arange(4), None)
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         rope.norm_rotate(x.half(), torch.arange(4), None)
+
+
+def test_packed_arguments_are_the_struct():
+    a = abi.RotateArgs.from_buffer_copy(rope._pack(*range(1, 9), 0.5, 2.0, *range(11, 35)))
+    got = [getattr(a, f) for f, _ in abi.RotateArgs._fields_[:-2]]
+    assert got == [*range(1, 9), 0.5, 2.0, 11, 12]
+    assert [getattr(s, f) for s in (a.q, a.k) for f, _ in abi.HeadRows._fields_] == list(range(13, 35))

@@ -85,7 +85,7 @@ struct Shape {
     static constexpr int SMEM = OFF_BAR + 8 * N_BAR + 16;
     // registers of a thread of the loading and MMA warps and of the softmax warps (setmaxnreg at entry): their sum over
     // three warpgroups fits the launch's, which the host checks
-    static constexpr int REG_LOW = WIDE ? 72 : C == 64 ? 88 : 120, REG_SOFT = WIDE ? 216 : C == 64 ? 208 : 192;
+    static constexpr int REG_LOW = WIDE ? 24 : C == 64 ? 88 : 120, REG_SOFT = WIDE ? 240 : C == 64 ? 208 : 192;
     static constexpr int HELD = WIDE ? 1 : 0;                       // d-blocks of O in registers
     static constexpr int T_S = 0, T_O = NS * N - HELD * N;          // d-block b at T_O + b * N
     static constexpr int OVER = D == 512 ? 1 : D == 256 ? 2 : 3;    // an item's start and end, in tiles
@@ -875,26 +875,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     is_full = false;
                     if ((miss >> (r >> (WIN ? 4 : min((raw ? p.raw : p.comp).page_log, 7)))) & 1) cb = ca;
                 }
-                // BL columns at a time: their logits from TMEM, those that are not seen to -infinity.  All columns at once
-                // where the registers are not needed for O: the logits then stay in them for the second pass.
-                constexpr int BL = S::HELD ? 32 : C;
-                float s[BL];
-                auto load = [&](int c0) {
+                // this row's logits from TMEM, those that are not seen to -infinity
+                float s[C];
+                auto load = [&]() {
 #pragma unroll
-                    for (int k = 0; k < BL; k += 32) tmem_ld32(lane_base + S::T_S + sb * N + col0 + c0 + k, s + k);
+                    for (int k = 0; k < C; k += 32) tmem_ld32(lane_base + S::T_S + sb * N + col0 + k, s + k);
                     ld_wait();
                 };
                 const uint32_t span = max(cb - ca, 0);
-                auto mask = [&](int c0) {
-                    if (ca > c0 || cb < c0 + BL) {
+                auto mask = [&]() {
+                    if (ca > 0 || cb < C) {
 #pragma unroll
-                        for (int c = 0; c < BL; c++) s[c] = (uint32_t)(c0 + c - ca) < span ? s[c] : -INFINITY;
+                        for (int c = 0; c < C; c++) s[c] = (uint32_t)(c - ca) < span ? s[c] : -INFINITY;
                     }
                 };
-                auto scale = [&](int c0) {                      // s * scale - reference
+                auto scale = [&]() {                      // s * scale - reference
 #pragma unroll
-                    for (int c = 0; c < BL; c += 4) {
-                        const float4 m = *reinterpret_cast<const float4 *>(gref + c0 + c);
+                    for (int c = 0; c < C; c += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(gref + c);
                         s[c] = fmaf(s[c], p.scale_log2, -m.x);
                         s[c + 1] = fmaf(s[c + 1], p.scale_log2, -m.y);
                         s[c + 2] = fmaf(s[c + 2], p.scale_log2, -m.z);
@@ -902,41 +900,37 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     }
                 };
                 float most = -INFINITY, least = is_full ? 0.f : INFINITY;   // fmaxf and fminf pass NaN over
-#pragma unroll
-                for (int c0 = 0; c0 < C; c0 += BL) {
-                    if (c0 >= mine) break;
-                    load(c0);
+                if (mine > 0) {
+                    load();
                     if (!is_full) {
-                        if (c0 + BL <= mine) {
+                        if (mine == C) {
 #pragma unroll
-                            for (int c = 0; c < BL; c++) least = fminf(least, fabsf(s[c]));
+                            for (int c = 0; c < C; c++) least = fminf(least, fabsf(s[c]));
                         } else {
 #pragma unroll
-                            for (int c = 0; c < BL; c++) least = c0 + c < mine ? fminf(least, fabsf(s[c])) : least;
+                            for (int c = 0; c < C; c++) least = c < mine ? fminf(least, fabsf(s[c])) : least;
                         }
-                        mask(c0);
+                        mask();
                     }
-                    scale(c0);
+                    scale();
 #pragma unroll
-                    for (int c = 0; c < BL; c += 2) most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
+                    for (int c = 0; c < C; c += 2) most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
                 }
                 const bool finite = least < INFINITY;           // some logit of the row is a number
                 const bool moves = group_any(id, most > TAU);
                 if (moves) {
                     // the tile's largest logit of each column, the new references and the factors 2^(old - new)
+                    if (mine > 0) {
+                        load();
+                        if (!is_full) mask();
+                        float m[C / 32];
 #pragma unroll
-                    for (int c0 = 0; c0 < C; c0 += BL) {
-                        if (c0 >= mine) break;
-                        load(c0);
-                        if (!is_full) mask(c0);
-                        float m[BL / 32];
-#pragma unroll
-                        for (int c = 0; c < BL; c++) {
+                        for (int c = 0; c < C; c++) {
                             const float x = warp_max(s[c] * p.scale_log2);
                             m[c / 32] = lane == c % 32 ? x : m[c / 32];
                         }
 #pragma unroll
-                        for (int k = 0; k < BL / 32; k++) red[q4 * C + c0 + 32 * k + lane] = m[k];
+                        for (int k = 0; k < C / 32; k++) red[q4 * C + 32 * k + lane] = m[k];
                     }
                     group_sync(id);
                     if (tid < C) {
@@ -945,7 +939,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         red[tid] = ex2(old - now);
                     }
                     group_sync(id);
-                    if (!S::HELD) scale(0);
+                    scale();
 #pragma unroll
                     for (int c = 0; c < C; c += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(red + c);
@@ -983,27 +977,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         }
                     st_wait();
                 }
-#pragma unroll
-                for (int c0 = 0; c0 < C; c0 += BL) {
-                    if (c0 >= mine) break;
-                    if (S::HELD) {
-                        load(c0);
-                        if (!is_full) mask(c0);
-                        scale(c0);
-                    }
+                if (mine > 0) {
                     if (!is_full && __any_sync(0xffffffffu, !finite)) {   // NaN to the columns that see the row
 #pragma unroll
-                        for (int c = 0; c < BL; c++)
-                            s[c] = finite ? s[c] : (uint32_t)(c0 + c - ca) < span ? __int_as_float(0x7fc00000) : -INFINITY;
+                        for (int c = 0; c < C; c++)
+                            s[c] = finite ? s[c] : (uint32_t)(c - ca) < span ? __int_as_float(0x7fc00000) : -INFINITY;
                     }
 #pragma unroll
-                    for (int c = 0; c < BL; c++) {
+                    for (int c = 0; c < C; c++) {
                         s[c] = ex2(s[c]);
-                        l[c0 + c] += s[c];
+                        l[c] += s[c];
                     }
 #pragma unroll
-                    for (int u = 0; u < BL / 8; u++)
-                        *reinterpret_cast<uint4 *>(prow + g % S::NP * S::P_BYTES + (((u0 + c0 / 8 + u) ^ (r & 7)) * 16)) =
+                    for (int u = 0; u < C / 8; u++)
+                        *reinterpret_cast<uint4 *>(prow + g % S::NP * S::P_BYTES + (((u0 + u) ^ (r & 7)) * 16)) =
                             make_uint4(pack(s[8 * u], s[8 * u + 1]), pack(s[8 * u + 2], s[8 * u + 3]), pack(s[8 * u + 4], s[8 * u + 5]),
                                        pack(s[8 * u + 6], s[8 * u + 7]));
                 }

@@ -24,6 +24,7 @@ DS4C_BF16 = 1
 DS4C_WAITS_QUANT_MATMUL = 0
 DS4C_WAITS_GEMM = 1
 DS4C_WAITS_ATTENTION = 2
+DS4C_WAITS_PAGED = 3
 DS4C_ROPE_PLAIN = 0
 DS4C_ROPE_LINEAR = 1
 DS4C_ROPE_YARN = 2

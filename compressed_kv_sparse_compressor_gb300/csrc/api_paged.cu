@@ -48,6 +48,7 @@ ds4c_status ds4c_paged_attn(const ds4c_paged_attn_args *args, void *ws, size_t w
     if (!(a.scale > 0.f) || !(a.scale <= 1e4f) || a.window > 0x7fffffffu || a.ratio > 0x7fffffffu) return DS4C_ERR_SHAPE;
     if (a.n_seq == 0 || a.n_tok == 0) return DS4C_OK;
     if (!a.q || !a.out || !a.start || !a.length) return DS4C_ERR_NULL;
+    if (a.q == a.out) return DS4C_ERR_SHAPE;
     if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.start, 4) || !aligned(a.length, 4)) return DS4C_ERR_SHAPE;
     if (!strides_ok(a, a.q_token, a.q_head) || !strides_ok(a, a.out_token, a.out_head)) return DS4C_ERR_SHAPE;
     if (!apart(a.n_tok, a.out_token, a.n_heads, a.out_head, a.head_dim) &&

@@ -55,6 +55,7 @@ cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
 cudaError_t gemm_tc_wait_selftest(int *answers, cudaStream_t s);
 cudaError_t attn_tc_wait_selftest(int *answers, cudaStream_t s);
 cudaError_t qmm_wait_selftest(int *answers, cudaStream_t s);
+cudaError_t paged_attn_wait_selftest(int *answers, cudaStream_t s);
 
 // Bounded wait of a whole warp for look() to be true in every lane.  The lanes look together and vote on every look,
 // so that none waits or goes on alone, and all get one answer, whatever each of them saw; what follows a wait (votes,

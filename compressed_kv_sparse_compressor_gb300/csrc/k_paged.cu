@@ -133,6 +133,7 @@ struct Params {
     int hg, tt, groups;        // heads and tokens of an item, head groups
     int over;                  // an item's start and end, in tiles
     int small, by_item;        // each CTA cuts for itself; parts lie by items
+    int max_items;             // of starts that rise within the tokens
     float scale_log2;
     Plan plan;
 };
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     }
     __syncthreads();
     // starts that overlap could make more items than there is room for
-    const int most = p.n_tok * p.groups, n_items = min(carry, most);
-    if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
+    const int n_items = min(carry, p.max_items);
+    if (carry > p.max_items && tid == 0) atomicOr(&g_paged_err, 2u);
     // each thread's items, one behind the other
     const int each = (n_items + PLAN_THREADS - 1) / PLAN_THREADS;
     auto walk = [&](int thread, auto visit) { walk_items(p, first, begin, length, thread * each, min(thread * each + each, n_items), visit); };
@@ -506,8 +507,8 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
     const int incl = block_scan<SMALL, int>(k, sums_i, carry);
     if (tid < p.n_seq) first[tid] = incl - k;
     __syncthreads();
-    const int most = p.n_tok * p.groups, n_items = min(carry, most);
-    if (carry > most && tid == 0) atomicOr(&g_paged_err, 2u);
+    const int n_items = min(carry, p.max_items);
+    if (carry > p.max_items && tid == 0) atomicOr(&g_paged_err, 2u);
     const int each = (n_items + SMALL - 1) / SMALL, i0 = tid * each, i1 = min(i0 + each, n_items);
     long long cost = 0;
     walk_items(p, first, begin, length, i0, i1, [&](int, const Item &it) {
@@ -519,7 +520,7 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
     const int ctas = n_items ? ctas_of(all, grid) : 0;
     if (tid == 0) *out = {{n_items, 0}, {n_items, 0}};
     if (!p.by_item && tid == 0) p.plan.parts[cta] = {cta, 0, 0, 0, 0};
-    if (p.by_item && cta == 0 && tid >= n_items && tid < most) p.plan.parts[tid] = {0, 0, 0, 0, 0};   // entries of no item
+    if (p.by_item && cta == 0 && tid >= n_items && tid < p.max_items) p.plan.parts[tid] = {0, 0, 0, 0, 0};   // entries of no item
     __syncthreads();
     if (cta < ctas) {
         const long long a = all * cta / ctas, b = all * (cta + 1) / ctas;      // this CTA's share: the places a .. b - 1
@@ -1223,6 +1224,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
     *reinterpret_cast<uint2 *>(p.out + to) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
 }
 
+__global__ void wait_selftest_kernel(int *answers) {
+    warp_wait_selftest(
+        answers,
+        [](auto look, volatile int *abort) { return warp_bounded_wait<16>(look, abort, g_paged_wait_ns, &g_paged_err); },
+        [](uint32_t bar, uint32_t parity, volatile int *abort) { return warp_wait(bar, parity, abort); });
+}
+
 // ---- host --------------------------------------------------------------------------------------
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1295,6 +1303,7 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
     const uint64_t items = (whole < a.n_tok ? whole : a.n_tok) * p.groups;
     p.small = a.n_seq <= SMALL && items <= SMALL_ITEMS;
     p.by_item = p.small && items <= FEW_ITEMS;
+    p.max_items = (int)items;
     CUtensorMap qm, rm, cm;
     {
         const cuuint64_t dims[3] = {D, a.n_heads, a.n_tok};
@@ -1368,6 +1377,11 @@ cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStrea
 }
 
 cudaError_t paged_attn_set_wait_ns(unsigned long long ns) { return cudaMemcpyToSymbol(g_paged_wait_ns, &ns, sizeof ns); }
+
+cudaError_t paged_attn_wait_selftest(int *answers, cudaStream_t s) {
+    wait_selftest_kernel<<<1, 32, 0, s>>>(answers);
+    return cudaGetLastError();
+}
 
 unsigned int paged_attn_read_clear_error() {
     unsigned int v = 0, z = 0;

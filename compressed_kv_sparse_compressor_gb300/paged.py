@@ -10,6 +10,8 @@ token looks, starts that fall, a kernel that gave up waiting) is reported by ``f
 
 from __future__ import annotations
 
+import struct
+
 import torch
 
 from . import abi
@@ -29,19 +31,27 @@ def workspace(n_seq: int, n_tok: int, n_heads: int, head_dim: int, device="cuda"
     return torch.empty(size, dtype=torch.uint8, device=device)
 
 
+_new_workspace = workspace
+
+
+# A call's arguments as the ABI's struct lays them out, packed at once
+_pack = struct.Struct("6If4x2P4N2P" + 2 * "2PN3I4x").pack
+_NO_POOL = (0,) * 6
+
+
 def _pool(cache, pages, n_seq, d, dev, what):
-    shape = cache.shape
+    """The struct's fields for a cache and its table."""
+    shape, ps = cache.shape, pages.shape
     if len(shape) != 3 or shape[2] != d or cache.dtype != _BF16 or cache.get_device() != dev or not cache.is_contiguous():
         raise ValueError(f"{what}: {cache.dtype} {tuple(shape)} on {cache.device}, expected contiguous bfloat16 (pages, page rows, "
                          f"{d}) on cuda:{dev}")
-    ps = pages.shape
     if len(ps) != 2 or ps[0] != n_seq or pages.dtype != _I32 or pages.get_device() != dev:
         raise ValueError(f"{what}'s table: {pages.dtype} {tuple(ps)} on {pages.device}, expected int32 ({n_seq}, entries) on "
                          f"cuda:{dev}")
     ld, col = pages.stride()
     if col != 1 and ps[1] > 1:
         raise ValueError(f"{what}'s table: the entries of a sequence must be contiguous")
-    return abi.PagePool(cache.data_ptr(), pages.data_ptr(), ld if n_seq > 1 else ps[1], shape[0], shape[1], ps[1])
+    return cache.data_ptr(), pages.data_ptr(), ld if n_seq > 1 else ps[1], shape[0], shape[1], ps[1]
 
 
 def _ints(t, n, dev, what):
@@ -72,17 +82,17 @@ def attention(q, cache, pages, start, length, *, window: int = 0, scale=None, co
     if od != 1:
         raise ValueError("out: the rows' elements must be contiguous")
     n_seq = length.shape[0] if length.dim() == 1 else -1
-    a = abi.PagedAttnArgs(n_seq if n_seq > 0 else 0, n, h, d, window, ratio, d ** -0.5 if scale is None else scale, q.data_ptr(),
-                          out.data_ptr(), qt if n > 1 else 0, qh if h > 1 else 0, ot if n > 1 else 0, oh if h > 1 else 0,
-                          _ints(start, n_seq + 1, dev, "start"), _ints(length, n_seq, dev, "length"),
-                          _pool(cache, pages, n_seq, d, dev, "cache"))
+    if not 0 <= window < 1 << 31 or not 0 <= ratio < 1 << 31:
+        raise ValueError(f"window {window}, ratio {ratio}: 0 to 2^31 - 1")
     if (comp is None) != (ratio == 0) or (comp is None) != (comp_pages is None):
         raise ValueError("comp, comp_pages and ratio: all or none")
-    if comp is not None:
-        a.comp = _pool(comp, comp_pages, n_seq, d, dev, "comp")
+    args = _pack(max(n_seq, 0), n, h, d, window, ratio, d ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
+                 qt if n > 1 else 0, qh if h > 1 else 0, ot if n > 1 else 0, oh if h > 1 else 0, _ints(start, n_seq + 1, dev, "start"),
+                 _ints(length, n_seq, dev, "length"), *_pool(cache, pages, n_seq, d, dev, "cache"),
+                 *(_NO_POOL if comp is None else _pool(comp, comp_pages, n_seq, d, dev, "comp")))
     if workspace is None:
-        workspace = globals()["workspace"](n_seq, n, h, d, q.device)
+        workspace = _new_workspace(n_seq, n, h, d, q.device)
     elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace: {workspace.dtype} on {workspace.device}, expected contiguous uint8 on cuda:{dev}")
-    run(dev, abi.ds4c_paged_attn, a, workspace.data_ptr(), workspace.numel())
+    run(dev, abi.ds4c_paged_attn, abi.PagedAttnArgs.from_buffer_copy(args), workspace.data_ptr(), workspace.numel())
     return out

@@ -239,6 +239,49 @@ def test_streams_graphs_and_equal_bits():
         assert e.value.status == abi.DS4C_ERR_WORKSPACE
 
 
+def test_waits_that_give_up():
+    """Half of the lanes see what they wait for: no lane goes on alone, a barrier that nothing arrives on gives the whole
+    warp one answer and raises the error word.  Then the attention in each of its forms under a limit of a few
+    nanoseconds: its waits give up or not, as the copies come; either way it ends with nothing in flight, and with the
+    default limit the same call is right."""
+    stream = torch.cuda.current_stream().cuda_stream
+    answers = torch.full((96,), -7, dtype=torch.int32, device="cuda")
+    fp8.sync()
+    assert abi.ds4c_test_set_wait_limit(20000) == abi.DS4C_OK
+    try:
+        assert abi.ds4c_test_warp_wait(abi.DS4C_WAITS_PAGED, answers.data_ptr(), stream) == abi.DS4C_OK
+        assert abi.ds4c_sync_status(stream) == abi.DS4C_ERR_DEVICE
+    finally:
+        assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
+    assert answers.tolist() == [0] * 64 + [1] * 32
+    for h, d, seqs, window in ((64, 512, [(1, 9000)] * 3, 0), (64, 512, [(300, 900)], 0), (64, 512, [(300, 900)], 128),
+                               (24, 256, [(200, 900)], 0), (16, 128, [(300, 900)], 50), (8, 64, [(300, 900)], 0)):
+        q, a, kw = setup(gen(22), h, d, 64, seqs, window)
+        assert abi.ds4c_test_set_wait_limit(1) == abi.DS4C_OK
+        try:
+            for _ in range(3):
+                paged.attention(q, **a, **kw)
+                assert abi.ds4c_sync_status(stream) in (abi.DS4C_OK, abi.DS4C_ERR_DEVICE)
+        finally:
+            assert abi.ds4c_test_set_wait_limit(0) == abi.DS4C_OK
+        check(q, a, kw, seqs)
+
+
+def test_starts_that_overlap_stay_in_bounds():
+    """More items than the tokens allow for: reported, and nothing beyond the outputs and the workspace is written."""
+    g = gen(23)
+    q, a, kw = setup(g, 8, 128, 16, [(48, 60)] * 3)
+    n = q.shape[0]
+    for starts in ([0, n, 0, n], [0, n, n, 0]):
+        a["start"] = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        size = paged.workspace(3, n, 8, 128).numel()
+        ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        paged.attention(q, workspace=ws[:size], **a, **kw)
+        with pytest.raises(abi.Ds4cError):
+            fp8.sync()
+        assert (ws[size:] == 0x5A).all()
+
+
 def test_pages_past_32_bits():
     """A pool of 6 GB: rows beyond 2^31 elements and 2^32 bytes."""
     g = gen(18)

@@ -42,7 +42,7 @@ def test_refusals():
                dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=1e5), dict(window=1 << 31), dict(ratio=1 << 31),
                dict(q=FAKE + 8), dict(out=FAKE + 8), dict(start=FAKE + 2), dict(length=FAKE + 2), dict(q_token=64 * 512 + 4),
                dict(q_head=516), dict(out_token=64 * 512 + 4), dict(out_head=516), dict(out_head=504), dict(out_token=63 * 512),
-               dict(ratio=4), dict(q_token=1 << 41)):
+               dict(ratio=4), dict(q_token=1 << 41), dict(q_token=0), dict(q_head=0), dict(out=FAKE)):
         assert call(**kw) == abi.DS4C_ERR_SHAPE, kw
     for kw in (dict(page_rows=8), dict(page_rows=48), dict(page_rows=2048), dict(page_rows=0), dict(n_pages=0), dict(n_pages=1 << 25),
                dict(pages_ld=7), dict(rows=FAKE + 8), dict(pages=FAKE + 2), dict(max_pages=(1 << 27) + 1, pages_ld=1 << 28)):
@@ -63,3 +63,9 @@ def test_python_refusals():
         paged.attention(q, cache, i[None], i, i[:1])
     with pytest.raises(ValueError, match="bfloat16"):
         paged.attention(q.float(), cache, i[None], i, i[:1])
+
+
+def test_packed_arguments_are_the_struct():
+    a = abi.PagedAttnArgs.from_buffer_copy(paged._pack(*range(1, 7), 0.5, *range(8, 28)))
+    assert [getattr(a, f) for f, _ in abi.PagedAttnArgs._fields_[:-2]] == [*range(1, 7), 0.5, *range(8, 16)]
+    assert [getattr(p, f) for p in (a.raw, a.comp) for f, _ in abi.PagePool._fields_] == list(range(16, 28))

@@ -55,7 +55,11 @@ constexpr int SMALL_ITEMS = 8 * SMALL;                              // and items
 constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
 constexpr int FEW_ITEMS = 64;                                       // joined by a block for each column
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
-constexpr uint32_t WIDE_TOKENS = 4;                                 // new tokens a sequence, from which items are wide
+// Columns (new tokens x heads) a sequence on average, from which items are wide at head_dim 512.  A wide tile takes 8.4k
+// cycles for 128 columns, a narrow one 5.2k (6.5k from memory) for 64: 4096 tokens at 12288 4.35 ms wide, 5.93 narrow; 2 tokens
+// of 64 heads at 20 contexts 111 and 117 us, 3 tokens 162 and 156; single tokens of 32 at 64K 471 and 355; 31 of those beside a
+// chunk of 64 582 and 457, of 512 936 and 881.  More than 64 heads are always wide: narrow items would read the rows twice.
+constexpr uint64_t WIDE_COLUMNS = 2048;
 constexpr int MIN_COST = 1;                                         // a CTA's share, in tiles, where there is little work
 
 // WIDE: 128 columns at head_dim 512.  O then has 512 columns of its own, all that TMEM has, so the first 128 of d
@@ -1362,7 +1366,7 @@ cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStrea
     p.n_seq = (int)a.n_seq; p.n_tok = (int)a.n_tok; p.n_heads = (int)a.n_heads;
     p.window = a.window >= (uint32_t)MAX_LENGTH ? 0 : (int)a.window;   // as long as any sequence: none
     p.ratio = (int)a.ratio;
-    const bool wide = a.head_dim == 512 && (a.n_heads > 64 || a.n_tok >= WIDE_TOKENS * a.n_seq);
+    const bool wide = a.head_dim == 512 && (a.n_heads > 64 || (uint64_t)a.n_tok * a.n_heads >= WIDE_COLUMNS * a.n_seq);
     const Split c = split_of(a.n_heads, a.head_dim, wide);
     p.hg = c.hg; p.groups = c.groups; p.tt = c.tt;
     p.scale_log2 = a.scale * 1.4426950408889634f;

@@ -108,7 +108,7 @@ def test_tokens_that_see_nothing():
                                      "length": a["length"]}).shape == (0, 16, 128)
 
 
-@pytest.mark.parametrize("h,d", [(64, 512), (8, 128), (40, 256), (3, 64)])
+@pytest.mark.parametrize("h,d", [(64, 512), (24, 512), (8, 128), (40, 256), (3, 64)])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 def test_rows_that_are_no_numbers(h, d, value):
     """A row with a NaN or an infinity poisons the tokens that see it, and no other."""
@@ -128,7 +128,7 @@ def test_rows_that_are_no_numbers(h, d, value):
         ref.assert_close(got[~sees], want[~sees], size[~sees])
 
 
-@pytest.mark.parametrize("h,d", [(64, 512), (16, 128), (8, 64)])
+@pytest.mark.parametrize("h,d", [(64, 512), (128, 512), (16, 128), (8, 64)])
 def test_logits_far_apart(h, d):
     """Logits of some thousands, that rise, fall, or are all equal along the sequence: one row takes all the weight, or
     all rows share it."""
@@ -377,7 +377,7 @@ def test_many_sequences_and_many_items(h, d):
 
 def test_few_tokens_each():
     """Sequences of one to three new tokens: items of 64 columns at head_dim 512, several tokens in one with few heads."""
-    for h in (8, 24, 32, 33, 64):
+    for h in (8, 24, 32, 33, 64, 128):
         g = gen(21 + h)
         seqs = [(1 + b % 3, 3 + 97 * b) for b in range(12)]
         check(*setup(g, h, 512, 64, seqs, 0, 16), seqs)

@@ -10,12 +10,14 @@
 // at a position of 10^6.)
 //
 // What bounds it: HBM for many tokens, launch and one chain load - sum - store for few.  A block takes one
-// token, so that its sines are computed once for all heads, in shared memory; a warp takes a row of 256
-// values and more, 8 or 16 lanes a shorter one, 16 bytes a lane and access, and loads its next row before
-// it works on this one.  Bfloat16, 4096 tokens of 64 + 1 heads of 512 with gains and a rotated tail of 64, inputs not in
-// L2: 100 us with blocks of 128 threads (102 with 256, 117 with 512, 103-107 with 64; 119 and 200 held to 12 and 16
-// blocks an SM; 110 with four tokens to a block; 113 with the last head in a block of its own), 5.4 TB/s; the
-// rotation alone, 64 heads, 90 us, 6.0 TB/s.
+// token, so that its sines are computed once for all heads, in shared memory, while the first rows are on their
+// way; a warp takes a row of 256 values and more, 8 or 16 lanes a shorter one, 16 bytes a lane and access, and loads
+// its next row before it works on this one.  Products go in pairs (fma.f32x2): with single ones the norm issued 3.0
+// instructions a cycle of 4 and took 95 us where it takes 88.  Bfloat16, 64 heads of 512, rotated tail of 64, 4096 tokens, launches
+// one behind the other: with norm, gains and a key head 88.4 us, 6.2 TB/s; rotation alone 82.2 us, 6.5 TB/s.  32
+// tokens 3.3 us, 1 token 2.4 and 1.7; float rows, 437 tokens of 24 heads of 128 4.0 and 5.0.
+// Blocks of 128 threads: before the pairs 100 us on cold inputs, 102 with 256, 117 with 512, 103-107 with 64; 110
+// with four tokens to a block, 113 with the last head in a block of its own.
 #include <cuda_bf16.h>
 
 #include "ds4c_internal.cuh"
@@ -72,6 +74,27 @@ __device__ __forceinline__ void load_vec(Vec<TI, V> &r, const TI *p) {
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// Two products at once (half the issue slots).
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y) {
+    asm("{\n\t.reg .b64 u, v;\n\t"
+        "mov.b64 u, {%0, %1};\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "mul.rn.f32x2 u, u, v;\n\t"
+        "mov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
+}
+// s += (a^2, b^2)
+__device__ __forceinline__ void square2(float2 &s, float a, float b) {
+    asm("{\n\t.reg .b64 u, v;\n\t"
+        "mov.b64 u, {%0, %1};\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "fma.rn.f32x2 u, v, v, u;\n\t"
+        "mov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(s.x), "+f"(s.y)
+        : "f"(a), "f"(b));
+}
+
 template <int V>
 __device__ __forceinline__ void store_vec(void *out, int64_t at, const float (&y)[V], int f32) {
     if (f32) {
@@ -98,8 +121,10 @@ __device__ __forceinline__ void store_vec(void *out, int64_t at, const float (&y
 // T lanes to a row, G vectors of V values to a lane (value e of the row in vector e / V, vector v in lane v % T).
 // V = 8 needs 16-byte aligned rows, d a multiple of 8 and pairs inside a vector or in the same place of two vectors;
 // V = 1 takes anything.
+// Rows of up to 16 values a lane: registers for 7 blocks an SM (4096 tokens with the norm 88.4 us, rotation alone 82.2; as the
+// compiler chooses 88.7 and 87.0, for 8 blocks 89.9 and 82.3).  More values a lane need what they need.
 template <typename TI, int V, int T, int G, bool NORM>
-__global__ void __launch_bounds__(THREADS) heads_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, V == 8 && G <= 2 ? 7 : 1) heads_kernel(const Params p) {
     extern __shared__ float4 smem4[];
     float2 *cs = reinterpret_cast<float2 *>(smem4);                       // [n_rot / 2]: magnitude * (cos, sin)
     constexpr int ROWS = 32 / T;                                          // rows a warp works on at a time
@@ -109,152 +134,174 @@ __global__ void __launch_bounds__(THREADS) heads_kernel(const Params p) {
     // the warps' rows of the rotated part, where pairs lie in different lanes
     float *buf = reinterpret_cast<float *>(smem4) + ((p.n_rot + 3) & ~3) + (warp * ROWS + lane / T) * p.n_rot;
     const bool exchange = V == 1 || p.half;
+    const bool whole = p.first % 8 == 0 && p.n_rot % 8 == 0;              // no group of 8 values lies partly in the rotated part
 
     pdl_wait();
     pdl_launch_dependents();
 
-    Vec<TI, V> x[G];
-    auto load = [&](int h) {
-        if (h >= h_end) return;
-        const Side &s = p.side[h >= p.side[0].heads];
-        const int hh = h >= p.side[0].heads ? h - p.side[0].heads : h;
-        const TI *row = static_cast<const TI *>(s.x) + token * s.x_token + hh * s.x_head;
+    bool first_side = true;
+    // queries, then keys: heads `from` .. `to` - 1 of the side, this lane's STEP apart; whole warps go round together, some of
+    // their rows may be past the end
+    for (int side = 0; side < 2; side++) {
+        constexpr int STEP = WARPS * ROWS;
+        const Side &s = p.side[side];
+        const int base = side ? p.side[0].heads : 0, from = max(h0 - base, 0), to = min(h_end - base, s.heads);
+        if (from >= to && !first_side) break;
+        int h = from + warp * ROWS + lane / T;
+        const TI *in = static_cast<const TI *>(s.x) + token * s.x_token + h * s.x_head + t * V;
+        Vec<TI, V> x[G];
+        auto load = [&]() {
 #pragma unroll
-        for (int g = 0; g < G; g++) {
-            const int e = (g * T + t) * V;
-            if (e < p.d) load_vec<TI, V>(x[g], row + e);
-        }
-    };
-    int h = h0 + warp * ROWS + lane / T;
-    load(h);
-    if ((int)threadIdx.x < p.n_rot / 2) {
-        const unsigned long long pos = (unsigned long long)p.pos[token];
-        for (int j = threadIdx.x; j < p.n_rot / 2; j += THREADS) {
-            const float2 v = cos_sin_turns(pos * p.turns[j]);
-            cs[j] = make_float2(p.magnitude * v.x, p.inverse ? -p.magnitude * v.y : p.magnitude * v.y);
-        }
-    }
-    __syncthreads();
-
-    // whole warps go round together: some of a warp's rows may be past the end
-    for (int hw = h0 + warp * ROWS; hw < h_end; hw += WARPS * ROWS, h += WARPS * ROWS) {
-        const bool live = h < h_end;
-        const Side &s = p.side[live && h >= p.side[0].heads];
-        const int hh = h >= p.side[0].heads ? h - p.side[0].heads : h;
-        float y[G][V];
-        float ss = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; g++) {
-            const bool in = live && (g * T + t) * V < p.d;
-#pragma unroll
-            for (int j = 0; j < V; j++) {
-                y[g][j] = in ? to_float(x[g].v[j]) : 0.f;
-                if (NORM) ss = fmaf(y[g][j], y[g][j], ss);
-            }
-        }
-        load(h + WARPS * ROWS);
-        if (NORM) {
-#pragma unroll
-            for (int o = T / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            float rstd = 1.0f / sqrtf(fmaf(ss, p.inv_d, p.eps));
-            if (__any_sync(0xffffffffu, ss > 3.0e38f)) {                 // squares past float's range: those rows at 2^-80
-                const float down = ss > 3.0e38f ? 0x1p-80f : 1.0f;
-                float s2 = 0.f;
-#pragma unroll
-                for (int g = 0; g < G; g++)
-#pragma unroll
-                    for (int j = 0; j < V; j++) {
-                        y[g][j] *= down;
-                        s2 = fmaf(y[g][j], y[g][j], s2);
-                    }
-#pragma unroll
-                for (int o = T / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                if (ss > 3.0e38f) rstd = 1.0f / sqrtf(s2 * p.inv_d);     // eps <= 1 is nothing beside such squares
-            }
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                const int e = (g * T + t) * V;
-#pragma unroll
-                for (int j = 0; j < V; j++) y[g][j] *= rstd;
-                if (s.gain && e < p.d) {
-                    if constexpr (V == 8) {
-                        const float4 a = reinterpret_cast<const float4 *>(s.gain + e)[0], b = reinterpret_cast<const float4 *>(s.gain + e)[1];
-                        y[g][0] *= a.x; y[g][1] *= a.y; y[g][2] *= a.z; y[g][3] *= a.w;
-                        y[g][4] *= b.x; y[g][5] *= b.y; y[g][6] *= b.z; y[g][7] *= b.w;
-                    } else {
-                        y[g][0] *= s.gain[e];
-                    }
+            for (int g = 0; g < G; g++)
+                if ((g * T + t) * V < p.d) load_vec<TI, V>(x[g], in + g * T * V);
+            in += STEP * s.x_head;
+        };
+        if (h < to) load();
+        if (first_side) {                                      // the sines, while the first rows come
+            if ((int)threadIdx.x < p.n_rot / 2) {
+                const unsigned long long pos = (unsigned long long)p.pos[token];
+                for (int j = threadIdx.x; j < p.n_rot / 2; j += THREADS) {
+                    const float2 v = cos_sin_turns(pos * p.turns[j]);
+                    cs[j] = make_float2(p.magnitude * v.x, p.inverse ? -p.magnitude * v.y : p.magnitude * v.y);
                 }
             }
+            __syncthreads();
         }
-        if (exchange && p.n_rot > 0) {
-            __syncwarp();
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                const int r = (g * T + t) * V - p.first;
-                if (r >= 0 && r < p.n_rot) {
-                    if constexpr (V == 8) {
-                        reinterpret_cast<float4 *>(buf + r)[0] = make_float4(y[g][0], y[g][1], y[g][2], y[g][3]);
-                        reinterpret_cast<float4 *>(buf + r)[1] = make_float4(y[g][4], y[g][5], y[g][6], y[g][7]);
-                    } else {
-                        buf[r] = y[g][0];
-                    }
-                }
-            }
-            __syncwarp();
-            const int hr = p.n_rot / 2;
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                const int r = (g * T + t) * V - p.first;
-                if (r >= 0 && r < p.n_rot) {
-                    const bool second = p.half ? r >= hr : (r & 1) != 0;     // the pair's b
-                    const int other = p.half ? (second ? r - hr : r + hr) : r ^ 1;
-                    const int pair = p.half ? (second ? r - hr : r) : r >> 1;
-                    if constexpr (V == 8) {
-                        const float4 u = reinterpret_cast<const float4 *>(buf + other)[0], w = reinterpret_cast<const float4 *>(buf + other)[1];
-                        const float o[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            const float4 c = *reinterpret_cast<const float4 *>(cs + pair + j);
-                            y[g][j] = second ? fmaf(o[j], c.y, y[g][j] * c.x) : fmaf(-o[j], c.y, y[g][j] * c.x);
-                            y[g][j + 1] = second ? fmaf(o[j + 1], c.w, y[g][j + 1] * c.z) : fmaf(-o[j + 1], c.w, y[g][j + 1] * c.z);
-                        }
-                    } else {
-                        const float o = buf[other];
-                        const float2 c = cs[pair];
-                        y[g][0] = second ? fmaf(o, c.y, y[g][0] * c.x) : fmaf(-o, c.y, y[g][0] * c.x);
-                    }
-                }
-            }
-        } else if constexpr (V == 8) {
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                const int r = (g * T + t) * V - p.first;                     // even
-                if (r > -V && r < p.n_rot) {
-#pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        if (r + j < 0 || r + j >= p.n_rot) continue;
-                        const float2 c = cs[(r + j) >> 1];
-                        const float a = y[g][j], b = y[g][j + 1];
-                        y[g][j] = fmaf(-b, c.y, a * c.x);
-                        y[g][j + 1] = fmaf(b, c.x, a * c.y);
-                    }
-                }
-            }
-        }
+        first_side = false;
+        if (from >= to) continue;
         int64_t row = token;
-        bool keep = live;
-        if (live && s.slots) {
+        bool keep = true;
+        if (s.slots) {
             row = s.slots[token];
             keep = row >= 0 && row < s.n_slots;
-            if (row >= s.n_slots && t == 0) atomicOr(&g_heads_err, 1u);
+            if (row >= s.n_slots && threadIdx.x == 0) atomicOr(&g_heads_err, 1u);
         }
-        if (keep) {
-            const int64_t at = row * s.out_token + hh * s.out_head;
+        int64_t o = row * s.out_token + h * s.out_head + t * V;
+        for (int hw = from + warp * ROWS; hw < to; hw += STEP, h += STEP, o += STEP * s.out_head) {
+            const bool live = h < to;
+            float y[G][V];
+            float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
             for (int g = 0; g < G; g++) {
-                const int e = (g * T + t) * V;
-                if (e < p.d) store_vec<V>(s.out, at + e, y[g], s.out_f32);
+                const bool in_row = live && (g * T + t) * V < p.d;
+#pragma unroll
+                for (int j = 0; j < V; j++) y[g][j] = in_row ? to_float(x[g].v[j]) : 0.f;
+                if constexpr (NORM && V == 8) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) square2(sq, y[g][j], y[g][j + 1]);
+                } else if constexpr (NORM) {
+                    sq.x = fmaf(y[g][0], y[g][0], sq.x);
+                }
+            }
+            if (h + STEP < to) load();
+            if constexpr (NORM) {
+                float ss = sq.x + sq.y;
+#pragma unroll
+                for (int k = T / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+                float rstd = 1.0f / sqrtf(fmaf(ss, p.inv_d, p.eps));
+                if (__any_sync(0xffffffffu, ss > 3.0e38f)) {             // squares past float's range: those rows at 2^-80
+                    const float down = ss > 3.0e38f ? 0x1p-80f : 1.0f;
+                    float s2 = 0.f;
+#pragma unroll
+                    for (int g = 0; g < G; g++)
+#pragma unroll
+                        for (int j = 0; j < V; j++) {
+                            y[g][j] *= down;
+                            s2 = fmaf(y[g][j], y[g][j], s2);
+                        }
+#pragma unroll
+                    for (int k = T / 2; k > 0; k >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, k);
+                    if (ss > 3.0e38f) rstd = 1.0f / sqrtf(s2 * p.inv_d); // eps <= 1 is nothing beside such squares
+                }
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    const int e = (g * T + t) * V;
+                    if constexpr (V == 8) {
+#pragma unroll
+                        for (int j = 0; j < V; j += 2) mul2(y[g][j], y[g][j + 1], rstd, rstd);
+                        if (s.gain && e < p.d) {
+                            const float4 a = reinterpret_cast<const float4 *>(s.gain + e)[0], b = reinterpret_cast<const float4 *>(s.gain + e)[1];
+                            mul2(y[g][0], y[g][1], a.x, a.y);
+                            mul2(y[g][2], y[g][3], a.z, a.w);
+                            mul2(y[g][4], y[g][5], b.x, b.y);
+                            mul2(y[g][6], y[g][7], b.z, b.w);
+                        }
+                    } else {
+                        y[g][0] *= rstd;
+                        if (s.gain && e < p.d) y[g][0] *= s.gain[e];
+                    }
+                }
+            }
+            if (exchange && p.n_rot > 0) {
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    const int r = (g * T + t) * V - p.first;
+                    if (r >= 0 && r < p.n_rot) {
+                        if constexpr (V == 8) {
+                            reinterpret_cast<float4 *>(buf + r)[0] = make_float4(y[g][0], y[g][1], y[g][2], y[g][3]);
+                            reinterpret_cast<float4 *>(buf + r)[1] = make_float4(y[g][4], y[g][5], y[g][6], y[g][7]);
+                        } else {
+                            buf[r] = y[g][0];
+                        }
+                    }
+                }
+                __syncwarp();
+                const int hr = p.n_rot / 2;
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    const int r = (g * T + t) * V - p.first;
+                    if (r >= 0 && r < p.n_rot) {
+                        const bool second = p.half ? r >= hr : (r & 1) != 0;     // the pair's b
+                        const int other = p.half ? (second ? r - hr : r + hr) : r ^ 1;
+                        const int pair = p.half ? (second ? r - hr : r) : r >> 1;
+                        if constexpr (V == 8) {
+                            const float4 u = reinterpret_cast<const float4 *>(buf + other)[0], w = reinterpret_cast<const float4 *>(buf + other)[1];
+                            const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                const float4 c = *reinterpret_cast<const float4 *>(cs + pair + j);
+                                y[g][j] = second ? fmaf(v[j], c.y, y[g][j] * c.x) : fmaf(-v[j], c.y, y[g][j] * c.x);
+                                y[g][j + 1] = second ? fmaf(v[j + 1], c.w, y[g][j + 1] * c.z) : fmaf(-v[j + 1], c.w, y[g][j + 1] * c.z);
+                            }
+                        } else {
+                            const float v = buf[other];
+                            const float2 c = cs[pair];
+                            y[g][0] = second ? fmaf(v, c.y, y[g][0] * c.x) : fmaf(-v, c.y, y[g][0] * c.x);
+                        }
+                    }
+                }
+            } else if constexpr (V == 8) {
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    const int r = (g * T + t) * V - p.first;                     // even
+                    if (r <= -V || r >= p.n_rot) continue;
+                    auto turn = [&](int j, float cx, float cy) {
+                        const float a = y[g][j], b = y[g][j + 1];
+                        y[g][j] = fmaf(-b, cy, a * cx);
+                        y[g][j + 1] = fmaf(b, cx, a * cy);
+                    };
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < V; j += 4) {
+                            const float4 c = *reinterpret_cast<const float4 *>(cs + ((r + j) >> 1));
+                            turn(j, c.x, c.y);
+                            turn(j + 2, c.z, c.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < V; j += 2) {
+                            if (r + j < 0 || r + j >= p.n_rot) continue;
+                            const float2 c = cs[(r + j) >> 1];
+                            turn(j, c.x, c.y);
+                        }
+                    }
+                }
+            }
+            if (live && keep) {
+#pragma unroll
+                for (int g = 0; g < G; g++)
+                    if ((g * T + t) * V < p.d) store_vec<V>(s.out, o + g * T * V, y[g], s.out_f32);
             }
         }
     }

@@ -2,28 +2,42 @@
 //   o[i][h] = sum_k p_k x_k / sum_k p_k,  p_k = 2^(scale_log2 q[i][h] . x_k - m),  m a running reference
 // over the rows x_k that the token sees (raw rows of a window, compressed rows), K = V = the row.
 //
-// A work item is a sequence's next tokens whose heads fill the N columns of the MMAs (64 at head_dim 512, 128
-// below: one token of 64 heads, or several tokens of fewer heads, or a group of a wide layer's heads).  For
+// A work item is a sequence's next tokens whose heads fill the N columns of the MMAs: N = 128 (one token of 128 heads,
+// several tokens of fewer, or a group of a wide layer's heads), at head_dim 512 64 where there are few columns (narrow
+// items, queries resident) and 128 where there are many (wide items).  For
 // each tile of 128 rows, rows on the TMEM lanes, (token, head) columns side by side:
 //   S^T[row][col] = sum_d X[row][d] Q[col][d]         M = 128 rows, K = head_dim
 //   O^T[d][col]  += sum_row X[row][d] P[row][col]     M = 128 of d, K = 128 rows
 // The tile is loaded once: its [128 rows][64 d] chunks in the 128-byte swizzle are the K-major operand of the first
 // product and, two chunks side by side, the MN-major operand of the second.  At head_dim 512 one tile
-// fills the ring, and the next one's chunks follow as the second product frees theirs.
+// fills the ring, and the next one's chunks follow as the second product frees theirs.  With a window a tile is
+// made of eight pieces of 16 rows, raw ones from the first that is seen and compressed ones behind them; without, of 128
+// rows of one kind from a multiple of 128 on, whole pages to a load.
 //
-// Work is cut evenly: the tiles of all items in a row (each item one tile longer, for its queries and output),
+// Work is cut evenly: the tiles of all items in a row (each with OVER places in front for its queries and output),
 // divided by the number of CTAs; an item that a cut divides leaves parts (sum, reference, denominator), which
-// a second kernel joins in the order of the CTAs.  Items of few tiles are not divided.  A one-block
-// kernel in front makes the items and cuts on the device, so that lengths are the device's own
-// and a captured call follows them.
+// a second kernel joins in the order of the CTAs.  Items of few tiles are not divided.  Starts and lengths are read on
+// the device, so that a captured call follows them: up to 3072 items of 384 sequences each CTA weighs all of them and
+// finds its own cuts (5 to 11 us less than with a kernel in front), more than that a one-block kernel in front does it.
 //
 // Softmax: a thread holds one row's logits for half of the columns (two warpgroups), the denominators as its own
 // partial sums, which meet at the end of the item.  The reference moves only when a logit exceeds it by
-// more than 2^8, so p <= 256, and O is rescaled in tensor memory only then; P is rounded to bfloat16, an error of 2^-9
-// of each weight that the output's own rounding is as large as.
+// more than 2^8, so p <= 256, and O is rescaled in tensor memory only then.  P is rounded to bfloat16, at most 2^-8
+// of each weight, errors that average over the rows and that the output's own rounding is as large as; twice
+// the MMAs would avoid it.  The MMAs add by cutting off low bits: outputs of 65536 equal rows in one CTA come out 2.5e-4
+// small, a fifteenth of the output's half step.
 // Rows that no column sees take no part; a row that is no number somewhere (stale or poisoned) would spoil columns
 // that do not see it through 0 * NaN, so where a tile is masked and all of a row's logits are not finite, the row
 // is set to zero in shared memory and the columns that see it get NaN weights.
+//
+// What bounds it (64 heads of 512 unless said, inputs not in L2):
+// 4096 tokens behind 8192, wide: 4.35 ms, 1.26 PFLOP/s of the 1.92 that a library product reaches.  A tile takes its CTA 8.3k
+//   cycles where its 64 MMAs take 4.1k alone: S and the first block of O take turns in the same columns, and the softmax
+//   of a tile (1.2k cycles) lies between its two products.  Without softmax 3.4 ms.
+// 32 sequences of one token at 65536, narrow: 350 us, 6.1 TB/s: memory.
+// One token at 8192: 20 us: launches, one tile and the parts' way through L2.
+// 64 sequences of 1 to 128 tokens, a window of 128 and compressed rows: 125 us; three chunks of 128 tokens, 24 heads of 128: 104 us:
+//   the softmax's warps between their barriers (1.6 instructions a cycle of 4), tensor pipe 27 %.
 //
 // Warps: 0 loads (queries and tiles by TMA, a box per page), 1 issues the MMAs, 4-7 and 8-11 softmax and output.
 // Every wait is bounded; after one gave up the warps go on through their loops without waiting, so that the
@@ -451,10 +465,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         int total;
         const int incl = block_scan<PLAN_THREADS, int>(k, sums_i, total);
         if (s < p.n_seq) first[s] = carry + incl - k;
-        carry += total;
+        carry = min(carry + total, 1 << 30);                   // starts that overlap could come to 2^31; a round to 2^29
     }
     __syncthreads();
-    // starts that overlap could make more items than there is room for
+    // and to more items than there is room for
     const int n_items = min(carry, p.max_items);
     if (carry > p.max_items && tid == 0) atomicOr(&g_paged_err, 2u);
     // each thread's items, one behind the other

@@ -31,10 +31,14 @@ class Table:
         if turns.dim() != 1 or turns.dtype != torch.int64 or turns.get_device() < 0 or not turns.is_contiguous():
             raise ValueError(f"turns: {turns.dtype} {tuple(turns.shape)} on {turns.device}, expected contiguous int64 (pairs,) on "
                              "a CUDA device")
-        self.turns, self.magnitude = turns, float(magnitude)
+        self._turns, self.magnitude = turns, float(magnitude)
         self.n_rot = 2 * turns.shape[0]
         self.device_index = turns.get_device()
         self._ptr = turns.data_ptr()
+
+    @property
+    def turns(self):
+        return self._turns
 
 
 def turns(n_rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0,

@@ -407,13 +407,13 @@ DS4C_API ds4c_status ds4c_rotate_heads(const ds4c_rotate_args *args, cudaStream_
  * ratio > 0, every compressed row c with (c + 1) * ratio <= t + 1, in one softmax over both:
  *   out[i][h] = sum over rows of softmax(scale * q[i][h] . row) * row,
  * accumulated in float with probabilities rounded to bfloat16 on the way into the second product; a token that sees no
- * row (t < 0) gives zeros.  q, out: [n_tok] tokens of n_heads heads at strides of elements (multiples of 8, 16-byte aligned,
+ * row (t < 0) gives zeros.  q, out: [n_tok] tokens of n_heads heads at strides of elements (multiples of 8 above 0, 16-byte aligned,
  * output rows apart); out may not overlap q or a pool.  Tokens outside every sequence (in front of start[0], behind
  * start[n_seq]) are left as they are.
  *
- * Only rows that some token of the call sees are waited for to hold numbers: pages behind a sequence's end or before its
- * windows may hold anything and need not be listed (-1).  A row that is no number somewhere makes NaN the outputs of the tokens that
- * see it, and of no other.  A page outside 0 .. n_pages - 1 or past max_pages where a visible row should be, and a
+ * Rows that no token of the call sees have no effect: pages behind a sequence's end or before its windows may hold
+ * anything and need not be listed (-1).  A row that is no number somewhere makes NaN the outputs of the tokens that see it,
+ * and of no other; so may a row whose products with every query of a group of tokens pass float's range.  A page outside 0 .. n_pages - 1 or past max_pages where a visible row should be, and a
  * start that falls or leaves 0 .. n_tok, or a length above 2^30, raise the device error word; such rows, and the tokens of
  * such sequences, count as not there.
  *

@@ -282,6 +282,20 @@ def test_starts_that_overlap_stay_in_bounds():
         assert (ws[size:] == 0x5A).all()
 
 
+def test_starts_that_overlap_past_31_bits():
+    """2048 sequences of the same 2^20 tokens, each followed by a start that falls: 2^31 items, a number that wraps."""
+    n, h, d = 1 << 20, 65, 64
+    q = torch.zeros(n * 8 + h * 8 + d, dtype=torch.bfloat16, device="cuda").as_strided((n, h, d), (8, 8, 1))
+    out = torch.full((n, h, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    start = torch.tensor([0, n], dtype=torch.int32, device="cuda").repeat(2048)
+    start = torch.cat([start, start[:1]])
+    paged.attention(q, torch.zeros(1, 16, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(4096, 1, dtype=torch.int32, device="cuda"),
+                    start, torch.zeros(4096, dtype=torch.int32, device="cuda"), out=out)
+    with pytest.raises(abi.Ds4cError):
+        fp8.sync()
+    assert (out[:1024] == 0).all() and ((out == 0) | (out == 7.0)).all()
+
+
 def test_pages_past_32_bits():
     """A pool of 6 GB: rows beyond 2^31 elements and 2^32 bytes."""
     g = gen(18)

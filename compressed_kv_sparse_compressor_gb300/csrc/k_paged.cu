@@ -36,7 +36,7 @@
 //   of a tile (1.2k cycles) lies between its two products.  Without softmax 3.4 ms.
 // 32 sequences of one token at 65536, narrow: 350 us, 6.1 TB/s: memory.
 // One token at 8192: 20 us: launches, one tile and the parts' way through L2.
-// 64 sequences of 1 to 128 tokens, a window of 128 and compressed rows: 125 us; three chunks of 128 tokens, 24 heads of 128: 104 us:
+// 1640 tokens of ten sequences, a window of 128 and compressed rows: 125 us; chunks of 1531, 700 and 64 tokens, 24 heads of 128: 104 us:
 //   the softmax's warps between their barriers (1.6 instructions a cycle of 4), tensor pipe 27 %.
 //
 // Warps: 0 loads (queries and tiles by TMA, a box per page), 1 issues the MMAs, 4-7 and 8-11 softmax and output.
@@ -149,6 +149,7 @@ struct Params {
     int raw_rows, comp_rows;   // rows of the pools: the first row past the end, which TMA fills with zeros
     int n_seq, n_tok, n_heads, window, ratio;
     int hg, tt, groups;        // heads and tokens of an item, head groups
+    int hg_inv;                // 65536 / hg + 1: column c < 128 is head c - (c * hg_inv >> 16) * hg of its group
     int over;                  // an item's start and end, in tiles
     int small, by_item;        // each CTA cuts for itself; parts lie by items
     int max_items;             // of starts that rise within the tokens
@@ -577,10 +578,14 @@ struct Work {
     const Params &p;
     Start from, to;
     int i;
-    Item it;
+    Item it, ahead;
     int tiles, tb, te;
     __device__ Work(const Params &p_, const Start &from_, const Start &to_) : p(p_), from(from_), to(to_), i(from_.item - 1) {}
-    __device__ __forceinline__ bool next() {                    // the next item that this CTA has something of
+    // Item i + 1, on its way before it is asked for.
+    __device__ __forceinline__ void fetch() {
+        if (i + 1 < to.item || (i + 1 == to.item && to.y > 0)) ahead = p.plan.items[i + 1];
+    }
+    __device__ __forceinline__ bool next() {                    // the next item that this CTA has something of; fetch() once before
         for (;;) {
             i++;
             if (i > to.item || (i == to.item && to.y == 0)) return false;
@@ -918,24 +923,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         s[c + 3] = fmaf(s[c + 3], p.scale_log2, -m.w);
                     }
                 };
-                float most = -INFINITY, least = is_full ? 0.f : INFINITY;   // fmaxf and fminf pass NaN over
+                float most = -INFINITY;                         // fmaxf and fminf pass NaN over
+                bool finite = true;                             // some logit of the row is a number
                 if (mine > 0) {
                     load();
                     if (!is_full) {
-                        if (mine == C) {
+                        float least = fabsf(s[0]);
+                        if (__any_sync(0xffffffffu, !(least < INFINITY))) {   // not the first: the others too
 #pragma unroll
-                            for (int c = 0; c < C; c++) least = fminf(least, fabsf(s[c]));
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < C; c++) least = c < mine ? fminf(least, fabsf(s[c])) : least;
+                            for (int c = 1; c < C; c++) least = c < mine ? fminf(least, fabsf(s[c])) : least;
                         }
+                        finite = least < INFINITY;
                         mask();
                     }
                     scale();
 #pragma unroll
                     for (int c = 0; c < C; c += 2) most = fmaxf(fmaxf(most, s[c]), s[c + 1]);
                 }
-                const bool finite = least < INFINITY;           // some logit of the row is a number
                 const bool moves = group_any(id, most > TAU);
                 if (moves) {
                     // the tile's largest logit of each column, the new references and the factors 2^(old - new)
@@ -1082,7 +1086,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             // four lanes store 64 bytes of a head.
             const uint32_t turn = smem_u32(sm + S::OFF_TURN) + (S::OWN_TURN ? grp * 8192 : grp * CHUNK) + q4 * 2048;
             const uint8_t *turned = sm + S::OFF_TURN + (S::OWN_TURN ? grp * 8192 : grp * CHUNK) + q4 * 2048;
-#pragma unroll
+#pragma unroll(S::HELD > 0 ? C / 32 : 1)
             for (int c0 = 0; c0 < C; c0 += 32) {
                 if (c0 >= mine || !ok || (D == 64 && q4 >= 2)) break;
                 float2 inv[4];                                  // of columns c0 + 8 i + 2 (lane % 4) and the next
@@ -1091,9 +1095,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 __nv_bfloat16 *dst[4];                          // rows 8 k + lane / 4, null out of use
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const int c = col0 + c0 + 8 * k + lane / 4, h = w.it.head0 + c % p.hg;
+                    const int c = col0 + c0 + 8 * k + lane / 4, tok = c * p.hg_inv >> 16, h = w.it.head0 + c - tok * p.hg;
                     dst[k] = c0 + 8 * k + lane / 4 < mine && h < p.n_heads
-                                 ? p.out + (w.it.tok0 + c / p.hg) * p.out_token + h * p.out_head + 32 * q4 + 8 * (lane % 4) : nullptr;
+                                 ? p.out + (w.it.tok0 + tok) * p.out_token + h * p.out_head + 32 * q4 + 8 * (lane % 4) : nullptr;
                 }
                 if (!whole) {                                   // as they are, a line of a column's d to a store
                     float *o = p.plan.part_o + (part * N + col0 + c0) * D + 32 * q4;
@@ -1173,6 +1177,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
 }
 
+// `op` over the block's values, in an order that is always the same; sums: a value for each warp.
+template <typename Op>
+__device__ __forceinline__ float block_all(float x, Op op, float *sums) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
+    __syncthreads();
+    float all = sums[0];
+#pragma unroll
+    for (int w = 1; w < JOIN_THREADS / 32; w++) all = op(all, sums[w]);
+    return all;
+}
+
 // Joins the parts of the divided items.  Few items (FEW), perhaps many parts: a block for each item, column and 128 of
 // d, whose threads share the parts; else, mostly two or three parts: a thread takes all parts of its values.
 template <int D, bool WIDE, bool FEW>
@@ -1180,7 +1197,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
     constexpr int N = Shape<D, WIDE>::N, SLICE = FEW && D > 128 ? 128 : D, SLICES = D / SLICE;
     constexpr int LANES = SLICE / 4;                           // threads of a column, four values each
     constexpr int COLS = FEW ? 1 : JOIN_THREADS / LANES, GROUPS = JOIN_THREADS / LANES / COLS;
-    __shared__ float weight[FEW ? MAX_GRID : 1], denom[FEW ? MAX_GRID : 1];
+    constexpr int AHEAD = 8;
+    static_assert(MAX_GRID <= JOIN_THREADS, "a thread for a part");
+    __shared__ float weight[FEW ? JOIN_THREADS : 1], red[2][JOIN_THREADS / 32];
     __shared__ __align__(16) float sums[FEW ? GROUPS : 1][SLICE];
     pdl_wait();
     pdl_launch_dependents();
@@ -1202,28 +1221,32 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
         acc.w = fmaf(f, v.w, acc.w);
     };
     if (FEW) {
-        // the first parts' values are on their way while the weights are formed
+        // The first AHEAD parts' values of each group are on their way while the weights are formed, a thread for a part.
         const float *src = o + (grp == 0 ? slot0 : slot1 + 2 * (grp - 1)) * N * D;
-        float4 first = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (grp < n) first = *reinterpret_cast<const float4 *>(src);
-        for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
-            weight[i] = m_of(i);
-            denom[i] = l_of(i);
+        float4 v[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; k++) {
+            if (grp + k * GROUPS < n) v[k] = *reinterpret_cast<const float4 *>(src);
+            src = k == 0 ? o + (slot1 + 2 * (grp + GROUPS - 1)) * N * D : src + (int64_t)2 * GROUPS * N * D;
         }
-        __syncthreads();
-        for (int i = 0; i < n; i++) m = fmaxf(m, weight[i]);
-        for (int i = 0; i < n; i++) den = fmaf(ex2(weight[i] - m), denom[i], den);
-        if (grp < n) add(first, ex2(weight[grp] - m));
-        src = o + (slot1 + 2 * (grp + GROUPS - 1)) * N * D;
+        const bool there = threadIdx.x < n;
+        const float mi = there ? m_of(threadIdx.x) : NONE, li = there ? l_of(threadIdx.x) : 0.f;
+        m = block_all(mi, [](float x, float y) { return fmaxf(x, y); }, red[0]);
+        const float f = ex2(mi - m);
+        weight[threadIdx.x] = f;
+        den = block_all(there ? f * li : 0.f, [](float x, float y) { return x + y; }, red[1]);
+#pragma unroll
+        for (int k = 0; k < AHEAD; k++)
+            if (grp + k * GROUPS < n) add(v[k], weight[grp + k * GROUPS]);
 #pragma unroll 4
-        for (int i = grp + GROUPS; i < n; i += GROUPS, src += (int64_t)2 * GROUPS * N * D)
-            add(*reinterpret_cast<const float4 *>(src), ex2(weight[i] - m));
+        for (int i = grp + AHEAD * GROUPS; i < n; i += GROUPS, src += (int64_t)2 * GROUPS * N * D)
+            add(*reinterpret_cast<const float4 *>(src), weight[i]);
         *reinterpret_cast<float4 *>(&sums[grp][4 * lane]) = acc;
         __syncthreads();
         if (grp > 0) return;
         for (int k = 1; k < GROUPS; k++) {
-            const float4 v = *reinterpret_cast<const float4 *>(&sums[k][4 * lane]);
-            acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+            const float4 u = *reinterpret_cast<const float4 *>(&sums[k][4 * lane]);
+            acc.x += u.x; acc.y += u.y; acc.z += u.z; acc.w += u.w;
         }
     } else {
         for (int i = 0; i < n; i++) m = fmaxf(m, m_of(i));
@@ -1383,6 +1406,7 @@ cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStrea
     const bool wide = a.head_dim == 512 && (a.n_heads > 64 || (uint64_t)a.n_tok * a.n_heads >= WIDE_COLUMNS * a.n_seq);
     const Split c = split_of(a.n_heads, a.head_dim, wide);
     p.hg = c.hg; p.groups = c.groups; p.tt = c.tt;
+    p.hg_inv = 65536 / c.hg + 1;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.n_heads, a.head_dim, wide);
     auto run = [&](auto win) {

@@ -3,7 +3,7 @@
 // over the rows x_k that the token sees (raw rows of a window, compressed rows), K = V = the row.
 //
 // A work item is a sequence's next tokens whose heads fill the N columns of the MMAs: N = 128 (one token of 128 heads,
-// several tokens of fewer, or a group of a wide layer's heads), at head_dim 512 64 where there are few columns (narrow
+// several tokens of fewer), at head_dim 512 64 where there are few columns (narrow
 // items, queries resident) and 128 where there are many (wide items).  For
 // each tile of 128 rows, rows on the TMEM lanes, (token, head) columns side by side:
 //   S^T[row][col] = sum_d X[row][d] Q[col][d]         M = 128 rows, K = head_dim
@@ -122,14 +122,14 @@ struct Pool {
     int64_t ld;
     int n_pages, page_log, max_pages;
 };
-struct Item {
-    int seq, tok0, n_tok, head0;
+struct __align__(16) Item {
+    int seq, tok0, n_tok;
+    int alone;                 // the sequence's only item: its rows come from memory
     int t0, raw0, raws, comps; // position of its first token, first raw row, 16-row pieces of raw and of compressed rows
-    int alone;                 // the sequence's only item (or the first group of its heads): its rows come from memory
 };
 struct Start { int item, y; };
 // The parts of a divided item: the second of CTA `cta`, then the first of the n - 1 CTAs behind it.
-struct Parts { int cta, n, tok0, cols, head0; };
+struct __align__(16) Parts { int cta, n, tok0, cols; };
 struct Totals { long long cost; int items, ctas; };
 // Workspace: totals, each CTA's first item and place in it, the parts of an item (by item if there are few, else by the
 // CTA that has its first tile), the items, the parts.
@@ -148,8 +148,8 @@ struct Params {
     Pool raw, comp;
     int raw_rows, comp_rows;   // rows of the pools: the first row past the end, which TMA fills with zeros
     int n_seq, n_tok, n_heads, window, ratio;
-    int hg, tt, groups;        // heads and tokens of an item, head groups
-    int hg_inv;                // 65536 / hg + 1: column c < 128 is head c - (c * hg_inv >> 16) * hg of its group
+    int tt;                    // tokens of an item
+    int heads_inv;             // 65536 / n_heads + 1: column c < 128 is of token c * heads_inv >> 16
     int over;                  // an item's start and end, in tiles
     int small, by_item;        // each CTA cuts for itself; parts lie by items
     int max_items;             // of starts that rise within the tokens
@@ -356,14 +356,13 @@ constexpr int MAX_LENGTH = 1 << 30;
 constexpr int PIECE = 16, PIECES = ROWS / PIECE;               // a tile is 8 pieces of 16 rows, one K step of the second product each
 __device__ __forceinline__ int tiles_of(const Item &it) { return (it.raws + it.comps + PIECES - 1) / PIECES; }
 
-// The item of tokens j .. and head group g of a sequence of n new tokens from token b on, `length` long with them.
-__device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n, int length, int j, int g) {
+// The item of tokens j .. of a sequence of n new tokens from token b on, `length` long with them.
+__device__ __forceinline__ Item make_item(const Params &p, int seq, int b, int n, int length, int j) {
     Item it;
     it.seq = seq;
     it.tok0 = b + j;
     it.n_tok = min(p.tt, n - j);
-    it.head0 = g * p.hg;
-    it.alone = n <= p.tt && g == 0;
+    it.alone = n <= p.tt;
     // positions t0 .. end - 1; a token before 0 sees nothing wherever it is
     it.t0 = max(length, 0) - n + j;
     const int end = it.t0 + it.n_tok;
@@ -384,7 +383,7 @@ __device__ __forceinline__ int items_of(const Params &p, int b, int e, int lengt
         if (report) atomicOr(&g_paged_err, 2u);
         return 0;
     }
-    return (e - b + p.tt - 1) / p.tt * p.groups;
+    return (e - b + p.tt - 1) / p.tt;
 }
 // The last of n ascending values v that is <= x.
 template <typename T>
@@ -406,11 +405,9 @@ template <typename Visit>
 __device__ __forceinline__ void walk_items(const Params &p, const int *first, const int *begin, const int *length, int from, int to, Visit visit) {
     if (from >= to) return;
     int s = last_at_most(first, p.n_seq, from), k = from - first[s];
-    int j = k / p.groups * p.tt, g = k % p.groups;
+    int j = k * p.tt;
     for (int i = from; i < to; i++) {
-        if (!visit(i, make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], j, g))) return;
-        if (++g < p.groups) continue;
-        g = 0;
+        if (!visit(i, make_item(p, s, begin[s], begin[s + 1] - begin[s], length[s], j))) return;
         j += p.tt;
         if (s + 1 < p.n_seq && first[s + 1] <= i + 1) {
             j = 0;
@@ -504,6 +501,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     if (tid == 0) *p.plan.totals = {all, n_items, ctas};
 }
 
+// Place k of n even cuts; small numbers by 32-bit arithmetic (a 64-bit division takes 100 instructions).
+__device__ __forceinline__ long long cut_at(long long all, int k, int n) {
+    if (all < 1 << 23) return (uint32_t)all * (uint32_t)k / (uint32_t)n;      // k <= MAX_GRID = 2^8
+    return all * k / n;
+}
+// The cut whose share has the place in front of `end`.
+__device__ __forceinline__ int cut_before(long long all, long long end, int n) {
+    if (all < 1 << 23) return (int)(((uint32_t)end * (uint32_t)n - 1) / (uint32_t)all);
+    return (int)((end * n - 1) / all);
+}
+
 // Few items: every CTA weighs them all and finds its own cuts.  Writes the items that it has something of, and who has the
 // parts of those it starts.  scratch: SMALL_SCRATCH bytes of shared memory, 16-byte aligned.
 constexpr int SMALL_SCRATCH = 3 * 4 * (SMALL + 4) + 16 * (SMALL / 32) + 64;
@@ -538,11 +546,11 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
     const long long end = block_scan<SMALL, long long>(cost, sums_l, all), here = end - cost;
     const int ctas = n_items ? ctas_of(all, grid) : 0;
     if (tid == 0) *out = {{n_items, 0}, {n_items, 0}};
-    if (!p.by_item && tid == 0) p.plan.parts[cta] = {cta, 0, 0, 0, 0};
-    if (p.by_item && cta == 0 && tid >= n_items && tid < p.max_items) p.plan.parts[tid] = {0, 0, 0, 0, 0};   // entries of no item
+    if (!p.by_item && tid == 0) p.plan.parts[cta] = {cta, 0, 0, 0};
+    if (p.by_item && cta == 0 && tid >= n_items && tid < p.max_items) p.plan.parts[tid] = {0, 0, 0, 0};   // entries of no item
     __syncthreads();
     if (cta < ctas) {
-        const long long a = all * cta / ctas, b = all * (cta + 1) / ctas;      // this CTA's share: the places a .. b - 1
+        const long long a = cut_at(all, cta, ctas), b = cut_at(all, cta + 1, ctas);      // this CTA's share: the places a .. b - 1
         if (a < end && b > here) {
             long long at = here;
             walk_items(p, first, begin, length, i0, i1, [&](int i, const Item &it) {
@@ -557,8 +565,8 @@ __device__ __forceinline__ Cuts plan_small(const Params &p, uint8_t *scratch) {
                     const int te = b < next ? tiles_before((int)(b - at), tiles, p.over) : tiles;
                     const bool divided = tb == 0 && te > 0 && te < tiles;
                     if (divided || (p.by_item && tb == 0 && (te > 0 || tiles == 0)))
-                        p.plan.parts[p.by_item ? i : cta] = {cta, divided ? (int)((next * ctas - 1) / all) - cta + 1 : 1, it.tok0,
-                                                             it.n_tok * p.hg, it.head0};
+                        p.plan.parts[p.by_item ? i : cta] = {cta, divided ? cut_before(all, next, ctas) - cta + 1 : 1, it.tok0,
+                                                             it.n_tok * p.n_heads};
                 }
                 at = next;
                 return at <= b;                                 // the item that starts at b too
@@ -578,14 +586,10 @@ struct Work {
     const Params &p;
     Start from, to;
     int i;
-    Item it, ahead;
+    Item it;
     int tiles, tb, te;
     __device__ Work(const Params &p_, const Start &from_, const Start &to_) : p(p_), from(from_), to(to_), i(from_.item - 1) {}
-    // Item i + 1, on its way before it is asked for.
-    __device__ __forceinline__ void fetch() {
-        if (i + 1 < to.item || (i + 1 == to.item && to.y > 0)) ahead = p.plan.items[i + 1];
-    }
-    __device__ __forceinline__ bool next() {                    // the next item that this CTA has something of; fetch() once before
+    __device__ __forceinline__ bool next() {                    // the next item that this CTA has something of
         for (;;) {
             i++;
             if (i > to.item || (i == to.item && to.y == 0)) return false;
@@ -669,14 +673,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         from = p.plan.start[blockIdx.x];
         to = p.plan.start[blockIdx.x + 1];
         if (threadIdx.x == 0) {
-            Parts parts{(int)blockIdx.x, 0, 0, 0, 0};
+            Parts parts{(int)blockIdx.x, 0, 0, 0};
             const Totals t = *p.plan.totals;
             if (to.y > 0) {
                 const Item it = p.plan.items[to.item];
                 const int tiles = tiles_of(it), te = tiles_before(to.y, tiles, p.over);
                 if (te > 0 && te < tiles && !(from.item == to.item && tiles_before(from.y, tiles, p.over) > 0)) {
                     const long long end = t.cost * (blockIdx.x + 1) / t.ctas - to.y + p.over + tiles;
-                    parts = {(int)blockIdx.x, (int)((end * t.ctas - 1) / t.cost) - (int)blockIdx.x + 1, it.tok0, it.n_tok * p.hg, it.head0};
+                    parts = {(int)blockIdx.x, (int)((end * t.ctas - 1) / t.cost) - (int)blockIdx.x + 1, it.tok0, it.n_tok * p.n_heads};
                 }
             }
             p.plan.parts[blockIdx.x] = parts;
@@ -698,9 +702,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 if (ok && n_q >= (uint32_t)S::NQ) ok = warp_wait(bar(B_QEMPTY) + 8 * i, (n_q / S::NQ - 1) & 1, abort);
                 if (!ok) return;
                 if (elect()) {
-                    mbar_expect_tx(fb, chunks * p.hg * p.tt * 128);
+                    mbar_expect_tx(fb, chunks * p.n_heads * p.tt * 128);
                     for (int c = 0; c < chunks; c++)
-                        tma_3d(smem_u32(sm + S::OFF_Q + (i * 2 + c) * S::Q_CHUNK), &q_map, 64 * (c0 + c), w.it.head0, w.it.tok0, fb);
+                        tma_3d(smem_u32(sm + S::OFF_Q + (i * 2 + c) * S::Q_CHUNK), &q_map, 64 * (c0 + c), 0, w.it.tok0, fb);
                 }
                 n_q++;
                 __syncwarp();
@@ -854,7 +858,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         const int u0 = C == 64 ? 0 : grp * 4;                   // first 16-byte unit of the group's columns
         uint32_t g = 0, items = 0;
         while (w.next()) {
-            const int n_cols = w.it.n_tok * p.hg, mine = min(max(n_cols - col0, 0), C);   // this group's columns in use
+            const int n_cols = w.it.n_tok * p.n_heads, mine = min(max(n_cols - col0, 0), C);   // this group's columns in use
             const int t0 = w.it.t0;
             // compressed rows that all, and that some of its tokens see
             const int comp_all = p.ratio && t0 >= 0 ? (t0 + 1) / p.ratio : 0, comp_some = p.ratio ? max(t0 + w.it.n_tok, 0) / p.ratio : 0;
@@ -889,8 +893,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     const int n = w.it.n_tok;
                     const int from = raw ? max(row - t0, 0) : row < comp_all ? 0 : row < comp_some ? (int)((long long)(row + 1) * p.ratio - 1 - t0) : n;
                     const int to = WIN && raw ? min(n, row - t0 + p.window) : n;
-                    ca = min(from, n) * p.hg - col0;
-                    cb = !WIN || q < w.it.raws + w.it.comps ? max(to, 0) * p.hg - col0 : ca;
+                    ca = min(from, n) * p.n_heads - col0;
+                    cb = !WIN || q < w.it.raws + w.it.comps ? max(to, 0) * p.n_heads - col0 : ca;
                 }
                 if (ok) ok = warp_wait(bar(B_SFULL + sb), (g / S::NS) & 1, abort);
                 fence_after();
@@ -1095,8 +1099,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 __nv_bfloat16 *dst[4];                          // rows 8 k + lane / 4, null out of use
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const int c = col0 + c0 + 8 * k + lane / 4, tok = c * p.hg_inv >> 16, h = w.it.head0 + c - tok * p.hg;
-                    dst[k] = c0 + 8 * k + lane / 4 < mine && h < p.n_heads
+                    const int c = col0 + c0 + 8 * k + lane / 4, tok = c * p.heads_inv >> 16, h = c - tok * p.n_heads;
+                    dst[k] = c0 + 8 * k + lane / 4 < mine
                                  ? p.out + (w.it.tok0 + tok) * p.out_token + h * p.out_head + 32 * q4 + 8 * (lane % 4) : nullptr;
                 }
                 if (!whole) {                                   // as they are, a line of a column's d to a store
@@ -1206,7 +1210,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
     const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, slice = blockIdx.x % SLICES, at = blockIdx.x / SLICES;
     const Parts parts = p.plan.parts[at / (N / COLS)];
     const int n = parts.n, col = at % (N / COLS) * COLS + (FEW ? 0 : grp);
-    if (n < 2 || col >= parts.cols || parts.head0 + col % p.hg >= p.n_heads) return;
+    if (n < 2 || col >= parts.cols) return;
     // part 0 lies alone, the others every second place behind it
     const int64_t slot0 = 2 * parts.cta + 1, slot1 = 2 * parts.cta + 2;
     const float *ml = p.plan.part_ml + col, *o = p.plan.part_o + (int64_t)col * D + slice * SLICE + 4 * lane;
@@ -1261,7 +1265,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
     }
     const float inv = den == 0.f ? 0.f : 1.0f / den;
     if (den == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t to = (parts.tok0 + col / p.hg) * p.out_token + (parts.head0 + col % p.hg) * p.out_head + slice * SLICE + 4 * lane;
+    const int tok = col * p.heads_inv >> 16;
+    const int64_t to = (parts.tok0 + tok) * p.out_token + (col - tok * p.n_heads) * p.out_head + slice * SLICE + 4 * lane;
     *reinterpret_cast<uint2 *>(p.out + to) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
 }
 
@@ -1311,14 +1316,11 @@ int sm_count() {
     return n > 0 ? n : 148;
 }
 
-struct Split { int n, hg, groups, tt; };
-Split split_of(uint32_t n_heads, uint32_t d, bool wide) {
-    const int n = d == 512 && !wide ? 64 : 128, h = (int)n_heads, groups = (h + n - 1) / n, hg = (h + groups - 1) / groups;
-    return {n, hg, groups, n / hg};
-}
+// Columns of an item; n_heads are at most that.
+int columns(uint32_t d, bool wide) { return d == 512 && !wide ? 64 : 128; }
 // The workspace's regions; returns its size.
-size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_heads, uint32_t d, bool wide) {
-    const Split c = split_of(n_heads, d, wide);
+size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t d, bool wide) {
+    const int n = columns(d, wide);
     size_t at = 0;
     auto region = [&](size_t bytes) {
         const size_t here = at;
@@ -1329,9 +1331,9 @@ size_t lay_out(Plan *plan, uint8_t *ws, int grid, uint32_t n_tok, uint32_t n_hea
     o.totals = reinterpret_cast<Totals *>(region(sizeof(Totals)));
     o.start = reinterpret_cast<Start *>(region(sizeof(Start) * (grid + 1)));
     o.parts = reinterpret_cast<Parts *>(region(sizeof(Parts) * (grid > FEW_ITEMS ? grid : FEW_ITEMS)));
-    o.items = reinterpret_cast<Item *>(region(sizeof(Item) * (size_t)n_tok * c.groups));
-    o.part_ml = reinterpret_cast<float *>(region((size_t)2 * grid * 2 * c.n * 4));
-    o.part_o = reinterpret_cast<float *>(region((size_t)2 * grid * c.n * d * 4));
+    o.items = reinterpret_cast<Item *>(region(sizeof(Item) * (size_t)n_tok));
+    o.part_ml = reinterpret_cast<float *>(region((size_t)2 * grid * 2 * n * 4));
+    o.part_o = reinterpret_cast<float *>(region((size_t)2 * grid * n * d * 4));
     if (plan) *plan = o;
     return at;
 }
@@ -1340,8 +1342,8 @@ template <int D, bool WIDE, bool WIN>
 cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream_t s) {
     using S = Shape<D, WIDE>;
     p.over = S::OVER;
-    const uint64_t whole = a.n_tok / (uint32_t)p.tt + a.n_seq;    // items of a head group, at most; none is without a token
-    const uint64_t items = (whole < a.n_tok ? whole : a.n_tok) * p.groups;
+    const uint64_t whole = a.n_tok / (uint32_t)p.tt + a.n_seq;    // items at most; none is without a token
+    const uint64_t items = whole < a.n_tok ? whole : a.n_tok;
     p.small = a.n_seq <= SMALL && items <= SMALL_ITEMS;
     p.by_item = p.small && items <= FEW_ITEMS;
     p.max_items = (int)items;
@@ -1349,7 +1351,7 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
     {
         const cuuint64_t dims[3] = {D, a.n_heads, a.n_tok};
         const cuuint64_t strides[2] = {a.n_heads > 1 ? (cuuint64_t)a.q_head * 2 : D * 2, a.n_tok > 1 ? (cuuint64_t)a.q_token * 2 : D * 2};
-        const cuuint32_t box[3] = {64, (cuuint32_t)p.hg, (cuuint32_t)p.tt};
+        const cuuint32_t box[3] = {64, a.n_heads, (cuuint32_t)p.tt};
         if (!make_map(&qm, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
     if (!pool_map(&rm, a.raw, D, WIN) || !pool_map(&cm, a.ratio ? a.comp : a.raw, D, WIN)) return cudaErrorInvalidValue;
@@ -1380,10 +1382,10 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
 
 }  // namespace
 
-size_t paged_attn_ws_bytes(uint32_t, uint32_t n_tok, uint32_t n_heads, uint32_t head_dim) {
+size_t paged_attn_ws_bytes(uint32_t, uint32_t n_tok, uint32_t, uint32_t head_dim) {
     const int grid = sm_count();
-    const size_t a = lay_out(nullptr, nullptr, grid, n_tok, n_heads, head_dim, false);
-    const size_t b = lay_out(nullptr, nullptr, grid, n_tok, n_heads, head_dim, true);
+    const size_t a = lay_out(nullptr, nullptr, grid, n_tok, head_dim, false);
+    const size_t b = lay_out(nullptr, nullptr, grid, n_tok, head_dim, true);
     return a > b ? a : b;
 }
 
@@ -1404,11 +1406,10 @@ cudaError_t launch_paged_attn(const ds4c_paged_attn_args &a, void *ws, cudaStrea
     p.window = a.window >= (uint32_t)MAX_LENGTH ? 0 : (int)a.window;   // as long as any sequence: none
     p.ratio = (int)a.ratio;
     const bool wide = a.head_dim == 512 && (a.n_heads > 64 || (uint64_t)a.n_tok * a.n_heads >= WIDE_COLUMNS * a.n_seq);
-    const Split c = split_of(a.n_heads, a.head_dim, wide);
-    p.hg = c.hg; p.groups = c.groups; p.tt = c.tt;
-    p.hg_inv = 65536 / c.hg + 1;
+    p.tt = columns(a.head_dim, wide) / p.n_heads;
+    p.heads_inv = 65536 / p.n_heads + 1;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.n_heads, a.head_dim, wide);
+    lay_out(&p.plan, static_cast<uint8_t *>(ws), grid, a.n_tok, a.head_dim, wide);
     auto run = [&](auto win) {
         constexpr bool WIN = decltype(win)::value;
         return a.head_dim == 64 ? launch<64, false, WIN>(a, p, grid, s) : a.head_dim == 128 ? launch<128, false, WIN>(a, p, grid, s)

@@ -67,7 +67,9 @@ constexpr int PLAN_THREADS = 1024;
 constexpr int SMALL = THREADS;                                      // sequences up to which each CTA cuts for itself,
 constexpr int SMALL_ITEMS = 8 * SMALL;                              // and items
 constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
-constexpr int FEW_ITEMS = 64;                                       // joined by a block for each column
+// Items up to which parts are joined by a block for each column, whose threads share them (single tokens of 64 heads: 6 at 20000
+// 51 us and 64 otherwise, 12 76 and 80, 24 123 and 117, 32 at 64K 363 and 352).
+constexpr int FEW_ITEMS = 16;
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
 // Columns (new tokens x heads) a sequence on average, from which items are wide at head_dim 512.  A wide tile takes 8.4k
 // cycles for 128 columns, a narrow one 5.2k (6.5k from memory) for 64: 4096 tokens at 12288 4.35 ms wide, 5.93 narrow; 2 tokens
@@ -1194,80 +1196,113 @@ __device__ __forceinline__ float block_all(float x, Op op, float *sums) {
     return all;
 }
 
-// Joins the parts of the divided items.  Few items (FEW), perhaps many parts: a block for each item, column and 128 of
-// d, whose threads share the parts; else, mostly two or three parts: a thread takes all parts of its values.
-template <int D, bool WIDE, bool FEW>
-__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
-    constexpr int N = Shape<D, WIDE>::N, SLICE = FEW && D > 128 ? 128 : D, SLICES = D / SLICE;
-    constexpr int LANES = SLICE / 4;                           // threads of a column, four values each
-    constexpr int COLS = FEW ? 1 : JOIN_THREADS / LANES, GROUPS = JOIN_THREADS / LANES / COLS;
-    constexpr int AHEAD = 8;
-    static_assert(MAX_GRID <= JOIN_THREADS, "a thread for a part");
-    __shared__ float weight[FEW ? JOIN_THREADS : 1], red[2][JOIN_THREADS / 32];
-    __shared__ __align__(16) float sums[FEW ? GROUPS : 1][SLICE];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, slice = blockIdx.x % SLICES, at = blockIdx.x / SLICES;
-    const Parts parts = p.plan.parts[at / (N / COLS)];
-    const int n = parts.n, col = at % (N / COLS) * COLS + (FEW ? 0 : grp);
-    if (n < 2 || col >= parts.cols) return;
-    // part 0 lies alone, the others every second place behind it
-    const int64_t slot0 = 2 * parts.cta + 1, slot1 = 2 * parts.cta + 2;
-    const float *ml = p.plan.part_ml + col, *o = p.plan.part_o + (int64_t)col * D + slice * SLICE + 4 * lane;
-    auto m_of = [&](int i) { return ml[(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * 2 * N]; };
-    auto l_of = [&](int i) { return ml[(i == 0 ? slot0 : slot1 + 2 * (i - 1)) * 2 * N + N]; };
-    float m = NONE, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4 &v, float f) {
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
-    };
-    if (FEW) {
-        // The first AHEAD parts' values of each group are on their way while the weights are formed, a thread for a part.
-        const float *src = o + (grp == 0 ? slot0 : slot1 + 2 * (grp - 1)) * N * D;
-        float4 v[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; k++) {
-            if (grp + k * GROUPS < n) v[k] = *reinterpret_cast<const float4 *>(src);
-            src = k == 0 ? o + (slot1 + 2 * (grp + GROUPS - 1)) * N * D : src + (int64_t)2 * GROUPS * N * D;
-        }
-        const bool there = threadIdx.x < n;
-        const float mi = there ? m_of(threadIdx.x) : NONE, li = there ? l_of(threadIdx.x) : 0.f;
-        m = block_all(mi, [](float x, float y) { return fmaxf(x, y); }, red[0]);
-        const float f = ex2(mi - m);
-        weight[threadIdx.x] = f;
-        den = block_all(there ? f * li : 0.f, [](float x, float y) { return x + y; }, red[1]);
-#pragma unroll
-        for (int k = 0; k < AHEAD; k++)
-            if (grp + k * GROUPS < n) add(v[k], weight[grp + k * GROUPS]);
-#pragma unroll 4
-        for (int i = grp + AHEAD * GROUPS; i < n; i += GROUPS, src += (int64_t)2 * GROUPS * N * D)
-            add(*reinterpret_cast<const float4 *>(src), weight[i]);
-        *reinterpret_cast<float4 *>(&sums[grp][4 * lane]) = acc;
-        __syncthreads();
-        if (grp > 0) return;
-        for (int k = 1; k < GROUPS; k++) {
-            const float4 u = *reinterpret_cast<const float4 *>(&sums[k][4 * lane]);
-            acc.x += u.x; acc.y += u.y; acc.z += u.z; acc.w += u.w;
-        }
-    } else {
-        for (int i = 0; i < n; i++) m = fmaxf(m, m_of(i));
-        const float *src = o + slot1 * N * D;
-        add(*reinterpret_cast<const float4 *>(o + slot0 * N * D), ex2(m_of(0) - m));
-        den = ex2(m_of(0) - m) * l_of(0);
-        for (int i = 1; i < n; i++, src += (int64_t)2 * N * D) {
-            const float f = ex2(m_of(i) - m);
-            add(*reinterpret_cast<const float4 *>(src), f);
-            den = fmaf(f, l_of(i), den);
-        }
-    }
+// The parts of a divided item: part 0 lies alone, the others every second place behind it.  A column's reference,
+// denominator and values.
+template <int D, int N>
+struct PartsOf {
+    const float *ml, *o;
+    int64_t slot0;
+    __device__ PartsOf(const Plan &plan, const Parts &parts) : ml(plan.part_ml), o(plan.part_o), slot0(2 * parts.cta + 1) {}
+    __device__ int64_t slot(int i) const { return i == 0 ? slot0 : slot0 + 2 * i - 1; }
+    __device__ float reference(int i, int col) const { return ml[slot(i) * 2 * N + col]; }
+    __device__ float denominator(int i, int col) const { return ml[slot(i) * 2 * N + N + col]; }
+    __device__ float4 values(int i, int col, int d) const { return *reinterpret_cast<const float4 *>(o + (slot(i) * N + col) * D + d); }
+};
+__device__ __forceinline__ void add(float4 &acc, const float4 &v, float f) {
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+}
+__device__ __forceinline__ void store_joined(const Params &p, const Parts &parts, int col, int d, float4 acc, float den) {
     const float inv = den == 0.f ? 0.f : 1.0f / den;
     if (den == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int tok = col * p.heads_inv >> 16;
-    const int64_t to = (parts.tok0 + tok) * p.out_token + (col - tok * p.n_heads) * p.out_head + slice * SLICE + 4 * lane;
+    const int64_t to = (parts.tok0 + tok) * p.out_token + (col - tok * p.n_heads) * p.out_head + d;
     *reinterpret_cast<uint2 *>(p.out + to) = make_uint2(pack(acc.x * inv, acc.y * inv), pack(acc.z * inv, acc.w * inv));
+}
+
+// Joins the parts of few items, perhaps many: a block for each item, column and 128 of d, whose threads share the parts.
+// The first AHEAD of each group's values are on their way while the weights are formed, a thread for a part (one token
+// at 8192, 64 parts: 15.5 us; 19.7 with every thread going through all weights first).
+template <int D, int N>
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_few_kernel(const __grid_constant__ Params p) {
+    constexpr int SLICE = D > 128 ? 128 : D, SLICES = D / SLICE;
+    constexpr int LANES = SLICE / 4, GROUPS = JOIN_THREADS / LANES, AHEAD = 8;
+    static_assert(MAX_GRID <= JOIN_THREADS, "a thread for a part");
+    __shared__ float weight[JOIN_THREADS], red[2][JOIN_THREADS / 32];
+    __shared__ __align__(16) float sums[GROUPS][SLICE];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, grp = tid / LANES, d = blockIdx.x % SLICES * SLICE + 4 * (tid % LANES), at = blockIdx.x / SLICES;
+    const Parts parts = p.plan.parts[at / N];
+    const int n = parts.n, col = at % N;
+    if (n < 2 || col >= parts.cols) return;
+    const PartsOf<D, N> of(p.plan, parts);
+    float4 v[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++)
+        if (grp + k * GROUPS < n) v[k] = of.values(grp + k * GROUPS, col, d);
+    const float mi = tid < n ? of.reference(tid, col) : NONE, li = tid < n ? of.denominator(tid, col) : 0.f;
+    const float f = ex2(mi - block_all(mi, [](float x, float y) { return fmaxf(x, y); }, red[0]));
+    weight[tid] = f;
+    const float den = block_all(tid < n ? f * li : 0.f, [](float x, float y) { return x + y; }, red[1]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++)
+        if (grp + k * GROUPS < n) add(acc, v[k], weight[grp + k * GROUPS]);
+#pragma unroll 4
+    for (int i = grp + AHEAD * GROUPS; i < n; i += GROUPS) add(acc, of.values(i, col, d), weight[i]);
+    *reinterpret_cast<float4 *>(&sums[grp][d % SLICE]) = acc;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int k = 1; k < GROUPS; k++) add(acc, *reinterpret_cast<const float4 *>(&sums[k][d % SLICE]), 1.0f);
+    store_joined(p, parts, col, d, acc, den);
+}
+
+// Joins the parts of many items, mostly two or three of each, one entry for each CTA, most of them empty: a thread takes
+// all parts of four values of each of EACH columns, so that the blocks are few.
+constexpr int EACH = 4;
+template <int D, int N>
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
+    constexpr int LANES = D / 4, COLS = JOIN_THREADS / LANES, BLOCKS = N / (COLS * EACH);
+    pdl_wait();
+    pdl_launch_dependents();
+    const Parts parts = p.plan.parts[blockIdx.x / BLOCKS];
+    const int d = threadIdx.x % LANES * 4, col0 = blockIdx.x % BLOCKS * COLS * EACH + threadIdx.x / LANES;
+    if (parts.n < 2 || col0 >= parts.cols) return;
+    const PartsOf<D, N> of(p.plan, parts);
+    float m[EACH], den[EACH];
+    float4 acc[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; e++) {
+        m[e] = NONE;
+        den[e] = 0.f;
+        acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int i = 0; i < parts.n; i++) {
+        float mi[EACH], li[EACH];
+        float4 v[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; e++) {
+            const int col = min(col0 + e * COLS, parts.cols - 1);
+            mi[e] = of.reference(i, col);
+            li[e] = of.denominator(i, col);
+            v[e] = of.values(i, col, d);
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; e++) {
+            const float now = fmaxf(m[e], mi[e]), old = ex2(m[e] - now), f = ex2(mi[e] - now);
+            m[e] = now;
+            den[e] = fmaf(f, li[e], old * den[e]);
+            acc[e] = make_float4(old * acc[e].x, old * acc[e].y, old * acc[e].z, old * acc[e].w);
+            add(acc[e], v[e], f);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < EACH; e++)
+        if (col0 + e * COLS < parts.cols) store_joined(p, parts, col0 + e * COLS, d, acc[e], den[e]);
 }
 
 __global__ void wait_selftest_kernel(int *answers) {
@@ -1375,9 +1410,8 @@ cudaError_t launch(const ds4c_paged_attn_args &a, Params p, int grid, cudaStream
     }
     e = launch_pdl(paged_attn_kernel<D, WIDE, WIN>, dim3(grid), dim3(THREADS), S::SMEM, s, qm, rm, cm, p);
     if (e != cudaSuccess) return e;
-    const int entries = p.by_item ? (int)items : grid;
-    if (p.by_item) return launch_pdl(paged_join_kernel<D, WIDE, true>, dim3(entries * S::N * (D > 128 ? D / 128 : 1)), dim3(JOIN_THREADS), 0, s, p);
-    return launch_pdl(paged_join_kernel<D, WIDE, false>, dim3(entries * (S::N / (JOIN_THREADS / (D / 4)))), dim3(JOIN_THREADS), 0, s, p);
+    if (p.by_item) return launch_pdl(paged_join_few_kernel<D, S::N>, dim3((unsigned)items * S::N * (D > 128 ? D / 128 : 1)), dim3(JOIN_THREADS), 0, s, p);
+    return launch_pdl(paged_join_kernel<D, S::N>, dim3(grid * (S::N / (JOIN_THREADS / (D / 4) * EACH))), dim3(JOIN_THREADS), 0, s, p);
 }
 
 }  // namespace

@@ -75,12 +75,14 @@ def attention(q, cache, pages, start, length, *, window: int = 0, scale=None, co
     if qd != 1:
         raise ValueError("q: the rows' elements must be contiguous")
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
-    if out.shape != shape or out.dtype != _BF16 or out.get_device() != dev:
-        raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, expected bfloat16 {tuple(shape)} on cuda:{dev}")
-    ot, oh, od = out.stride()
-    if od != 1:
-        raise ValueError("out: the rows' elements must be contiguous")
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ot, oh = h * d, d
+    else:
+        if out.shape != shape or out.dtype != _BF16 or out.get_device() != dev:
+            raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, expected bfloat16 {tuple(shape)} on cuda:{dev}")
+        ot, oh, od = out.stride()
+        if od != 1:
+            raise ValueError("out: the rows' elements must be contiguous")
     n_seq = length.shape[0] if length.dim() == 1 else -1
     if not 0 <= window < 1 << 31 or not 0 <= ratio < 1 << 31:
         raise ValueError(f"window {window}, ratio {ratio}: 0 to 2^31 - 1")

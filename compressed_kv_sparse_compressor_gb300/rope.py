@@ -88,19 +88,22 @@ def _rows(t, what):
 
 
 def _side(x, out, gain, n, d, dev, what):
-    """The struct's fields for x -> out (the same shape, float32 or bfloat16)."""
+    """The struct's fields for x -> out (the same shape, float32 or bfloat16; allocated in x's type if None), and out."""
     xn, heads, xd, xt, xh = _rows(x, what)
     if xn != n or xd != d or x.get_device() != dev:
         raise ValueError(f"{what}: {tuple(x.shape)} on {x.device}, expected {n} tokens of {d} values on cuda:{dev}")
-    dt = _DTYPES.get(out.dtype)
-    if out is x:
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ot, oh = heads * d, d
+    elif out is x:
         ot, oh = xt, xh
     else:
-        if out.shape != x.shape or out.get_device() != dev or dt is None:
+        if out.shape != x.shape or out.get_device() != dev or out.dtype not in _DTYPES:
             raise ValueError(f"{what}'s output: {out.dtype} {tuple(out.shape)} on {out.device}, expected float32 or bfloat16 "
                              f"{tuple(x.shape)} on cuda:{dev}")
         _, _, _, ot, oh = _rows(out, f"{what}'s output")
-    return x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, 0 if gain is None else _gain(gain, d, dev, what), 0, 0, heads, dt
+    return (x.data_ptr(), out.data_ptr(), xt, xh, ot, oh, 0 if gain is None else _gain(gain, d, dev, what), 0, 0, heads,
+            _DTYPES[out.dtype]), out
 
 
 def _gain(gain, d, dev, what):
@@ -147,9 +150,8 @@ def rotate(x, positions, table: Table, *, first=None, half: bool = False, invers
     undoes a rotation of magnitude 1 and is the gradient of any).  out: x's shape, float32 or bfloat16, x itself
     allowed; allocated in x's type if None."""
     n, d, dev = _check(x, "x")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _run(x, positions, table, first, half, inverse, 0, 0.0, n, d, dev, _side(x, out, None, n, d, dev, "x"), _NO_ROWS)
+    rows, out = _side(x, out, None, n, d, dev, "x")
+    _run(x, positions, table, first, half, inverse, 0, 0.0, n, d, dev, rows, _NO_ROWS)
     return out
 
 
@@ -162,8 +164,7 @@ def norm_rotate(q, positions, table: Table | None, *, gain=None, k=None, k_gain=
     (k's shape, k itself allowed), or to a cache [pages, page rows, d] (one head) or [pages, page rows, k heads, d]:
     token i's rows to slot slots[i] = page * page rows + row (int64; below 0: nowhere)."""
     n, d, dev = _check(q, "q")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rows, out = _side(q, out, gain, n, d, dev, "q")
     if k is None:
         if k_out is not None or cache is not None or slots is not None or k_gain is not None:
             raise ValueError("k's output, gain or slots without k")
@@ -173,8 +174,8 @@ def norm_rotate(q, positions, table: Table | None, *, gain=None, k=None, k_gain=
             raise ValueError(f"k: {k.dtype}, expected q's {q.dtype}")
         if (k_out is None) == (cache is None) or (cache is None) != (slots is None):
             raise ValueError("k needs k_out, or cache and slots")
-        kr = _side(k, k_out, k_gain, n, d, dev, "k") if cache is None else _cached(k, cache, slots, k_gain, n, d, dev)
-    _run(q, positions, table, first, half, False, 1, eps, n, d, dev, _side(q, out, gain, n, d, dev, "q"), kr)
+        kr = _side(k, k_out, k_gain, n, d, dev, "k")[0] if cache is None else _cached(k, cache, slots, k_gain, n, d, dev)
+    _run(q, positions, table, first, half, False, 1, eps, n, d, dev, rows, kr)
     return out
 
 

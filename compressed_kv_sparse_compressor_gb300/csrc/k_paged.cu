@@ -31,12 +31,12 @@
 // is set to zero in shared memory and the columns that see it get NaN weights.
 //
 // What bounds it (64 heads of 512 unless said, inputs not in L2):
-// 4096 tokens behind 8192, wide: 4.35 ms, 1.26 PFLOP/s of the 1.92 that a library product reaches.  A tile takes its CTA 8.3k
+// 4096 tokens behind 8192, wide: 4.30 ms, 1.28 PFLOP/s of the 1.92 that a library product reaches.  A tile takes its CTA 8.3k
 //   cycles where its 64 MMAs take 4.1k alone: S and the first block of O take turns in the same columns, and the softmax
 //   of a tile (1.2k cycles) lies between its two products.  Without softmax 3.4 ms.
-// 32 sequences of one token at 65536, narrow: 350 us, 6.1 TB/s: memory.
-// One token at 8192: 20 us: launches, one tile and the parts' way through L2.
-// 1640 tokens of ten sequences, a window of 128 and compressed rows: 125 us; chunks of 1531, 700 and 64 tokens, 24 heads of 128: 104 us:
+// 32 sequences of one token at 65536, narrow: 335 us, 6.4 TB/s: memory.
+// One token at 8192: 16 us: launches, one tile and the parts' way through L2.
+// 1640 tokens of ten sequences, a window of 128 and compressed rows: 116 us; chunks of 1531, 700 and 64 tokens, 24 heads of 128: 98 us:
 //   the softmax's warps between their barriers (1.6 instructions a cycle of 4), tensor pipe 27 %.
 //
 // Warps: 0 loads (queries and tiles by TMA, a box per page), 1 issues the MMAs, 4-7 and 8-11 softmax and output.
@@ -72,7 +72,7 @@ constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
 constexpr int FEW_ITEMS = 16;
 constexpr int SHORT = 4;                                            // items of up to this many tiles are not divided
 // Columns (new tokens x heads) a sequence on average, from which items are wide at head_dim 512.  A wide tile takes 8.4k
-// cycles for 128 columns, a narrow one 5.2k (6.5k from memory) for 64: 4096 tokens at 12288 4.35 ms wide, 5.93 narrow; 2 tokens
+// cycles for 128 columns, a narrow one 5.2k (6.5k from memory) for 64: 4096 tokens at 12288 4.30 ms wide, 5.93 narrow; 2 tokens
 // of 64 heads at 20 contexts 111 and 117 us, 3 tokens 162 and 156; single tokens of 32 at 64K 471 and 355; 31 of those beside a
 // chunk of 64 582 and 457, of 512 936 and 881.  More than 64 heads are always wide: narrow items would read the rows twice.
 constexpr uint64_t WIDE_COLUMNS = 2048;

@@ -17,7 +17,7 @@
 // Work is cut evenly: the tiles of all items in a row (each with OVER places in front for its queries and output),
 // divided by the number of CTAs; an item that a cut divides leaves parts (sum, reference, denominator), which
 // a second kernel joins in the order of the CTAs.  Items of few tiles are not divided.  Starts and lengths are read on
-// the device, so that a captured call follows them: up to 3072 items of 384 sequences each CTA weighs all of them and
+// the device, so that a captured call follows them: up to 4096 items of 384 sequences each CTA weighs all of them and
 // finds its own cuts (5 to 11 us less than with a kernel in front), more than that a one-block kernel in front does it.
 //
 // Softmax: a thread holds one row's logits for half of the columns (two warpgroups), the denominators as its own
@@ -64,8 +64,9 @@ constexpr int MASKS = 8;                                            // tiles who
 constexpr float TAU = 8.0f;
 constexpr float NONE = -3.0e38f;                                    // reference of a column that saw nothing yet
 constexpr int PLAN_THREADS = 1024;
-constexpr int SMALL = THREADS;                                      // sequences up to which each CTA cuts for itself,
-constexpr int SMALL_ITEMS = 8 * SMALL;                              // and items
+// Sequences and items up to which each CTA cuts for itself (7000 tokens of one sequence, a window of 128, 3500 items: 346 us, and
+// 356 with a kernel in front; 1200 items 135 and 140).
+constexpr int SMALL = THREADS, SMALL_ITEMS = 4096;
 constexpr int JOIN_THREADS = 256, MAX_GRID = 256;
 // Items up to which parts are joined by a block for each column, whose threads share them (single tokens of 64 heads: 6 at 20000
 // 51 us and 64 otherwise, 12 76 and 80, 24 123 and 117, 32 at 64K 363 and 352).

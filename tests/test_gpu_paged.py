@@ -168,6 +168,21 @@ def test_strides():
     assert e.value.status == abi.DS4C_ERR_SHAPE
 
 
+@pytest.mark.parametrize("h,d", [(64, 512), (24, 128)])
+def test_pages_of_several_sequences_and_a_larger_workspace(h, d):
+    """Sequences that begin with the same pages (a shared prompt), and a workspace made for larger calls."""
+    g = gen(24)
+    seqs = [(9, 205), (1, 191), (60, 178), (1, 128)]
+    q, a, kw = setup(g, h, d, 16, seqs, ratio=4)
+    a["pages"][1:, :8] = a["pages"][0, :8]
+    a["comp_pages"][1:, :2] = a["comp_pages"][0, :2]
+    check(q, a, kw, seqs)
+    ws = paged.workspace(40, 5000, 128, 512)
+    out = paged.attention(q, workspace=ws, **a, **kw)
+    fp8.sync()
+    assert torch.equal(out, paged.attention(q, **a, **kw))
+
+
 def test_bad_pages_and_starts_are_reported():
     g = gen(16)
     seqs = [(40, 200), (1, 90), (3, 77)]
@@ -377,7 +392,7 @@ def test_many_sequences_and_many_items(h, d):
     seqs = [(b % 3 if b % 7 else 5, 0) for b in range(450)]
     seqs = [(n, n + int(torch.randint(0, 400, (1,), generator=g, device="cuda"))) for n, _ in seqs]
     check(*setup(g, h, d, 32, seqs, 64 if h == 128 else 0, 4 if h == 64 else 0, tail=2), seqs)
-    seqs = [(1700, 1900), (1, 3000)] if h == 128 else [(7000, 7100), (3, 900)] if h == 64 else [(30000, 30000)]
+    seqs = [(1700, 1900), (1, 3000)] if h == 128 else [(9000, 9100), (3, 900)] if h == 64 else [(30000, 30000)]
     q, a, kw = setup(g, h, d, 128, seqs, 100)
     out = paged.attention(q, **a, **kw)
     fp8.sync()
